@@ -495,6 +495,89 @@ int mimo_pixel_embed(int32_t n, const mimo_image_desc *desc, const uint8_t *src,
                      void *out, int64_t capacity_rows, void *workspace, size_t workspace_bytes,
                      void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention over the plan's chunks.  NeMo Automodel "mimo_v2_flash.vision",
+ * MiMoVisionAttention; docs.rs "cortiq_engine::mimo_vision" module
+ * conventions (each frame its own chunk, grouped heads, band |i - j| <= window
+ * over chunk-local indices, sinks added to key 0's logit).  For row i of a
+ * chunk, query head h and key head g = h / (q_heads / kv_heads):
+ *   s_ij  = scale * q_i . k_j + [j = 0] sink_h   for |i - j| <= window
+ *   lse_i = log sum_j exp s_ij,  p_ij = exp(s_ij - lse_i)
+ *   out_i = sum_j p_ij v_j
+ * A row that sees nothing (sink_h = -inf where key 0 is all its band holds)
+ * has out = 0 and lse = -inf.  Runs on the matrix cores in bf16; logits,
+ * softmax statistics and sums are float32, the probabilities are rounded to
+ * bf16 before their product.  Values of a chunk have to be finite: a NaN or
+ * an infinity in it may reach any of the chunk's rows, but no other chunk's.
+ * Results do not depend on how calls run next to each other (no atomics).
+ * ------------------------------------------------------------------------ */
+
+#define MIMO_HEAD_DIM_MAX 128
+
+/* A bf16 tensor [rows][heads][head_dim] on the device, 16-byte aligned; the
+ * innermost axis is dense, the strides (in values, multiples of 8) are free
+ * otherwise: row_stride in [head_dim, 2^22], head_stride >= 0, and a tensor
+ * that is written must not overlap itself. */
+typedef struct mimo_heads {
+    void *data;
+    int64_t row_stride;
+    int64_t head_stride;
+} mimo_heads;
+
+typedef struct mimo_attention {
+    int64_t rows;       /* rows of every tensor, at most 2^30 */
+    int32_t q_heads;    /* a multiple of kv_heads, at most 65536 */
+    int32_t kv_heads;
+    int32_t head_dim;   /* a multiple of 8 in [8, MIMO_HEAD_DIM_MAX] */
+    int32_t chunks;
+    int32_t window;     /* band half-width; negative: every row sees its whole chunk */
+    float scale;        /* in [1e-18, 1e18]; 1 / sqrt(head_dim) in the tower */
+    const int32_t *cu_seqlens; /* device [chunks + 1]: mimo_chunk_seqlens' boundaries */
+    const float *sink;  /* device [q_heads], or NULL */
+    mimo_heads q, k, v; /* q: q_heads heads; k, v: kv_heads */
+    mimo_heads out;     /* q_heads heads */
+    float *lse;         /* device [q_heads][rows], or NULL (forward only) */
+} mimo_attention;
+
+typedef struct mimo_attention_grads {
+    mimo_heads dout, dq, dk, dv; /* as out, q, k, v */
+    float *dsink;       /* device [q_heads], or NULL */
+} mimo_attention_grads;
+
+/*
+ * Forward: writes out, and lse unless it is NULL (the backward pass needs
+ * it).  The boundaries are read on the device, so a call can be captured into
+ * a graph and replayed for other boundaries of as many chunks.  Chunks may be
+ * empty.  Rows behind the last boundary are neither read nor written.  A
+ * boundary outside [0, rows] or a descending pair makes its chunk empty;
+ * boundaries that make chunks overlap give undefined values in out.
+ * out must not overlap an input.  One kernel launch.  Returns MIMO_OK,
+ * MIMO_E_INVALID, MIMO_E_TOO_LARGE (more than 2^30 rows or chunks, or
+ * (rows / 128 + chunks) * q_heads above 2^31 - 1) or MIMO_E_HIP.
+ */
+int mimo_chunk_attention(const mimo_attention *args, void *stream);
+
+/* Device workspace bytes of the backward pass (0 for sizes it refuses). */
+size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t chunks);
+
+/*
+ * Backward: args as the forward call's, with its out and lse; writes dq, dk,
+ * dv, and dsink unless it is NULL.  The probabilities are recomputed from
+ * lse.  With delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
+ *   dq_i = scale sum_j ds_ij k_j       dk_j = scale sum_{h, i} ds_ij q_i
+ *   dv_j = sum_{h, i} p_ij dout_i      dsink_h = sum_i ds_i0
+ * (the sums over h run over the query heads that share a key head).  ds is
+ * rounded to bf16 before its products; sums are float32.  Gradients are
+ * overwritten, not added to; they must not overlap an input or each other.
+ * Rows behind the last boundary are left as they were.
+ *   workspace  device, >= mimo_chunk_attention_workspace_bytes(...), 16-byte
+ *              aligned; calls that may run at the same time need one each.
+ * Two kernel launches, and one for dsink.  Returns MIMO_OK, MIMO_E_INVALID,
+ * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_chunk_attention_backward(const mimo_attention *args, const mimo_attention_grads *grads, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
 /*
  * Instrumentation.  When start and stop are non-null hipEvent_t handles
  * (passed as void*), every later kernel launch that the library makes on the

@@ -30,3 +30,21 @@ from .processor import (  # noqa: F401
     BatchPlan, ImageProcessor, VideoProcessor, embed_pixels, plan_batch, plan_batch_hf, plan_media,
     prepare_pixel_embed_weights, preprocess, preprocess_hf, stats255, vit_tables,
 )
+
+# The tower's operators work on torch tensors throughout: their module, and
+# torch with it, is imported when the first of them is asked for.
+_TOWER = ("chunk_attention", "chunk_attention_backward", "chunk_attention_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _TOWER or name == "tower":
+        import importlib
+        tower = importlib.import_module(".tower", __name__)
+        for n in _TOWER:
+            globals()[n] = getattr(tower, n)
+        return tower if name == "tower" else globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_TOWER))

@@ -14,11 +14,13 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmimopre.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["plan.cpp", "runtime.hip", "preprocess.hip", "vit_tables.hip", "patch_embed.hip", "hf_resize.hip",
-           "pixel_embed.hip"]
+           "pixel_embed.hip", "chunk_attention.hip"]
 # Code-generation options of one source only.  The contrast kernel's
 # matrix-core products chain through VALU shifts, so their accumulators
-# belong in ordinary VGPRs; the GEMM kernels keep theirs in AGPRs.
-SOURCE_FLAGS = {"hf_resize.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# belong in ordinary VGPRs, as do the attention kernels', which the softmax
+# reads and writes; the GEMM kernels keep theirs in AGPRs.
+SOURCE_FLAGS = {"hf_resize.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "chunk_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 ARCH = "gfx950"
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
