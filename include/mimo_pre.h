@@ -578,12 +578,96 @@ size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32
 int mimo_chunk_attention_backward(const mimo_attention *args, const mimo_attention_grads *grads, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Layer norm of rows of embeddings (the stock Qwen2-VL tower's; the vision
+ * page's PatchMerger norms before it merges units), with its backward pass.
+ * For a row x of width n:
+ *   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+ *   out = (x - mean) rstd weight + bias
+ * Everything is float32 inside; inputs and outputs are float32 or bf16
+ * (rounded to nearest even once), dense [rows][width].  Rows of a width that
+ * is a multiple of 8 at 16-byte aligned addresses run fastest.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Forward, one kernel launch.
+ *   width    in [1, 65536].
+ *   weight, bias  device float32 [width], either may be NULL (ones, zeros).
+ *   eps      finite, >= 0.  (A row of equal values has rstd = 1 / sqrt(eps).)
+ *   out      device, out_dtype; may be x where the dtypes agree.
+ *   mean, rstd    device float32 [rows], or NULL: the backward pass takes them.
+ * Pointers are aligned to their values.  Returns MIMO_OK, MIMO_E_INVALID,
+ * MIMO_E_TOO_LARGE (width, or more than 2^31 - 1 rows) or MIMO_E_HIP.
+ */
+int mimo_layer_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const float *weight, const float *bias,
+                    float eps, int32_t out_dtype, void *out, float *mean, float *rstd, void *stream);
+
+/* Device workspace bytes of the backward pass (0 for sizes it refuses). */
+size_t mimo_layer_norm_workspace_bytes(int64_t rows, int32_t width);
+
+/*
+ * Backward, for dout of dout_dtype: with xh = (x - mean) rstd and g = dout weight,
+ *   dx = rstd (g - sum g / n - xh sum(g xh) / n)    (x's dtype)
+ *   dweight = sum over rows of dout xh,  dbias = sum over rows of dout
+ * dweight and dbias are device float32 [width], either may be NULL; they are
+ * overwritten, and their sums have a fixed order.  dx must not be x or dout.
+ *   workspace  device, >= mimo_layer_norm_workspace_bytes(rows, width), 16-byte
+ *              aligned, or NULL if both sums are; calls that may run at the
+ *              same time need one each.
+ * One kernel launch, and one for the sums (two for widths above 16384, or
+ * above 8192 where rows are not aligned).  Returns MIMO_OK, MIMO_E_INVALID,
+ * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *dout, int32_t dout_dtype,
+                             const float *weight, const float *mean, const float *rstd, void *dx, float *dweight,
+                             float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Matrix product in 8-bit integers, with a scale for each row and each output
+ * channel: the patch embedding and the tower's projections with 8-bit weights
+ * and activations (docs.rs "cortiq_engine::mimo_vision" measures its tower so).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rows to 8-bit integers (activations row by row, a weight channel by
+ * channel), one kernel launch:
+ *   scale[r] = max |x[r]| / 127,  q[r][k] = x[r][k] / scale[r] rounded to
+ *   nearest, ties to even (both float32 divisions)
+ * A row of zeros has the scale 0; a row that holds a NaN or an infinity has
+ * the scale NaN, and zeros.
+ *   width    in [1, 130944].
+ *   x        device, x_dtype (MIMO_F32 or MIMO_BF16), dense, aligned to its values.
+ *   q        device int8 [rows][padded], padded = width rounded up to a
+ *            multiple of 128 (the rest is set to zero), 16-byte aligned.
+ *   scale    device float32 [rows].
+ * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE (width, or more than
+ * 2^31 - 1 rows) or MIMO_E_HIP.
+ */
+int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dtype, void *q, float *scale, void *stream);
+
+/*
+ * out[r][e] = (sum_k xq[r][k] wq[e][k]) x_scale[r] w_scale[e] (+ bias[e]), one
+ * kernel launch; the sum is exact (32-bit integers on the matrix cores).
+ *   k        a multiple of 128, at most 130944.
+ *   xq, wq   device int8 [n_rows][k], [embed_dim][k] (mimo_quantize_rows'
+ *            padded rows), 16-byte aligned.
+ *   x_scale, w_scale, bias  device float32 [n_rows], [embed_dim],
+ *            [embed_dim] or NULL.
+ *   embed_dim  in [1, 2^24].
+ *   out      device [n_rows][embed_dim] of out_dtype (MIMO_F32 or MIMO_BF16,
+ *            rounded to nearest even), 16-byte aligned.
+ * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float *x_scale, int32_t embed_dim, const void *wq,
+                          const float *w_scale, const float *bias, int32_t out_dtype, void *out, void *stream);
+
 /*
  * Instrumentation.  When start and stop are non-null hipEvent_t handles
  * (passed as void*), every later kernel launch that the library makes on the
  * calling thread records `start` on the launch stream immediately before
  * the kernel and `stop` immediately after it, so the pair times the kernel
- * alone (the descriptor upload falls outside).  NULL, NULL switches it off.
+ * alone (the descriptor upload falls outside); where an entry point launches
+ * several kernels, the pair is around all of them.  NULL, NULL switches it off.
  * Thread-local; the caller owns the events.  Returns MIMO_OK, or MIMO_E_INVALID if only one is null.
  */
 int mimo_set_launch_events(void *start, void *stop);

@@ -65,3 +65,43 @@ def chunk_attention(q, k, v, cu, window=-1, scale=None, sink=None, dout=None):
             r["dsink"][h] += ds[:, 0].sum()
             r["parts"].append((a, b, h, g, p, dp, ds))
     return r
+
+
+def layer_norm(x, weight, bias, eps, dout=None):
+    """x [rows, n] (float64), weight and bias [n] or None.
+
+    Returns a dict: out, mean, rstd, hat, and with dout dx, dweight, dbias."""
+    n = x.shape[1]
+    mean = x.sum(axis=1) / n
+    d = x - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).sum(axis=1) / n + eps)
+    hat = d * rstd[:, None]
+    w = np.ones(n) if weight is None else weight
+    r = {"out": hat * w + (0.0 if bias is None else bias), "mean": mean, "rstd": rstd, "hat": hat}
+    if dout is not None:
+        g = dout * w
+        s1, s2 = g.sum(axis=1) / n, (g * hat).sum(axis=1) / n
+        r.update(dx=rstd[:, None] * (g - s1[:, None] - hat * s2[:, None]), dweight=(dout * hat).sum(axis=0),
+                 dbias=dout.sum(axis=0), g=g, s1=s1, s2=s2)
+    return r
+
+
+def quantize_rows(x):
+    """(q int64 [rows, n], scale float32 [rows]) of float32 rows, by the
+    definition: both quotients are float32 divisions."""
+    x = np.asarray(x, dtype=np.float32)
+    top = np.abs(x).max(axis=1)
+    finite = np.isfinite(x).all(axis=1)
+    scale = np.where(finite, top / np.float32(127.0), np.float32(np.nan)).astype(np.float32)
+    usable = finite & (scale > 0)
+    q = np.zeros(x.shape, dtype=np.int64)
+    q[usable] = np.clip(np.rint(x[usable] / scale[usable][:, None]), -127, 127).astype(np.int64)
+    return q, scale
+
+
+def quantized_linear(xq, x_scale, wq, w_scale, bias=None):
+    """(out, |sum| scaled) in float64, from exact integer sums."""
+    total = (np.asarray(xq, dtype=np.float64) @ np.asarray(wq, dtype=np.float64).T)
+    s = np.asarray(x_scale, dtype=np.float64)[:, None] * np.asarray(w_scale, dtype=np.float64)[None, :]
+    out = total * s
+    return (out if bias is None else out + np.asarray(bias, dtype=np.float64)), np.abs(total * s)

@@ -62,3 +62,32 @@ def test_attention_closed_cases():
     r = tower.chunk_attention(q, k, v, [0, 9], 0, None, np.array([-np.inf, 0.0]), np.ones_like(q))
     assert (r["out"][0, 0] == 0).all() and r["lse"][0, 0] == -np.inf and np.isfinite(r["dq"]).all()
     assert np.allclose(r["out"][0, 1], v[0, 1])
+
+
+def test_norm_gradients_against_differences():
+    rng = np.random.default_rng(7)
+    x, dout = rng.normal(1.0, 2.0, (5, 7)), rng.normal(size=(5, 7))
+    w, b = rng.normal(size=7), rng.normal(size=7)
+
+    def loss():
+        return float((tower.layer_norm(x, w, b, 1e-3)["out"] * dout).sum())
+
+    r = tower.layer_norm(x, w, b, 1e-3, dout)
+    for name, t in (("dx", x), ("dweight", w), ("dbias", b)):
+        _near(r[name], _differences(loss, t))
+
+
+def test_norm_closed_cases():
+    r = tower.layer_norm(np.array([[3.0, 3.0], [1.0, -1.0]]), None, None, 0.25)
+    assert (r["out"][0] == 0).all() and r["rstd"][0] == 2.0
+    assert np.allclose(r["out"][1], np.array([1, -1]) / np.sqrt(1.25))
+
+
+def test_quantized_closed_cases():
+    # scale 1 / 127 * 127 = 1: values are their own quotients, ties go to even
+    x = np.array([[127.0, 0.5, 1.5, 2.5, -0.5, -1.5], [0, 0, 0, 0, 0, 0], [1, 2, np.nan, 0, 0, 0], [np.inf, 1, 0, 0, 0, 0]])
+    q, s = tower.quantize_rows(x)
+    assert q[0].tolist() == [127, 0, 2, 2, 0, -2] and s[0] == 1
+    assert (q[1:] == 0).all() and s[1] == 0 and np.isnan(s[2:]).all()
+    out, _ = tower.quantized_linear(q[:1], s[:1], np.array([[1, 2, 0, 0, 0, 0]]), np.array([0.5]), np.array([3.0]))
+    assert out.tolist() == [[66.5]]

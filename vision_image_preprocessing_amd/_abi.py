@@ -108,6 +108,11 @@ SIGNATURES = {
     "mimo_chunk_attention": ([_P, _P], ctypes.c_int),
     "mimo_chunk_attention_workspace_bytes": ([_I64, _I32, _I32], _SZ),
     "mimo_chunk_attention_backward": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
+    "mimo_layer_norm": ([_I64, _I32, _P, _I32, _P, _P, ctypes.c_float, _I32, _P, _P, _P, _P], ctypes.c_int),
+    "mimo_layer_norm_workspace_bytes": ([_I64, _I32], _SZ),
+    "mimo_layer_norm_backward": ([_I64, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "mimo_quantize_rows": ([_I64, _I32, _P, _I32, _P, _P, _P], ctypes.c_int),
+    "mimo_quantized_linear": ([_I64, _I32, _P, _P, _I32, _P, _P, _P, _I32, _P, _P], ctypes.c_int),
 }
 
 _lock = threading.Lock()

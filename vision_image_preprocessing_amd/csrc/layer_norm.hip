@@ -1,0 +1,489 @@
+// layer_norm.hip -- layer norm of rows of embeddings and its backward pass
+// with the reduction of the weight's and bias's gradients, for AMD Instinct
+// MI355X (gfx950).
+//
+// What is computed, for a row x of n values (the norm of the stock Qwen2-VL
+// tower, over embeddings or over whole merge units of four rows):
+//   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+//   xh = (x - mean) rstd,  out = xh w + b
+// and for dout, with g = dout w:
+//   dx = rstd (g - sum g / n - xh sum(g xh) / n)
+//   dw = sum over rows of dout xh,  db = sum over rows of dout
+//
+// Everything is float32 inside; inputs and outputs are float32 or bf16, each
+// rounded once.  The variance is the sum of squared distances from the mean,
+// formed after it from the row in registers, so that a large mean costs no
+// precision.
+//
+// Both kernels are one pass over memory.  A row is held in registers by one
+// wave (up to 1536 values) or one workgroup (up to 16384); wider rows are
+// read again from cache for each sum.  In the backward kernel a wave keeps
+// its columns from row to row, so the parameter gradients accumulate in
+// registers, over a fixed set of rows; a second kernel adds the workgroups'
+// partial sums in a fixed order, and no atomics are needed.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "device_util.h"
+#include "internal.h"
+#include "row_ops.h"
+#include "runtime.h"
+
+namespace mimo {
+namespace {
+
+using namespace rows;
+
+constexpr int kMaxWidth = 65536;
+constexpr int kMaxGroups = 1024;   // workgroups of the backward pass, and partial sums of each column
+constexpr int kSumColumns = 32, kSumParts = 32;  // of the reduction kernel's workgroup
+
+struct NormArgs {
+    const void *x, *dout;
+    const float *weight, *bias;  // or null
+    float *mean, *rstd;          // forward: outputs or null
+    void *out;                   // out, or dx
+    float *part;                 // [groups][2][width]: dw, db (backward), or null
+    int64_t rows;
+    int32_t width;
+    float eps;
+};
+
+// Chunks of kVec values: chunk i of a thread is i * kThreads + its number.
+template <typename TX, typename TO, int kVec, int kThreads, int kChunks>
+__global__ __launch_bounds__(kRowWgThreads) void layer_norm_kernel(NormArgs a) {
+    __shared__ float lds[2][4];
+    const int tid = threadIdx.x % kThreads;
+    const int64_t row = int64_t(blockIdx.x) * (kRowWgThreads / kThreads) + threadIdx.x / kThreads;
+    if (row >= a.rows) return;  // whole waves, and only where a wave is a row
+    const TX *x = static_cast<const TX *>(a.x) + row * a.width;
+    const int chunks = a.width / kVec;
+    float v[kChunks][kVec];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = i * kThreads + tid;
+        if (c < chunks) {
+            load_values(x + c * kVec, v[i]);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) sum += v[i][j];
+        }
+    }
+    const float mean = row_sum<kThreads>(sum, lds[0]) / float(a.width);
+    float squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+        if (i * kThreads + tid < chunks) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                v[i][j] -= mean;
+                squares = fmaf(v[i][j], v[i][j], squares);
+            }
+        }
+    const float rstd = 1.0f / sqrtf(row_sum<kThreads>(squares, lds[1]) / float(a.width) + a.eps);
+    TO *out = static_cast<TO *>(a.out) + row * a.width;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = i * kThreads + tid;
+        if (c < chunks) {
+            float w[kVec], b[kVec];
+            if (a.weight) load_values(a.weight + c * kVec, w);
+            if (a.bias) load_values(a.bias + c * kVec, b);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                v[i][j] *= rstd;
+                if (a.weight) v[i][j] *= w[j];
+                if (a.bias) v[i][j] += b[j];
+            }
+            store_values(out + c * kVec, v[i]);
+        }
+    }
+    if (tid == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+}
+
+// Rows of any width, one workgroup each, read once for each sum.
+template <typename TX, typename TO>
+__global__ __launch_bounds__(kRowWgThreads) void layer_norm_wide_kernel(NormArgs a) {
+    __shared__ float lds[2][4];
+    const int64_t row = blockIdx.x;
+    const TX *x = static_cast<const TX *>(a.x) + row * a.width;
+    float sum = 0.0f;
+    for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) sum += float(x[c]);
+    const float mean = row_sum<256>(sum, lds[0]) / float(a.width);
+    float squares = 0.0f;
+    for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) {
+        const float d = float(x[c]) - mean;
+        squares = fmaf(d, d, squares);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<256>(squares, lds[1]) / float(a.width) + a.eps);
+    TO *out = static_cast<TO *>(a.out) + row * a.width;
+    for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) {
+        float v = (float(x[c]) - mean) * rstd;
+        if (a.weight) v *= a.weight[c];
+        if (a.bias) v += a.bias[c];
+        out[c] = TO(v);
+    }
+    if (threadIdx.x == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+}
+
+// dx of rows first, first + step, ...; partial dw and db of those rows.
+template <typename TX, typename TG, int kVec, int kThreads, int kChunks>
+__global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(NormArgs a) {
+    constexpr int kRows = kRowWgThreads / kThreads;  // rows of the workgroup at a time
+    __shared__ float lds[4][4];
+    const int tid = threadIdx.x % kThreads;
+    const int chunks = a.width / kVec;
+    const float inv_n = 1.0f / float(a.width);
+    float w[kChunks][kVec], dw[kChunks][kVec], db[kChunks][kVec];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            dw[i][j] = db[i][j] = 0.0f;
+            w[i][j] = 1.0f;
+        }
+        if (a.weight && i * kThreads + tid < chunks) load_values(a.weight + (i * kThreads + tid) * kVec, w[i]);
+    }
+    int turn = 0;
+    for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kThreads; row < a.rows; row += int64_t(gridDim.x) * kRows, turn ^= 1) {
+        const TX *x = static_cast<const TX *>(a.x) + row * a.width;
+        const TG *dout = static_cast<const TG *>(a.dout) + row * a.width;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float h[kChunks][kVec], g[kChunks][kVec];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = i * kThreads + tid;
+            if (c < chunks) {
+                load_values(x + c * kVec, h[i]);
+                load_values(dout + c * kVec, g[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+            if (i * kThreads + tid < chunks) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    h[i][j] = (h[i][j] - mean) * rstd;
+                    dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
+                    db[i][j] += g[i][j];
+                    g[i][j] *= w[i][j];
+                    s1 += g[i][j];
+                    s2 = fmaf(g[i][j], h[i][j], s2);
+                }
+            }
+        // a turn's reductions use other words than the turn before, which a
+        // slower wave may still read
+        s1 = row_sum<kThreads>(s1, lds[2 * turn]) * inv_n;
+        s2 = row_sum<kThreads>(s2, lds[2 * turn + 1]) * inv_n;
+        TX *dx = static_cast<TX *>(a.out) + row * a.width;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = i * kThreads + tid;
+            if (c < chunks) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) h[i][j] = rstd * (g[i][j] - fmaf(h[i][j], s2, s1));
+                store_values(dx + c * kVec, h[i]);
+            }
+        }
+    }
+    if (!a.part) return;
+    float *part = a.part + int64_t(blockIdx.x) * 2 * a.width;
+    if constexpr (kRows == 1) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = i * kThreads + tid;
+            if (c < chunks) {
+                store_values(part + c * kVec, dw[i]);
+                store_values(part + a.width + c * kVec, db[i]);
+            }
+        }
+    } else {
+        // the waves hold the same columns: added up in LDS, chunk by chunk
+        __shared__ float sum[kRows][kThreads * kVec];
+        const int wave = threadIdx.x / kThreads;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) sum[wave][j * kThreads + tid] = k ? db[i][j] : dw[i][j];
+                __syncthreads();
+                for (int e = threadIdx.x; e < kThreads * kVec; e += kRowWgThreads) {
+                    const int col = (i * kThreads + e % kThreads) * kVec + e / kThreads;
+                    if (i * kThreads + e % kThreads < chunks) part[k * a.width + col] = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
+                }
+            }
+    }
+}
+
+// dx of one row of any width.
+template <typename TX, typename TG>
+__global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_wide_kernel(NormArgs a) {
+    __shared__ float lds[2][4];
+    const int64_t row = blockIdx.x;
+    const TX *x = static_cast<const TX *>(a.x) + row * a.width;
+    const TG *dout = static_cast<const TG *>(a.dout) + row * a.width;
+    const float mean = a.mean[row], rstd = a.rstd[row], inv_n = 1.0f / float(a.width);
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) {
+        const float g = float(dout[c]) * (a.weight ? a.weight[c] : 1.0f);
+        s1 += g;
+        s2 = fmaf(g, (float(x[c]) - mean) * rstd, s2);
+    }
+    s1 = row_sum<256>(s1, lds[0]) * inv_n;
+    s2 = row_sum<256>(s2, lds[1]) * inv_n;
+    TX *dx = static_cast<TX *>(a.out) + row * a.width;
+    for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) {
+        const float g = float(dout[c]) * (a.weight ? a.weight[c] : 1.0f);
+        dx[c] = TX(rstd * (g - fmaf((float(x[c]) - mean) * rstd, s2, s1)));
+    }
+}
+
+// Partial dw and db of 256 columns over every gridDim.y-th row.
+template <typename TX, typename TG>
+__global__ __launch_bounds__(kRowWgThreads) void layer_norm_columns_kernel(NormArgs a) {
+    const int c = blockIdx.x * kRowWgThreads + threadIdx.x;
+    if (c >= a.width) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float g = float(static_cast<const TG *>(a.dout)[row * a.width + c]);
+        const float h = (float(static_cast<const TX *>(a.x)[row * a.width + c]) - a.mean[row]) * a.rstd[row];
+        dw = fmaf(g, h, dw);
+        db += g;
+    }
+    float *part = a.part + int64_t(blockIdx.y) * 2 * a.width;
+    part[c] = dw;
+    part[a.width + c] = db;
+}
+
+// dweight and dbias: the partial sums of each column, added in a fixed order.
+__global__ __launch_bounds__(kSumColumns *kSumParts) void layer_norm_sum_kernel(const float *part, int32_t groups, int32_t width,
+                                                                               float *dweight, float *dbias) {
+    __shared__ float lds[kSumParts][kSumColumns + 1];
+    const int column = threadIdx.x % kSumColumns, first = threadIdx.x / kSumColumns;
+    const int64_t c = int64_t(blockIdx.x) * kSumColumns + column;  // of 2 width
+    float v = 0.0f;
+    if (c < 2 * int64_t(width)) {
+#pragma unroll 8
+        for (int g = first; g < groups; g += kSumParts) v += part[int64_t(g) * 2 * width + c];
+    }
+    lds[first][column] = v;
+    __syncthreads();
+#pragma unroll
+    for (int n = kSumParts / 2; n > 0; n >>= 1) {
+        if (first < n) lds[first][column] += lds[first + n][column];
+        __syncthreads();
+    }
+    if (first == 0 && c < 2 * int64_t(width)) {
+        if (c < width) {
+            if (dweight) dweight[c] = lds[0][column];
+        } else if (dbias) {
+            dbias[c - width] = lds[0][column];
+        }
+    }
+}
+
+// How a width is laid over threads: values a chunk, threads a row, chunks a
+// thread; threads = 0: the row is read again for each sum.
+struct Shape {
+    int vec, threads, chunks;
+};
+Shape choose_shape(int32_t width, bool aligned) {
+    if (aligned && width % 8 == 0) {
+        if (width <= 64 * 8) return {8, 64, 1};
+        if (width <= 64 * 8 * 3) return {8, 64, 3};
+        if (width <= 256 * 8 * 2) return {8, 256, 2};
+        if (width <= 256 * 8 * 8) return {8, 256, 8};
+    } else {
+        if (width <= 64 * 4) return {1, 64, 4};
+        if (width <= 256 * 8) return {1, 256, 8};
+        if (width <= 256 * 32) return {1, 256, 32};
+    }
+    return {1, 0, 0};
+}
+
+// Workgroups of the backward kernel: each then adds up so many rows.
+int32_t backward_groups(int64_t rows, int32_t width) {
+    const int64_t per = width <= 64 * 8 * 3 ? 4 : 1;
+    const int64_t groups = (rows + per - 1) / per;
+    return int32_t(groups < kMaxGroups ? groups : kMaxGroups);
+}
+
+bool is_dtype(int32_t d) { return d == MIMO_F32 || d == MIMO_BF16; }
+
+template <typename TX, typename TO>
+void launch_forward(const Shape &s, const NormArgs &a, hipStream_t stream) {
+    const dim3 block{unsigned(kRowWgThreads), 1, 1};
+    const dim3 grid{unsigned(s.threads == 64 ? (a.rows + 3) / 4 : a.rows), 1, 1};
+#define MIMO_NORM(V, T, C)                                                                      \
+    if (s.vec == V && s.threads == T && s.chunks == C) {                                        \
+        hipLaunchKernelGGL((layer_norm_kernel<TX, TO, V, T, C>), grid, block, 0, stream, a);    \
+        return;                                                                                 \
+    }
+    MIMO_NORM(8, 64, 1)
+    MIMO_NORM(8, 64, 3)
+    MIMO_NORM(8, 256, 2)
+    MIMO_NORM(8, 256, 8)
+    MIMO_NORM(1, 64, 4)
+    MIMO_NORM(1, 256, 8)
+    MIMO_NORM(1, 256, 32)
+#undef MIMO_NORM
+    hipLaunchKernelGGL((layer_norm_wide_kernel<TX, TO>), grid, block, 0, stream, a);
+}
+
+template <typename TX, typename TG>
+void launch_backward(const Shape &s, const NormArgs &a, int32_t groups, hipStream_t stream) {
+    const dim3 block{unsigned(kRowWgThreads), 1, 1}, grid{unsigned(groups), 1, 1};
+#define MIMO_NORM(V, T, C)                                                                               \
+    if (s.vec == V && s.threads == T && s.chunks == C) {                                                 \
+        hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TG, V, T, C>), grid, block, 0, stream, a);    \
+        return;                                                                                          \
+    }
+    MIMO_NORM(8, 64, 1)
+    MIMO_NORM(8, 64, 3)
+    MIMO_NORM(8, 256, 2)
+    MIMO_NORM(8, 256, 8)
+    MIMO_NORM(1, 64, 4)
+    MIMO_NORM(1, 256, 8)
+    MIMO_NORM(1, 256, 32)
+#undef MIMO_NORM
+    hipLaunchKernelGGL((layer_norm_backward_wide_kernel<TX, TG>), dim3(unsigned(a.rows), 1, 1), block, 0, stream, a);
+    if (a.part)
+        hipLaunchKernelGGL((layer_norm_columns_kernel<TX, TG>),
+                           dim3(unsigned((a.width + kRowWgThreads - 1) / kRowWgThreads), unsigned(groups), 1), block, 0, stream, a);
+}
+
+int check_norm(const char *who, int64_t rows, int32_t width) {
+    const std::string w(who);
+    if (rows < 0 || width < 1) return set_error(MIMO_E_INVALID, w + ": rows must be >= 0 and width >= 1");
+    if (width > kMaxWidth || rows > 0x7FFFFFFFll)
+        return set_error(MIMO_E_TOO_LARGE, w + ": width above 65536 or more than 2^31 - 1 rows");
+    return MIMO_OK;
+}
+
+}  // namespace
+}  // namespace mimo
+
+using namespace mimo;
+
+extern "C" {
+
+int mimo_layer_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const float *weight, const float *bias,
+                    float eps, int32_t out_dtype, void *out, float *mean, float *rstd, void *stream) {
+    clear_error();
+    int st = check_norm("layer_norm", rows, width);
+    if (st != MIMO_OK) return st;
+    if (!is_dtype(x_dtype) || !is_dtype(out_dtype))
+        return set_error(MIMO_E_INVALID, "layer_norm: dtypes must be MIMO_F32 or MIMO_BF16");
+    if (!(eps >= 0.0f) || std::isinf(eps)) return set_error(MIMO_E_INVALID, "layer_norm: eps must be finite and >= 0");
+    if (rows == 0) return MIMO_OK;
+    if (!x || !out || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(out, out_dtype == MIMO_F32 ? 4 : 2) ||
+        !check_ptr_align(weight, 4) || !check_ptr_align(bias, 4) || !check_ptr_align(mean, 4) || !check_ptr_align(rstd, 4))
+        return set_error(MIMO_E_INVALID, "layer_norm: null or misaligned pointer (each aligned to its values)");
+    if (out == x && x_dtype != out_dtype)
+        return set_error(MIMO_E_INVALID, "layer_norm: out may be x only in x's dtype");
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.out = out;
+    a.rows = rows;
+    a.width = width;
+    a.eps = eps;
+    const bool aligned = check_ptr_align(x, 16) && check_ptr_align(out, 16) && check_ptr_align(weight, 16) && check_ptr_align(bias, 16);
+    const Shape shape = choose_shape(width, aligned);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = timed_launch(s, [&] {
+        if (x_dtype == MIMO_F32 && out_dtype == MIMO_F32)
+            launch_forward<float, float>(shape, a, s);
+        else if (x_dtype == MIMO_F32)
+            launch_forward<float, __bf16>(shape, a, s);
+        else if (out_dtype == MIMO_F32)
+            launch_forward<__bf16, float>(shape, a, s);
+        else
+            launch_forward<__bf16, __bf16>(shape, a, s);
+    });
+    if (e != hipSuccess) return hip_error(e, "layer_norm: kernel launch");
+    g_dispatches.fetch_add(1);
+    return MIMO_OK;
+}
+
+size_t mimo_layer_norm_workspace_bytes(int64_t rows, int32_t width) {
+    if (rows < 0 || width < 1 || width > kMaxWidth) return 0;
+    return size_t(backward_groups(rows, width)) * 2 * size_t(width) * sizeof(float);
+}
+
+int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *dout, int32_t dout_dtype,
+                             const float *weight, const float *mean, const float *rstd, void *dx, float *dweight,
+                             float *dbias, void *workspace, size_t workspace_bytes, void *stream) {
+    clear_error();
+    const char *who = "layer_norm_backward";
+    int st = check_norm(who, rows, width);
+    if (st != MIMO_OK) return st;
+    if (!is_dtype(x_dtype) || !is_dtype(dout_dtype))
+        return set_error(MIMO_E_INVALID, "layer_norm_backward: dtypes must be MIMO_F32 or MIMO_BF16");
+    const bool sums = dweight || dbias;
+    if (rows == 0 && !sums) return MIMO_OK;
+    if (!check_ptr_align(dweight, 4) || !check_ptr_align(dbias, 4))
+        return set_error(MIMO_E_INVALID, "layer_norm_backward: dweight and dbias must be 4-byte aligned");
+    if (rows > 0) {
+        if (!x || !dout || !mean || !rstd || !dx || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) ||
+            !check_ptr_align(dx, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(dout, dout_dtype == MIMO_F32 ? 4 : 2) ||
+            !check_ptr_align(weight, 4) || !check_ptr_align(mean, 4) || !check_ptr_align(rstd, 4))
+            return set_error(MIMO_E_INVALID, "layer_norm_backward: null or misaligned pointer (each aligned to its values)");
+        if (sums && (!workspace || !check_ptr_align(workspace, 16)))
+            return set_error(MIMO_E_INVALID, "layer_norm_backward: workspace must be non-null and 16-byte aligned");
+        if (sums && workspace_bytes < mimo_layer_norm_workspace_bytes(rows, width))
+            return set_error(MIMO_E_CAPACITY, "layer_norm_backward: workspace smaller than mimo_layer_norm_workspace_bytes");
+        if (dx == x || dx == dout) return set_error(MIMO_E_INVALID, "layer_norm_backward: dx must not be an input");
+    }
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.dout = dout;
+    a.weight = weight;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.out = dx;
+    a.part = sums ? static_cast<float *>(workspace) : nullptr;
+    a.rows = rows;
+    a.width = width;
+    const int32_t groups = backward_groups(rows, width);
+    const bool aligned = check_ptr_align(x, 16) && check_ptr_align(dout, 16) && check_ptr_align(weight, 16) && check_ptr_align(dx, 16);
+    const Shape shape = choose_shape(width, aligned);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = timed_launch(s, [&] {
+        if (rows > 0) {
+            if (x_dtype == MIMO_F32 && dout_dtype == MIMO_F32)
+                launch_backward<float, float>(shape, a, groups, s);
+            else if (x_dtype == MIMO_F32)
+                launch_backward<float, __bf16>(shape, a, groups, s);
+            else if (dout_dtype == MIMO_F32)
+                launch_backward<__bf16, float>(shape, a, groups, s);
+            else
+                launch_backward<__bf16, __bf16>(shape, a, groups, s);
+        }
+        if (sums)
+            hipLaunchKernelGGL(layer_norm_sum_kernel, dim3(unsigned((2 * int64_t(width) + kSumColumns - 1) / kSumColumns), 1, 1),
+                               dim3(kSumColumns * kSumParts, 1, 1), 0, s, a.part, groups, width, dweight, dbias);
+    });
+    if (e != hipSuccess) return hip_error(e, "layer_norm_backward: kernel launch");
+    g_dispatches.fetch_add((rows > 0 ? 1 : 0) + (rows > 0 && sums && shape.threads == 0 ? 1 : 0) + (sums ? 1 : 0));
+    return MIMO_OK;
+}
+
+}  // extern "C"

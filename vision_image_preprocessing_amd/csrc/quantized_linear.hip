@@ -1,0 +1,383 @@
+// quantized_linear.hip -- rows quantised to 8-bit integers and the matrix
+// product of two such matrices, for AMD Instinct MI355X (gfx950, CDNA4).
+//
+// What is computed.  quantize_rows: scale = max |x| / 127 of each row, q =
+// x / scale rounded to the nearest integer (ties to even), so that x is near
+// scale * q; the same for the rows of a weight, whose rows are its output
+// channels.  quantized_linear: with rows' scales s_r and channels' scales t_e,
+//   out[r][e] = (sum_k xq[r][k] wq[e][k]) s_r t_e + bias[e]
+// The sum is exact: products of 8-bit integers on v_mfma_i32_32x32x32_i8 into
+// 32-bit integers, which 2^17 of them cannot overflow.
+//
+// Quantised rows are padded with zeros to a multiple of 128 bytes: rows of
+// whole 128-byte K steps, so the product needs no tail in K.
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+#include <string>
+
+#include "device_util.h"
+#include "internal.h"
+#include "row_ops.h"
+#include "runtime.h"
+
+namespace mimo {
+namespace {
+
+using namespace rows;
+
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kPadK = 128;          // quantised rows are multiples of this
+constexpr int kMaxK = 130944;       // 2^14 kMaxK < 2^31: no overflow, values of -128 included
+constexpr int kThreads = 256;
+
+struct QuantizeArgs {
+    const void *x;
+    int8_t *q;      // [rows][padded]
+    float *scale;   // [rows]
+    int64_t rows;
+    int32_t width, padded;
+};
+
+// |v| as an unsigned integer: the order of the magnitudes, NaN above all.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+template <int kThreadsRow>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *lds) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v = max(v, uint32_t(__shfl_xor(int(v), m)));
+    if constexpr (kThreadsRow == 256) {
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = max(max(lds[0], lds[1]), max(lds[2], lds[3]));
+    }
+    return v;
+}
+
+// The definition's quotient: float32 division, rounded to the nearest
+// integer, ties to even.  A quotient beyond 127 is possible only where the
+// scale is so small that float32 holds it with a few bits.
+__device__ __forceinline__ int quantize(float v, float scale) {
+    return int(fminf(fmaxf(__builtin_rintf(v / scale), -127.0f), 127.0f));
+}
+
+// One row by a wave (kThreadsRow = 64) or the workgroup, held in registers
+// (kChunks chunks of kVec values a thread), or read twice (kChunks = 0).
+template <typename T, int kVec, int kThreadsRow, int kChunks>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a) {
+    __shared__ uint32_t lds[4];
+    const int tid = threadIdx.x % kThreadsRow;
+    const int64_t row = int64_t(blockIdx.x) * (kThreads / kThreadsRow) + threadIdx.x / kThreadsRow;
+    if (row >= a.rows) return;
+    const T *x = static_cast<const T *>(a.x) + row * a.width;
+    int8_t *q = a.q + row * a.padded;
+    const int chunks = a.width / kVec, all = a.padded / kVec;
+    constexpr int kHeld = kChunks ? kChunks : 1;
+    float v[kHeld][kVec];
+    uint32_t top = 0;
+    auto write = [&](int c, const float (&w)[kVec], float scale, bool zero) {
+        if constexpr (kVec == 8) {
+            u32x2 p = {0, 0};
+            if (!zero) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t(quantize(w[j], scale)) & 0xFFu) << (8 * (j % 4));
+            }
+            *reinterpret_cast<u32x2 *>(q + c * 8) = p;
+        } else {
+            q[c] = zero ? int8_t(0) : int8_t(quantize(w[0], scale));
+        }
+    };
+    if constexpr (kChunks > 0) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = i * kThreadsRow + tid;
+            if (c < chunks) {
+                load_values(x + c * kVec, v[i]);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) top = max(top, magnitude(v[i][j]));
+            }
+        }
+    } else {
+        for (int c = tid; c < chunks; c += kThreadsRow) {
+            load_values(x + c * kVec, v[0]);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) top = max(top, magnitude(v[0][j]));
+        }
+    }
+    top = row_max<kThreadsRow>(top, lds);
+    // a row that is not finite has the scale NaN and zeros, which make its
+    // outputs NaN; a row of zeros (or too small for a scale) has the scale 0
+    const bool finite = top < 0x7F800000u;
+    const float scale = finite ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
+    const bool none = !finite || scale == 0.0f;
+    if constexpr (kChunks > 0) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = i * kThreadsRow + tid;
+            if (c < all) write(c, v[i], scale, none || c >= chunks);
+        }
+        // the padding behind what the threads hold
+        for (int c = kChunks * kThreadsRow + tid; c < all; c += kThreadsRow) write(c, v[0], scale, true);
+    } else {
+        for (int c = tid; c < all; c += kThreadsRow) {
+            if (c < chunks) load_values(x + c * kVec, v[0]);
+            write(c, v[0], scale, none || c >= chunks);
+        }
+    }
+    if (tid == 0) a.scale[row] = scale;
+}
+
+struct LinearArgs {
+    const int8_t *x, *w;          // [n_rows][k], [e][k]
+    const float *x_scale, *w_scale, *bias;  // bias or null
+    void *out;                    // OutT [n_rows][e]
+    int64_t n_rows;
+    int32_t e, k;                 // k: a multiple of 128
+    int32_t n_tiles;              // tiles along e
+};
+
+__device__ __forceinline__ i32x16 mfma(const i32x4 &a, const i32x4 &b, const i32x16 &c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+
+// LDS position (in bytes) of 16-byte chunk v of row r: 128-byte rows whose
+// chunks are XOR-swizzled by the row.
+__device__ __forceinline__ int lds_at(int r, int v) { return r * 128 + ((v ^ ((r ^ (r >> 3)) & 7)) << 4); }
+
+// Four consecutive channels of one row to memory.
+template <typename OutT>
+__device__ __forceinline__ void store_four(OutT *out, const float (&v)[4], int left, bool aligned) {
+    if (aligned && left >= 4) {
+        if constexpr (sizeof(OutT) == 4) {
+            *reinterpret_cast<f32x4 *>(out) = f32x4{v[0], v[1], v[2], v[3]};
+        } else {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<bf16x4 *>(out) = bf16x4{__bf16(v[0]), __bf16(v[1]), __bf16(v[2]), __bf16(v[3])};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) out[j] = OutT(v[j]);
+    }
+}
+
+// A 32 (channels) x 32 (rows) result block: value r of a lane is channel
+// 8 (r / 4) + 4 (lane / 32) + r % 4 of row lane % 32.
+template <typename OutT>
+__device__ __forceinline__ void store_block(const LinearArgs &a, const i32x16 &acc, int64_t row, int channel0) {
+    if (row >= a.n_rows) return;
+    const float s = a.x_scale[row];
+    OutT *out = static_cast<OutT *>(a.out) + row * a.e;
+    const bool aligned = a.e % 4 == 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int c = channel0 + 8 * g + 4 * ((threadIdx.x >> 5) & 1);
+        if (c >= a.e) continue;
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = min(c + j, a.e - 1);
+            v[j] = float(acc[4 * g + j]) * (s * a.w_scale[e]);
+            if (a.bias) v[j] += a.bias[e];
+        }
+        store_four(out + c, v, a.e - c, aligned);
+    }
+}
+
+// A 128 x 128 tile by four waves, 64 x 64 each, K in steps of 128 bytes
+// through two LDS buffers.
+template <typename OutT>
+__global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
+    constexpr int kTile = 128;
+    __shared__ uint8_t sx[2][kTile * 128], sw[2][kTile * 128];
+    const int64_t tile = xcd_contiguous_tile(blockIdx.x, gridDim.x);
+    const int64_t mt = tile / a.n_tiles;
+    const int64_t m0 = mt * kTile;
+    const int n0 = int(tile - mt * a.n_tiles) * kTile;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+    // rows past the last one read the last one; they are not stored
+    u32x4 gx[4], gw[4];
+    const int chunk = threadIdx.x & 7, first = threadIdx.x >> 3;
+    const int8_t *px[4], *pw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        px[i] = a.x + min(m0 + first + 32 * i, a.n_rows - 1) * a.k + chunk * 16;
+        pw[i] = a.w + int64_t(min(n0 + first + 32 * i, a.e - 1)) * a.k + chunk * 16;
+    }
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            gx[i] = *reinterpret_cast<const u32x4 *>(px[i] + k0);
+            gw[i] = *reinterpret_cast<const u32x4 *>(pw[i] + k0);
+        }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<u32x4 *>(sx[buf] + lds_at(first + 32 * i, chunk)) = gx[i];
+            *reinterpret_cast<u32x4 *>(sw[buf] + lds_at(first + 32 * i, chunk)) = gw[i];
+        }
+    };
+    i32x16 acc[2][2];  // [rows][channels]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
+    load(0);
+    store(0);
+    int buf = 0;
+    for (int k0 = 0; k0 < a.k; k0 += 128, buf ^= 1) {
+        const bool more = k0 + 128 < a.k;
+        if (more) load(k0 + 128);
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            i32x4 fx[2], fw[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fx[i] = *reinterpret_cast<const i32x4 *>(sx[buf] + lds_at(wm + 32 * i + (lane & 31), 2 * s + (lane >> 5)));
+                fw[i] = *reinterpret_cast<const i32x4 *>(sw[buf] + lds_at(wn + 32 * i + (lane & 31), 2 * s + (lane >> 5)));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
+        }
+        if (more) store(buf ^ 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store_block<OutT>(a, acc[i][j], m0 + wm + 32 * i + (lane & 31), n0 + wn + 32 * j);
+}
+
+// Few rows: a workgroup takes 32 rows and 32 channels and its waves share K,
+// operands straight from memory; the waves' sums meet in LDS.
+template <typename OutT>
+__global__ __launch_bounds__(kThreads) void linear_few_kernel(LinearArgs a) {
+    __shared__ int32_t part[4][16][64];
+    const int64_t mt = blockIdx.x / a.n_tiles;
+    const int64_t m0 = mt * 32;
+    const int n0 = int(blockIdx.x - mt * a.n_tiles) * 32;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int8_t *x = a.x + min(m0 + (lane & 31), a.n_rows - 1) * a.k + 16 * (lane >> 5);
+    const int8_t *w = a.w + int64_t(min(n0 + (lane & 31), a.e - 1)) * a.k + 16 * (lane >> 5);
+    i32x16 acc{};
+#pragma unroll 4
+    for (int k0 = 32 * wave; k0 < a.k; k0 += 128)
+        acc = mfma(*reinterpret_cast<const i32x4 *>(w + k0), *reinterpret_cast<const i32x4 *>(x + k0), acc);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) part[wave][r][lane] = acc[r];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = (part[0][r][lane] + part[1][r][lane]) + (part[2][r][lane] + part[3][r][lane]);
+    store_block<OutT>(a, acc, m0 + (lane & 31), n0);
+}
+
+}  // namespace
+}  // namespace mimo
+
+using namespace mimo;
+
+extern "C" {
+
+int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dtype, void *q, float *scale, void *stream) {
+    clear_error();
+    if (rows < 0 || width < 1) return set_error(MIMO_E_INVALID, "quantize_rows: rows must be >= 0 and width >= 1");
+    if (width > kMaxK || rows > 0x7FFFFFFFll)
+        return set_error(MIMO_E_TOO_LARGE, "quantize_rows: width above 130944 or more than 2^31 - 1 rows");
+    if (x_dtype != MIMO_F32 && x_dtype != MIMO_BF16)
+        return set_error(MIMO_E_INVALID, "quantize_rows: x_dtype must be MIMO_F32 or MIMO_BF16");
+    if (rows == 0) return MIMO_OK;
+    if (!x || !q || !scale || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(q, 16) || !check_ptr_align(scale, 4))
+        return set_error(MIMO_E_INVALID, "quantize_rows: null or misaligned pointer (x to its values, q 16 bytes, scale 4)");
+    QuantizeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.q = static_cast<int8_t *>(q);
+    a.scale = scale;
+    a.rows = rows;
+    a.width = width;
+    a.padded = (width + kPadK - 1) / kPadK * kPadK;
+    const bool vec = width % 8 == 0 && check_ptr_align(x, 16);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const dim3 block{unsigned(kThreads), 1, 1};
+    auto launch = [&](auto type) {
+        typedef decltype(type) T;
+        const dim3 waves{unsigned((rows + 3) / 4), 1, 1}, groups{unsigned(rows), 1, 1};
+        if (vec && width <= 64 * 8)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 64, 1>), waves, block, 0, s, a);
+        else if (vec && width <= 64 * 8 * 3)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 64, 3>), waves, block, 0, s, a);
+        else if (vec && width <= 256 * 8 * 3)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 256, 3>), groups, block, 0, s, a);
+        else if (vec)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 256, 0>), groups, block, 0, s, a);
+        else if (width <= 64 * 4)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 64, 4>), waves, block, 0, s, a);
+        else if (width <= 256 * 8)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 256, 8>), groups, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 256, 0>), groups, block, 0, s, a);
+    };
+    const hipError_t e = timed_launch(s, [&] {
+        if (x_dtype == MIMO_F32)
+            launch(float());
+        else
+            launch(__bf16());
+    });
+    if (e != hipSuccess) return hip_error(e, "quantize_rows: kernel launch");
+    g_dispatches.fetch_add(1);
+    return MIMO_OK;
+}
+
+int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float *x_scale, int32_t embed_dim, const void *wq,
+                          const float *w_scale, const float *bias, int32_t out_dtype, void *out, void *stream) {
+    clear_error();
+    if (n_rows < 0 || embed_dim < 1 || k < kPadK || k % kPadK)
+        return set_error(MIMO_E_INVALID, "quantized_linear: n_rows must be >= 0, embed_dim >= 1, k a multiple of 128");
+    if (k > kMaxK || embed_dim > (1 << 24) || n_rows > 0x7FFFFFFFll)
+        return set_error(MIMO_E_TOO_LARGE, "quantized_linear: k above 130944, embed_dim above 2^24 or more than 2^31 - 1 rows");
+    if (out_dtype != MIMO_F32 && out_dtype != MIMO_BF16)
+        return set_error(MIMO_E_INVALID, "quantized_linear: out_dtype must be MIMO_F32 or MIMO_BF16");
+    if (n_rows == 0) return MIMO_OK;
+    if (!xq || !x_scale || !wq || !w_scale || !out || !check_ptr_align(xq, 16) || !check_ptr_align(wq, 16) || !check_ptr_align(out, 16) ||
+        !check_ptr_align(x_scale, 4) || !check_ptr_align(w_scale, 4) || !check_ptr_align(bias, 4))
+        return set_error(MIMO_E_INVALID, "quantized_linear: null or misaligned pointer (xq, wq, out: 16 bytes; scales and bias: 4)");
+    LinearArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = static_cast<const int8_t *>(xq);
+    a.w = static_cast<const int8_t *>(wq);
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    a.bias = bias;
+    a.out = out;
+    a.n_rows = n_rows;
+    a.e = embed_dim;
+    a.k = k;
+    const int64_t m128 = (n_rows + 127) / 128, n128 = (embed_dim + 127) / 128;
+    const bool few = m128 * n128 < 128;
+    const int64_t tiles = few ? (n_rows + 31) / 32 * ((int64_t(embed_dim) + 31) / 32) : m128 * n128;
+    if (tiles > 0x7FFFFFFFll) return set_error(MIMO_E_TOO_LARGE, "quantized_linear: more than 2^31 - 1 tiles");
+    a.n_tiles = few ? (embed_dim + 31) / 32 : int32_t(n128);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const dim3 grid{unsigned(tiles), 1, 1}, block{unsigned(kThreads), 1, 1};
+    const hipError_t e = timed_launch(s, [&] {
+        if (few && out_dtype == MIMO_F32)
+            hipLaunchKernelGGL(linear_few_kernel<float>, grid, block, 0, s, a);
+        else if (few)
+            hipLaunchKernelGGL(linear_few_kernel<__bf16>, grid, block, 0, s, a);
+        else if (out_dtype == MIMO_F32)
+            hipLaunchKernelGGL(linear_tile_kernel<float>, grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL(linear_tile_kernel<__bf16>, grid, block, 0, s, a);
+    });
+    if (e != hipSuccess) return hip_error(e, "quantized_linear: kernel launch");
+    g_dispatches.fetch_add(1);
+    return MIMO_OK;
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 """The vision tower's operators over patch embeddings, on torch tensors:
-attention over the plan's chunks with its backward pass.
+attention over the plan's chunks and layer norm, each with its backward pass,
+and the matrix product in 8-bit integers.
 
 Argument checks and allocation only: the work runs in the HIP library
 (``include/mimo_pre.h``), on the tensors' device and on ``stream`` (default:
@@ -184,3 +185,185 @@ def chunk_attention_backward(dout, q, k, v, out, lse, cu_seqlens, window=-1, sca
 def chunk_attention_workspace_bytes(rows: int, q_heads: int, chunks: int) -> int:
     """mimo_chunk_attention_workspace_bytes."""
     return int(_abi.load().mimo_chunk_attention_workspace_bytes(int(rows), int(q_heads), int(chunks)))
+
+
+_TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+_CODES = {torch.float32: _abi.MIMO_F32, torch.bfloat16: _abi.MIMO_BF16}
+_KINDS = (torch.float32, torch.bfloat16)
+
+
+def _out_type(what, out_dtype, default=None):
+    if out_dtype is None and default is not None:
+        return default
+    _require(out_dtype in _TYPES, lambda: f"{what}: out_dtype {out_dtype!r} is not f32 or bf16")
+    return _TYPES[out_dtype]
+
+
+def _matrix(t, what, name, shape=None, dtypes=_KINDS):
+    """A dense [rows, width] tensor of one of dtypes."""
+    _require(t.dim() == 2 and t.dtype in dtypes and t.is_contiguous(),
+             lambda: f"{what}: {name} must be a contiguous [rows, width] tensor of "
+                     f"{' or '.join(str(d) for d in dtypes)}, got {tuple(t.shape)} {t.dtype}"
+                     + ("" if t.is_contiguous() else " (not contiguous)"))
+    _require(shape is None or t.shape == shape, lambda: f"{what}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, return_stats: bool = False,
+               mean=None, rstd=None, stream=None):
+    """mimo_layer_norm: (x - mean) * rstd * weight + bias of each row of x
+    [rows, width] (float32 or bf16, contiguous; merge units are a view of four
+    rows as one); weight and bias float32 [width] or None.
+
+    Returns out [rows, width] of out_dtype ("f32" or "bf16"; x's by default),
+    or with return_stats=True (out, mean, rstd) with float32 [rows]
+    statistics, which the backward pass takes.  out may be x itself where the
+    dtypes agree.
+    """
+    what = "layer_norm"
+    _matrix(x, what, "x")
+    rows, width = x.shape
+    _require(width >= 1, lambda: f"{what}: x has no columns")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _vector(t, what, name, width, torch.float32)
+    dev = x.device
+    dtype = out.dtype if out is not None else _out_type(what, out_dtype, x.dtype)
+    if out is not None:
+        _matrix(out, what, "out", x.shape)
+    _abi._check_device((x, weight, bias, out, mean, rstd), what)
+    with _on(dev, stream, (x, weight, bias, out, mean, rstd), what):
+        if out is None:
+            out = torch.empty((rows, width), dtype=dtype, device=dev)
+        if return_stats:
+            if mean is None:
+                mean = torch.empty(rows, dtype=torch.float32, device=dev)
+            if rstd is None:
+                rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _vector(t, what, name, rows, torch.float32)
+        _check(_abi.load().mimo_layer_norm(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(weight), _pointer(bias),
+                                           float(eps), _CODES[dtype], out.data_ptr(), _pointer(mean), _pointer(rstd),
+                                           _abi._stream_handle(stream, dev)), what)
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_backward(dout, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, affine=None, workspace=None,
+                        stream=None):
+    """mimo_layer_norm_backward: the gradients of layer_norm's x, weight and
+    bias for dout [rows, width] (float32 or bf16), given x and the forward
+    call's mean and rstd.
+
+    Returns (dx, dweight, dbias): x's dtype, and float32 [width] each.  The
+    sums over rows are made where weight is given, or with affine=True (a norm
+    with a bias alone needs dbias too); otherwise, or with affine=False, those
+    two that are not passed in are None.  ``workspace``: uint8, at least
+    layer_norm_workspace_bytes(rows, width) bytes; calls that may run at the
+    same time need one each.
+    """
+    what = "layer_norm_backward"
+    _matrix(x, what, "x")
+    rows, width = x.shape
+    _require(width >= 1, lambda: f"{what}: x has no columns")
+    _matrix(dout, what, "dout", x.shape)
+    for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (weight, "weight", width), (dweight, "dweight", width),
+                       (dbias, "dbias", width)):
+        if t is not None:
+            _vector(t, what, name, n, torch.float32)
+    _require(mean is not None and rstd is not None, f"{what}: mean and rstd are needed (layer_norm returns them with return_stats=True)")
+    if dx is not None:
+        _matrix(dx, what, "dx", x.shape, (x.dtype,))
+    dev = x.device
+    tensors = (dout, x, mean, rstd, weight, dx, dweight, dbias, workspace)
+    _abi._check_device(tensors, what)
+    with _on(dev, stream, tensors, what):
+        if dx is None:
+            dx = torch.empty((rows, width), dtype=x.dtype, device=dev)
+        if weight is not None if affine is None else affine:
+            if dweight is None:
+                dweight = torch.empty(width, dtype=torch.float32, device=dev)
+            if dbias is None:
+                dbias = torch.empty(width, dtype=torch.float32, device=dev)
+        if workspace is not None:
+            _abi._check_bytes(workspace, what + ": workspace")
+        elif dweight is not None or dbias is not None:
+            workspace = torch.empty(max(layer_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8, device=dev)
+        _check(_abi.load().mimo_layer_norm_backward(
+            rows, width, x.data_ptr(), _CODES[x.dtype], dout.data_ptr(), _CODES[dout.dtype], _pointer(weight),
+            mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _pointer(dweight), _pointer(dbias), _pointer(workspace),
+            0 if workspace is None else workspace.numel(), _abi._stream_handle(stream, dev)), what)
+    return dx, dweight, dbias
+
+
+def layer_norm_workspace_bytes(rows: int, width: int) -> int:
+    """mimo_layer_norm_workspace_bytes."""
+    return int(_abi.load().mimo_layer_norm_workspace_bytes(int(rows), int(width)))
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """mimo_quantize_rows: x [rows, width] (float32 or bf16, contiguous) to
+    8-bit integers, row by row: activations, or a weight [out, in] by output
+    channels.
+
+    Returns (q, scale): int8 [rows, padded], padded = width rounded up to a
+    multiple of 128 (zeros behind width), and float32 [rows]; x is near
+    q[:, :width] * scale[:, None].
+    """
+    what = "quantize_rows"
+    _matrix(x, what, "x")
+    rows, width = x.shape
+    _require(width >= 1, lambda: f"{what}: x has no columns")
+    padded = (width + 127) // 128 * 128
+    if q is not None:
+        _matrix(q, what, "q", (rows, padded), (torch.int8,))
+    if scale is not None:
+        _vector(scale, what, "scale", rows, torch.float32)
+    dev = x.device
+    _abi._check_device((x, q, scale), what)
+    with _on(dev, stream, (x, q, scale), what):
+        if q is None:
+            q = torch.empty((rows, padded), dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=dev)
+        _check(_abi.load().mimo_quantize_rows(rows, width, x.data_ptr(), _CODES[x.dtype], q.data_ptr(), scale.data_ptr(),
+                                              _abi._stream_handle(stream, dev)), what)
+    return q, scale
+
+
+def quantized_linear(xq, x_scale, wq, w_scale, bias=None, out=None, out_dtype: str = "bf16", stream=None):
+    """mimo_quantized_linear: (xq @ wq.T) * x_scale[:, None] * w_scale + bias,
+    the product in 8-bit integers with exact sums.
+
+    xq int8 [rows, k] and x_scale float32 [rows], wq int8 [out, k] and w_scale
+    float32 [out]: quantize_rows' outputs of the activations and the weight (k
+    is its padded width); bias float32 [out] or None.  Returns out [rows, out]
+    of out_dtype ("f32" or "bf16").
+    """
+    what = "quantized_linear"
+    _matrix(xq, what, "xq", dtypes=(torch.int8,))
+    _matrix(wq, what, "wq", dtypes=(torch.int8,))
+    rows, k = xq.shape
+    n = wq.shape[0]
+    _require(wq.shape[1] == k and k >= 128 and k % 128 == 0 and n >= 1,
+             lambda: f"{what}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must share a width that is a multiple of 128")
+    _vector(x_scale, what, "x_scale", rows, torch.float32)
+    _vector(w_scale, what, "w_scale", n, torch.float32)
+    if bias is not None:
+        _vector(bias, what, "bias", n, torch.float32)
+    dtype = out.dtype if out is not None else _out_type(what, out_dtype)
+    if out is not None:
+        _matrix(out, what, "out", (rows, n))
+    dev = xq.device
+    tensors = (xq, x_scale, wq, w_scale, bias, out)
+    _abi._check_device(tensors, what)
+    with _on(dev, stream, tensors, what):
+        if out is None:
+            out = torch.empty((rows, n), dtype=dtype, device=dev)
+        _check(_abi.load().mimo_quantized_linear(rows, k, xq.data_ptr(), x_scale.data_ptr(), n, wq.data_ptr(),
+                                                 w_scale.data_ptr(), _pointer(bias), _CODES[dtype], out.data_ptr(),
+                                                 _abi._stream_handle(stream, dev)), what)
+    return out
