@@ -558,7 +558,8 @@ typedef struct mimo_attention_grads {
 int mimo_chunk_attention(const mimo_attention *args, void *stream);
 
 /* Device workspace bytes of the backward pass (0 for sizes it refuses). */
-size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t chunks);
+size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                            int32_t chunks);
 
 /*
  * Backward: args as the forward call's, with its out and lse; writes dq, dk,

@@ -71,7 +71,7 @@ def test_attention_backward_refuses(bad):
 
 def test_attention_backward_workspace_and_nulls():
     lib = V.load()
-    need = V.chunk_attention_workspace_bytes(10, 4, 1)
+    need = V.chunk_attention_workspace_bytes(10, 4, 2, 64, 1)
     assert need >= 10 * 4 * 4
     assert lib.mimo_chunk_attention_backward(_attention(), _grads(), P, need - 1, None) == V.MIMO_E_CAPACITY
     assert lib.mimo_chunk_attention_backward(_attention(), _grads(), None, need, None) == V.MIMO_E_INVALID
@@ -80,7 +80,8 @@ def test_attention_backward_workspace_and_nulls():
     assert lib.mimo_chunk_attention_backward(_attention(), None, P, need, None) == V.MIMO_E_INVALID
     assert lib.mimo_chunk_attention_backward(None, _grads(), P, need, None) == V.MIMO_E_INVALID
     assert lib.mimo_chunk_attention(None, None) == V.MIMO_E_INVALID
-    for bad in ((-1, 4, 1), (1, 0, 1), (1, 1, -1), ((1 << 30) + 1, 1, 1)):
+    for bad in ((-1, 4, 2, 64, 1), (1, 0, 1, 64, 1), (1, 4, 3, 64, 1), (1, 1, 1, 60, 1), (1, 1, 1, 136, 1), (1, 1, 1, 64, -1),
+                ((1 << 30) + 1, 1, 1, 64, 1)):
         assert V.chunk_attention_workspace_bytes(*bad) == 0
     # nothing to do: no pointer is looked at
     assert lib.mimo_chunk_attention(_attention(rows=0, cu=0, q=(0, 8, 0)), None) == V.MIMO_OK

@@ -106,7 +106,7 @@ SIGNATURES = {
     "mimo_prepare_pixel_embed": ([_I32, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "mimo_pixel_embed": ([_I32, _P, _P, _I64, _I32, _P, _P, _I32, _P, _I64, _P, _SZ, _P], ctypes.c_int),
     "mimo_chunk_attention": ([_P, _P], ctypes.c_int),
-    "mimo_chunk_attention_workspace_bytes": ([_I64, _I32, _I32], _SZ),
+    "mimo_chunk_attention_workspace_bytes": ([_I64, _I32, _I32, _I32, _I32], _SZ),
     "mimo_chunk_attention_backward": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
     "mimo_layer_norm": ([_I64, _I32, _P, _I32, _P, _P, ctypes.c_float, _I32, _P, _P, _P, _P], ctypes.c_int),
     "mimo_layer_norm_workspace_bytes": ([_I64, _I32], _SZ),

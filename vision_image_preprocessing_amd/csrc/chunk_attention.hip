@@ -724,8 +724,10 @@ int mimo_chunk_attention(const mimo_attention *p, void *stream) {
     return MIMO_OK;
 }
 
-size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t chunks) {
-    if (rows < 0 || rows > kMaxRows || q_heads < 1 || q_heads > 65536 || chunks < 0 || chunks > kMaxRows) return 0;
+size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t chunks) {
+    if (rows < 0 || rows > kMaxRows || chunks < 0 || chunks > kMaxRows || kv_heads < 1 || q_heads < kv_heads ||
+        q_heads % kv_heads || q_heads > 65536 || head_dim < 8 || head_dim > MIMO_HEAD_DIM_MAX || head_dim % 8)
+        return 0;
     return delta_bytes(rows, q_heads) + align256(size_t(rows / kTileRows + chunks) * size_t(q_heads) * sizeof(float));
 }
 
@@ -758,7 +760,7 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
         }
         if (!workspace || !check_ptr_align(workspace, 16))
             return set_error(MIMO_E_INVALID, std::string(who) + ": workspace must be non-null and 16-byte aligned");
-        if (workspace_bytes < mimo_chunk_attention_workspace_bytes(a.rows, a.q_heads, a.chunks))
+        if (workspace_bytes < mimo_chunk_attention_workspace_bytes(a.rows, a.q_heads, a.kv_heads, a.head_dim, a.chunks))
             return set_error(MIMO_E_CAPACITY,
                              std::string(who) + ": workspace smaller than mimo_chunk_attention_workspace_bytes");
     } else if (!g->dsink) {

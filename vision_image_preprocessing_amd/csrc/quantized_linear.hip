@@ -15,6 +15,7 @@
 
 #include <cstring>
 #include <string>
+#include <type_traits>
 
 #include "device_util.h"
 #include "internal.h"
@@ -253,6 +254,221 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
         for (int j = 0; j < 2; ++j) store_block<OutT>(a, acc[i][j], m0 + wm + 32 * i + (lane & 31), n0 + wn + 32 * j);
 }
 
+// A 256 x 256 tile by four waves, 128 x 128 each (256 accumulators a lane),
+// which keeps the LDS bytes per product low enough that the matrix cores set
+// the pace.  K advances 128 bytes a stage; operands go from memory straight
+// into LDS (buffer_load ... lds), x two stages ahead of the products (three
+// buffers), the weight one (two buffers): 160 KB, one workgroup a CU.  The
+// five buffers are arrays of their own, so that the compiler sees that the
+// loads into one never meet the reads of another; the stage loop is unrolled
+// six times, after which both rings are back where they were.  Stages past
+// the end are loaded through an empty resource: zeros, without memory traffic.
+constexpr int kBig = 256;
+typedef __attribute__((address_space(3))) void *lds_void_ptr;
+constexpr int kWord3 = 0x00020000;            // raw buffer resource word 3
+constexpr int kRecords = 0x7FFFFFF0;          // its size; tile offsets are below 2^25
+// s_waitcnt immediates (gfx9 layout: vmcnt in bits 3:0 and 15:14, expcnt in
+// 6:4, lgkmcnt in 11:8; a field at its maximum does not wait).
+constexpr int kWaitAll = 0;
+constexpr int kWaitVmemButX = 0x0F78;         // vmcnt(8): one stage of x may stay in flight
+constexpr int kWaitLdsVmemButX = 0x0078;      // lgkmcnt(0) and vmcnt(8)
+
+template <typename OutT>
+__global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
+    constexpr int kGroups = kBig / 8 / 4;     // groups of eight rows a wave loads of each operand
+    constexpr int kSteps = 4;                 // products of 32 bytes of K in a stage
+    __shared__ uint8_t sx0[kBig * 128], sx1[kBig * 128], sx2[kBig * 128];
+    __shared__ uint8_t sw0[kBig * 128], sw1[kBig * 128];
+    const int64_t tile = xcd_contiguous_tile(blockIdx.x, gridDim.x);
+    const int64_t mt = tile / a.n_tiles;
+    const int64_t m0 = mt * kBig;
+    const int n0 = int(tile - mt * a.n_tiles) * kBig;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int stages = a.k / 128;
+
+    // Lane l of a wave's load lands at row l / 8, chunk l % 8 of a group of
+    // eight rows, so it fetches the chunk that the swizzle puts there.  Rows
+    // past the last one read the last one; they are not stored.
+    auto rsrc = [&](const int8_t *p, int s) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(p), 0, s < stages ? kRecords : 0, kWord3);
+    };
+    auto x_rsrc = [&](int s) { return rsrc(a.x + m0 * a.k, s); };
+    auto w_rsrc = [&](int s) { return rsrc(a.w + int64_t(n0) * a.k, s); };
+    uint32_t x_off[kGroups], w_off[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int r = (wave * kGroups + i) * 8 + (lane >> 3);
+        const int v = (lane & 7) ^ ((r ^ (r >> 3)) & 7);
+        x_off[i] = uint32_t(int(min(m0 + r, a.n_rows - 1) - m0) * a.k + v * 16);
+        w_off[i] = uint32_t((min(n0 + r, a.e - 1) - n0) * a.k + v * 16);
+    }
+    auto load = [&](const __amdgpu_buffer_rsrc_t &r, uint32_t off, int i, int s, uint8_t *d) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)(d + (wave * kGroups + i) * 1024), 16, off, s < stages ? s * 128 : 0, 0, 0);
+    };
+    auto load_x = [&](int i, int s, uint8_t *d) { load(x_rsrc(s), x_off[i], i, s, d); };
+    auto load_w = [&](int i, int s, uint8_t *d) { load(w_rsrc(s), w_off[i], i, s, d); };
+    // between stages: each wave has waited for its own loads and reads
+    auto barrier = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    i32x16 acc[4][4];  // [rows][channels]
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+    i32x4 fx[2][4], fw[2][4];
+    auto read = [&](const uint8_t *tx, const uint8_t *tw, int s, i32x4 (&x)[4], i32x4 (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const i32x4 *>(tx + lds_at(wm * 128 + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const i32x4 *>(tw + lds_at(wn * 128 + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
+    };
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_x(i, 0, sx0);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_w(i, 0, sw0);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_x(i, 1, sx1);
+    __builtin_amdgcn_s_waitcnt(kWaitVmemButX);
+    barrier();
+    read(sx0, sw0, 0, fx[0], fw[0]);
+    // One stage: the next step's operands are read while this one's products
+    // run; the loads go out in its first half, two after each row of four
+    // products; before the last step's products, whose operands are in
+    // registers, the waves meet and read the next stage's first operands.
+    auto stage = [&](int s, const uint8_t *tx, const uint8_t *tw, uint8_t *nw, uint8_t *nx2, const uint8_t *nx,
+                     const uint8_t *nwr) __attribute__((always_inline)) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+            if (ks + 1 < kSteps) {
+                read(tx, tw, ks + 1, fx[(ks + 1) & 1], fw[(ks + 1) & 1]);
+            } else {
+                __builtin_amdgcn_s_waitcnt(kWaitLdsVmemButX);
+                barrier();
+                read(nx, nwr, 0, fx[0], fw[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
+                const int slot = ks * 4 + i;
+                if (slot < 4) {
+                    load_w(2 * slot, s + 1, nw);
+                    load_w(2 * slot + 1, s + 1, nw);
+                } else if (slot < 8) {
+                    load_x(2 * slot - 8, s + 2, nx2);
+                    load_x(2 * slot - 7, s + 2, nx2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    // stage u of a group of six
+    auto ring = [&](int s, auto number) __attribute__((always_inline)) {
+        constexpr int u = decltype(number)::value;
+        uint8_t *const x = u % 3 == 0 ? sx0 : u % 3 == 1 ? sx1 : sx2, *const x1 = u % 3 == 0 ? sx1 : u % 3 == 1 ? sx2 : sx0;
+        uint8_t *const x2 = u % 3 == 0 ? sx2 : u % 3 == 1 ? sx0 : sx1;
+        uint8_t *const w = u % 2 ? sw1 : sw0, *const w1 = u % 2 ? sw0 : sw1;
+        stage(s, x, w, w1, x2, x1, w1);
+    };
+    typedef std::integral_constant<int, 0> U0;
+    typedef std::integral_constant<int, 1> U1;
+    typedef std::integral_constant<int, 2> U2;
+    typedef std::integral_constant<int, 3> U3;
+    typedef std::integral_constant<int, 4> U4;
+    typedef std::integral_constant<int, 5> U5;
+    int s = 0;
+    for (; s + 6 <= stages; s += 6) {
+        ring(s, U0());
+        ring(s + 1, U1());
+        ring(s + 2, U2());
+        ring(s + 3, U3());
+        ring(s + 4, U4());
+        ring(s + 5, U5());
+    }
+    // the rest, nested: where two paths met, the compiler could not tell which
+    // loads are in flight and would wait for all of them before the next read
+    const int rest = stages - s;
+    if (rest > 0) {
+        ring(s, U0());
+        if (rest > 1) {
+            ring(s + 1, U1());
+            if (rest > 2) {
+                ring(s + 2, U2());
+                if (rest > 3) {
+                    ring(s + 3, U3());
+                    if (rest > 4) ring(s + 4, U4());
+                }
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    barrier();
+
+    // Each wave turns its block in 16 KB of LDS, 32 rows at a time (rows of
+    // 512 bytes, 16-byte chunks XOR-swizzled by the row): a lane then holds
+    // whole pieces of rows, whose channels are the same for every row.
+    uint8_t *region = (wave < 2 ? sx0 : sx1) + (wave & 1) * 16384;
+    constexpr int kOut = 16 / int(sizeof(OutT)), kLanes = 128 / kOut, kPass = 64 / kLanes;
+    const int piece = lane % kLanes;
+    const int col = n0 + wn * 128 + piece * kOut;
+    float t[kOut], b[kOut];
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+        const int e = min(col + j, a.e - 1);
+        t[j] = a.w_scale[e];
+        b[j] = a.bias ? a.bias[e] : 0.0f;
+    }
+    const bool whole = a.e % kOut == 0 && col + kOut <= a.e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = lane & 31;
+        const float xs = a.x_scale[min(m0 + wm * 128 + i * 32 + r, a.n_rows - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = j * 8 + 2 * g + (lane >> 5);
+                const f32x4 v = {float(acc[i][j][4 * g]) * xs, float(acc[i][j][4 * g + 1]) * xs, float(acc[i][j][4 * g + 2]) * xs,
+                                 float(acc[i][j][4 * g + 3]) * xs};
+                *reinterpret_cast<f32x4 *>(region + r * 512 + ((c ^ r) % 32) * 16) = v;
+            }
+#pragma unroll
+        for (int p = 0; p < 32 / kPass; ++p) {
+            const int rr = p * kPass + lane / kLanes;
+            float v[kOut];
+#pragma unroll
+            for (int k = 0; k < kOut / 4; ++k) {
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(region + rr * 512 + (((piece * (kOut / 4) + k) ^ rr) % 32) * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * k + j] = fmaf(w[j], t[4 * k + j], b[4 * k + j]);
+            }
+            const int64_t row = m0 + wm * 128 + i * 32 + rr;
+            if (row >= a.n_rows) continue;
+            OutT *out = static_cast<OutT *>(a.out) + row * a.e + col;
+            if (whole) {
+                if constexpr (sizeof(OutT) == 4) {
+                    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4 *>(out));
+                } else {
+                    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+                    bf16x8 h;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
+                    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<u32x4 *>(out));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kOut; ++j)
+                    if (col + j < a.e) out[j] = OutT(v[j]);
+            }
+        }
+    }
+}
+
 // Few rows: a workgroup takes 32 rows and 32 channels and its waves share K,
 // operands straight from memory; the waves' sums meet in LDS.
 template <typename OutT>
@@ -359,10 +575,11 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
     a.e = embed_dim;
     a.k = k;
     const int64_t m128 = (n_rows + 127) / 128, n128 = (embed_dim + 127) / 128;
-    const bool few = m128 * n128 < 128;
-    const int64_t tiles = few ? (n_rows + 31) / 32 * ((int64_t(embed_dim) + 31) / 32) : m128 * n128;
+    const int64_t m256 = (n_rows + 255) / 256, n256 = (embed_dim + 255) / 256;
+    const bool few = m128 * n128 < 128, big = m256 * n256 >= 512;
+    const int64_t tiles = few ? (n_rows + 31) / 32 * ((int64_t(embed_dim) + 31) / 32) : big ? m256 * n256 : m128 * n128;
     if (tiles > 0x7FFFFFFFll) return set_error(MIMO_E_TOO_LARGE, "quantized_linear: more than 2^31 - 1 tiles");
-    a.n_tiles = few ? (embed_dim + 31) / 32 : int32_t(n128);
+    a.n_tiles = few ? (embed_dim + 31) / 32 : int32_t(big ? n256 : n128);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 grid{unsigned(tiles), 1, 1}, block{unsigned(kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
@@ -370,6 +587,10 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
             hipLaunchKernelGGL(linear_few_kernel<float>, grid, block, 0, s, a);
         else if (few)
             hipLaunchKernelGGL(linear_few_kernel<__bf16>, grid, block, 0, s, a);
+        else if (big && out_dtype == MIMO_F32)
+            hipLaunchKernelGGL(linear_big_kernel<float>, grid, block, 0, s, a);
+        else if (big)
+            hipLaunchKernelGGL(linear_big_kernel<__bf16>, grid, block, 0, s, a);
         else if (out_dtype == MIMO_F32)
             hipLaunchKernelGGL(linear_tile_kernel<float>, grid, block, 0, s, a);
         else

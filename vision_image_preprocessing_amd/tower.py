@@ -7,6 +7,11 @@ Argument checks and allocation only: the work runs in the HIP library
 torch's current stream there).  Outputs and workspaces that are not passed in
 are allocated by torch on that stream.  The framework keeps no autograd
 graph: each backward pass is a call of its own.
+
+A small call is bound by the host, so the checks are written to cost a few
+hundred nanoseconds: attributes compared in place, messages formed on failure
+only (one small image's norm: 10.7 us a call with a message closure and a
+device object for every check, against the figure in the design notes).
 """
 from __future__ import annotations
 
@@ -16,16 +21,48 @@ import struct
 import torch
 
 from . import _abi
-from ._abi import MIMO_OK, _require
+from ._abi import MIMO_BF16, MIMO_E_INVALID, MIMO_F32, MimoError
+
+_F32, _BF16, _I8, _I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
+_TYPES = {"f32": _F32, "bf16": _BF16}
+_CODES = {_F32: MIMO_F32, _BF16: MIMO_BF16}
+_empty = torch.empty
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 # mimo_attention and mimo_attention_grads (include/mimo_pre.h)
 _ATTENTION = struct.Struct("<q5if2Q" + "Qqq" * 4 + "Q")
 _GRADS = struct.Struct("<" + "Qqq" * 4 + "Q")
 
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = _abi.load()
+    return _lib
+
+
+def _refuse(message):
+    raise MimoError(MIMO_E_INVALID, message)
+
+
+def _one_device(what, tensors):
+    """The GPU every tensor is on (the first is not None)."""
+    index = tensors[0].get_device()
+    if index >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return index
+    _abi._check_device(tensors, what)
+    return index
+
 
 @contextlib.contextmanager
-def _entered(device, stream, tensors):
-    index = device.index
+def _entered(index, stream, tensors):
     with contextlib.ExitStack() as stack:
         if index != torch.cuda.current_device():
             stack.enter_context(torch.cuda.device(index))
@@ -37,70 +74,83 @@ def _entered(device, stream, tensors):
         yield
 
 
-_NOTHING = contextlib.nullcontext()
+_HERE = contextlib.nullcontext()
 
 
-def _on(device, stream, tensors, what):
+def _on(what, index, stream, tensors):
     """The context a call runs in: the tensors' device current, and the
     caller's stream, if one is given, current and known to the allocator as a
     user of the tensors."""
-    if stream is not None:
-        _require(stream.device == device, lambda: f"{what}: the stream belongs to {stream.device}, the tensors to {device}")
-    elif device.index == torch.cuda.current_device():
-        return _NOTHING
-    return _entered(device, stream, tensors)
+    if stream is None:
+        return _HERE if _device_now() == index else _entered(index, None, ())
+    if stream.device.index != index:
+        _refuse(f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
+    return _entered(index, stream, tensors)
 
 
-def _check(code, what):
-    if code != MIMO_OK:
-        _abi._check(code, what)
+def _check_vector(what, name, t, n, dtype):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _refuse(f"{what}: {name} must be contiguous {dtype} [{n}], got {tuple(t.shape)} {t.dtype}")
 
 
-def _heads(t, what, name, shape=None):
+def _check_matrix(what, name, t, dtypes=_CODES):
+    if t.dim() != 2 or t.dtype not in dtypes or not t.is_contiguous():
+        _refuse(f"{what}: {name} must be a contiguous [rows, width] tensor of {' or '.join(str(d) for d in dtypes)}, "
+                f"got {tuple(t.shape)} {t.dtype}" + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+def _check_shape(what, name, t, shape):
+    if t.shape != shape:
+        _refuse(f"{what}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------------ attention
+
+def _heads(what, name, t, shape):
     """(pointer, row stride, head stride) of a bf16 [rows, heads, head_dim] tensor."""
-    _require(t.dtype == torch.bfloat16 and t.dim() == 3,
-             lambda: f"{what}: {name} must be bfloat16 [rows, heads, head_dim], got {tuple(t.shape)} {t.dtype}")
-    _require(shape is None or t.shape == shape, lambda: f"{what}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != _BF16 or t.shape != shape:
+        _refuse(f"{what}: {name} must be bfloat16 {tuple(shape)} ([rows, heads, head_dim]), got {tuple(t.shape)} {t.dtype}")
     row, head, inner = t.stride()
-    rows, heads, dim = t.shape
-    _require(inner == 1 or dim == 1, lambda: f"{what}: {name}'s innermost axis must be dense, got strides {t.stride()}")
+    rows, heads, dim = shape
+    if inner != 1 and dim != 1:
+        _refuse(f"{what}: {name}'s innermost axis must be dense, got strides {t.stride()}")
     # torch leaves the stride of an axis of one free: the library asks for a valid one
     return t.data_ptr(), row if rows > 1 else max(dim, 8), head if heads > 1 else 0
 
 
-def _vector(t, what, name, n, dtype):
-    _require(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-             lambda: f"{what}: {name} must be contiguous {dtype} [{n}], got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
-
-
-def _pack_attention(what, q, k, v, cu_seqlens, window, scale, sink, out, lse):
+def _check_qkv(what, q, k, v, cu_seqlens, sink, lse):
+    if q.dim() != 3 or k.dim() != 3:
+        _refuse(f"{what}: {'q' if q.dim() != 3 else 'k'} must be [rows, heads, head_dim], got "
+                f"{tuple(q.shape if q.dim() != 3 else k.shape)}")
     rows, q_heads, head_dim = q.shape
-    _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] >= 1
-             and cu_seqlens.is_contiguous(),
-             lambda: f"{what}: cu_seqlens must be contiguous int32 [chunks + 1], got {tuple(cu_seqlens.shape)} "
-                     f"{cu_seqlens.dtype}")
-    if lse is not None:
-        _require(lse.dtype == torch.float32 and lse.shape == (q_heads, rows) and lse.is_contiguous(),
-                 lambda: f"{what}: lse must be contiguous float32 [{q_heads}, {rows}], got {tuple(lse.shape)} {lse.dtype}")
-    if window is None or window < 0:
-        window = -1
+    krows, kv_heads, kdim = k.shape
+    if krows != rows or kdim != head_dim or kv_heads < 1 or q_heads < 1 or q_heads % kv_heads:
+        _refuse(f"{what}: q {tuple(q.shape)} and k {tuple(k.shape)} must agree in rows and head_dim, and q's heads must be a "
+                "multiple of k's")
+    if v.shape != k.shape:
+        _refuse(f"{what}: v must be of k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    if cu_seqlens.dtype != _I32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+        _refuse(f"{what}: cu_seqlens must be contiguous int32 [chunks + 1], got {tuple(cu_seqlens.shape)} {cu_seqlens.dtype}")
+    if sink is not None:
+        _check_vector(what, "sink", sink, q_heads, _F32)
+    if lse is not None and (lse.dtype != _F32 or lse.shape != (q_heads, rows) or not lse.is_contiguous()):
+        _refuse(f"{what}: lse must be contiguous float32 [{q_heads}, {rows}], got {tuple(lse.shape)} {lse.dtype}")
+    return rows, q_heads, kv_heads, head_dim
+
+
+def _pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse):
+    rows, q_heads, kv_heads, head_dim = sizes
+    kv = k.shape
     return _ATTENTION.pack(
-        rows, q_heads, k.shape[1], head_dim, cu_seqlens.shape[0] - 1, min(int(window), 2 ** 31 - 1),
-        head_dim ** -0.5 if scale is None else float(scale), cu_seqlens.data_ptr(),
-        0 if sink is None else _vector(sink, what, "sink", q_heads, torch.float32),
-        *_heads(q, what, "q"), *_heads(k, what, "k"), *_heads(v, what, "v", k.shape),
-        *_heads(out, what, "out", q.shape), 0 if lse is None else lse.data_ptr())
-
-
-def _check_qkv(what, q, k, v):
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _require(t.dim() == 3, lambda: f"{what}: {name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
-    rows, q_heads, head_dim = q.shape
-    _require(k.shape[0] == rows and k.shape[2] == head_dim and k.shape[1] >= 1 and q_heads >= 1
-             and q_heads % k.shape[1] == 0,
-             lambda: f"{what}: q {tuple(q.shape)} and k {tuple(k.shape)} must agree in rows and head_dim, and q's heads "
-                     "must be a multiple of k's")
+        rows, q_heads, kv_heads, head_dim, cu_seqlens.shape[0] - 1,
+        -1 if window is None or window < 0 else min(int(window), 0x7FFFFFFF),
+        head_dim ** -0.5 if scale is None and head_dim else float(scale or 0.0), cu_seqlens.data_ptr(),
+        0 if sink is None else sink.data_ptr(), *_heads(what, "q", q, q.shape), *_heads(what, "k", k, kv),
+        *_heads(what, "v", v, kv), *_heads(what, "out", out, q.shape), 0 if lse is None else lse.data_ptr())
 
 
 def chunk_attention(q, k, v, cu_seqlens, window=-1, scale=None, sink=None, out=None, lse=None,
@@ -122,17 +172,21 @@ def chunk_attention(q, k, v, cu_seqlens, window=-1, scale=None, sink=None, out=N
     allocated here).
     """
     what = "chunk_attention"
-    _check_qkv(what, q, k, v)
-    dev = q.device
-    with _on(dev, stream, (q, k, v, cu_seqlens, sink, out, lse), what) if dev.type == "cuda" else _NOTHING:
-        if dev.type == "cuda":
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-            if lse is None and return_lse:
-                lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
-        args = _pack_attention(what, q, k, v, cu_seqlens, window, scale, sink, q if out is None else out, lse)
-        _abi._check_device((q, k, v, cu_seqlens, sink, out, lse), what)
-        _check(_abi.load().mimo_chunk_attention(args, _abi._stream_handle(stream, dev)), what)
+    sizes = _check_qkv(what, q, k, v, cu_seqlens, sink, lse)
+    if out is None:
+        _heads(what, "q", q, q.shape)  # before anything is allocated for it
+    else:
+        _heads(what, "out", out, q.shape)
+    index = _one_device(what, (q, k, v, cu_seqlens, sink, out, lse))
+    with _on(what, index, stream, (q, k, v, cu_seqlens, sink, out, lse)):
+        if out is None:
+            out = _empty(q.shape, dtype=_BF16, device=q.device)
+        if return_lse and lse is None:
+            lse = _empty((sizes[1], sizes[0]), dtype=_F32, device=q.device)
+        code = _library().mimo_chunk_attention(_pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse),
+                                               _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return (out, lse) if return_lse else out
 
 
@@ -146,70 +200,64 @@ def chunk_attention_backward(dout, q, k, v, out, lse, cu_seqlens, window=-1, sca
     Returns (dq, dk, dv, dsink): bf16 of q's, k's and v's shapes, and float32
     [q_heads], or None without sink.  Gradients are overwritten; rows behind
     cu_seqlens[-1] are left as they were.  ``workspace``: uint8, at least
-    chunk_attention_workspace_bytes(rows, q_heads, chunks) bytes; calls that
-    may run at the same time need one each.
+    chunk_attention_workspace_bytes(rows, q_heads, kv_heads, head_dim, chunks)
+    bytes; calls that may run at the same time need one each.
     """
     what = "chunk_attention_backward"
-    _check_qkv(what, q, k, v)
-    _require(dsink is None or sink is not None, f"{what}: dsink is given without sink")
-    rows, q_heads, _ = q.shape
-    dev = q.device
-    _require(lse is not None, f"{what}: lse is None (chunk_attention returns it with return_lse=True)")
-    ins = (dout, q, k, v, out, lse, cu_seqlens, sink)
-    with _on(dev, stream, (*ins, dq, dk, dv, dsink, workspace), what) if dev.type == "cuda" else _NOTHING:
-        args = _pack_attention(what, q, k, v, cu_seqlens, window, scale, sink, out, lse)
-        dout_heads = _heads(dout, what, "dout", q.shape)
-        _abi._check_device(ins, what)
+    if lse is None:
+        _refuse(f"{what}: lse is None (chunk_attention returns it with return_lse=True)")
+    sizes = _check_qkv(what, q, k, v, cu_seqlens, sink, lse)
+    if dsink is not None:
+        if sink is None:
+            _refuse(f"{what}: dsink is given without sink")
+        _check_vector(what, "dsink", dsink, sizes[1], _F32)
+    if workspace is not None:
+        _abi._check_bytes(workspace, what + ": workspace")
+    args = _pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse)
+    dout_heads = _heads(what, "dout", dout, q.shape)
+    tensors = (q, k, v, out, lse, cu_seqlens, sink, dout, dq, dk, dv, dsink, workspace)
+    index = _one_device(what, tensors)
+    with _on(what, index, stream, tensors):
+        dev = q.device
         if dq is None:
-            dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            dq = _empty(q.shape, dtype=_BF16, device=dev)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+            dk = _empty(k.shape, dtype=_BF16, device=dev)
         if dv is None:
-            dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+            dv = _empty(v.shape, dtype=_BF16, device=dev)
         if dsink is None and sink is not None:
-            dsink = torch.empty(q_heads, dtype=torch.float32, device=dev)
+            dsink = _empty(sizes[1], dtype=_F32, device=dev)
+        lib = _library()
         if workspace is None:
-            workspace = torch.empty(max(chunk_attention_workspace_bytes(rows, q_heads, cu_seqlens.shape[0] - 1), 16),
-                                    dtype=torch.uint8, device=dev)
-        else:
-            _abi._check_bytes(workspace, what + ": workspace")
-        grads = _GRADS.pack(*dout_heads, *_heads(dq, what, "dq", q.shape), *_heads(dk, what, "dk", k.shape),
-                            *_heads(dv, what, "dv", v.shape),
-                            0 if dsink is None else _vector(dsink, what, "dsink", q_heads, torch.float32))
-        _abi._check_device((q, dq, dk, dv, dsink, workspace), what)
-        _check(_abi.load().mimo_chunk_attention_backward(args, grads, workspace.data_ptr(), workspace.numel(),
-                                                         _abi._stream_handle(stream, dev)), what)
+            need = lib.mimo_chunk_attention_workspace_bytes(*sizes, cu_seqlens.shape[0] - 1)
+            workspace = _empty(max(need, 16), dtype=torch.uint8, device=dev)
+        grads = _GRADS.pack(*dout_heads, *_heads(what, "dq", dq, q.shape), *_heads(what, "dk", dk, k.shape),
+                            *_heads(what, "dv", dv, v.shape), 0 if dsink is None else dsink.data_ptr())
+        code = lib.mimo_chunk_attention_backward(args, grads, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return dq, dk, dv, dsink
 
 
-def chunk_attention_workspace_bytes(rows: int, q_heads: int, chunks: int) -> int:
+def chunk_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int, chunks: int) -> int:
     """mimo_chunk_attention_workspace_bytes."""
-    return int(_abi.load().mimo_chunk_attention_workspace_bytes(int(rows), int(q_heads), int(chunks)))
+    return int(_library().mimo_chunk_attention_workspace_bytes(int(rows), int(q_heads), int(kv_heads), int(head_dim), int(chunks)))
 
 
-_TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
-_CODES = {torch.float32: _abi.MIMO_F32, torch.bfloat16: _abi.MIMO_BF16}
-_KINDS = (torch.float32, torch.bfloat16)
+# ----------------------------------------------------------------- layer norm
 
-
-def _out_type(what, out_dtype, default=None):
-    if out_dtype is None and default is not None:
-        return default
-    _require(out_dtype in _TYPES, lambda: f"{what}: out_dtype {out_dtype!r} is not f32 or bf16")
+def _out_type(what, out_dtype):
+    if out_dtype not in _TYPES:
+        _refuse(f"{what}: out_dtype {out_dtype!r} is not f32 or bf16")
     return _TYPES[out_dtype]
 
 
-def _matrix(t, what, name, shape=None, dtypes=_KINDS):
-    """A dense [rows, width] tensor of one of dtypes."""
-    _require(t.dim() == 2 and t.dtype in dtypes and t.is_contiguous(),
-             lambda: f"{what}: {name} must be a contiguous [rows, width] tensor of "
-                     f"{' or '.join(str(d) for d in dtypes)}, got {tuple(t.shape)} {t.dtype}"
-                     + ("" if t.is_contiguous() else " (not contiguous)"))
-    _require(shape is None or t.shape == shape, lambda: f"{what}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _pointer(t):
-    return None if t is None else t.data_ptr()
+def _rows_of(what, x):
+    _check_matrix(what, "x", x)
+    rows, width = x.shape
+    if width < 1:
+        _refuse(f"{what}: x has no columns")
+    return rows, width
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, return_stats: bool = False,
@@ -224,31 +272,34 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
     dtypes agree.
     """
     what = "layer_norm"
-    _matrix(x, what, "x")
-    rows, width = x.shape
-    _require(width >= 1, lambda: f"{what}: x has no columns")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _vector(t, what, name, width, torch.float32)
-    dev = x.device
-    dtype = out.dtype if out is not None else _out_type(what, out_dtype, x.dtype)
+    rows, width = _rows_of(what, x)
+    if weight is not None:
+        _check_vector(what, "weight", weight, width, _F32)
+    if bias is not None:
+        _check_vector(what, "bias", bias, width, _F32)
+    if mean is not None:
+        _check_vector(what, "mean", mean, rows, _F32)
+    if rstd is not None:
+        _check_vector(what, "rstd", rstd, rows, _F32)
     if out is not None:
-        _matrix(out, what, "out", x.shape)
-    _abi._check_device((x, weight, bias, out, mean, rstd), what)
-    with _on(dev, stream, (x, weight, bias, out, mean, rstd), what):
+        _check_matrix(what, "out", out)
+        _check_shape(what, "out", out, x.shape)
+        dtype = out.dtype
+    else:
+        dtype = x.dtype if out_dtype is None else _out_type(what, out_dtype)
+    index = _one_device(what, (x, weight, bias, out, mean, rstd))
+    with _on(what, index, stream, (x, weight, bias, out, mean, rstd)):
         if out is None:
-            out = torch.empty((rows, width), dtype=dtype, device=dev)
+            out = _empty((rows, width), dtype=dtype, device=x.device)
         if return_stats:
             if mean is None:
-                mean = torch.empty(rows, dtype=torch.float32, device=dev)
+                mean = _empty(rows, dtype=_F32, device=x.device)
             if rstd is None:
-                rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None:
-                _vector(t, what, name, rows, torch.float32)
-        _check(_abi.load().mimo_layer_norm(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(weight), _pointer(bias),
-                                           float(eps), _CODES[dtype], out.data_ptr(), _pointer(mean), _pointer(rstd),
-                                           _abi._stream_handle(stream, dev)), what)
+                rstd = _empty(rows, dtype=_F32, device=x.device)
+        code = _library().mimo_layer_norm(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(weight), _pointer(bias), eps,
+                                          _CODES[dtype], out.data_ptr(), _pointer(mean), _pointer(rstd), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return (out, mean, rstd) if return_stats else out
 
 
@@ -266,43 +317,53 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, dx=None, dweight=None,
     same time need one each.
     """
     what = "layer_norm_backward"
-    _matrix(x, what, "x")
-    rows, width = x.shape
-    _require(width >= 1, lambda: f"{what}: x has no columns")
-    _matrix(dout, what, "dout", x.shape)
-    for t, name, n in ((mean, "mean", rows), (rstd, "rstd", rows), (weight, "weight", width), (dweight, "dweight", width),
-                       (dbias, "dbias", width)):
-        if t is not None:
-            _vector(t, what, name, n, torch.float32)
-    _require(mean is not None and rstd is not None, f"{what}: mean and rstd are needed (layer_norm returns them with return_stats=True)")
+    rows, width = _rows_of(what, x)
+    _check_matrix(what, "dout", dout)
+    _check_shape(what, "dout", dout, x.shape)
+    if mean is None or rstd is None:
+        _refuse(f"{what}: mean and rstd are needed (layer_norm returns them with return_stats=True)")
+    _check_vector(what, "mean", mean, rows, _F32)
+    _check_vector(what, "rstd", rstd, rows, _F32)
+    if weight is not None:
+        _check_vector(what, "weight", weight, width, _F32)
+    if dweight is not None:
+        _check_vector(what, "dweight", dweight, width, _F32)
+    if dbias is not None:
+        _check_vector(what, "dbias", dbias, width, _F32)
     if dx is not None:
-        _matrix(dx, what, "dx", x.shape, (x.dtype,))
-    dev = x.device
-    tensors = (dout, x, mean, rstd, weight, dx, dweight, dbias, workspace)
-    _abi._check_device(tensors, what)
-    with _on(dev, stream, tensors, what):
+        _check_matrix(what, "dx", dx, (x.dtype,))
+        _check_shape(what, "dx", dx, x.shape)
+    if workspace is not None:
+        _abi._check_bytes(workspace, what + ": workspace")
+    tensors = (x, dout, mean, rstd, weight, dx, dweight, dbias, workspace)
+    index = _one_device(what, tensors)
+    with _on(what, index, stream, tensors):
+        dev = x.device
         if dx is None:
-            dx = torch.empty((rows, width), dtype=x.dtype, device=dev)
+            dx = _empty((rows, width), dtype=x.dtype, device=dev)
         if weight is not None if affine is None else affine:
             if dweight is None:
-                dweight = torch.empty(width, dtype=torch.float32, device=dev)
+                dweight = _empty(width, dtype=_F32, device=dev)
             if dbias is None:
-                dbias = torch.empty(width, dtype=torch.float32, device=dev)
-        if workspace is not None:
-            _abi._check_bytes(workspace, what + ": workspace")
-        elif dweight is not None or dbias is not None:
-            workspace = torch.empty(max(layer_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8, device=dev)
-        _check(_abi.load().mimo_layer_norm_backward(
+                dbias = _empty(width, dtype=_F32, device=dev)
+        lib = _library()
+        if workspace is None and (dweight is not None or dbias is not None):
+            workspace = _empty(max(lib.mimo_layer_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8, device=dev)
+        code = lib.mimo_layer_norm_backward(
             rows, width, x.data_ptr(), _CODES[x.dtype], dout.data_ptr(), _CODES[dout.dtype], _pointer(weight),
             mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _pointer(dweight), _pointer(dbias), _pointer(workspace),
-            0 if workspace is None else workspace.numel(), _abi._stream_handle(stream, dev)), what)
+            0 if workspace is None else workspace.numel(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return dx, dweight, dbias
 
 
 def layer_norm_workspace_bytes(rows: int, width: int) -> int:
     """mimo_layer_norm_workspace_bytes."""
-    return int(_abi.load().mimo_layer_norm_workspace_bytes(int(rows), int(width)))
+    return int(_library().mimo_layer_norm_workspace_bytes(int(rows), int(width)))
 
+
+# ------------------------------------------------------ 8-bit matrix product
 
 def quantize_rows(x, q=None, scale=None, stream=None):
     """mimo_quantize_rows: x [rows, width] (float32 or bf16, contiguous) to
@@ -314,23 +375,23 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     q[:, :width] * scale[:, None].
     """
     what = "quantize_rows"
-    _matrix(x, what, "x")
-    rows, width = x.shape
-    _require(width >= 1, lambda: f"{what}: x has no columns")
-    padded = (width + 127) // 128 * 128
+    rows, width = _rows_of(what, x)
+    padded = (width + 127) & -128
     if q is not None:
-        _matrix(q, what, "q", (rows, padded), (torch.int8,))
+        _check_matrix(what, "q", q, (_I8,))
+        _check_shape(what, "q", q, (rows, padded))
     if scale is not None:
-        _vector(scale, what, "scale", rows, torch.float32)
-    dev = x.device
-    _abi._check_device((x, q, scale), what)
-    with _on(dev, stream, (x, q, scale), what):
+        _check_vector(what, "scale", scale, rows, _F32)
+    index = _one_device(what, (x, q, scale))
+    with _on(what, index, stream, (x, q, scale)):
         if q is None:
-            q = torch.empty((rows, padded), dtype=torch.int8, device=dev)
+            q = _empty((rows, padded), dtype=_I8, device=x.device)
         if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=dev)
-        _check(_abi.load().mimo_quantize_rows(rows, width, x.data_ptr(), _CODES[x.dtype], q.data_ptr(), scale.data_ptr(),
-                                              _abi._stream_handle(stream, dev)), what)
+            scale = _empty(rows, dtype=_F32, device=x.device)
+        code = _library().mimo_quantize_rows(rows, width, x.data_ptr(), _CODES[x.dtype], q.data_ptr(), scale.data_ptr(),
+                                             _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return q, scale
 
 
@@ -344,26 +405,29 @@ def quantized_linear(xq, x_scale, wq, w_scale, bias=None, out=None, out_dtype: s
     of out_dtype ("f32" or "bf16").
     """
     what = "quantized_linear"
-    _matrix(xq, what, "xq", dtypes=(torch.int8,))
-    _matrix(wq, what, "wq", dtypes=(torch.int8,))
+    _check_matrix(what, "xq", xq, (_I8,))
+    _check_matrix(what, "wq", wq, (_I8,))
     rows, k = xq.shape
-    n = wq.shape[0]
-    _require(wq.shape[1] == k and k >= 128 and k % 128 == 0 and n >= 1,
-             lambda: f"{what}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must share a width that is a multiple of 128")
-    _vector(x_scale, what, "x_scale", rows, torch.float32)
-    _vector(w_scale, what, "w_scale", n, torch.float32)
+    n, wk = wq.shape
+    if wk != k or k < 128 or k % 128 or n < 1:
+        _refuse(f"{what}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must share a width that is a multiple of 128")
+    _check_vector(what, "x_scale", x_scale, rows, _F32)
+    _check_vector(what, "w_scale", w_scale, n, _F32)
     if bias is not None:
-        _vector(bias, what, "bias", n, torch.float32)
-    dtype = out.dtype if out is not None else _out_type(what, out_dtype)
+        _check_vector(what, "bias", bias, n, _F32)
     if out is not None:
-        _matrix(out, what, "out", (rows, n))
-    dev = xq.device
-    tensors = (xq, x_scale, wq, w_scale, bias, out)
-    _abi._check_device(tensors, what)
-    with _on(dev, stream, tensors, what):
+        _check_matrix(what, "out", out)
+        _check_shape(what, "out", out, (rows, n))
+        dtype = out.dtype
+    else:
+        dtype = _out_type(what, out_dtype)
+    index = _one_device(what, (xq, x_scale, wq, w_scale, bias, out))
+    with _on(what, index, stream, (xq, x_scale, wq, w_scale, bias, out)):
         if out is None:
-            out = torch.empty((rows, n), dtype=dtype, device=dev)
-        _check(_abi.load().mimo_quantized_linear(rows, k, xq.data_ptr(), x_scale.data_ptr(), n, wq.data_ptr(),
-                                                 w_scale.data_ptr(), _pointer(bias), _CODES[dtype], out.data_ptr(),
-                                                 _abi._stream_handle(stream, dev)), what)
+            out = _empty((rows, n), dtype=dtype, device=xq.device)
+        code = _library().mimo_quantized_linear(rows, k, xq.data_ptr(), x_scale.data_ptr(), n, wq.data_ptr(),
+                                                w_scale.data_ptr(), _pointer(bias), _CODES[dtype], out.data_ptr(),
+                                                _raw_stream(index))
+    if code:
+        _abi._check(code, what)
     return out
