@@ -111,7 +111,8 @@ def test_few(V, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(2048, 1280, 1536), (2049, 1283, 256), (4100, 514, 1280), (1500, 3001, 128),
-                                   (333, 8200, 640), (70000, 130, 256), (20000, 7, 128)])
+                                   (333, 8200, 640), (70000, 130, 256), (20000, 7, 128), (8200, 8200, 256),
+                                   (262144, 200, 128), (32, 20000, 640), (600, 1000, 896), (1000, 300, 1408)])
 @pytest.mark.parametrize("out_kind", ["f32", "bf16"])
 def test_many(V, m, n, k, out_kind):
     _check_linear(V, m, n, k, out_kind, out_kind == "bf16", seed=m)

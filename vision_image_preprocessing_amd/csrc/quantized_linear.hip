@@ -32,6 +32,7 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 constexpr int kPadK = 128;          // quantised rows are multiples of this
 constexpr int kMaxK = 130944;       // 2^14 kMaxK < 2^31: no overflow, values of -128 included
 constexpr int kThreads = 256;
+constexpr int kFewThreads = 512;
 
 struct QuantizeArgs {
     const void *x;
@@ -146,143 +147,40 @@ __device__ __forceinline__ i32x16 mfma(const i32x4 &a, const i32x4 &b, const i32
 // chunks are XOR-swizzled by the row.
 __device__ __forceinline__ int lds_at(int r, int v) { return r * 128 + ((v ^ ((r ^ (r >> 3)) & 7)) << 4); }
 
-// Four consecutive channels of one row to memory.
-template <typename OutT>
-__device__ __forceinline__ void store_four(OutT *out, const float (&v)[4], int left, bool aligned) {
-    if (aligned && left >= 4) {
-        if constexpr (sizeof(OutT) == 4) {
-            *reinterpret_cast<f32x4 *>(out) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<bf16x4 *>(out) = bf16x4{__bf16(v[0]), __bf16(v[1]), __bf16(v[2]), __bf16(v[3])};
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < left) out[j] = OutT(v[j]);
-    }
-}
-
-// A 32 (channels) x 32 (rows) result block: value r of a lane is channel
-// 8 (r / 4) + 4 (lane / 32) + r % 4 of row lane % 32.
-template <typename OutT>
-__device__ __forceinline__ void store_block(const LinearArgs &a, const i32x16 &acc, int64_t row, int channel0) {
-    if (row >= a.n_rows) return;
-    const float s = a.x_scale[row];
-    OutT *out = static_cast<OutT *>(a.out) + row * a.e;
-    const bool aligned = a.e % 4 == 0;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int c = channel0 + 8 * g + 4 * ((threadIdx.x >> 5) & 1);
-        if (c >= a.e) continue;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = min(c + j, a.e - 1);
-            v[j] = float(acc[4 * g + j]) * (s * a.w_scale[e]);
-            if (a.bias) v[j] += a.bias[e];
-        }
-        store_four(out + c, v, a.e - c, aligned);
-    }
-}
-
-// A 128 x 128 tile by four waves, 64 x 64 each, K in steps of 128 bytes
-// through two LDS buffers.
-template <typename OutT>
-__global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
-    constexpr int kTile = 128;
-    __shared__ uint8_t sx[2][kTile * 128], sw[2][kTile * 128];
-    const int64_t tile = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-    const int64_t mt = tile / a.n_tiles;
-    const int64_t m0 = mt * kTile;
-    const int n0 = int(tile - mt * a.n_tiles) * kTile;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    // rows past the last one read the last one; they are not stored
-    u32x4 gx[4], gw[4];
-    const int chunk = threadIdx.x & 7, first = threadIdx.x >> 3;
-    const int8_t *px[4], *pw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        px[i] = a.x + min(m0 + first + 32 * i, a.n_rows - 1) * a.k + chunk * 16;
-        pw[i] = a.w + int64_t(min(n0 + first + 32 * i, a.e - 1)) * a.k + chunk * 16;
-    }
-    auto load = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            gx[i] = *reinterpret_cast<const u32x4 *>(px[i] + k0);
-            gw[i] = *reinterpret_cast<const u32x4 *>(pw[i] + k0);
-        }
-    };
-    auto store = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<u32x4 *>(sx[buf] + lds_at(first + 32 * i, chunk)) = gx[i];
-            *reinterpret_cast<u32x4 *>(sw[buf] + lds_at(first + 32 * i, chunk)) = gw[i];
-        }
-    };
-    i32x16 acc[2][2];  // [rows][channels]
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = i32x16{};
-    load(0);
-    store(0);
-    int buf = 0;
-    for (int k0 = 0; k0 < a.k; k0 += 128, buf ^= 1) {
-        const bool more = k0 + 128 < a.k;
-        if (more) load(k0 + 128);
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            i32x4 fx[2], fw[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fx[i] = *reinterpret_cast<const i32x4 *>(sx[buf] + lds_at(wm + 32 * i + (lane & 31), 2 * s + (lane >> 5)));
-                fw[i] = *reinterpret_cast<const i32x4 *>(sw[buf] + lds_at(wn + 32 * i + (lane & 31), 2 * s + (lane >> 5)));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
-        }
-        if (more) store(buf ^ 1);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) store_block<OutT>(a, acc[i][j], m0 + wm + 32 * i + (lane & 31), n0 + wn + 32 * j);
-}
-
-// A 256 x 256 tile by four waves, 128 x 128 each (256 accumulators a lane),
-// which keeps the LDS bytes per product low enough that the matrix cores set
-// the pace.  K advances 128 bytes a stage; operands go from memory straight
-// into LDS (buffer_load ... lds), x two stages ahead of the products (three
-// buffers), the weight one (two buffers): 160 KB, one workgroup a CU.  The
-// five buffers are arrays of their own, so that the compiler sees that the
-// loads into one never meet the reads of another; the stage loop is unrolled
-// six times, after which both rings are back where they were.  Stages past
-// the end are loaded through an empty resource: zeros, without memory traffic.
-constexpr int kBig = 256;
+// A kTile x kTile tile by four waves, a quarter each: 256 x 256 (256
+// accumulators a lane, one workgroup a CU), whose LDS bytes per product are
+// low enough that the matrix cores set the pace, or 128 x 128 (two workgroups
+// a CU) where larger tiles would leave CUs idle.  K advances 128 bytes a
+// stage; operands go from memory straight into LDS (buffer_load ... lds), x
+// two stages ahead of the products (three buffers), the weight one (two
+// buffers).  The five buffers are arrays of their own, so that the compiler
+// sees that the loads into one never meet the reads of another; the stage
+// loop is unrolled six times, after which both rings are back where they
+// were.  Stages past the end are loaded through an empty resource: zeros,
+// without memory traffic.
 typedef __attribute__((address_space(3))) void *lds_void_ptr;
 constexpr int kWord3 = 0x00020000;            // raw buffer resource word 3
 constexpr int kRecords = 0x7FFFFFF0;          // its size; tile offsets are below 2^25
 // s_waitcnt immediates (gfx9 layout: vmcnt in bits 3:0 and 15:14, expcnt in
 // 6:4, lgkmcnt in 11:8; a field at its maximum does not wait).
 constexpr int kWaitAll = 0;
-constexpr int kWaitVmemButX = 0x0F78;         // vmcnt(8): one stage of x may stay in flight
-constexpr int kWaitLdsVmemButX = 0x0078;      // lgkmcnt(0) and vmcnt(8)
 
-template <typename OutT>
-__global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
-    constexpr int kGroups = kBig / 8 / 4;     // groups of eight rows a wave loads of each operand
+template <typename OutT, int kTile>
+__global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
+    constexpr int kWave = kTile / 2, kBlocks = kWave / 32;  // a wave's quarter, in blocks of 32
+    constexpr int kGroups = kTile / 8 / 4;    // groups of eight rows a wave loads of each operand
     constexpr int kSteps = 4;                 // products of 32 bytes of K in a stage
-    __shared__ uint8_t sx0[kBig * 128], sx1[kBig * 128], sx2[kBig * 128];
-    __shared__ uint8_t sw0[kBig * 128], sw1[kBig * 128];
+    constexpr int kWaitVmemButX = 0x0F70 | kGroups;     // vmcnt: one stage of x may stay in flight
+    constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;  // the same, and lgkmcnt(0)
+    // two loads go out after each row of products, the weight's first: all of
+    // them before the stage's wait, which counts on x's being the newest
+    static_assert(kGroups <= 15 && kGroups <= (kSteps - 1) * kBlocks, "every load is issued before the last step");
+    __shared__ uint8_t sx0[kTile * 128], sx1[kTile * 128], sx2[kTile * 128];
+    __shared__ uint8_t sw0[kTile * 128], sw1[kTile * 128];
     const int64_t tile = xcd_contiguous_tile(blockIdx.x, gridDim.x);
     const int64_t mt = tile / a.n_tiles;
-    const int64_t m0 = mt * kBig;
-    const int n0 = int(tile - mt * a.n_tiles) * kBig;
+    const int64_t m0 = mt * kTile;
+    const int n0 = int(tile - mt * a.n_tiles) * kTile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int stages = a.k / 128;
@@ -314,17 +212,17 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    i32x16 acc[4][4];  // [rows][channels]
+    i32x16 acc[kBlocks][kBlocks];  // [rows][channels]
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
-    i32x4 fx[2][4], fw[2][4];
-    auto read = [&](const uint8_t *tx, const uint8_t *tw, int s, i32x4 (&x)[4], i32x4 (&w)[4]) {
+        for (int j = 0; j < kBlocks; ++j) acc[i][j] = i32x16{};
+    i32x4 fx[2][kBlocks], fw[2][kBlocks];
+    auto read = [&](const uint8_t *tx, const uint8_t *tw, int s, i32x4 (&x)[kBlocks], i32x4 (&w)[kBlocks]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const i32x4 *>(tx + lds_at(wm * 128 + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
+        for (int i = 0; i < kBlocks; ++i) x[i] = *reinterpret_cast<const i32x4 *>(tx + lds_at(wm * kWave + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const i32x4 *>(tw + lds_at(wn * 128 + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
+        for (int i = 0; i < kBlocks; ++i) w[i] = *reinterpret_cast<const i32x4 *>(tw + lds_at(wn * kWave + i * 32 + (lane & 31), 2 * s + (lane >> 5)));
     };
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, 0, sx0);
@@ -352,16 +250,16 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
-                const int slot = ks * 4 + i;
-                if (slot < 4) {
-                    load_w(2 * slot, s + 1, nw);
-                    load_w(2 * slot + 1, s + 1, nw);
-                } else if (slot < 8) {
-                    load_x(2 * slot - 8, s + 2, nx2);
-                    load_x(2 * slot - 7, s + 2, nx2);
+                for (int j = 0; j < kBlocks; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
+                const int slot = ks * kBlocks + i;
+#pragma unroll
+                for (int n = 2 * slot; n < 2 * slot + 2; ++n) {
+                    if (n < kGroups)
+                        load_w(n, s + 1, nw);
+                    else if (n < 2 * kGroups)
+                        load_x(n - kGroups, s + 2, nx2);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -409,13 +307,15 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
     __builtin_amdgcn_s_waitcnt(kWaitAll);
     barrier();
 
-    // Each wave turns its block in 16 KB of LDS, 32 rows at a time (rows of
-    // 512 bytes, 16-byte chunks XOR-swizzled by the row): a lane then holds
-    // whole pieces of rows, whose channels are the same for every row.
-    uint8_t *region = (wave < 2 ? sx0 : sx1) + (wave & 1) * 16384;
-    constexpr int kOut = 16 / int(sizeof(OutT)), kLanes = 128 / kOut, kPass = 64 / kLanes;
+    // Each wave turns its block in LDS, 32 rows at a time (float32, 16-byte
+    // chunks XOR-swizzled by the row): a lane then holds whole pieces of
+    // rows, whose channels are the same for every row.
+    constexpr int kRowBytes = kWave * 4, kChunks = kRowBytes / 16;
+    uint8_t *region = (wave < 2 ? sx0 : sx1) + (wave & 1) * (32 * kRowBytes);
+    static_assert(2 * 32 * kRowBytes <= kTile * 128, "two waves share a buffer");
+    constexpr int kOut = 16 / int(sizeof(OutT)), kLanes = kWave / kOut, kPass = 64 / kLanes;
     const int piece = lane % kLanes;
-    const int col = n0 + wn * 128 + piece * kOut;
+    const int col = n0 + wn * kWave + piece * kOut;
     float t[kOut], b[kOut];
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
@@ -425,17 +325,17 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
     }
     const bool whole = a.e % kOut == 0 && col + kOut <= a.e;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kBlocks; ++i) {
         const int r = lane & 31;
-        const float xs = a.x_scale[min(m0 + wm * 128 + i * 32 + r, a.n_rows - 1)];
+        const float xs = a.x_scale[min(m0 + wm * kWave + i * 32 + r, a.n_rows - 1)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int c = j * 8 + 2 * g + (lane >> 5);
                 const f32x4 v = {float(acc[i][j][4 * g]) * xs, float(acc[i][j][4 * g + 1]) * xs, float(acc[i][j][4 * g + 2]) * xs,
                                  float(acc[i][j][4 * g + 3]) * xs};
-                *reinterpret_cast<f32x4 *>(region + r * 512 + ((c ^ r) % 32) * 16) = v;
+                *reinterpret_cast<f32x4 *>(region + r * kRowBytes + ((c ^ r) % kChunks) * 16) = v;
             }
 #pragma unroll
         for (int p = 0; p < 32 / kPass; ++p) {
@@ -443,11 +343,11 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
             float v[kOut];
 #pragma unroll
             for (int k = 0; k < kOut / 4; ++k) {
-                const f32x4 w = *reinterpret_cast<const f32x4 *>(region + rr * 512 + (((piece * (kOut / 4) + k) ^ rr) % 32) * 16);
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(region + rr * kRowBytes + (((piece * (kOut / 4) + k) ^ rr) % kChunks) * 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[4 * k + j] = fmaf(w[j], t[4 * k + j], b[4 * k + j]);
             }
-            const int64_t row = m0 + wm * 128 + i * 32 + rr;
+            const int64_t row = m0 + wm * kWave + i * 32 + rr;
             if (row >= a.n_rows) continue;
             OutT *out = static_cast<OutT *>(a.out) + row * a.e + col;
             if (whole) {
@@ -469,11 +369,14 @@ __global__ __launch_bounds__(kThreads) void linear_big_kernel(LinearArgs a) {
     }
 }
 
-// Few rows: a workgroup takes 32 rows and 32 channels and its waves share K,
-// operands straight from memory; the waves' sums meet in LDS.
+// Few rows: a workgroup takes 32 rows and 32 channels, its eight waves share
+// K, and each has the operands of eight products (2 KB of K over the
+// workgroup) on the way from memory at once, which is what such a call waits
+// for; the waves' sums meet in LDS.
 template <typename OutT>
-__global__ __launch_bounds__(kThreads) void linear_few_kernel(LinearArgs a) {
-    __shared__ int32_t part[4][16][64];
+__global__ __launch_bounds__(kFewThreads) void linear_few_kernel(LinearArgs a) {
+    constexpr int kWaves = kFewThreads / 64, kDeep = 8;
+    __shared__ int32_t part[kWaves][16][64];
     const int64_t mt = blockIdx.x / a.n_tiles;
     const int64_t m0 = mt * 32;
     const int n0 = int(blockIdx.x - mt * a.n_tiles) * 32;
@@ -481,16 +384,42 @@ __global__ __launch_bounds__(kThreads) void linear_few_kernel(LinearArgs a) {
     const int8_t *x = a.x + min(m0 + (lane & 31), a.n_rows - 1) * a.k + 16 * (lane >> 5);
     const int8_t *w = a.w + int64_t(min(n0 + (lane & 31), a.e - 1)) * a.k + 16 * (lane >> 5);
     i32x16 acc{};
-#pragma unroll 4
-    for (int k0 = 32 * wave; k0 < a.k; k0 += 128)
-        acc = mfma(*reinterpret_cast<const i32x4 *>(w + k0), *reinterpret_cast<const i32x4 *>(x + k0), acc);
+    for (int k0 = 32 * wave; k0 < a.k; k0 += 32 * kWaves * kDeep) {
+        i32x4 fx[kDeep], fw[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int k = k0 + 32 * kWaves * i;
+            if (k < a.k) {
+                fw[i] = *reinterpret_cast<const i32x4 *>(w + k);
+                fx[i] = *reinterpret_cast<const i32x4 *>(x + k);
+            } else {
+                fw[i] = fx[i] = i32x4{};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) acc = mfma(fw[i], fx[i], acc);
+    }
 #pragma unroll
     for (int r = 0; r < 16; ++r) part[wave][r][lane] = acc[r];
     __syncthreads();
-    if (wave > 0) return;
+    // two channels of a row each: value r of lane l is channel 8 (r / 4) +
+    // 4 (l / 32) + r % 4 of row l % 32
+    const int64_t row = m0 + threadIdx.x / 16;
+    if (row >= a.n_rows) return;
+    const float s = a.x_scale[row];
+    OutT *out = static_cast<OutT *>(a.out) + row * a.e;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = (part[0][r][lane] + part[1][r][lane]) + (part[2][r][lane] + part[3][r][lane]);
-    store_block<OutT>(a, acc, m0 + (lane & 31), n0);
+    for (int j = 0; j < 2; ++j) {
+        const int c = 2 * (threadIdx.x % 16) + j, e = n0 + c;
+        if (e >= a.e) return;
+        const int r = 4 * (c / 8) + c % 4, l = int(threadIdx.x / 16) + 32 * ((c >> 2) & 1);
+        int32_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) sum += part[i][r][l];
+        float v = float(sum) * (s * a.w_scale[e]);
+        if (a.bias) v += a.bias[e];
+        out[e] = OutT(v);
+    }
 }
 
 }  // namespace
@@ -574,27 +503,36 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
     a.n_rows = n_rows;
     a.e = embed_dim;
     a.k = k;
-    const int64_t m128 = (n_rows + 127) / 128, n128 = (embed_dim + 127) / 128;
-    const int64_t m256 = (n_rows + 255) / 256, n256 = (embed_dim + 255) / 256;
-    const bool few = m128 * n128 < 128, big = m256 * n256 >= 512;
-    const int64_t tiles = few ? (n_rows + 31) / 32 * ((int64_t(embed_dim) + 31) / 32) : big ? m256 * n256 : m128 * n128;
+    // Which kernel, by size alone (us, 128 x 128 tiles against the other, K
+    // 1280 or 1536 unless said).  Blocks of 32 x 32, while at most one falls
+    // to each CU or one row of them reads the weight once: 4 rows x 1280: 7.8
+    // against 6.5; 128 x 1280: 8.8 against 6.8; 32 x 5120, K 5120: 17.0
+    // against 12.9; past that, 256 x 1280: 8.9 against 9.8.  256 x 256 tiles,
+    // from four rounds of the card's 256 CUs on: 65536 x 1280: 148 against
+    // 144; 65536 x 5120: 620 against 530; 131072 x 1280, K 5120: 947 against
+    // 755; before that, 32768 x 1280: 77 against 83.
+    const int64_t m32 = (n_rows + 31) / 32, n32 = (int64_t(embed_dim) + 31) / 32;
+    const int64_t m128 = (n_rows + 127) / 128, n128 = (int64_t(embed_dim) + 127) / 128;
+    const int64_t m256 = (n_rows + 255) / 256, n256 = (int64_t(embed_dim) + 255) / 256;
+    const bool few = m32 == 1 || m32 * n32 <= 256, big = !few && m256 * n256 >= 1024;
+    const int64_t tiles = few ? m32 * n32 : big ? m256 * n256 : m128 * n128;
+    a.n_tiles = int32_t(few ? n32 : big ? n256 : n128);
     if (tiles > 0x7FFFFFFFll) return set_error(MIMO_E_TOO_LARGE, "quantized_linear: more than 2^31 - 1 tiles");
-    a.n_tiles = few ? (embed_dim + 31) / 32 : int32_t(big ? n256 : n128);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid{unsigned(tiles), 1, 1}, block{unsigned(kThreads), 1, 1};
+    const dim3 grid{unsigned(tiles), 1, 1}, block{unsigned(few ? kFewThreads : kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
         if (few && out_dtype == MIMO_F32)
             hipLaunchKernelGGL(linear_few_kernel<float>, grid, block, 0, s, a);
         else if (few)
             hipLaunchKernelGGL(linear_few_kernel<__bf16>, grid, block, 0, s, a);
         else if (big && out_dtype == MIMO_F32)
-            hipLaunchKernelGGL(linear_big_kernel<float>, grid, block, 0, s, a);
+            hipLaunchKernelGGL((linear_tile_kernel<float, 256>), grid, block, 0, s, a);
         else if (big)
-            hipLaunchKernelGGL(linear_big_kernel<__bf16>, grid, block, 0, s, a);
+            hipLaunchKernelGGL((linear_tile_kernel<__bf16, 256>), grid, block, 0, s, a);
         else if (out_dtype == MIMO_F32)
-            hipLaunchKernelGGL(linear_tile_kernel<float>, grid, block, 0, s, a);
+            hipLaunchKernelGGL((linear_tile_kernel<float, 128>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL(linear_tile_kernel<__bf16>, grid, block, 0, s, a);
+            hipLaunchKernelGGL((linear_tile_kernel<__bf16, 128>), grid, block, 0, s, a);
     });
     if (e != hipSuccess) return hip_error(e, "quantized_linear: kernel launch");
     g_dispatches.fetch_add(1);
