@@ -615,8 +615,7 @@ size_t mimo_layer_norm_workspace_bytes(int64_t rows, int32_t width);
  *   workspace  device, >= mimo_layer_norm_workspace_bytes(rows, width), 16-byte
  *              aligned, or NULL if both sums are; calls that may run at the
  *              same time need one each.
- * One kernel launch, and one for the sums (two for widths above 16384, or
- * above 8192 where rows are not aligned).  Returns MIMO_OK, MIMO_E_INVALID,
+ * One kernel launch, and one for the sums (two for widths above 16384).  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
  */
 int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *dout, int32_t dout_dtype,

@@ -15,8 +15,8 @@
 // formed after it from the row in registers, so that a large mean costs no
 // precision.
 //
-// Both kernels are one pass over memory.  A row is held in registers by one
-// wave (up to 1536 values) or one workgroup (up to 16384); wider rows are
+// Both kernels are one pass over memory, which bounds them.  A row is held in
+// registers by a wave or a workgroup (up to 16384 values); wider rows are
 // read again from cache for each sum.  In the backward kernel a wave keeps
 // its columns from row to row, so the parameter gradients accumulate in
 // registers, over a fixed set of rows; a second kernel adds the workgroups'
@@ -52,55 +52,52 @@ struct NormArgs {
     float eps;
 };
 
-// Chunks of kVec values: chunk i of a thread is i * kThreads + its number.
-template <typename TX, typename TO, int kVec, int kThreads, int kChunks>
+// Chunks of eight values: chunk i of a thread is i * kThreads + its number.
+template <typename TX, typename TO, bool kRagged, int kThreads, int kChunks>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_kernel(NormArgs a) {
     __shared__ float lds[2][4];
     const int tid = threadIdx.x % kThreads;
     const int64_t row = int64_t(blockIdx.x) * (kRowWgThreads / kThreads) + threadIdx.x / kThreads;
     if (row >= a.rows) return;  // whole waves, and only where a wave is a row
     const TX *x = static_cast<const TX *>(a.x) + row * a.width;
-    const int chunks = a.width / kVec;
-    float v[kChunks][kVec];
+    auto column = [&](int i) { return (i * kThreads + tid) * 8; };
+    float v[kChunks][8];
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = i * kThreads + tid;
-        if (c < chunks) {
-            load_values(x + c * kVec, v[i]);
+    for (int i = 0; i < kChunks; ++i)
+        if (column(i) < a.width) {
+            load_values<kRagged>(x + column(i), a.width - column(i), v[i]);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) sum += v[i][j];
+            for (int j = 0; j < 8; ++j) sum += v[i][j];
         }
-    }
     const float mean = row_sum<kThreads>(sum, lds[0]) / float(a.width);
     float squares = 0.0f;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
-        if (i * kThreads + tid < chunks) {
+        if (column(i) < a.width) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                v[i][j] -= mean;
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] = !kRagged || column(i) + j < a.width ? v[i][j] - mean : 0.0f;
                 squares = fmaf(v[i][j], v[i][j], squares);
             }
         }
     const float rstd = 1.0f / sqrtf(row_sum<kThreads>(squares, lds[1]) / float(a.width) + a.eps);
     TO *out = static_cast<TO *>(a.out) + row * a.width;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = i * kThreads + tid;
-        if (c < chunks) {
-            float w[kVec], b[kVec];
-            if (a.weight) load_values(a.weight + c * kVec, w);
-            if (a.bias) load_values(a.bias + c * kVec, b);
+    for (int i = 0; i < kChunks; ++i)
+        if (column(i) < a.width) {
+            const int left = a.width - column(i);
+            float w[8], b[8];
+            if (a.weight) load_values<kRagged>(a.weight + column(i), left, w);
+            if (a.bias) load_values<kRagged>(a.bias + column(i), left, b);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 v[i][j] *= rstd;
                 if (a.weight) v[i][j] *= w[j];
                 if (a.bias) v[i][j] += b[j];
             }
-            store_values(out + c * kVec, v[i]);
+            store_values<kRagged>(out + column(i), left, v[i]);
         }
-    }
     if (tid == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
@@ -136,43 +133,42 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_wide_kernel(NormArgs
 }
 
 // dx of rows first, first + step, ...; partial dw and db of those rows.
-template <typename TX, typename TG, int kVec, int kThreads, int kChunks>
+template <typename TX, typename TG, bool kRagged, int kThreads, int kChunks>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(NormArgs a) {
     constexpr int kRows = kRowWgThreads / kThreads;  // rows of the workgroup at a time
     __shared__ float lds[4][4];
     const int tid = threadIdx.x % kThreads;
-    const int chunks = a.width / kVec;
     const float inv_n = 1.0f / float(a.width);
-    float w[kChunks][kVec], dw[kChunks][kVec], db[kChunks][kVec];
+    auto column = [&](int i) { return (i * kThreads + tid) * 8; };
+    float w[kChunks][8], dw[kChunks][8], db[kChunks][8];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < 8; ++j) {
             dw[i][j] = db[i][j] = 0.0f;
             w[i][j] = 1.0f;
         }
-        if (a.weight && i * kThreads + tid < chunks) load_values(a.weight + (i * kThreads + tid) * kVec, w[i]);
+        if (a.weight && column(i) < a.width) load_values<kRagged>(a.weight + column(i), a.width - column(i), w[i]);
     }
     int turn = 0;
     for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kThreads; row < a.rows; row += int64_t(gridDim.x) * kRows, turn ^= 1) {
         const TX *x = static_cast<const TX *>(a.x) + row * a.width;
         const TG *dout = static_cast<const TG *>(a.dout) + row * a.width;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float h[kChunks][kVec], g[kChunks][kVec];
+        float h[kChunks][8], g[kChunks][8];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = i * kThreads + tid;
-            if (c < chunks) {
-                load_values(x + c * kVec, h[i]);
-                load_values(dout + c * kVec, g[i]);
+        for (int i = 0; i < kChunks; ++i)
+            if (column(i) < a.width) {
+                load_values<kRagged>(x + column(i), a.width - column(i), h[i]);
+                load_values<kRagged>(dout + column(i), a.width - column(i), g[i]);
             }
-        }
+        // past a ragged row's end dout is zero, and with it every sum
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
-            if (i * kThreads + tid < chunks) {
+            if (column(i) < a.width) {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     h[i][j] = (h[i][j] - mean) * rstd;
                     dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
                     db[i][j] += g[i][j];
@@ -187,29 +183,25 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(Norm
         s2 = row_sum<kThreads>(s2, lds[2 * turn + 1]) * inv_n;
         TX *dx = static_cast<TX *>(a.out) + row * a.width;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = i * kThreads + tid;
-            if (c < chunks) {
+        for (int i = 0; i < kChunks; ++i)
+            if (column(i) < a.width) {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] = rstd * (g[i][j] - fmaf(h[i][j], s2, s1));
-                store_values(dx + c * kVec, h[i]);
+                for (int j = 0; j < 8; ++j) h[i][j] = rstd * (g[i][j] - fmaf(h[i][j], s2, s1));
+                store_values<kRagged>(dx + column(i), a.width - column(i), h[i]);
             }
-        }
     }
     if (!a.part) return;
     float *part = a.part + int64_t(blockIdx.x) * 2 * a.width;
     if constexpr (kRows == 1) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = i * kThreads + tid;
-            if (c < chunks) {
-                store_values(part + c * kVec, dw[i]);
-                store_values(part + a.width + c * kVec, db[i]);
+        for (int i = 0; i < kChunks; ++i)
+            if (column(i) < a.width) {
+                store_values<kRagged>(part + column(i), a.width - column(i), dw[i]);
+                store_values<kRagged>(part + a.width + column(i), a.width - column(i), db[i]);
             }
-        }
     } else {
         // the waves hold the same columns: added up in LDS, chunk by chunk
-        __shared__ float sum[kRows][kThreads * kVec];
+        __shared__ float sum[kRows][kThreads * 8];
         const int wave = threadIdx.x / kThreads;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
@@ -217,11 +209,11 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(Norm
             for (int k = 0; k < 2; ++k) {
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) sum[wave][j * kThreads + tid] = k ? db[i][j] : dw[i][j];
+                for (int j = 0; j < 8; ++j) sum[wave][j * kThreads + tid] = k ? db[i][j] : dw[i][j];
                 __syncthreads();
-                for (int e = threadIdx.x; e < kThreads * kVec; e += kRowWgThreads) {
-                    const int col = (i * kThreads + e % kThreads) * kVec + e / kThreads;
-                    if (i * kThreads + e % kThreads < chunks) part[k * a.width + col] = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
+                for (int e = threadIdx.x; e < kThreads * 8; e += kRowWgThreads) {
+                    const int col = (i * kThreads + e % kThreads) * 8 + e / kThreads;
+                    if (col < a.width) part[k * a.width + col] = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
                 }
             }
     }
@@ -294,28 +286,41 @@ __global__ __launch_bounds__(kSumColumns *kSumParts) void layer_norm_sum_kernel(
     }
 }
 
-// How a width is laid over threads: values a chunk, threads a row, chunks a
-// thread; threads = 0: the row is read again for each sum.
+// How a width is laid over threads: whether rows are ragged, threads a row,
+// chunks a thread; threads = 0: the row is read again for each sum.  As few
+// chunks as hold the row, for the registers they take.
 struct Shape {
-    int vec, threads, chunks;
+    bool ragged;
+    int threads, chunks;
 };
-Shape choose_shape(int32_t width, bool aligned) {
-    if (aligned && width % 8 == 0) {
-        if (width <= 64 * 8) return {8, 64, 1};
-        if (width <= 64 * 8 * 3) return {8, 64, 3};
-        if (width <= 256 * 8 * 2) return {8, 256, 2};
-        if (width <= 256 * 8 * 8) return {8, 256, 8};
-    } else {
-        if (width <= 64 * 4) return {1, 64, 4};
-        if (width <= 256 * 8) return {1, 256, 8};
-        if (width <= 256 * 32) return {1, 256, 32};
-    }
-    return {1, 0, 0};
+// Forward: a wave holds a row as long as that is three chunks, since it then
+// needs no barrier (131072 x 1280 bf16: 149 us, 4.5 TB/s, against 226 with
+// the workgroup).
+Shape forward_shape(int32_t width, bool aligned) {
+    const bool ragged = !aligned || width % 8;
+    if (width <= 64 * 8) return {ragged, 64, 1};
+    if (width <= 64 * 8 * 3) return {ragged, 64, 3};
+    if (width <= 256 * 8 * 3) return {ragged, 256, 3};
+    if (width <= 256 * 8 * 8) return {ragged, 256, 8};
+    return {ragged, 0, 0};
+}
+// Backward: a thread's columns cost five registers a value, so the workgroup
+// holds a row from one chunk of a wave on (131072 x 1280 bf16: 222 us against
+// 273; 4099 x 1283 float32: 21 against 26).
+Shape backward_shape(int32_t width, bool aligned) {
+    const bool ragged = !aligned || width % 8;
+    if (width <= 64 * 8) return {ragged, 64, 1};
+    if (width <= 256 * 8) return {ragged, 256, 1};
+    if (width <= 256 * 8 * 3) return {ragged, 256, 3};
+    if (width <= 256 * 8 * 8) return {ragged, 256, 8};
+    return {ragged, 0, 0};
 }
 
-// Workgroups of the backward kernel: each then adds up so many rows.
+// Workgroups of the backward kernel, each of which adds up every so many
+// rows: more of them hide memory better, but each writes partial sums
+// (131072 x 1280 bf16, sums included: 512 workgroups 365 us, 1024 222, 2048 249).
 int32_t backward_groups(int64_t rows, int32_t width) {
-    const int64_t per = width <= 64 * 8 * 3 ? 4 : 1;
+    const int64_t per = width <= 64 * 8 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
     return int32_t(groups < kMaxGroups ? groups : kMaxGroups);
 }
@@ -326,18 +331,19 @@ template <typename TX, typename TO>
 void launch_forward(const Shape &s, const NormArgs &a, hipStream_t stream) {
     const dim3 block{unsigned(kRowWgThreads), 1, 1};
     const dim3 grid{unsigned(s.threads == 64 ? (a.rows + 3) / 4 : a.rows), 1, 1};
-#define MIMO_NORM(V, T, C)                                                                      \
-    if (s.vec == V && s.threads == T && s.chunks == C) {                                        \
-        hipLaunchKernelGGL((layer_norm_kernel<TX, TO, V, T, C>), grid, block, 0, stream, a);    \
+#define MIMO_NORM(R, T, C)  \
+    if (s.ragged == R && s.threads == T && s.chunks == C) {  \
+        hipLaunchKernelGGL((layer_norm_kernel<TX, TO, R, T, C>), grid, block, 0, stream, a);    \
         return;                                                                                 \
     }
-    MIMO_NORM(8, 64, 1)
-    MIMO_NORM(8, 64, 3)
-    MIMO_NORM(8, 256, 2)
-    MIMO_NORM(8, 256, 8)
-    MIMO_NORM(1, 64, 4)
-    MIMO_NORM(1, 256, 8)
-    MIMO_NORM(1, 256, 32)
+    MIMO_NORM(false, 64, 1)
+    MIMO_NORM(false, 64, 3)
+    MIMO_NORM(false, 256, 3)
+    MIMO_NORM(false, 256, 8)
+    MIMO_NORM(true, 64, 1)
+    MIMO_NORM(true, 64, 3)
+    MIMO_NORM(true, 256, 3)
+    MIMO_NORM(true, 256, 8)
 #undef MIMO_NORM
     hipLaunchKernelGGL((layer_norm_wide_kernel<TX, TO>), grid, block, 0, stream, a);
 }
@@ -345,18 +351,19 @@ void launch_forward(const Shape &s, const NormArgs &a, hipStream_t stream) {
 template <typename TX, typename TG>
 void launch_backward(const Shape &s, const NormArgs &a, int32_t groups, hipStream_t stream) {
     const dim3 block{unsigned(kRowWgThreads), 1, 1}, grid{unsigned(groups), 1, 1};
-#define MIMO_NORM(V, T, C)                                                                               \
-    if (s.vec == V && s.threads == T && s.chunks == C) {                                                 \
-        hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TG, V, T, C>), grid, block, 0, stream, a);    \
+#define MIMO_NORM(R, T, C)  \
+    if (s.ragged == R && s.threads == T && s.chunks == C) {  \
+        hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TG, R, T, C>), grid, block, 0, stream, a);    \
         return;                                                                                          \
     }
-    MIMO_NORM(8, 64, 1)
-    MIMO_NORM(8, 64, 3)
-    MIMO_NORM(8, 256, 2)
-    MIMO_NORM(8, 256, 8)
-    MIMO_NORM(1, 64, 4)
-    MIMO_NORM(1, 256, 8)
-    MIMO_NORM(1, 256, 32)
+    MIMO_NORM(false, 64, 1)
+    MIMO_NORM(false, 256, 1)
+    MIMO_NORM(false, 256, 3)
+    MIMO_NORM(false, 256, 8)
+    MIMO_NORM(true, 64, 1)
+    MIMO_NORM(true, 256, 1)
+    MIMO_NORM(true, 256, 3)
+    MIMO_NORM(true, 256, 8)
 #undef MIMO_NORM
     hipLaunchKernelGGL((layer_norm_backward_wide_kernel<TX, TG>), dim3(unsigned(a.rows), 1, 1), block, 0, stream, a);
     if (a.part)
@@ -405,7 +412,7 @@ int mimo_layer_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype,
     a.width = width;
     a.eps = eps;
     const bool aligned = check_ptr_align(x, 16) && check_ptr_align(out, 16) && check_ptr_align(weight, 16) && check_ptr_align(bias, 16);
-    const Shape shape = choose_shape(width, aligned);
+    const Shape shape = forward_shape(width, aligned);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = timed_launch(s, [&] {
         if (x_dtype == MIMO_F32 && out_dtype == MIMO_F32)
@@ -464,7 +471,7 @@ int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t
     a.width = width;
     const int32_t groups = backward_groups(rows, width);
     const bool aligned = check_ptr_align(x, 16) && check_ptr_align(dout, 16) && check_ptr_align(weight, 16) && check_ptr_align(dx, 16);
-    const Shape shape = choose_shape(width, aligned);
+    const Shape shape = backward_shape(width, aligned);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = timed_launch(s, [&] {
         if (rows > 0) {

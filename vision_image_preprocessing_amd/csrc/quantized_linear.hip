@@ -65,8 +65,8 @@ __device__ __forceinline__ int quantize(float v, float scale) {
 }
 
 // One row by a wave (kThreadsRow = 64) or the workgroup, held in registers
-// (kChunks chunks of kVec values a thread), or read twice (kChunks = 0).
-template <typename T, int kVec, int kThreadsRow, int kChunks>
+// (kChunks chunks of eight values a thread), or read twice (kChunks = 0).
+template <typename T, bool kRagged, int kThreadsRow, int kChunks>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a) {
     __shared__ uint32_t lds[4];
     const int tid = threadIdx.x % kThreadsRow;
@@ -74,38 +74,29 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a)
     if (row >= a.rows) return;
     const T *x = static_cast<const T *>(a.x) + row * a.width;
     int8_t *q = a.q + row * a.padded;
-    const int chunks = a.width / kVec, all = a.padded / kVec;
-    constexpr int kHeld = kChunks ? kChunks : 1;
-    float v[kHeld][kVec];
+    const int count = (a.padded / 8 + kThreadsRow - 1) / kThreadsRow;
+    float v[kChunks ? kChunks : 1][8];
     uint32_t top = 0;
-    auto write = [&](int c, const float (&w)[kVec], float scale, bool zero) {
-        if constexpr (kVec == 8) {
-            u32x2 p = {0, 0};
-            if (!zero) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t(quantize(w[j], scale)) & 0xFFu) << (8 * (j % 4));
-            }
-            *reinterpret_cast<u32x2 *>(q + c * 8) = p;
+    auto column = [&](int i) { return (i * kThreadsRow + tid) * 8; };
+    // past the row's end a chunk reads zeros, which is what padding holds
+    auto load = [&](int i, float (&w)[8]) {
+        if (column(i) < a.width) {
+            load_values<kRagged>(x + column(i), a.width - column(i), w);
         } else {
-            q[c] = zero ? int8_t(0) : int8_t(quantize(w[0], scale));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 0.0f;
         }
+    };
+    auto look = [&](int i, float (&w)[8]) {
+        load(i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, magnitude(w[j]));
     };
     if constexpr (kChunks > 0) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = i * kThreadsRow + tid;
-            if (c < chunks) {
-                load_values(x + c * kVec, v[i]);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) top = max(top, magnitude(v[i][j]));
-            }
-        }
+        for (int i = 0; i < kChunks; ++i) look(i, v[i]);
     } else {
-        for (int c = tid; c < chunks; c += kThreadsRow) {
-            load_values(x + c * kVec, v[0]);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) top = max(top, magnitude(v[0][j]));
-        }
+        for (int i = 0; i < count; ++i) look(i, v[0]);
     }
     top = row_max<kThreadsRow>(top, lds);
     // a row that is not finite has the scale NaN and zeros, which make its
@@ -113,18 +104,21 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a)
     const bool finite = top < 0x7F800000u;
     const float scale = finite ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
     const bool none = !finite || scale == 0.0f;
+    auto write = [&](int i, const float (&w)[8]) {
+        u32x2 p = {0, 0};
+        if (!none) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t(quantize(w[j], scale)) & 0xFFu) << (8 * (j % 4));
+        }
+        if (column(i) < a.padded) *reinterpret_cast<u32x2 *>(q + column(i)) = p;
+    };
     if constexpr (kChunks > 0) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = i * kThreadsRow + tid;
-            if (c < all) write(c, v[i], scale, none || c >= chunks);
-        }
-        // the padding behind what the threads hold
-        for (int c = kChunks * kThreadsRow + tid; c < all; c += kThreadsRow) write(c, v[0], scale, true);
+        for (int i = 0; i < kChunks; ++i) write(i, v[i]);
     } else {
-        for (int c = tid; c < all; c += kThreadsRow) {
-            if (c < chunks) load_values(x + c * kVec, v[0]);
-            write(c, v[0], scale, none || c >= chunks);
+        for (int i = 0; i < count; ++i) {
+            load(i, v[0]);
+            write(i, v[0]);
         }
     }
     if (tid == 0) a.scale[row] = scale;
@@ -447,32 +441,33 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
     a.rows = rows;
     a.width = width;
     a.padded = (width + kPadK - 1) / kPadK * kPadK;
-    const bool vec = width % 8 == 0 && check_ptr_align(x, 16);
+    const bool ragged = width % 8 || !check_ptr_align(x, 16);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 block{unsigned(kThreads), 1, 1};
-    auto launch = [&](auto type) {
+    // the padding is written by the threads that hold the row, so the widths
+    // are those that the padded row fits
+    auto launch = [&](auto type, auto ragged) {
         typedef decltype(type) T;
+        constexpr bool R = decltype(ragged)::value;
         const dim3 waves{unsigned((rows + 3) / 4), 1, 1}, groups{unsigned(rows), 1, 1};
-        if (vec && width <= 64 * 8)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 64, 1>), waves, block, 0, s, a);
-        else if (vec && width <= 64 * 8 * 3)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 64, 3>), waves, block, 0, s, a);
-        else if (vec && width <= 256 * 8 * 3)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 256, 3>), groups, block, 0, s, a);
-        else if (vec)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 8, 256, 0>), groups, block, 0, s, a);
-        else if (width <= 64 * 4)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 64, 4>), waves, block, 0, s, a);
-        else if (width <= 256 * 8)
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 256, 8>), groups, block, 0, s, a);
+        if (a.padded <= 64 * 8)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, R, 64, 1>), waves, block, 0, s, a);
+        else if (a.padded <= 64 * 8 * 3)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, R, 64, 3>), waves, block, 0, s, a);
+        else if (a.padded <= 256 * 8 * 3)
+            hipLaunchKernelGGL((quantize_rows_kernel<T, R, 256, 3>), groups, block, 0, s, a);
         else
-            hipLaunchKernelGGL((quantize_rows_kernel<T, 1, 256, 0>), groups, block, 0, s, a);
+            hipLaunchKernelGGL((quantize_rows_kernel<T, R, 256, 0>), groups, block, 0, s, a);
     };
     const hipError_t e = timed_launch(s, [&] {
-        if (x_dtype == MIMO_F32)
-            launch(float());
+        if (x_dtype == MIMO_F32 && ragged)
+            launch(float(), std::true_type());
+        else if (x_dtype == MIMO_F32)
+            launch(float(), std::false_type());
+        else if (ragged)
+            launch(__bf16(), std::true_type());
         else
-            launch(__bf16());
+            launch(__bf16(), std::false_type());
     });
     if (e != hipSuccess) return hip_error(e, "quantize_rows: kernel launch");
     g_dispatches.fetch_add(1);

@@ -13,55 +13,87 @@ namespace rows {
 
 constexpr int kRowWgThreads = 256;
 
-// kVec values of a row as float32: kVec = 8 reads 16 or 32 aligned bytes,
-// kVec = 1 one value (widths or addresses that are not aligned).
-template <int kVec>
-__device__ __forceinline__ void load_values(const float *p, float (&v)[kVec]) {
-    if constexpr (kVec == 8) {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+// Eight values of a row as float32, from one or two 16-byte accesses.
+// kRagged: rows of any width at any address of the type (the accesses are
+// then aligned to the values only, which the hardware takes), with n of the
+// eight inside the row; values past it read as zeros and are not written.
+template <bool kRagged>
+__device__ __forceinline__ void load_values(const float *p, int n, float (&v)[8]) {
+    typedef f32x4 any_f32x4 __attribute__((aligned(4)));
+    if (!kRagged || n >= 8) {
+        f32x4 a, b;
+        if constexpr (kRagged) {
+            a = *reinterpret_cast<const any_f32x4 *>(p);
+            b = *reinterpret_cast<const any_f32x4 *>(p + 4);
+        } else {
+            a = *reinterpret_cast<const f32x4 *>(p);
+            b = *reinterpret_cast<const f32x4 *>(p + 4);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[j] = a[j];
             v[4 + j] = b[j];
         }
     } else {
-        v[0] = *p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.0f;
     }
 }
-template <int kVec>
-__device__ __forceinline__ void load_values(const __bf16 *p, float (&v)[kVec]) {
-    if constexpr (kVec == 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+template <bool kRagged>
+__device__ __forceinline__ void load_values(const __bf16 *p, int n, float (&v)[8]) {
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    if (!kRagged || n >= 8) {
+        u32x4 w;
+        if constexpr (kRagged)
+            w = *reinterpret_cast<const any_u32x4 *>(p);
+        else
+            w = *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
             v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
         }
     } else {
-        v[0] = float(*p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? float(p[j]) : 0.0f;
     }
 }
 
 // The same values out, rounded once (to nearest even) where the type is bf16.
-template <int kVec>
-__device__ __forceinline__ void store_values(float *p, const float (&v)[kVec]) {
-    if constexpr (kVec == 8) {
-        *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+template <bool kRagged>
+__device__ __forceinline__ void store_values(float *p, int n, const float (&v)[8]) {
+    typedef f32x4 any_f32x4 __attribute__((aligned(4)));
+    if (!kRagged || n >= 8) {
+        const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if constexpr (kRagged) {
+            *reinterpret_cast<any_f32x4 *>(p) = a;
+            *reinterpret_cast<any_f32x4 *>(p + 4) = b;
+        } else {
+            *reinterpret_cast<f32x4 *>(p) = a;
+            *reinterpret_cast<f32x4 *>(p + 4) = b;
+        }
     } else {
-        *p = v[0];
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = v[j];
     }
 }
-template <int kVec>
-__device__ __forceinline__ void store_values(__bf16 *p, const float (&v)[kVec]) {
-    if constexpr (kVec == 8) {
-        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-        bf16x8 h;
+template <bool kRagged>
+__device__ __forceinline__ void store_values(__bf16 *p, int n, const float (&v)[8]) {
+    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+    typedef bf16x8 any_bf16x8 __attribute__((aligned(2)));
+    bf16x8 h;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
-        *reinterpret_cast<bf16x8 *>(p) = h;
+    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
+    if (!kRagged || n >= 8) {
+        if constexpr (kRagged)
+            *reinterpret_cast<any_bf16x8 *>(p) = h;
+        else
+            *reinterpret_cast<bf16x8 *>(p) = h;
     } else {
-        *p = __bf16(v[0]);
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = h[j];
     }
 }
 
