@@ -30,6 +30,7 @@
 // operands, as q, k, v and do come in; outputs are rounded once.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <string>
@@ -45,12 +46,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_ptr;
+typedef __attribute__((address_space(3))) void *lds_void_ptr;
 
 constexpr int kThreads = 256;
 constexpr int kWaveRows = 32;                 // rows (or keys) one wave owns
 constexpr int kTileRows = 4 * kWaveRows;      // of one workgroup
 constexpr int kStep = 64;                     // keys (or rows) staged in LDS at a time
-constexpr int kPanel = 64;                    // head columns of one LDS panel: rows of 128 bytes
+constexpr int kPanelBytes = kStep * 128;      // kStep rows of 64 head columns
 constexpr int kWord3 = 0x00020000;            // raw buffer resource word 3
 constexpr uint32_t kOutside = 0x7FFFFFF8u;    // a byte offset past every resource: reads zeros
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -71,34 +73,38 @@ struct AttentionArgs {
     const int32_t *cu;   // [chunks + 1]
     const float *sink;   // [q_heads] or null
     float *lse;          // [q_heads][rows], or null (forward)
-    float *delta;        // [q_heads][rows] (backward)
+    float *neg_lse;      // [q_heads][rows]: -lse / scale (backward)
+    float *neg_delta;    // [q_heads][rows]: -delta (backward)
     float *dsink_part;   // [q_heads][tiles], or null
+    float *part;         // [slices][2][kv_heads][rows][head_dim]: dk, dv of each slice, or null
     int64_t rows;
     int32_t q_heads, kv_heads, head_dim, chunks;
     int32_t window;      // < 0: none
-    int32_t tiles;       // rows / kTileRows + chunks
+    int32_t tiles;       // of the launch: rows / its tile rows + chunks
+    int32_t slices;      // parts that dk's and dv's sums are split into
     float scale;
 };
 
-// A workgroup's tile: rows [first, first + kTileRows) of the chunk of len
-// rows that starts at row begin; len = 0 for a tile that holds nothing.
+// A workgroup's tile: its first row within the chunk of len rows that starts
+// at row begin; len = 0 for a tile that holds nothing.
 struct Tile {
     int64_t begin;
     int32_t len, first;
 };
 
-// Tile t of the batch: chunk c's tiles are numbered from cu[c] / kTileRows + c,
-// which leaves each chunk as many numbers as it needs or one more, so that
-// the grid is known from the row and chunk counts alone.  A boundary outside
-// [0, rows] or a descending pair gives an empty tile: nothing is read or
-// written through it.
+// Tile t of the batch, kRows rows each: chunk c's tiles are numbered from
+// cu[c] / kRows + c, which leaves each chunk as many numbers as it needs or
+// one more, so that the grid is known from the row and chunk counts alone.
+// A boundary outside [0, rows] or a descending pair gives an empty tile:
+// nothing is read or written through it.
+template <int kRows>
 __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t rows, int64_t t) {
     const int lane = threadIdx.x & 63;
     int lo = 0, hi = chunks;
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) >> 6;
         const int idx = lo + lane * step;
-        const bool le = idx < hi && int64_t(cu[idx]) / kTileRows + idx <= t;
+        const bool le = idx < hi && int64_t(cu[idx]) / kRows + idx <= t;
         const int k = max(__popcll(__ballot(le)) - 1, 0);
         lo += k * step;
         hi = min(lo + step, hi);
@@ -106,7 +112,7 @@ __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int64_t b = cu[lo], e = cu[lo + 1];
     Tile r{0, 0, 0};
-    const int64_t first = (t - (b / kTileRows + lo)) * kTileRows;
+    const int64_t first = (t - (b / kRows + lo)) * kRows;
     if (b < 0 || e > rows || first < 0 || first >= e - b) return r;
     r.begin = b;
     r.len = __builtin_amdgcn_readfirstlane(int(e - b));
@@ -114,10 +120,44 @@ __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t
     return r;
 }
 
-// LDS position (in values) of 16-byte chunk v of panel row r: chunks are
-// XOR-swizzled by the row, so that the same chunk of eight rows (operand
-// reads) and half rows of eight rows (transposed reads) cover every bank.
-__device__ __forceinline__ int lds_at(int r, int v) { return r * kPanel + ((v ^ ((r ^ (r >> 3)) & 7)) << 3); }
+// Staged tiles.  Panel rows are 128 bytes, eight 16-byte chunks; chunk v of
+// row r lies at position v ^ (r ^ r / 8) % 8, so that the same chunk of eight
+// rows (operand reads) and half rows of eight rows (transposed reads) cover
+// every bank.  The swizzle is an exclusive or, so a lane needs few distinct
+// addresses, formed once; everything else is a constant offset.
+struct LdsAddress {
+    int row[4];  // operand reads: chunk 2 s + l / 32 of row l % 32, by s ^ 2 (block)
+    int col[8];  // transposed reads, by chunk ^ row / 8
+};
+__device__ __forceinline__ LdsAddress lds_address() {
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+    LdsAddress a;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a.row[j] = l * 128 + (((h ^ ((l ^ (l >> 3)) & 7)) ^ (2 * j)) << 4);
+    const int x = 4 * h + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a.col[j] = x * 128 + ((c ^ x ^ j) << 4) + (lane & 1) * 8;
+    return a;
+}
+
+// First operand, rows of 32-row block b, 16-wide column step s.
+__device__ __forceinline__ bf16x8 read_rows(const uint8_t *lds, const LdsAddress &a, int b, int s) {
+    return *reinterpret_cast<const bf16x8 *>(lds + a.row[(s & 3) ^ (2 * b)] + (s / 4) * kPanelBytes + b * 32 * 128);
+}
+
+// First operand, transposed: 32-column block d as its rows, over the 16
+// staged rows from 16 s in the order the header gives.
+__device__ __forceinline__ bf16x8 read_columns(const uint8_t *lds, const LdsAddress &a, int d, int s) {
+    const int c = (4 * (d & 1)) ^ (2 * s);
+    const uint8_t *p = lds + (d / 2) * kPanelBytes + s * 16 * 128;
+    union {
+        s16x4 h[2];
+        bf16x8 f;
+    } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + a.col[c]));
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + a.col[c ^ 1] + 8 * 128));
+    return u.f;
+}
 
 // A resource over one head's rows from `row` on, `left` of them: reads past
 // them (rows behind the chunk, columns behind head_dim) give zeros.
@@ -131,6 +171,51 @@ __device__ __forceinline__ uint32_t head_offset(const Heads &t, int r, int col, 
     return col < head_dim ? uint32_t(r * int(t.row) + col) * 2 : kOutside;
 }
 
+// 16 bytes a lane straight into LDS, one after the other.  The host's pass
+// over this file does not know the size (and would drop every kernel that
+// contains it), so it does not see the call.
+__device__ __forceinline__ void load_to_lds(const __amdgpu_buffer_rsrc_t &rsrc, uint8_t *lds, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_ptr)lds, 16, off, 0, 0, 0);
+#endif
+}
+
+// kStep rows of one head straight into LDS, 1 KB (eight rows of a panel) a
+// load: by the workgroup's four waves, or by each wave for itself.
+template <int kPanels, int kWaves>
+struct Loader {
+    static constexpr int kN = kPanels * 8 / kWaves;
+    uint32_t off[kN];
+    __device__ __forceinline__ Loader(const Heads &t, int wave, int head_dim) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int n = kWaves == 1 ? i : i * kWaves + wave, g = n % 8;
+            const int v = (lane & 7) ^ ((lane >> 3) ^ g);
+            off[i] = head_offset(t, g * 8 + (lane >> 3), (n / 8) * 64 + v * 8, head_dim);
+        }
+    }
+    __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t &rsrc, int wave, uint8_t *lds) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int n = kWaves == 1 ? i : i * kWaves + wave;
+            load_to_lds(rsrc, lds + n * 1024, off[i]);
+        }
+    }
+};
+
+// Every load into LDS that this wave made has landed; with kWaves = 4 those
+// of the others too, and every wave has read what it wanted of the tiles
+// before.  (__syncthreads would do, with a fence that the loads issued next
+// need not wait for.)
+template <int kWaves>
+__device__ __forceinline__ void tiles_ready() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0);
+    if constexpr (kWaves > 1) __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // The operand rows of a wave straight from memory: lane l holds row l % 32,
 // columns 16 s + 8 (l / 32) .. + 7 of step s.
 template <int kD>
@@ -141,53 +226,6 @@ __device__ __forceinline__ void load_operand(const Heads &t, int64_t row, int he
     for (int s = 0; s < kD / 16; ++s)
         f[s] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
                                               rsrc, head_offset(t, lane & 31, 16 * s + 8 * (lane >> 5), head_dim), 0, 0));
-}
-
-// kStep rows of one head between memory and LDS, through registers: panels
-// of 64 columns, rows of eight 16-byte chunks, two chunks a thread and panel.
-template <int kD>
-struct Staged {
-    static constexpr int kN = kStep * kD / 8 / kThreads;
-    u32x4 v[kN];
-    __device__ __forceinline__ void load(const Heads &t, int64_t row, int head, int left, int head_dim) {
-        const __amdgpu_buffer_rsrc_t rsrc = head_rsrc(t, row, head, left, head_dim);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int id = (i % 2) * kThreads + threadIdx.x;
-            v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 rsrc, head_offset(t, id >> 3, (i / 2) * kPanel + (id & 7) * 8, head_dim), 0, 0));
-        }
-    }
-    __device__ __forceinline__ void store(uint16_t *lds) const {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int id = (i % 2) * kThreads + threadIdx.x;
-            *reinterpret_cast<u32x4 *>(lds + (i / 2) * kStep * kPanel + lds_at(id >> 3, id & 7)) = v[i];
-        }
-    }
-};
-
-// First operand, rows of 32-row block b, 16-wide column step s.
-__device__ __forceinline__ bf16x8 read_rows(const uint16_t *lds, int b, int s) {
-    const int lane = threadIdx.x & 63;
-    return *reinterpret_cast<const bf16x8 *>(lds + (s / 4) * kStep * kPanel +
-                                             lds_at(b * 32 + (lane & 31), 2 * (s % 4) + (lane >> 5)));
-}
-
-// First operand, transposed: 32-column block d as its rows, over the 16
-// staged rows from 16 s in the order the header gives.
-__device__ __forceinline__ bf16x8 read_columns(const uint16_t *lds, int d, int s) {
-    const int lane = threadIdx.x & 63;
-    const int col = (d % 2) * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-    const int row = 16 * s + 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const uint16_t *p = lds + (d / 2) * kStep * kPanel;
-    union {
-        s16x4 h[2];
-        bf16x8 f;
-    } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + lds_at(row, col >> 3) + (col & 7)));
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + lds_at(row + 8, col >> 3) + (col & 7)));
-    return u.f;
 }
 
 // Values 8 s .. 8 s + 7 as a bf16 operand.
@@ -212,31 +250,65 @@ __device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A wave's [32 columns d][32 rows] blocks, times mul, to rows of a head: the
-// halves exchange groups of four so that each lane stores eight columns.
-template <int kD>
-__device__ __forceinline__ void store_rows(const Heads &t, int64_t row, int head, int left, int head_dim, const f32x16 (&o)[kD / 32],
-                                           float mul) {
+// Values 8 g .. 8 g + 7 of a [32 columns][32 rows] block d, times mul, to
+// rows of a head: the halves exchange groups of four so that each lane
+// stores eight columns.
+__device__ __forceinline__ void store_columns(const Heads &t, int64_t row, int head, int left, int head_dim, int d, int g,
+                                              const float (&v)[8], float mul) {
     const int lane = threadIdx.x & 63;
     uint16_t *p = t.p + (row + (lane & 31)) * t.row + head * t.head;
+    union {
+        __bf16 h[8];
+        uint32_t w[4];
+    } a;
 #pragma unroll
-    for (int d = 0; d < kD / 32; ++d)
+    for (int e = 0; e < 8; ++e) a.h[e] = __bf16(v[e] * mul);
+    // words 0, 1: columns 8 (2 g) + 4 (lane / 32) on; words 2, 3: eight
+    // further; the low half takes both parts of the first, the high half of
+    // the second
+    const auto x = __builtin_amdgcn_permlane32_swap(a.w[0], a.w[2], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a.w[1], a.w[3], false, false);
+    const u32x4 w = {x[0], y[0], x[1], y[1]};
+    const int col = d * 32 + 16 * g + 8 * (lane >> 5);
+    if ((lane & 31) < left && col < head_dim) *reinterpret_cast<u32x4 *>(p + col) = w;
+}
+
+template <int kBlocks>
+__device__ __forceinline__ void store_rows(const Heads &t, int64_t row, int head, int left, int head_dim, const f32x16 (&o)[kBlocks],
+                                           float mul) {
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            union {
-                __bf16 h[8];
-                uint32_t w[4];
-            } a;
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a.h[e] = __bf16(o[d][8 * g + e] * mul);
-            // words 0, 1: group 2 g; words 2, 3: group 2 g + 1; the low half
-            // takes both parts of the first, the high half of the second
-            const auto x = __builtin_amdgcn_permlane32_swap(a.w[0], a.w[2], false, false);
-            const auto y = __builtin_amdgcn_permlane32_swap(a.w[1], a.w[3], false, false);
-            const u32x4 v = {x[0], y[0], x[1], y[1]};
-            const int col = d * 32 + 16 * g + 8 * (lane >> 5);
-            if ((lane & 31) < left && col < head_dim) *reinterpret_cast<u32x4 *>(p + col) = v;
+            for (int e = 0; e < 8; ++e) v[e] = o[d][8 * g + e];
+            store_columns(t, row, head, left, head_dim, d, g, v, mul);
         }
+}
+
+// Four waves' blocks of the same rows, each times its own factor, added up
+// and stored: through LDS (4 x 4 KB a block), each wave taking some columns.
+template <int kBlocks>
+__device__ __forceinline__ void store_rows_of_four(float *lds, const Heads &t, int64_t row, int head, int left, int head_dim,
+                                                   const f32x16 (&o)[kBlocks], float factor, float mul, int wave) {
+    const int lane = threadIdx.x & 63;
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) lds[((wave * kBlocks + d) * 16 + r) * 64 + lane] = o[d][r] * factor;
+    __syncthreads();
+    for (int u = wave; u < 2 * kBlocks; u += 4) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v[e] += lds[((w * kBlocks + u / 2) * 16 + 8 * (u & 1) + e) * 64 + lane];
+        }
+        store_columns(t, row, head, left, head_dim, u / 2, u & 1, v, mul);
+    }
 }
 
 // Key range [lo, hi) that rows [first, first + count) of a chunk see.
@@ -274,25 +346,77 @@ __device__ __forceinline__ Seen seen_by(int row, int len, int window) {
     return Seen{first, uint32_t(max(end - first, 0))};
 }
 
-template <int kD>
+// How the kernels over query rows are laid out.  kSplit = 1: the workgroup
+// has 128 rows, 32 a wave, and stages keys and values for all four.  kSplit =
+// 4, for calls that would leave CUs idle: it has 32 rows, and its waves take
+// every fourth step of the keys, each staging its own, and join their sums at
+// the end.
+template <int kD, int kSplit>
+struct RowsShape {
+    static constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
+    static constexpr int kRows = kSplit == 1 ? kTileRows : kWaveRows;
+    static constexpr int kWaves = 4 / kSplit;                       // that share a staged tile
+    static constexpr int kTileBytes = kPanels * kPanelBytes;
+    static constexpr int kBuffers = kSplit == 4 && kPanels == 2 ? 1 : 2;  // as LDS allows
+};
+
+// Calls step(k0, buffer number) for every kStep keys of this wave from lo to
+// hi, the next tiles' loads under way meanwhile (with two buffers).
+template <typename S, int kSplit, typename Load, typename Step>
+__device__ __forceinline__ void over_keys(int lo, int hi, int wave, Load load, Step step) {
+    constexpr int kStride = kStep * kSplit;
+    const int from = kSplit == 1 ? lo : lo + kStep * wave;
+    if (from >= hi) return;
+    if constexpr (S::kBuffers == 1) {
+        for (int k0 = from; k0 < hi; k0 += kStride) {
+            load(k0, 0);
+            tiles_ready<S::kWaves>();
+            step(k0, 0);
+            __builtin_amdgcn_s_waitcnt(0);  // the tiles are read before they are loaded again
+        }
+    } else {
+        load(from, 0);
+        for (int k0 = from;; k0 += 2 * kStride) {
+            const bool more = k0 + kStride < hi;
+            tiles_ready<S::kWaves>();
+            if (more) load(k0 + kStride, 1);
+            step(k0, 0);
+            if (!more) break;
+            const bool again = k0 + 2 * kStride < hi;
+            tiles_ready<S::kWaves>();
+            if (again) load(k0 + 2 * kStride, 0);
+            step(k0 + kStride, 1);
+            if (!again) break;
+        }
+    }
+}
+
+template <int kD, int kSplit>
 __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionArgs a) {
-    constexpr int kSteps = kD / 16, kBlocks = kD / 32;
-    __shared__ uint16_t sk[2][kStep * kD], sv[2][kStep * kD];
+    typedef RowsShape<kD, kSplit> S;
+    constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
+    // arrays of their own, so that the compiler sees that loads into one
+    // never meet reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * kSplit], sv0[S::kTileBytes * kSplit];
+    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16],
+        sv1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16];
     const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
     const int head = int(id / a.tiles);
-    const Tile tile = find_tile(a.cu, a.chunks, a.rows, id - int64_t(head) * a.tiles);
+    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, id - int64_t(head) * a.tiles);
     if (tile.len == 0) return;
     const int kv = head / (a.q_heads / a.kv_heads);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int len = tile.len, window = min(a.window, len);
-    const int r0 = tile.first + wave * kWaveRows;
+    const int r0 = tile.first + (kSplit == 1 ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
+    const int own = kSplit == 1 ? 0 : wave * S::kTileBytes;  // this wave's tiles
     const Seen seen = seen_by(row, len, window);
+    const LdsAddress at = lds_address();
 
     bf16x8 q[kSteps];
     load_operand<kD>(a.q, tile.begin + r0, head, len - r0, a.head_dim, q);
     int lo, hi;
-    band(tile.first, kTileRows, len, window, lo, hi);
+    band(tile.first, S::kRows, len, window, lo, hi);
     const float c2 = a.scale * kLog2e;
     const float sink = a.sink ? a.sink[head] / a.scale : 0.0f;  // in the unscaled logits' units
     f32x16 o[kBlocks];
@@ -301,94 +425,119 @@ __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionAr
     float top = -INFINITY;  // the raised maximum, in powers of two
     float sum = 0.0f;       // of this half-wave's keys
 
-    Staged<kD> gk, gv;
-    gk.load(a.k, tile.begin + lo, kv, len - lo, a.head_dim);
-    gv.load(a.v, tile.begin + lo, kv, len - lo, a.head_dim);
-    gk.store(sk[0]);
-    gv.store(sv[0]);
-    int buf = 0;
-    for (int k0 = lo; k0 < hi; k0 += kStep, buf ^= 1) {
-        const bool more = k0 + kStep < hi;
-        if (more) {
-            gk.load(a.k, tile.begin + k0 + kStep, kv, len - k0 - kStep, a.head_dim);
-            gv.load(a.v, tile.begin + k0 + kStep, kv, len - k0 - kStep, a.head_dim);
+    const Loader<S::kPanels, S::kWaves> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
+    auto load = [&](int k0, int n) __attribute__((always_inline)) {
+        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sk1 : sk0) + own);
+        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sv1 : sv0) + own);
+    };
+    auto step = [&](int k0, int n) __attribute__((always_inline)) {
+        const uint8_t *tk = (n ? sk1 : sk0) + own, *tv = (n ? sv1 : sv0) + own;
+        if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
+        f32x16 s[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            s[b] = f32x16{};
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) s[b] = mfma(read_rows(tk, at, b, i), q[i], s[b]);
         }
-        __syncthreads();  // this step's tiles are written, the other buffers read
-        if (r0 < len && any_visible(r0, k0, kStep, window)) {
-            const uint16_t *tk = sk[buf], *tv = sv[buf];
-            f32x16 s[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                s[b] = f32x16{};
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) s[b] = mfma(read_rows(tk, b, i), q[i], s[b]);
-            }
-            if (k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
-            if (!all_visible(r0, k0, kStep, len, window)) {
-                const int at = k0 + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[b][r] = uint32_t(at + 32 * b + row_of(r)) < seen.count ? s[b][r] : -INFINITY;
-            }
-            float m = s[0][0];
+        if (k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
+        if (!all_visible(r0, k0, kStep, len, window)) {
+            const int from = k0 + 4 * (lane >> 5) - seen.first;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) m = fmaxf(m, s[b][r]);
-            m = max_halves(m) * c2;
-            if (__any(m > top + kRaise)) {
-                // a row that has seen nothing yet keeps -inf and zero sums
-                const float next = fmaxf(top, m);
-                const float alpha = top == next ? 1.0f : __builtin_amdgcn_exp2f(top - next);
-                top = next;
-                sum *= alpha;
-#pragma unroll
-                for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
-            }
-            const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c2, -base));
-                    sum += s[b][r];
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bf16x8 p = pack(s[i >> 1], i & 1);
-#pragma unroll
-                for (int d = 0; d < kBlocks; ++d) o[d] = mfma(read_columns(tv, d, i), p, o[d]);
-            }
+                for (int r = 0; r < 16; ++r) s[b][r] = uint32_t(from + 32 * b + row_of(r)) < seen.count ? s[b][r] : -INFINITY;
         }
-        if (more) {
-            gk.store(sk[buf ^ 1]);
-            gv.store(sv[buf ^ 1]);
+        float m = s[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) m = fmaxf(m, s[b][r]);
+        m = max_halves(m) * c2;
+        if (__any(m > top + kRaise)) {
+            // a row that has seen nothing yet keeps -inf and zero sums
+            const float next = fmaxf(top, m);
+            const float alpha = top == next ? 1.0f : __builtin_amdgcn_exp2f(top - next);
+            top = next;
+            sum *= alpha;
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
         }
-    }
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c2, -base));
+                sum += s[b][r];
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bf16x8 p = pack(s[i >> 1], i & 1);
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d) o[d] = mfma(read_columns(tv, at, d, i), p, o[d]);
+        }
+    };
+    over_keys<S, kSplit>(lo, hi, wave, load, step);
+
     sum = sum_halves(sum);
-    if (r0 >= len) return;
-    store_rows<kD>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o, sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f);
+    float factor = 1.0f;
+    if constexpr (kSplit == 4) {
+        // the waves' maxima and sums of the same rows
+        __shared__ float tops[4][32], sums[4][32];
+        if (lane < 32) {
+            tops[wave][lane] = top;
+            sums[wave][lane] = sum;
+        }
+        __syncthreads();
+        float all = -INFINITY, total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) all = fmaxf(all, tops[w][lane & 31]);
+        const float base = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) total += sums[w][lane & 31] * __builtin_amdgcn_exp2f(tops[w][lane & 31] - base);
+        factor = __builtin_amdgcn_exp2f(top - base);
+        top = all;
+        sum = total;
+    }
+    const float mul = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    if constexpr (kSplit == 4) {
+        store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.out, tile.begin + r0, head, len - r0, a.head_dim, o, factor, mul,
+                                    wave);
+        if (wave > 0) return;
+    } else {
+        if (r0 >= len) return;
+        store_rows<kBlocks>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o, mul);
+    }
     if (a.lse && lane < 32 && row < len)
         a.lse[int64_t(head) * a.rows + tile.begin + row] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
 }
 
 // dq, delta and the sink's partial sums: the forward kernel's shape, with the
-// probabilities from lse.  The partial sums use sum_j p_ij dp_ij in place of
-// delta: the same number without out's rounding, which dsink (float32, a sum
-// over every row) would show.
-template <int kD>
+// probabilities from lse.
+//
+// delta is do . out, which has out's rounding; the rounding of one row's
+// delta moves all of its ds alike, and where few keys share the probability
+// it is as large as the roundings of ds itself.  So rows that see at most
+// kFewKeys keys take delta = sum_j p_ij dp_ij, the same number, from a pass
+// over their keys of its own (two products more on a few keys); dsink, which
+// is float32, always does, at the end of the one pass.
+constexpr int kFewKeys = 64;
+
+template <int kD, int kSplit>
 __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a) {
-    constexpr int kSteps = kD / 16, kBlocks = kD / 32;
-    __shared__ uint16_t sk[2][kStep * kD], sv[2][kStep * kD];
-    __shared__ float part[4];
+    typedef RowsShape<kD, kSplit> S;
+    constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * kSplit], sv0[S::kTileBytes * kSplit];
+    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16],
+        sv1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16];
+    __shared__ float part[4][32], whole[4];
     const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
     const int head = int(id / a.tiles);
     const int64_t t = id - int64_t(head) * a.tiles;
-    const Tile tile = find_tile(a.cu, a.chunks, a.rows, t);
+    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, t);
     float *dsink = a.dsink_part ? a.dsink_part + int64_t(head) * a.tiles + t : nullptr;
     if (tile.len == 0) {
         if (dsink && threadIdx.x == 0) *dsink = 0.0f;
@@ -397,16 +546,70 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
     const int kv = head / (a.q_heads / a.kv_heads);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int len = tile.len, window = min(a.window, len);
-    const int r0 = tile.first + wave * kWaveRows;
+    const int r0 = tile.first + (kSplit == 1 ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
+    const int64_t stat = int64_t(head) * a.rows + tile.begin + row;
+    const int own = kSplit == 1 ? 0 : wave * S::kTileBytes;
     const Seen seen = seen_by(row, len, window);
-    const int64_t at = int64_t(head) * a.rows + tile.begin + row;
+    const LdsAddress at = lds_address();
 
     bf16x8 q[kSteps], g[kSteps];
     load_operand<kD>(a.q, tile.begin + r0, head, len - r0, a.head_dim, q);
     load_operand<kD>(a.dout, tile.begin + r0, head, len - r0, a.head_dim, g);
-    float delta = 0.0f, lse2 = 0.0f;
-    {
+    int lo, hi;
+    band(tile.first, S::kRows, len, window, lo, hi);
+    const float c2 = a.scale * kLog2e;
+    const float sink = a.sink ? a.sink[head] / a.scale : 0.0f;
+    float lse2 = row < len ? a.lse[stat] * kLog2e : 0.0f;
+    if (lse2 == -INFINITY) lse2 = INFINITY;  // a row that saw nothing: every probability is zero
+    f32x16 dq[kBlocks];
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d) dq[d] = f32x16{};
+    float delta = 0.0f, pdp = 0.0f, p0 = 0.0f, p0dp0 = 0.0f;
+
+    const Loader<S::kPanels, S::kWaves> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
+    auto load = [&](int k0, int n) __attribute__((always_inline)) {
+        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sk1 : sk0) + own);
+        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sv1 : sv0) + own);
+    };
+    // probabilities and dp of 32 keys
+    auto block = [&](int k0, int b, const uint8_t *tk, const uint8_t *tv, bool all, f32x16 &s, f32x16 &dp) __attribute__((always_inline)) {
+        s = f32x16{};
+        dp = f32x16{};
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) s = mfma(read_rows(tk, at, b, i), q[i], s);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(tv, at, b, i), g[i], dp);
+        if (b == 0 && k0 == 0 && a.sink) s[0] += lane < 32 ? sink : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2));
+        if (!all) {
+            const int from = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = uint32_t(from + row_of(r)) < seen.count ? s[r] : 0.0f;
+        }
+    };
+    if (min(len, window < 0 ? len : 2 * window + 1) <= kFewKeys) {
+        auto sums = [&](int k0, int n) __attribute__((always_inline)) {
+            if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
+            const bool all = all_visible(r0, k0, kStep, len, window);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                f32x16 s, dp;
+                block(k0, b, (n ? sk1 : sk0) + own, (n ? sv1 : sv0) + own, all, s, dp);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) delta = fmaf(s[r], dp[r], delta);
+            }
+        };
+        over_keys<S, kSplit>(lo, hi, wave, load, sums);
+        delta = sum_halves(delta);
+        if constexpr (kSplit == 4) {
+            if (lane < 32) part[wave][lane] = delta;
+            __syncthreads();
+            delta = (part[0][lane & 31] + part[1][lane & 31]) + (part[2][lane & 31] + part[3][lane & 31]);
+        }
+        __syncthreads();  // the tiles are read before the next pass loads them, and part before it is used again
+    } else {
         bf16x8 o[kSteps];
         load_operand<kD>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o);
 #pragma unroll
@@ -414,100 +617,81 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e) delta = fmaf(float(o[i][e]), float(g[i][e]), delta);
         delta = sum_halves(delta);
-        if (row < len) {
-            lse2 = a.lse[at] * kLog2e;
-            if (lane < 32) a.delta[at] = delta;
-        }
     }
-    // a row that saw nothing: every probability is zero
-    if (lse2 == -INFINITY) lse2 = INFINITY;
-    int lo, hi;
-    band(tile.first, kTileRows, len, window, lo, hi);
-    const float c2 = a.scale * kLog2e;
-    const float sink = a.sink ? a.sink[head] / a.scale : 0.0f;
-    f32x16 dq[kBlocks];
+    if (row < len && lane < 32 && (kSplit == 1 || wave == 0)) {
+        a.neg_lse[stat] = lse2 == INFINITY ? -INFINITY : -a.lse[stat] / a.scale;
+        a.neg_delta[stat] = -delta;
+    }
+    auto step = [&](int k0, int n) __attribute__((always_inline)) {
+        const uint8_t *tk = (n ? sk1 : sk0) + own, *tv = (n ? sv1 : sv0) + own;
+        if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
+        const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
-    for (int d = 0; d < kBlocks; ++d) dq[d] = f32x16{};
-    float p0 = 0.0f, p0dp0 = 0.0f, pdp = 0.0f;
-
-    Staged<kD> gk, gv;
-    gk.load(a.k, tile.begin + lo, kv, len - lo, a.head_dim);
-    gv.load(a.v, tile.begin + lo, kv, len - lo, a.head_dim);
-    gk.store(sk[0]);
-    gv.store(sv[0]);
-    int buf = 0;
-    for (int k0 = lo; k0 < hi; k0 += kStep, buf ^= 1) {
-        const bool more = k0 + kStep < hi;
-        if (more) {
-            gk.load(a.k, tile.begin + k0 + kStep, kv, len - k0 - kStep, a.head_dim);
-            gv.load(a.v, tile.begin + k0 + kStep, kv, len - k0 - kStep, a.head_dim);
-        }
-        __syncthreads();
-        if (r0 < len && any_visible(r0, k0, kStep, window)) {
-            const uint16_t *tk = sk[buf], *tv = sv[buf];
-            const bool all = all_visible(r0, k0, kStep, len, window);
+        for (int b = 0; b < 2; ++b) {
+            f32x16 s, dp;
+            block(k0, b, tk, tv, all, s, dp);
+            if (a.sink) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                f32x16 s{}, dp{};
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) s = mfma(read_rows(tk, b, i), q[i], s);
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(tv, b, i), g[i], dp);
-                if (b == 0 && k0 == 0 && a.sink) s[0] += lane < 32 ? sink : 0.0f;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2));
-                if (!all) {
-                    const int at = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = uint32_t(at + row_of(r)) < seen.count ? s[r] : 0.0f;
-                }
-                if (a.sink) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) pdp = fmaf(s[r], dp[r], pdp);
-                    if (b == 0 && k0 == 0) {
-                        p0 = s[0];
-                        p0dp0 = s[0] * dp[0];
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bf16x8 ds = pack(s, i);
-#pragma unroll
-                    for (int d = 0; d < kBlocks; ++d) dq[d] = mfma(read_columns(tk, d, 2 * b + i), ds, dq[d]);
+                for (int r = 0; r < 16; ++r) pdp = fmaf(s[r], dp[r], pdp);
+                if (b == 0 && k0 == 0) {
+                    p0 = s[0];
+                    p0dp0 = s[0] * dp[0];
                 }
             }
-        }
-        if (more) {
-            gk.store(sk[buf ^ 1]);
-            gv.store(sv[buf ^ 1]);
-        }
-    }
-    if (r0 < len) store_rows<kD>(a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, a.scale);
-    if (dsink) {
-        pdp = sum_halves(pdp);
-        float v = lane < 32 && row < len ? p0dp0 - p0 * pdp : 0.0f;
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-        if (lane == 0) part[wave] = v;
+            for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bf16x8 ds = pack(s, i);
+#pragma unroll
+                for (int d = 0; d < kBlocks; ++d) dq[d] = mfma(read_columns(tk, at, d, 2 * b + i), ds, dq[d]);
+            }
+        }
+    };
+    over_keys<S, kSplit>(lo, hi, wave, load, step);
+
+    if constexpr (kSplit == 4)
+        store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, 1.0f, a.scale,
+                                    wave);
+    else if (r0 < len)
+        store_rows<kBlocks>(a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, a.scale);
+    if (!dsink) return;
+    pdp = sum_halves(pdp);
+    if constexpr (kSplit == 4) {
+        // wave 0 has key 0 (where the tile sees it), all have a part of the sum
+        if (lane < 32) part[wave][lane] = pdp;
         __syncthreads();
-        if (threadIdx.x == 0) *dsink = (part[0] + part[1]) + (part[2] + part[3]);
+        pdp = (part[0][lane & 31] + part[1][lane & 31]) + (part[2][lane & 31] + part[3][lane & 31]);
+        if (wave > 0) return;
     }
+    float v = lane < 32 && row < len ? p0dp0 - p0 * pdp : 0.0f;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    if constexpr (kSplit == 1) {
+        if (lane == 0) whole[wave] = v;
+        __syncthreads();
+        v = (whole[0] + whole[1]) + (whole[2] + whole[3]);
+    }
+    if (threadIdx.x == 0) *dsink = v;
 }
 
-// dk and dv of one tile of keys of one key head: every query head of the
-// group and every row in the band, in a fixed order, into registers.  The
-// products' accumulators start from -lse / scale and -delta of their row, so
-// that the exponent and dp - delta need no further operation.
+// dk and dv of one tile of keys of one key head: the query heads of the group
+// and the rows in the band, in a fixed order, into registers; or a slice of
+// them, as float32 partial sums, where there are too few tiles for the CUs.
+// The products' accumulators start from -lse / scale and -delta of their
+// row, so that the exponent and dp - delta need no further operation.  (Rows
+// behind the chunk read as zeros: their p is not, but q and do are.)
 template <int kD>
 __global__ __launch_bounds__(kThreads) void attention_dkdv_kernel(AttentionArgs a) {
-    constexpr int kSteps = kD / 16, kBlocks = kD / 32;
-    __shared__ uint16_t sq[2][kStep * kD], sg[2][kStep * kD];
-    __shared__ float sl[2][kStep], sd[2][kStep];
+    constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
+    __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
+    __shared__ __attribute__((aligned(16))) float sl0[2][kStep], sl1[2][kStep];  // -lse / scale, -delta
     const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-    const int kv = int(id / a.tiles);
-    const Tile tile = find_tile(a.cu, a.chunks, a.rows, id - int64_t(kv) * a.tiles);
+    const int64_t pair = id / a.slices;
+    const int slice = int(id - pair * a.slices);
+    const int kv = int(pair / a.tiles);
+    const Tile tile = find_tile<kTileRows>(a.cu, a.chunks, a.rows, pair - int64_t(kv) * a.tiles);
     if (tile.len == 0) return;
     const int group = a.q_heads / a.kv_heads;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -515,108 +699,161 @@ __global__ __launch_bounds__(kThreads) void attention_dkdv_kernel(AttentionArgs 
     const int c0 = tile.first + wave * kWaveRows;  // this wave's keys
     const int key = c0 + (lane & 31);
     const Seen seen = seen_by(key, len, window);
+    const LdsAddress at = lds_address();
 
     bf16x8 k[kSteps], v[kSteps];
     load_operand<kD>(a.k, tile.begin + c0, kv, len - c0, a.head_dim, k);
     load_operand<kD>(a.v, tile.begin + c0, kv, len - c0, a.head_dim, v);
     int lo, hi;
     band(tile.first, kTileRows, len, window, lo, hi);
+    // steps of this slice, out of the group's heads' one after the other
     const int per_head = (hi - lo + kStep - 1) / kStep;
-    const int total = per_head * group;
-    const float c2 = a.scale * kLog2e, inv_scale = 1.0f / a.scale;
+    const int64_t all_steps = int64_t(per_head) * group;
+    const int64_t from = all_steps * slice / a.slices, end = all_steps * (slice + 1) / a.slices;
+    const float c2 = a.scale * kLog2e;
     f32x16 dk[kBlocks], dv[kBlocks];
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d) dk[d] = dv[d] = f32x16{};
 
-    Staged<kD> gq, gg;
-    float gl = 0.0f;
-    // thread 0 .. 63: lse of a row; 64 .. 127: delta of a row
-    auto load = [&](int h, int q0) {
-        const int head = kv * group + h;
-        gq.load(a.q, tile.begin + q0, head, len - q0, a.head_dim);
-        gg.load(a.dout, tile.begin + q0, head, len - q0, a.head_dim);
-        const int r = q0 + (threadIdx.x & 63);
-        if (threadIdx.x < 128) {
-            const bool delta = threadIdx.x >= 64;
-            gl = 0.0f;
-            if (r < len) gl = (delta ? a.delta : a.lse)[int64_t(head) * a.rows + tile.begin + r];
-            // rows behind the chunk and rows that saw nothing: probability zero
-            gl = delta ? -gl : r < len && gl != -INFINITY ? -gl * inv_scale : -INFINITY;
+    const Loader<kPanels, 4> lq(a.q, wave, a.head_dim), lg(a.dout, wave, a.head_dim);
+    auto load = [&](int head, int q0, int n) __attribute__((always_inline)) {
+        lq.load(head_rsrc(a.q, tile.begin + q0, head, len - q0, a.head_dim), wave, n ? sq1 : sq0);
+        lg.load(head_rsrc(a.dout, tile.begin + q0, head, len - q0, a.head_dim), wave, n ? sg1 : sg0);
+        if (wave < 2) {
+            float *p = (wave ? a.neg_delta : a.neg_lse) + int64_t(head) * a.rows + tile.begin + q0;
+            const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, min(len - q0, kStep) * 4, kWord3);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_ptr)((n ? sl1 : sl0)[wave]), 4, lane * 4, 0, 0, 0);
         }
     };
-    auto store = [&](int buf) {
-        gq.store(sq[buf]);
-        gg.store(sg[buf]);
-        if (threadIdx.x < 64)
-            sl[buf][threadIdx.x] = gl;
-        else if (threadIdx.x < 128)
-            sd[buf][threadIdx.x - 64] = gl;
-    };
-    load(0, lo);
-    store(0);
-    int h = 0, q0 = lo;
-    for (int n = 0; n < total; ++n) {
-        const int buf = n & 1;
-        int h1 = h, q1 = q0 + kStep;
-        if (q1 >= hi) {
-            ++h1;
-            q1 = lo;
-        }
-        const bool more = n + 1 < total;
-        if (more) load(h1, q1);
-        __syncthreads();
-        if (c0 < len) {
-            const float kb = a.sink && key == 0 ? a.sink[kv * group + h] * kLog2e : 0.0f;
+    auto step = [&](int head, int q0, int n) __attribute__((always_inline)) {
+        const uint8_t *tq = n ? sq1 : sq0, *tg = n ? sg1 : sg0;
+        const float *tl = n ? sl1[0] : sl0[0], *td = n ? sl1[1] : sl0[1];
+        if (c0 >= len) return;
+        const float kb = a.sink && key == 0 ? a.sink[head] * kLog2e : 0.0f;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int rb = q0 + 32 * b;
-                if (rb >= len || !any_visible(c0, rb, 32, window)) continue;
-                f32x16 s, dp;
+        for (int b = 0; b < 2; ++b) {
+            const int rb = q0 + 32 * b;
+            if (rb >= len || !any_visible(c0, rb, 32, window)) continue;
+            f32x16 s, dp;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int off = 32 * b + 8 * g + 4 * (lane >> 5);
-                    const f32x4 l = *reinterpret_cast<const f32x4 *>(&sl[buf][off]);
-                    const f32x4 d = *reinterpret_cast<const f32x4 *>(&sd[buf][off]);
+            for (int g = 0; g < 4; ++g) {
+                const int off = 32 * b + 8 * g + 4 * (lane >> 5);
+                const f32x4 l = *reinterpret_cast<const f32x4 *>(tl + off);
+                const f32x4 d = *reinterpret_cast<const f32x4 *>(td + off);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[4 * g + e] = l[e];
-                        dp[4 * g + e] = d[e];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) s = mfma(read_rows(sq[buf], b, i), k[i], s);
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(sg[buf], b, i), v[i], dp);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, kb));
-                if (!all_visible(c0, rb, 32, len, window)) {
-                    const int at = rb + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = uint32_t(at + row_of(r)) < seen.count ? s[r] : 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bf16x8 p = pack(s, i);
-#pragma unroll
-                    for (int d = 0; d < kBlocks; ++d) dv[d] = mfma(read_columns(sg[buf], d, 2 * b + i), p, dv[d]);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] *= dp[r];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bf16x8 ds = pack(s, i);
-#pragma unroll
-                    for (int d = 0; d < kBlocks; ++d) dk[d] = mfma(read_columns(sq[buf], d, 2 * b + i), ds, dk[d]);
+                for (int e = 0; e < 4; ++e) {
+                    s[4 * g + e] = l[e];
+                    dp[4 * g + e] = d[e];
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) s = mfma(read_rows(tq, at, b, i), k[i], s);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(tg, at, b, i), v[i], dp);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, kb));
+            if (!all_visible(c0, rb, 32, len, window)) {
+                const int off = rb + 4 * (lane >> 5) - seen.first;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = uint32_t(off + row_of(r)) < seen.count ? s[r] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bf16x8 p = pack(s, i);
+#pragma unroll
+                for (int d = 0; d < kBlocks; ++d) dv[d] = mfma(read_columns(tg, at, d, 2 * b + i), p, dv[d]);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] *= dp[r];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bf16x8 ds = pack(s, i);
+#pragma unroll
+                for (int d = 0; d < kBlocks; ++d) dk[d] = mfma(read_columns(tq, at, d, 2 * b + i), ds, dk[d]);
+            }
         }
-        if (more) store(buf ^ 1);
-        h = h1;
-        q0 = q1;
+    };
+    if (from < end) {
+        int h = int(from / per_head), q0 = lo + int(from - int64_t(h) * per_head) * kStep;
+        h += kv * group;
+        int64_t left = end - from;
+        auto next = [&](int &h, int &q0) __attribute__((always_inline)) {
+            q0 += kStep;
+            if (q0 >= hi) {
+                q0 = lo;
+                ++h;
+            }
+        };
+        load(h, q0, 0);
+        for (;;) {
+            int h1 = h, q1 = q0;
+            next(h1, q1);
+            tiles_ready<4>();
+            if (left > 1) load(h1, q1, 1);
+            step(h, q0, 0);
+            if (left <= 1) break;
+            h = h1;
+            q0 = q1;
+            next(h, q0);
+            tiles_ready<4>();
+            if (left > 2) load(h, q0, 0);
+            step(h1, q1, 1);
+            left -= 2;
+            if (left <= 0) break;
+        }
     }
     if (c0 >= len) return;
-    store_rows<kD>(a.dk, tile.begin + c0, kv, len - c0, a.head_dim, dk, a.scale);
-    store_rows<kD>(a.dv, tile.begin + c0, kv, len - c0, a.head_dim, dv, 1.0f);
+    if (a.slices == 1) {
+        store_rows<kBlocks>(a.dk, tile.begin + c0, kv, len - c0, a.head_dim, dk, a.scale);
+        store_rows<kBlocks>(a.dv, tile.begin + c0, kv, len - c0, a.head_dim, dv, 1.0f);
+        return;
+    }
+    if (key >= len) return;
+    const int64_t plane = int64_t(a.kv_heads) * a.rows * a.head_dim;
+    float *p = a.part + 2 * slice * plane + (int64_t(kv) * a.rows + tile.begin + key) * a.head_dim;
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int col = d * 32 + 8 * g + 4 * (lane >> 5);
+            if (col >= a.head_dim) continue;
+            *reinterpret_cast<f32x4 *>(p + col) = f32x4{dk[d][4 * g], dk[d][4 * g + 1], dk[d][4 * g + 2], dk[d][4 * g + 3]};
+            *reinterpret_cast<f32x4 *>(p + plane + col) = f32x4{dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
+        }
+}
+
+// dk and dv from the slices' partial sums, added in order; four values a
+// thread.  Rows of no chunk have no partial sums and are left as they are.
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
+    const int per_row = a.head_dim / 4;
+    const int64_t n = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t line = n / per_row;  // of [kv_heads][rows]
+    const int col = int(n - line * per_row) * 4;
+    const int kv = int(line / a.rows);
+    const int64_t row = line - int64_t(kv) * a.rows;
+    if (kv >= a.kv_heads) return;
+    // the row's chunk: the last one that starts at or before it
+    int lo = 0, hi = a.chunks;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid] <= row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    if (row < a.cu[lo] || row >= a.cu[lo + 1] || a.cu[lo] < 0 || a.cu[lo + 1] > a.rows) return;
+    const int64_t plane = int64_t(a.kv_heads) * a.rows * a.head_dim;
+    const float *p = a.part + line * a.head_dim + col;
+    f32x4 dk = {}, dv = {};
+    for (int s = 0; s < a.slices; ++s, p += 2 * plane) {
+        dk += *reinterpret_cast<const f32x4 *>(p);
+        dv += *reinterpret_cast<const f32x4 *>(p + plane);
+    }
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<bf16x4 *>(a.dk.p + row * a.dk.row + kv * a.dk.head + col) =
+        bf16x4{__bf16(dk[0] * a.scale), __bf16(dk[1] * a.scale), __bf16(dk[2] * a.scale), __bf16(dk[3] * a.scale)};
+    *reinterpret_cast<bf16x4 *>(a.dv.p + row * a.dv.row + kv * a.dv.head + col) =
+        bf16x4{__bf16(dv[0]), __bf16(dv[1]), __bf16(dv[2]), __bf16(dv[3])};
 }
 
 // dsink[h]: the tiles' partial sums, in float64 and a fixed order.
@@ -633,6 +870,26 @@ __global__ __launch_bounds__(kThreads) void attention_dsink_kernel(const float *
         __syncthreads();
     }
     if (threadIdx.x == 0) dsink[blockIdx.x] = float(lds[0]);
+}
+
+// Launch shapes, from sizes alone.
+#ifndef SPLIT_BELOW
+#define SPLIT_BELOW 512
+#define SLICE_TO 512
+#endif
+struct LaunchShape {
+    bool split;       // the kernels over query rows run with kSplit = 4
+    int32_t tiles;    // their tiles
+    int32_t key_tiles, slices;  // of the dk, dv kernel
+};
+LaunchShape launch_shape(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t chunks) {
+    LaunchShape r;
+    r.key_tiles = int32_t(rows / kTileRows + chunks);
+    r.split = int64_t(r.key_tiles) * q_heads < SPLIT_BELOW;
+    r.tiles = r.split ? int32_t(rows / kWaveRows + chunks) : r.key_tiles;
+    const int64_t groups = int64_t(r.key_tiles) * kv_heads;
+    r.slices = groups >= SLICE_TO ? 1 : int32_t(std::min<int64_t>(8, (SLICE_TO + groups - 1) / std::max<int64_t>(groups, 1)));
+    return r;
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
@@ -671,9 +928,8 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     a.chunks = p->chunks;
     a.window = p->window < 0 ? -1 : p->window;
     a.scale = p->scale;
-    a.tiles = int32_t(p->rows / kTileRows + p->chunks);
     if (p->rows == 0 || p->chunks == 0) return MIMO_OK;
-    if (int64_t(a.tiles) * p->q_heads > 0x7FFFFFFFll)
+    if ((p->rows / kTileRows + p->chunks) * p->q_heads > 0x7FFFFFFFll)
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 tiles");
     if (!p->cu_seqlens || !check_ptr_align(p->cu_seqlens, 4) || !check_ptr_align(p->sink, 4))
         return set_error(MIMO_E_INVALID, w + ": cu_seqlens must be non-null; it and sink 4-byte aligned");
@@ -692,7 +948,19 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     return MIMO_OK;
 }
 
-size_t delta_bytes(int64_t rows, int32_t q_heads) { return align256(size_t(rows) * size_t(q_heads) * sizeof(float)); }
+// The backward pass's workspace: -lse / scale and -delta of every row and
+// head, the sink's partial sums of every tile, the slices' dk and dv.
+struct Workspace {
+    size_t stats, sums, part, total;
+};
+Workspace workspace_layout(const LaunchShape &l, int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    Workspace w;
+    w.stats = align256(size_t(rows) * size_t(q_heads) * sizeof(float));
+    w.sums = align256(size_t(l.tiles) * size_t(q_heads) * sizeof(float));
+    w.part = l.slices == 1 ? 0 : align256(size_t(l.slices) * 2 * size_t(kv_heads) * size_t(rows) * size_t(head_dim) * sizeof(float));
+    w.total = 2 * w.stats + w.sums + w.part;
+    return w;
+}
 
 }  // namespace
 }  // namespace mimo
@@ -712,12 +980,18 @@ int mimo_chunk_attention(const mimo_attention *p, void *stream) {
     if (p->out.data == p->q.data || p->out.data == p->k.data || p->out.data == p->v.data)
         return set_error(MIMO_E_INVALID, "chunk_attention: out must not be an input");
     hipStream_t s = static_cast<hipStream_t>(stream);
+    const LaunchShape l = launch_shape(a.rows, a.q_heads, a.kv_heads, a.chunks);
+    a.tiles = l.tiles;
     const dim3 grid{unsigned(a.tiles) * unsigned(a.q_heads), 1, 1}, block{unsigned(kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
-        if (a.head_dim <= 64)
-            hipLaunchKernelGGL(attention_forward_kernel<64>, grid, block, 0, s, a);
+        if (a.head_dim <= 64 && l.split)
+            hipLaunchKernelGGL((attention_forward_kernel<64, 4>), grid, block, 0, s, a);
+        else if (a.head_dim <= 64)
+            hipLaunchKernelGGL((attention_forward_kernel<64, 1>), grid, block, 0, s, a);
+        else if (l.split)
+            hipLaunchKernelGGL((attention_forward_kernel<128, 4>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL(attention_forward_kernel<128>, grid, block, 0, s, a);
+            hipLaunchKernelGGL((attention_forward_kernel<128, 1>), grid, block, 0, s, a);
     });
     if (e != hipSuccess) return hip_error(e, "chunk_attention: kernel launch");
     g_dispatches.fetch_add(1);
@@ -728,7 +1002,7 @@ size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32
     if (rows < 0 || rows > kMaxRows || chunks < 0 || chunks > kMaxRows || kv_heads < 1 || q_heads < kv_heads ||
         q_heads % kv_heads || q_heads > 65536 || head_dim < 8 || head_dim > MIMO_HEAD_DIM_MAX || head_dim % 8)
         return 0;
-    return delta_bytes(rows, q_heads) + align256(size_t(rows / kTileRows + chunks) * size_t(q_heads) * sizeof(float));
+    return workspace_layout(launch_shape(rows, q_heads, kv_heads, chunks), rows, q_heads, kv_heads, head_dim).total;
 }
 
 int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_grads *g, void *workspace,
@@ -771,24 +1045,44 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
     a.dq = heads(g->dq);
     a.dk = heads(g->dk);
     a.dv = heads(g->dv);
-    a.delta = static_cast<float *>(workspace);
-    if (g->dsink)
-        a.dsink_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + delta_bytes(a.rows, a.q_heads));
-    const int32_t tiles = a.rows && a.chunks ? a.tiles : 0;
-    const dim3 dq_grid{unsigned(tiles) * unsigned(a.q_heads), 1, 1}, dkdv_grid{unsigned(tiles) * unsigned(a.kv_heads), 1, 1};
-    const dim3 block{unsigned(kThreads), 1, 1}, sink_grid{unsigned(a.q_heads), 1, 1};
+    const bool work = a.rows && a.chunks;
+    LaunchShape l = launch_shape(a.rows, a.q_heads, a.kv_heads, a.chunks);
+    if (!work) l.tiles = l.key_tiles = 0;
+    const Workspace w = workspace_layout(l, a.rows, a.q_heads, a.kv_heads, a.head_dim);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (work) {
+        a.neg_lse = reinterpret_cast<float *>(ws);
+        a.neg_delta = reinterpret_cast<float *>(ws + w.stats);
+        if (g->dsink) a.dsink_part = reinterpret_cast<float *>(ws + 2 * w.stats);
+        if (l.slices > 1) a.part = reinterpret_cast<float *>(ws + 2 * w.stats + w.sums);
+    }
+    a.slices = l.slices;
+    a.tiles = l.tiles;
+    AttentionArgs b = a;  // of the dk, dv kernel
+    b.tiles = l.key_tiles;
+    const int64_t join = (int64_t(a.kv_heads) * a.rows * (a.head_dim / 4) + kThreads - 1) / kThreads;
+    const dim3 dq_grid{unsigned(a.tiles) * unsigned(a.q_heads), 1, 1};
+    const dim3 dkdv_grid{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices), 1, 1};
+    const dim3 block{unsigned(kThreads), 1, 1}, sink_grid{unsigned(a.q_heads), 1, 1}, join_grid{unsigned(join), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
-        if (tiles && a.head_dim <= 64) {
-            hipLaunchKernelGGL(attention_dq_kernel<64>, dq_grid, block, 0, s, a);
-            hipLaunchKernelGGL(attention_dkdv_kernel<64>, dkdv_grid, block, 0, s, a);
-        } else if (tiles) {
-            hipLaunchKernelGGL(attention_dq_kernel<128>, dq_grid, block, 0, s, a);
-            hipLaunchKernelGGL(attention_dkdv_kernel<128>, dkdv_grid, block, 0, s, a);
+        if (work && a.head_dim <= 64) {
+            if (l.split)
+                hipLaunchKernelGGL((attention_dq_kernel<64, 4>), dq_grid, block, 0, s, a);
+            else
+                hipLaunchKernelGGL((attention_dq_kernel<64, 1>), dq_grid, block, 0, s, a);
+            hipLaunchKernelGGL(attention_dkdv_kernel<64>, dkdv_grid, block, 0, s, b);
+        } else if (work) {
+            if (l.split)
+                hipLaunchKernelGGL((attention_dq_kernel<128, 4>), dq_grid, block, 0, s, a);
+            else
+                hipLaunchKernelGGL((attention_dq_kernel<128, 1>), dq_grid, block, 0, s, a);
+            hipLaunchKernelGGL(attention_dkdv_kernel<128>, dkdv_grid, block, 0, s, b);
         }
-        if (g->dsink) hipLaunchKernelGGL(attention_dsink_kernel, sink_grid, block, 0, s, a.dsink_part, tiles, g->dsink);
+        if (work && l.slices > 1) hipLaunchKernelGGL(attention_join_kernel, join_grid, block, 0, s, b);
+        if (g->dsink) hipLaunchKernelGGL(attention_dsink_kernel, sink_grid, block, 0, s, a.dsink_part, l.tiles, g->dsink);
     });
     if (e != hipSuccess) return hip_error(e, "chunk_attention_backward: kernel launch");
-    g_dispatches.fetch_add((tiles ? 2 : 0) + (g->dsink ? 1 : 0));
+    g_dispatches.fetch_add((work ? 2 : 0) + (work && l.slices > 1 ? 1 : 0) + (g->dsink ? 1 : 0));
     return MIMO_OK;
 }
 
