@@ -346,26 +346,51 @@ __device__ __forceinline__ Seen seen_by(int row, int len, int window) {
     return Seen{first, uint32_t(max(end - first, 0))};
 }
 
-// How the kernels over query rows are laid out.  kSplit = 1: the workgroup
-// has 128 rows, 32 a wave, and stages keys and values for all four.  kSplit =
-// 4, for calls that would leave CUs idle: it has 32 rows, and its waves take
-// every fourth step of the keys, each staging its own, and join their sums at
-// the end.
-template <int kD, int kSplit>
+// How the kernels over query rows are laid out, four waves of 32 rows.
+//   kRowsOfOne: 128 rows of one head, and one staged tile of keys and values
+//     for all four waves.
+//   kHeadsOfFour: 32 rows of four heads that share a key head: the waves see
+//     the same keys, so a band costs them 32 + 2 window keys, not 128 + 2 window.
+//   kKeysOfOne: 32 rows of one head; the waves take every fourth step of the
+//     keys, each staging its own, and join their sums at the end: for calls
+//     that would leave CUs idle.
+#ifndef FWD_WAVES
+#define FWD_WAVES 4
+#define DQ_WAVES 3
+#define DKDV_WAVES 2
+#endif
+enum Layout { kRowsOfOne, kHeadsOfFour, kKeysOfOne };
+template <int kD, Layout kLayout>
 struct RowsShape {
     static constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
-    static constexpr int kRows = kSplit == 1 ? kTileRows : kWaveRows;
-    static constexpr int kWaves = 4 / kSplit;                       // that share a staged tile
+    static constexpr bool kSplit = kLayout == kKeysOfOne;
+    static constexpr int kRows = kLayout == kRowsOfOne ? kTileRows : kWaveRows;
+    static constexpr int kWaves = kSplit ? 1 : 4;                   // that share a staged tile
+    static constexpr int kTiles = kSplit ? 4 : 1;                   // staged at a time
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kBuffers = kSplit == 4 && kPanels == 2 ? 1 : 2;  // as LDS allows
+    static constexpr int kBuffers = kSplit && kPanels == 2 ? 1 : 2;  // as LDS allows
+};
+// Where a workgroup's part of the launch is: with kHeadsOfFour, `head` of the
+// launch counts groups of four heads.
+template <Layout kLayout>
+struct Place {
+    int head, kv;
+    int64_t tile;
+    __device__ __forceinline__ Place(const AttentionArgs &a, int wave) {
+        const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
+        const int n = int(id / a.tiles);
+        tile = id - int64_t(n) * a.tiles;
+        head = kLayout == kHeadsOfFour ? 4 * n + wave : n;
+        kv = (kLayout == kHeadsOfFour ? 4 * n : n) / (a.q_heads / a.kv_heads);
+    }
 };
 
 // Calls step(k0, buffer number) for every kStep keys of this wave from lo to
 // hi, the next tiles' loads under way meanwhile (with two buffers).
-template <typename S, int kSplit, typename Load, typename Step>
+template <typename S, typename Load, typename Step>
 __device__ __forceinline__ void over_keys(int lo, int hi, int wave, Load load, Step step) {
-    constexpr int kStride = kStep * kSplit;
-    const int from = kSplit == 1 ? lo : lo + kStep * wave;
+    constexpr int kStride = kStep * S::kTiles;
+    const int from = S::kSplit ? lo + kStep * wave : lo;
     if (from >= hi) return;
     if constexpr (S::kBuffers == 1) {
         for (int k0 = from; k0 < hi; k0 += kStride) {
@@ -391,25 +416,24 @@ __device__ __forceinline__ void over_keys(int lo, int hi, int wave, Load load, S
     }
 }
 
-template <int kD, int kSplit>
-__global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionArgs a) {
-    typedef RowsShape<kD, kSplit> S;
+template <int kD, Layout kLayout, bool kBand>
+__global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_WAVES : 1) void attention_forward_kernel(AttentionArgs a) {
+    typedef RowsShape<kD, kLayout> S;
     constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
     // arrays of their own, so that the compiler sees that loads into one
     // never meet reads of another
-    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * kSplit], sv0[S::kTileBytes * kSplit];
-    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16],
-        sv1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16];
-    const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-    const int head = int(id / a.tiles);
-    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, id - int64_t(head) * a.tiles);
-    if (tile.len == 0) return;
-    const int kv = head / (a.q_heads / a.kv_heads);
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * S::kTiles], sv0[S::kTileBytes * S::kTiles];
+    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16],
+        sv1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int len = tile.len, window = min(a.window, len);
-    const int r0 = tile.first + (kSplit == 1 ? wave * kWaveRows : 0);
+    const Place<kLayout> place(a, wave);
+    const int head = place.head, kv = place.kv;
+    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, place.tile);
+    if (tile.len == 0) return;
+    const int len = tile.len, window = kBand ? min(a.window, len) : -1;
+    const int r0 = tile.first + (kLayout == kRowsOfOne ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
-    const int own = kSplit == 1 ? 0 : wave * S::kTileBytes;  // this wave's tiles
+    const int own = S::kSplit ? wave * S::kTileBytes : 0;  // this wave's tiles
     const Seen seen = seen_by(row, len, window);
     const LdsAddress at = lds_address();
 
@@ -433,20 +457,37 @@ __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionAr
     auto step = [&](int k0, int n) __attribute__((always_inline)) {
         const uint8_t *tk = (n ? sk1 : sk0) + own, *tv = (n ? sv1 : sv0) + own;
         if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
+        // with a band, 32 keys that no row sees are left out; without one
+        // the two blocks are always taken together
+        bool take[2] = {true, true};
+        if constexpr (kBand) {
+            take[0] = any_visible(r0, k0, 32, window);
+            take[1] = k0 + 32 < len && any_visible(r0, k0 + 32, 32, window);
+        }
         f32x16 s[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+            if (kBand && !take[b]) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[b][r] = -INFINITY;
+                continue;
+            }
             s[b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) s[b] = mfma(read_rows(tk, at, b, i), q[i], s[b]);
+            if (b == 0 && k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
+            if (kBand && !all_visible(r0, k0 + 32 * b, 32, len, window)) {
+                const int from = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[b][r] = uint32_t(from + row_of(r)) < seen.count ? s[b][r] : -INFINITY;
+            }
         }
-        if (k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
-        if (!all_visible(r0, k0, kStep, len, window)) {
-            const int from = k0 + 4 * (lane >> 5) - seen.first;
+        if (!kBand && k0 + kStep > len) {
+            const int left = len - k0 - 4 * (lane >> 5);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = uint32_t(from + 32 * b + row_of(r)) < seen.count ? s[b][r] : -INFINITY;
+                for (int r = 0; r < 16; ++r) s[b][r] = 32 * b + row_of(r) < left ? s[b][r] : -INFINITY;
         }
         float m = s[0][0];
 #pragma unroll
@@ -467,24 +508,26 @@ __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionAr
         }
         const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b) {
+            if (kBand && !take[b]) continue;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c2, -base));
                 sum += s[b][r];
             }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bf16x8 p = pack(s[i >> 1], i & 1);
+            for (int i = 2 * b; i < 2 * b + 2; ++i) {
+                const bf16x8 p = pack(s[b], i & 1);
 #pragma unroll
-            for (int d = 0; d < kBlocks; ++d) o[d] = mfma(read_columns(tv, at, d, i), p, o[d]);
+                for (int d = 0; d < kBlocks; ++d) o[d] = mfma(read_columns(tv, at, d, i), p, o[d]);
+            }
         }
     };
-    over_keys<S, kSplit>(lo, hi, wave, load, step);
+    over_keys<S>(lo, hi, wave, load, step);
 
     sum = sum_halves(sum);
     float factor = 1.0f;
-    if constexpr (kSplit == 4) {
+    if constexpr (S::kSplit) {
         // the waves' maxima and sums of the same rows
         __shared__ float tops[4][32], sums[4][32];
         if (lane < 32) {
@@ -503,7 +546,7 @@ __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionAr
         sum = total;
     }
     const float mul = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    if constexpr (kSplit == 4) {
+    if constexpr (S::kSplit) {
         store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.out, tile.begin + r0, head, len - r0, a.head_dim, o, factor, mul,
                                     wave);
         if (wave > 0) return;
@@ -526,30 +569,29 @@ __global__ __launch_bounds__(kThreads) void attention_forward_kernel(AttentionAr
 // is float32, always does, at the end of the one pass.
 constexpr int kFewKeys = 64;
 
-template <int kD, int kSplit>
-__global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a) {
-    typedef RowsShape<kD, kSplit> S;
+template <int kD, Layout kLayout>
+__global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WAVES : 1) void attention_dq_kernel(AttentionArgs a) {
+    typedef RowsShape<kD, kLayout> S;
     constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
-    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * kSplit], sv0[S::kTileBytes * kSplit];
-    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16],
-        sv1[S::kBuffers == 2 ? S::kTileBytes * kSplit : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * S::kTiles], sv0[S::kTileBytes * S::kTiles];
+    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16],
+        sv1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16];
     __shared__ float part[4][32], whole[4];
-    const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-    const int head = int(id / a.tiles);
-    const int64_t t = id - int64_t(head) * a.tiles;
-    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, t);
-    float *dsink = a.dsink_part ? a.dsink_part + int64_t(head) * a.tiles + t : nullptr;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place<kLayout> place(a, wave);
+    const int head = place.head, kv = place.kv;
+    const Tile tile = find_tile<S::kRows>(a.cu, a.chunks, a.rows, place.tile);
+    // one partial sum for each head and tile
+    float *dsink = a.dsink_part ? a.dsink_part + int64_t(head) * a.tiles + place.tile : nullptr;
     if (tile.len == 0) {
-        if (dsink && threadIdx.x == 0) *dsink = 0.0f;
+        if (dsink && (kLayout == kHeadsOfFour ? lane == 0 : threadIdx.x == 0)) *dsink = 0.0f;
         return;
     }
-    const int kv = head / (a.q_heads / a.kv_heads);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int len = tile.len, window = min(a.window, len);
-    const int r0 = tile.first + (kSplit == 1 ? wave * kWaveRows : 0);
+    const int r0 = tile.first + (kLayout == kRowsOfOne ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
     const int64_t stat = int64_t(head) * a.rows + tile.begin + row;
-    const int own = kSplit == 1 ? 0 : wave * S::kTileBytes;
+    const int own = S::kSplit ? wave * S::kTileBytes : 0;
     const Seen seen = seen_by(row, len, window);
     const LdsAddress at = lds_address();
 
@@ -583,7 +625,7 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
         if (b == 0 && k0 == 0 && a.sink) s[0] += lane < 32 ? sink : 0.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2));
-        if (!all) {
+        if (!all && !all_visible(r0, k0 + 32 * b, 32, len, window)) {
             const int from = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = uint32_t(from + row_of(r)) < seen.count ? s[r] : 0.0f;
@@ -595,15 +637,16 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
             const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                if (!all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
                 f32x16 s, dp;
                 block(k0, b, (n ? sk1 : sk0) + own, (n ? sv1 : sv0) + own, all, s, dp);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) delta = fmaf(s[r], dp[r], delta);
             }
         };
-        over_keys<S, kSplit>(lo, hi, wave, load, sums);
+        over_keys<S>(lo, hi, wave, load, sums);
         delta = sum_halves(delta);
-        if constexpr (kSplit == 4) {
+        if constexpr (S::kSplit) {
             if (lane < 32) part[wave][lane] = delta;
             __syncthreads();
             delta = (part[0][lane & 31] + part[1][lane & 31]) + (part[2][lane & 31] + part[3][lane & 31]);
@@ -618,7 +661,7 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
             for (int e = 0; e < 8; ++e) delta = fmaf(float(o[i][e]), float(g[i][e]), delta);
         delta = sum_halves(delta);
     }
-    if (row < len && lane < 32 && (kSplit == 1 || wave == 0)) {
+    if (row < len && lane < 32 && (!S::kSplit || wave == 0)) {
         a.neg_lse[stat] = lse2 == INFINITY ? -INFINITY : -a.lse[stat] / a.scale;
         a.neg_delta[stat] = -delta;
     }
@@ -628,6 +671,7 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
         const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+            if (!all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
             f32x16 s, dp;
             block(k0, b, tk, tv, all, s, dp);
             if (a.sink) {
@@ -648,16 +692,16 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
             }
         }
     };
-    over_keys<S, kSplit>(lo, hi, wave, load, step);
+    over_keys<S>(lo, hi, wave, load, step);
 
-    if constexpr (kSplit == 4)
+    if constexpr (S::kSplit)
         store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, 1.0f, a.scale,
                                     wave);
     else if (r0 < len)
         store_rows<kBlocks>(a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, a.scale);
     if (!dsink) return;
     pdp = sum_halves(pdp);
-    if constexpr (kSplit == 4) {
+    if constexpr (S::kSplit) {
         // wave 0 has key 0 (where the tile sees it), all have a part of the sum
         if (lane < 32) part[wave][lane] = pdp;
         __syncthreads();
@@ -667,12 +711,13 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
     float v = lane < 32 && row < len ? p0dp0 - p0 * pdp : 0.0f;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    if constexpr (kSplit == 1) {
+    if constexpr (kLayout == kRowsOfOne) {
         if (lane == 0) whole[wave] = v;
         __syncthreads();
         v = (whole[0] + whole[1]) + (whole[2] + whole[3]);
+        if (wave > 0) return;
     }
-    if (threadIdx.x == 0) *dsink = v;
+    if (lane == 0) *dsink = v;
 }
 
 // dk and dv of one tile of keys of one key head: the query heads of the group
@@ -682,7 +727,7 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttentionArgs a)
 // row, so that the exponent and dp - delta need no further operation.  (Rows
 // behind the chunk read as zeros: their p is not, but q and do are.)
 template <int kD>
-__global__ __launch_bounds__(kThreads) void attention_dkdv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, kD == 64 ? DKDV_WAVES : 1) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
     __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
@@ -878,15 +923,26 @@ __global__ __launch_bounds__(kThreads) void attention_dsink_kernel(const float *
 #define SLICE_TO 512
 #endif
 struct LaunchShape {
-    bool split;       // the kernels over query rows run with kSplit = 4
-    int32_t tiles;    // their tiles
+    Layout layout;    // of the kernels over query rows
+    int32_t tiles, heads;  // their tiles, and heads (or groups of four) of the launch
     int32_t key_tiles, slices;  // of the dk, dv kernel
 };
 LaunchShape launch_shape(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t chunks) {
     LaunchShape r;
     r.key_tiles = int32_t(rows / kTileRows + chunks);
-    r.split = int64_t(r.key_tiles) * q_heads < SPLIT_BELOW;
-    r.tiles = r.split ? int32_t(rows / kWaveRows + chunks) : r.key_tiles;
+    const int32_t row_tiles = int32_t(std::min<int64_t>(rows / kWaveRows + chunks, 0x7FFFFFFF));
+    r.heads = q_heads;
+    if (int64_t(r.key_tiles) * q_heads < SPLIT_BELOW) {
+        r.layout = kKeysOfOne;
+        r.tiles = row_tiles;
+    } else if (q_heads / kv_heads % 4 == 0) {
+        r.layout = kHeadsOfFour;
+        r.tiles = row_tiles;
+        r.heads = q_heads / 4;
+    } else {
+        r.layout = kRowsOfOne;
+        r.tiles = r.key_tiles;
+    }
     const int64_t groups = int64_t(r.key_tiles) * kv_heads;
     r.slices = groups >= SLICE_TO ? 1 : int32_t(std::min<int64_t>(8, (SLICE_TO + groups - 1) / std::max<int64_t>(groups, 1)));
     return r;
@@ -929,6 +985,7 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     a.window = p->window < 0 ? -1 : p->window;
     a.scale = p->scale;
     if (p->rows == 0 || p->chunks == 0) return MIMO_OK;
+    // (groups of four heads take at most as many workgroups as 128 rows do, and their empty tiles)
     if ((p->rows / kTileRows + p->chunks) * p->q_heads > 0x7FFFFFFFll)
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 tiles");
     if (!p->cu_seqlens || !check_ptr_align(p->cu_seqlens, 4) || !check_ptr_align(p->sink, 4))
@@ -962,6 +1019,39 @@ Workspace workspace_layout(const LaunchShape &l, int64_t rows, int32_t q_heads, 
     return w;
 }
 
+// The narrowest instance that holds head_dim: 64, 96 or 128 columns.
+template <int kD, bool kBand>
+void launch_forward_as(const LaunchShape &l, const AttentionArgs &a, hipStream_t s) {
+    const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
+    if (l.layout == kRowsOfOne)
+        hipLaunchKernelGGL((attention_forward_kernel<kD, kRowsOfOne, kBand>), grid, block, 0, s, a);
+    else if (l.layout == kHeadsOfFour)
+        hipLaunchKernelGGL((attention_forward_kernel<kD, kHeadsOfFour, kBand>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((attention_forward_kernel<kD, kKeysOfOne, kBand>), grid, block, 0, s, a);
+}
+
+template <int kD>
+void launch_forward(const LaunchShape &l, const AttentionArgs &a, hipStream_t s) {
+    if (a.window < 0)
+        launch_forward_as<kD, false>(l, a, s);
+    else
+        launch_forward_as<kD, true>(l, a, s);
+}
+
+template <int kD>
+void launch_backward(const LaunchShape &l, const AttentionArgs &a, const AttentionArgs &b, hipStream_t s) {
+    const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
+    const dim3 keys{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices), 1, 1};
+    if (l.layout == kRowsOfOne)
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kRowsOfOne>), grid, block, 0, s, a);
+    else if (l.layout == kHeadsOfFour)
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kHeadsOfFour>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kKeysOfOne>), grid, block, 0, s, a);
+    hipLaunchKernelGGL(attention_dkdv_kernel<kD>, keys, block, 0, s, b);
+}
+
 }  // namespace
 }  // namespace mimo
 
@@ -982,16 +1072,13 @@ int mimo_chunk_attention(const mimo_attention *p, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
     const LaunchShape l = launch_shape(a.rows, a.q_heads, a.kv_heads, a.chunks);
     a.tiles = l.tiles;
-    const dim3 grid{unsigned(a.tiles) * unsigned(a.q_heads), 1, 1}, block{unsigned(kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
-        if (a.head_dim <= 64 && l.split)
-            hipLaunchKernelGGL((attention_forward_kernel<64, 4>), grid, block, 0, s, a);
-        else if (a.head_dim <= 64)
-            hipLaunchKernelGGL((attention_forward_kernel<64, 1>), grid, block, 0, s, a);
-        else if (l.split)
-            hipLaunchKernelGGL((attention_forward_kernel<128, 4>), grid, block, 0, s, a);
+        if (a.head_dim <= 64)
+            launch_forward<64>(l, a, s);
+        else if (a.head_dim <= 96)
+            launch_forward<96>(l, a, s);
         else
-            hipLaunchKernelGGL((attention_forward_kernel<128, 1>), grid, block, 0, s, a);
+            launch_forward<128>(l, a, s);
     });
     if (e != hipSuccess) return hip_error(e, "chunk_attention: kernel launch");
     g_dispatches.fetch_add(1);
@@ -1061,23 +1148,14 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
     AttentionArgs b = a;  // of the dk, dv kernel
     b.tiles = l.key_tiles;
     const int64_t join = (int64_t(a.kv_heads) * a.rows * (a.head_dim / 4) + kThreads - 1) / kThreads;
-    const dim3 dq_grid{unsigned(a.tiles) * unsigned(a.q_heads), 1, 1};
-    const dim3 dkdv_grid{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices), 1, 1};
     const dim3 block{unsigned(kThreads), 1, 1}, sink_grid{unsigned(a.q_heads), 1, 1}, join_grid{unsigned(join), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
-        if (work && a.head_dim <= 64) {
-            if (l.split)
-                hipLaunchKernelGGL((attention_dq_kernel<64, 4>), dq_grid, block, 0, s, a);
-            else
-                hipLaunchKernelGGL((attention_dq_kernel<64, 1>), dq_grid, block, 0, s, a);
-            hipLaunchKernelGGL(attention_dkdv_kernel<64>, dkdv_grid, block, 0, s, b);
-        } else if (work) {
-            if (l.split)
-                hipLaunchKernelGGL((attention_dq_kernel<128, 4>), dq_grid, block, 0, s, a);
-            else
-                hipLaunchKernelGGL((attention_dq_kernel<128, 1>), dq_grid, block, 0, s, a);
-            hipLaunchKernelGGL(attention_dkdv_kernel<128>, dkdv_grid, block, 0, s, b);
-        }
+        if (work && a.head_dim <= 64)
+            launch_backward<64>(l, a, b, s);
+        else if (work && a.head_dim <= 96)
+            launch_backward<96>(l, a, b, s);
+        else if (work)
+            launch_backward<128>(l, a, b, s);
         if (work && l.slices > 1) hipLaunchKernelGGL(attention_join_kernel, join_grid, block, 0, s, b);
         if (g->dsink) hipLaunchKernelGGL(attention_dsink_kernel, sink_grid, block, 0, s, a.dsink_part, l.tiles, g->dsink);
     });
