@@ -573,7 +573,8 @@ size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32
  * Rows behind the last boundary are left as they were.
  *   workspace  device, >= mimo_chunk_attention_workspace_bytes(...), 16-byte
  *              aligned; calls that may run at the same time need one each.
- * Two kernel launches, and one for dsink.  Returns MIMO_OK, MIMO_E_INVALID,
+ * Two kernel launches, or three where dk's and dv's sums are split among
+ * workgroups (few rows).  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
  */
 int mimo_chunk_attention_backward(const mimo_attention *args, const mimo_attention_grads *grads, void *workspace,

@@ -75,12 +75,15 @@ struct AttentionArgs {
     float *lse;          // [q_heads][rows], or null (forward)
     float *neg_lse;      // [q_heads][rows]: -lse / scale (backward)
     float *neg_delta;    // [q_heads][rows]: -delta (backward)
-    float *dsink_part;   // [q_heads][tiles], or null
+    float *dsink_part;   // [q_heads][row_tiles], or null
+    float *dsink;        // [q_heads], or null
     float *part;         // [slices][2][kv_heads][rows][head_dim]: dk, dv of each slice, or null
     int64_t rows;
     int32_t q_heads, kv_heads, head_dim, chunks;
+    int32_t group;       // q_heads / kv_heads
     int32_t window;      // < 0: none
     int32_t tiles;       // of the launch: rows / its tile rows + chunks
+    int32_t row_tiles;   // of the dq kernel
     int32_t slices;      // parts that dk's and dv's sums are split into
     float scale;
 };
@@ -92,19 +95,25 @@ struct Tile {
     int32_t len, first;
 };
 
+// xcd_contiguous_tile in 32 bits (a launch has fewer than 2^31 workgroups).
+__device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t grid) {
+    const uint32_t per = grid / kXcds;
+    return b < per * kXcds ? (b % kXcds) * per + b / kXcds : b;
+}
+
 // Tile t of the batch, kRows rows each: chunk c's tiles are numbered from
 // cu[c] / kRows + c, which leaves each chunk as many numbers as it needs or
 // one more, so that the grid is known from the row and chunk counts alone.
 // A boundary outside [0, rows] or a descending pair gives an empty tile:
 // nothing is read or written through it.
 template <int kRows>
-__device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t rows, int64_t t) {
+__device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t rows, int t) {
     const int lane = threadIdx.x & 63;
     int lo = 0, hi = chunks;
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) >> 6;
         const int idx = lo + lane * step;
-        const bool le = idx < hi && int64_t(cu[idx]) / kRows + idx <= t;
+        const bool le = idx < hi && int64_t(cu[idx] / kRows) + idx <= t;
         const int k = max(__popcll(__ballot(le)) - 1, 0);
         lo += k * step;
         hi = min(lo + step, hi);
@@ -112,7 +121,7 @@ __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int64_t b = cu[lo], e = cu[lo + 1];
     Tile r{0, 0, 0};
-    const int64_t first = (t - (b / kRows + lo)) * kRows;
+    const int64_t first = (t - (cu[lo] / kRows + int64_t(lo))) * kRows;
     if (b < 0 || e > rows || first < 0 || first >= e - b) return r;
     r.begin = b;
     r.len = __builtin_amdgcn_readfirstlane(int(e - b));
@@ -374,14 +383,12 @@ struct RowsShape {
 // launch counts groups of four heads.
 template <Layout kLayout>
 struct Place {
-    int head, kv;
-    int64_t tile;
+    int head, kv, tile;
     __device__ __forceinline__ Place(const AttentionArgs &a, int wave) {
-        const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-        const int n = int(id / a.tiles);
-        tile = id - int64_t(n) * a.tiles;
-        head = kLayout == kHeadsOfFour ? 4 * n + wave : n;
-        kv = (kLayout == kHeadsOfFour ? 4 * n : n) / (a.q_heads / a.kv_heads);
+        const uint32_t id = tile_of_xcd(blockIdx.x, gridDim.x), n = id / uint32_t(a.tiles);
+        tile = int(id - n * uint32_t(a.tiles));
+        head = int(kLayout == kHeadsOfFour ? 4 * n + wave : n);
+        kv = int((kLayout == kHeadsOfFour ? 4 * n : n) / uint32_t(a.group));
     }
 };
 
@@ -720,6 +727,22 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
     if (lane == 0) *dsink = v;
 }
 
+// dsink of a head: the partial sums of the dq kernel's tiles, in float64 and a
+// fixed order; by workgroups of their own behind the dk, dv kernel's.
+__device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, double *lds) {
+    const float *p = a.dsink_part + int64_t(head) * a.row_tiles;
+    double v = 0.0;
+    for (int i = threadIdx.x; i < a.row_tiles; i += kThreads) v += double(p[i]);
+    lds[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll
+    for (int n = kThreads / 2; n > 0; n >>= 1) {
+        if (int(threadIdx.x) < n) lds[threadIdx.x] += lds[threadIdx.x + n];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) a.dsink[head] = float(lds[0]);
+}
+
 // dk and dv of one tile of keys of one key head: the query heads of the group
 // and the rows in the band, in a fixed order, into registers; or a slice of
 // them, as float32 partial sums, where there are too few tiles for the CUs.
@@ -732,13 +755,16 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? DKDV_WAVES : 1) void attention
     __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) float sl0[2][kStep], sl1[2][kStep];  // -lse / scale, -delta
-    const int64_t id = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-    const int64_t pair = id / a.slices;
-    const int slice = int(id - pair * a.slices);
-    const int kv = int(pair / a.tiles);
-    const Tile tile = find_tile<kTileRows>(a.cu, a.chunks, a.rows, pair - int64_t(kv) * a.tiles);
+    const uint32_t tiles = uint32_t(a.tiles) * uint32_t(a.kv_heads) * uint32_t(a.slices);
+    if (blockIdx.x >= tiles) {
+        sum_dsink(a, int(blockIdx.x - tiles), reinterpret_cast<double *>(sq0));
+        return;
+    }
+    const uint32_t id = tile_of_xcd(blockIdx.x, tiles), pair = id / uint32_t(a.slices);
+    const int slice = int(id - pair * uint32_t(a.slices)), kv = int(pair / uint32_t(a.tiles));
+    const Tile tile = find_tile<kTileRows>(a.cu, a.chunks, a.rows, int(pair - uint32_t(kv) * uint32_t(a.tiles)));
     if (tile.len == 0) return;
-    const int group = a.q_heads / a.kv_heads;
+    const int group = a.group;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int len = tile.len, window = min(a.window, len);
     const int c0 = tile.first + wave * kWaveRows;  // this wave's keys
@@ -901,20 +927,9 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
         bf16x4{__bf16(dv[0]), __bf16(dv[1]), __bf16(dv[2]), __bf16(dv[3])};
 }
 
-// dsink[h]: the tiles' partial sums, in float64 and a fixed order.
-__global__ __launch_bounds__(kThreads) void attention_dsink_kernel(const float *part, int32_t tiles, float *dsink) {
-    __shared__ double lds[kThreads];
-    const float *p = part + int64_t(blockIdx.x) * tiles;
-    double v = 0.0;
-    for (int i = threadIdx.x; i < tiles; i += kThreads) v += double(p[i]);
-    lds[threadIdx.x] = v;
-    __syncthreads();
-#pragma unroll
-    for (int n = kThreads / 2; n > 0; n >>= 1) {
-        if (int(threadIdx.x) < n) lds[threadIdx.x] += lds[threadIdx.x + n];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) dsink[blockIdx.x] = float(lds[0]);
+// dsink without rows: zeros.
+__global__ __launch_bounds__(kThreads) void attention_no_rows_kernel(AttentionArgs a) {
+    if (threadIdx.x == 0) a.dsink[blockIdx.x] = 0.0f;
 }
 
 // Launch shapes, from sizes alone.
@@ -952,34 +967,35 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxRowStride = int64_t(1) << 22;  // a 64-row tile's byte offsets stay below 2^31
 
 int check_heads(const mimo_heads &t, const char *who, const char *name, int64_t rows, int32_t heads, int32_t head_dim, bool written) {
-    const std::string at = std::string(who) + ": " + name;
+    const auto at = [&] { return std::string(who) + ": " + name; };
     if (!t.data || !check_ptr_align(t.data, 16))
-        return set_error(MIMO_E_INVALID, at + " must be non-null and 16-byte aligned");
+        return set_error(MIMO_E_INVALID, at() + " must be non-null and 16-byte aligned");
     if (t.row_stride % 8 || t.head_stride % 8 || t.row_stride < head_dim || t.head_stride < 0 ||
         t.row_stride > kMaxRowStride || t.head_stride > (int64_t(1) << 40))
-        return set_error(MIMO_E_INVALID, at + "'s strides must be multiples of 8 values, row_stride in [head_dim, 2^22], head_stride >= 0");
+        return set_error(MIMO_E_INVALID, at() + "'s strides must be multiples of 8 values, row_stride in [head_dim, 2^22], head_stride >= 0");
     if (!written) return MIMO_OK;
     const bool head_inside = heads == 1 || (t.head_stride >= head_dim && t.row_stride >= (heads - 1) * t.head_stride + head_dim);
     const bool row_inside = t.head_stride >= (rows - 1) * t.row_stride + head_dim;
-    if (!head_inside && !row_inside) return set_error(MIMO_E_INVALID, at + " is written, so its rows and heads must not overlap");
+    if (!head_inside && !row_inside) return set_error(MIMO_E_INVALID, at() + " is written, so its rows and heads must not overlap");
     return MIMO_OK;
 }
 
 // What forward and backward check alike; fills the kernels' arguments.
 int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) {
-    const std::string w(who);
-    if (!p) return set_error(MIMO_E_INVALID, w + ": null arguments");
+    const auto w = [&] { return std::string(who); };
+    if (!p) return set_error(MIMO_E_INVALID, w() + ": null arguments");
     if (p->rows < 0 || p->chunks < 0 || p->q_heads < 1 || p->kv_heads < 1 || p->q_heads % p->kv_heads || p->q_heads > 65536)
-        return set_error(MIMO_E_INVALID, w + ": rows and chunks must be >= 0, q_heads a multiple of kv_heads >= 1, at most 65536");
+        return set_error(MIMO_E_INVALID, w() + ": rows and chunks must be >= 0, q_heads a multiple of kv_heads >= 1, at most 65536");
     if (p->head_dim < 8 || p->head_dim > MIMO_HEAD_DIM_MAX || p->head_dim % 8)
-        return set_error(MIMO_E_INVALID, w + ": head_dim must be a multiple of 8 in [8, 128]");
-    if (!(p->scale >= 1e-18f && p->scale <= 1e18f)) return set_error(MIMO_E_INVALID, w + ": scale must be in [1e-18, 1e18]");
+        return set_error(MIMO_E_INVALID, w() + ": head_dim must be a multiple of 8 in [8, 128]");
+    if (!(p->scale >= 1e-18f && p->scale <= 1e18f)) return set_error(MIMO_E_INVALID, w() + ": scale must be in [1e-18, 1e18]");
     if (p->rows > kMaxRows || p->chunks > kMaxRows)
-        return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^30 rows or chunks");
+        return set_error(MIMO_E_TOO_LARGE, w() + ": more than 2^30 rows or chunks");
     std::memset(&a, 0, sizeof(a));
     a.rows = p->rows;
     a.q_heads = p->q_heads;
     a.kv_heads = p->kv_heads;
+    a.group = p->q_heads / p->kv_heads;
     a.head_dim = p->head_dim;
     a.chunks = p->chunks;
     a.window = p->window < 0 ? -1 : p->window;
@@ -987,9 +1003,9 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     if (p->rows == 0 || p->chunks == 0) return MIMO_OK;
     // (groups of four heads take at most as many workgroups as 128 rows do, and their empty tiles)
     if ((p->rows / kTileRows + p->chunks) * p->q_heads > 0x7FFFFFFFll)
-        return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 tiles");
+        return set_error(MIMO_E_TOO_LARGE, w() + ": more than 2^31 - 1 tiles");
     if (!p->cu_seqlens || !check_ptr_align(p->cu_seqlens, 4) || !check_ptr_align(p->sink, 4))
-        return set_error(MIMO_E_INVALID, w + ": cu_seqlens must be non-null; it and sink 4-byte aligned");
+        return set_error(MIMO_E_INVALID, w() + ": cu_seqlens must be non-null; it and sink 4-byte aligned");
     int st;
     if ((st = check_heads(p->q, who, "q", p->rows, p->q_heads, p->head_dim, false)) != MIMO_OK) return st;
     if ((st = check_heads(p->k, who, "k", p->rows, p->kv_heads, p->head_dim, false)) != MIMO_OK) return st;
@@ -1042,7 +1058,7 @@ void launch_forward(const LaunchShape &l, const AttentionArgs &a, hipStream_t s)
 template <int kD>
 void launch_backward(const LaunchShape &l, const AttentionArgs &a, const AttentionArgs &b, hipStream_t s) {
     const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
-    const dim3 keys{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices), 1, 1};
+    const dim3 keys{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices) + unsigned(b.dsink ? b.q_heads : 0), 1, 1};
     if (l.layout == kRowsOfOne)
         hipLaunchKernelGGL((attention_dq_kernel<kD, kRowsOfOne>), grid, block, 0, s, a);
     else if (l.layout == kHeadsOfFour)
@@ -1143,6 +1159,8 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
         if (g->dsink) a.dsink_part = reinterpret_cast<float *>(ws + 2 * w.stats);
         if (l.slices > 1) a.part = reinterpret_cast<float *>(ws + 2 * w.stats + w.sums);
     }
+    a.dsink = g->dsink;
+    a.row_tiles = l.tiles;
     a.slices = l.slices;
     a.tiles = l.tiles;
     AttentionArgs b = a;  // of the dk, dv kernel
@@ -1157,10 +1175,10 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
         else if (work)
             launch_backward<128>(l, a, b, s);
         if (work && l.slices > 1) hipLaunchKernelGGL(attention_join_kernel, join_grid, block, 0, s, b);
-        if (g->dsink) hipLaunchKernelGGL(attention_dsink_kernel, sink_grid, block, 0, s, a.dsink_part, l.tiles, g->dsink);
+        if (!work) hipLaunchKernelGGL(attention_no_rows_kernel, sink_grid, block, 0, s, a);
     });
     if (e != hipSuccess) return hip_error(e, "chunk_attention_backward: kernel launch");
-    g_dispatches.fetch_add((work ? 2 : 0) + (work && l.slices > 1 ? 1 : 0) + (g->dsink ? 1 : 0));
+    g_dispatches.fetch_add(work ? (l.slices > 1 ? 3 : 2) : 1);
     return MIMO_OK;
 }
 

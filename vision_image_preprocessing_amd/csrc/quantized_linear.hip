@@ -141,6 +141,21 @@ __device__ __forceinline__ i32x16 mfma(const i32x4 &a, const i32x4 &b, const i32
 // chunks are XOR-swizzled by the row.
 __device__ __forceinline__ int lds_at(int r, int v) { return r * 128 + ((v ^ ((r ^ (r >> 3)) & 7)) << 4); }
 
+// 16 bytes of a row, non-temporal; rows of any width start at any address of
+// the type, which the hardware takes.
+__device__ __forceinline__ void store_piece(float *p, const float (&v)[4]) {
+    typedef f32x4 any_f32x4 __attribute__((aligned(4)));
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<any_f32x4 *>(p));
+}
+__device__ __forceinline__ void store_piece(__bf16 *p, const float (&v)[8]) {
+    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    bf16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<any_u32x4 *>(p));
+}
+
 // A kTile x kTile tile by four waves, a quarter each: 256 x 256 (256
 // accumulators a lane, one workgroup a CU), whose LDS bytes per product are
 // low enough that the matrix cores set the pace, or 128 x 128 (two workgroups
@@ -317,7 +332,7 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
         t[j] = a.w_scale[e];
         b[j] = a.bias ? a.bias[e] : 0.0f;
     }
-    const bool whole = a.e % kOut == 0 && col + kOut <= a.e;
+    const bool whole = col + kOut <= a.e;  // at any address of the type: see store_piece
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
         const int r = lane & 31;
@@ -345,15 +360,7 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a) {
             if (row >= a.n_rows) continue;
             OutT *out = static_cast<OutT *>(a.out) + row * a.e + col;
             if (whole) {
-                if constexpr (sizeof(OutT) == 4) {
-                    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4 *>(out));
-                } else {
-                    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-                    bf16x8 h;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
-                    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<u32x4 *>(out));
-                }
+                store_piece(out, v);
             } else {
 #pragma unroll
                 for (int j = 0; j < kOut; ++j)
