@@ -553,7 +553,7 @@ typedef struct mimo_attention_grads {
  * boundaries that make chunks overlap give undefined values in out.
  * out must not overlap an input.  One kernel launch.  Returns MIMO_OK,
  * MIMO_E_INVALID, MIMO_E_TOO_LARGE (more than 2^30 rows or chunks, or
- * (rows / 128 + chunks) * q_heads above 2^31 - 1) or MIMO_E_HIP.
+ * (rows / 128 + chunks + 1) * q_heads above 2^24 - 1) or MIMO_E_HIP.
  */
 int mimo_chunk_attention(const mimo_attention *args, void *stream);
 

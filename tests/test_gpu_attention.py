@@ -134,12 +134,16 @@ def test_lengths(V, lengths, window, sink):
 
 @pytest.mark.parametrize("lengths", [[1], [2, 1, 3], [31, 33], [64, 63], [0, 5, 0, 0, 129, 0], [300]])
 @pytest.mark.parametrize("window,sink", [(-1, False), (64, True), (5, True), (0, True)])
-@pytest.mark.parametrize("hq,hk,d", [(512, 128, 64), (512, 512, 64), (512, 128, 128)])
-def test_lengths_many_heads(V, lengths, window, sink, hq, hk, d):
-    """Enough heads that a workgroup has 128 rows, with dk's and dv's sums in slices and whole."""
-    if d == 128 and len(lengths) < 2:
-        pytest.skip("the wide heads run the ragged lengths")
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (4, 1, 88), (12, 3, 128)])
+def test_lengths_of_four_heads(V, lengths, window, sink, hq, hk, d):
+    """Heads in groups of four, which share a workgroup."""
     _check(V, lengths, hq, hk, d, window, sink, seed=sum(lengths) + window + hk)
+
+
+@pytest.mark.parametrize("hq,hk,d,window", [(256, 256, 64, -1), (256, 256, 64, 20), (1024, 256, 64, -1), (256, 256, 128, 50)])
+def test_sums_that_are_not_sliced(V, hq, hk, d, window):
+    """Enough key heads that dk's and dv's sums are not split among workgroups."""
+    _check(V, [70, 130], hq, hk, d, window, True, seed=hq + d)
 
 
 @pytest.mark.parametrize("hq,hk,d", [(1, 1, 64), (8, 8, 8), (8, 2, 32), (6, 1, 72), (8, 2, 80), (4, 2, 128), (4, 4, 96),

@@ -189,17 +189,17 @@ __device__ __forceinline__ void load_to_lds(const __amdgpu_buffer_rsrc_t &rsrc, 
 #endif
 }
 
-// kStep rows of one head straight into LDS, 1 KB (eight rows of a panel) a
-// load: by the workgroup's four waves, or by each wave for itself.
-template <int kPanels, int kWaves>
+// kStep rows of one head straight into LDS by the workgroup's four waves, 1 KB
+// (eight rows of a panel) a load.
+template <int kPanels>
 struct Loader {
-    static constexpr int kN = kPanels * 8 / kWaves;
+    static constexpr int kN = kPanels * 8 / 4;
     uint32_t off[kN];
     __device__ __forceinline__ Loader(const Heads &t, int wave, int head_dim) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int n = kWaves == 1 ? i : i * kWaves + wave, g = n % 8;
+            const int n = i * 4 + wave, g = n % 8;
             const int v = (lane & 7) ^ ((lane >> 3) ^ g);
             off[i] = head_offset(t, g * 8 + (lane >> 3), (n / 8) * 64 + v * 8, head_dim);
         }
@@ -207,21 +207,18 @@ struct Loader {
     __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t &rsrc, int wave, uint8_t *lds) const {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int n = kWaves == 1 ? i : i * kWaves + wave;
-            load_to_lds(rsrc, lds + n * 1024, off[i]);
+            load_to_lds(rsrc, lds + (i * 4 + wave) * 1024, off[i]);
         }
     }
 };
 
-// Every load into LDS that this wave made has landed; with kWaves = 4 those
-// of the others too, and every wave has read what it wanted of the tiles
-// before.  (__syncthreads would do, with a fence that the loads issued next
-// need not wait for.)
-template <int kWaves>
+// The loads into LDS that the workgroup's waves made have landed, and every
+// wave has read what it wanted of the tiles before.  (__syncthreads would do,
+// with a fence that the loads issued next need not wait for.)
 __device__ __forceinline__ void tiles_ready() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0);
-    if constexpr (kWaves > 1) __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -296,30 +293,6 @@ __device__ __forceinline__ void store_rows(const Heads &t, int64_t row, int head
         }
 }
 
-// Four waves' blocks of the same rows, each times its own factor, added up
-// and stored: through LDS (4 x 4 KB a block), each wave taking some columns.
-template <int kBlocks>
-__device__ __forceinline__ void store_rows_of_four(float *lds, const Heads &t, int64_t row, int head, int left, int head_dim,
-                                                   const f32x16 (&o)[kBlocks], float factor, float mul, int wave) {
-    const int lane = threadIdx.x & 63;
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) lds[((wave * kBlocks + d) * 16 + r) * 64 + lane] = o[d][r] * factor;
-    __syncthreads();
-    for (int u = wave; u < 2 * kBlocks; u += 4) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) v[e] += lds[((w * kBlocks + u / 2) * 16 + 8 * (u & 1) + e) * 64 + lane];
-        }
-        store_columns(t, row, head, left, head_dim, u / 2, u & 1, v, mul);
-    }
-}
-
 // Key range [lo, hi) that rows [first, first + count) of a chunk see.
 __device__ __forceinline__ void band(int first, int count, int len, int window, int &lo, int &hi) {
     lo = 0;
@@ -355,29 +328,21 @@ __device__ __forceinline__ Seen seen_by(int row, int len, int window) {
     return Seen{first, uint32_t(max(end - first, 0))};
 }
 
-// How the kernels over query rows are laid out, four waves of 32 rows.
-//   kRowsOfOne: 128 rows of one head, and one staged tile of keys and values
-//     for all four waves.
+// How the kernels over query rows are laid out, four waves of 32 rows that
+// share each staged tile of keys and values.
+//   kRowsOfOne: 128 rows of one head.
 //   kHeadsOfFour: 32 rows of four heads that share a key head: the waves see
-//     the same keys, so a band costs them 32 + 2 window keys, not 128 + 2 window.
-//   kKeysOfOne: 32 rows of one head; the waves take every fourth step of the
-//     keys, each staging its own, and join their sums at the end: for calls
-//     that would leave CUs idle.
-#ifndef FWD_WAVES
-#define FWD_WAVES 4
-#define DQ_WAVES 3
-#define DKDV_WAVES 2
-#endif
-enum Layout { kRowsOfOne, kHeadsOfFour, kKeysOfOne };
+//     the same keys, so a band costs them 32 + 2 window keys, not 128 + 2
+//     window (band of 64 over 32 x 3520 rows: 382 us against 471).
+// Sharing out a row's keys among waves, to be joined at the end, was measured
+// for calls that leave CUs idle, and gained nothing that a call shows (12
+// heads of 2000 rows: 33 us against 31; 32 heads of 216 rows: 7.8 against 8.2).
+enum Layout { kRowsOfOne, kHeadsOfFour };
 template <int kD, Layout kLayout>
 struct RowsShape {
     static constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
-    static constexpr bool kSplit = kLayout == kKeysOfOne;
     static constexpr int kRows = kLayout == kRowsOfOne ? kTileRows : kWaveRows;
-    static constexpr int kWaves = kSplit ? 1 : 4;                   // that share a staged tile
-    static constexpr int kTiles = kSplit ? 4 : 1;                   // staged at a time
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kBuffers = kSplit && kPanels == 2 ? 1 : 2;  // as LDS allows
 };
 // Where a workgroup's part of the launch is: with kHeadsOfFour, `head` of the
 // launch counts groups of four heads.
@@ -392,46 +357,34 @@ struct Place {
     }
 };
 
-// Calls step(k0, buffer number) for every kStep keys of this wave from lo to
-// hi, the next tiles' loads under way meanwhile (with two buffers).
-template <typename S, typename Load, typename Step>
-__device__ __forceinline__ void over_keys(int lo, int hi, int wave, Load load, Step step) {
-    constexpr int kStride = kStep * S::kTiles;
-    const int from = S::kSplit ? lo + kStep * wave : lo;
-    if (from >= hi) return;
-    if constexpr (S::kBuffers == 1) {
-        for (int k0 = from; k0 < hi; k0 += kStride) {
-            load(k0, 0);
-            tiles_ready<S::kWaves>();
-            step(k0, 0);
-            __builtin_amdgcn_s_waitcnt(0);  // the tiles are read before they are loaded again
-        }
-    } else {
-        load(from, 0);
-        for (int k0 = from;; k0 += 2 * kStride) {
-            const bool more = k0 + kStride < hi;
-            tiles_ready<S::kWaves>();
-            if (more) load(k0 + kStride, 1);
-            step(k0, 0);
-            if (!more) break;
-            const bool again = k0 + 2 * kStride < hi;
-            tiles_ready<S::kWaves>();
-            if (again) load(k0 + 2 * kStride, 0);
-            step(k0 + kStride, 1);
-            if (!again) break;
-        }
+// Calls step(k0, buffer number) for every kStep keys from lo to hi, the next
+// tiles' loads under way meanwhile.
+template <typename Load, typename Step>
+__device__ __forceinline__ void over_keys(int lo, int hi, Load load, Step step) {
+    if (lo >= hi) return;
+    load(lo, 0);
+    for (int k0 = lo;; k0 += 2 * kStep) {
+        const bool more = k0 + kStep < hi;
+        tiles_ready();
+        if (more) load(k0 + kStep, 1);
+        step(k0, 0);
+        if (!more) break;
+        const bool again = k0 + 2 * kStep < hi;
+        tiles_ready();
+        if (again) load(k0 + 2 * kStep, 0);
+        step(k0 + kStep, 1);
+        if (!again) break;
     }
 }
 
 template <int kD, Layout kLayout, bool kBand>
-__global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_WAVES : 1) void attention_forward_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_kernel(AttentionArgs a) {
     typedef RowsShape<kD, kLayout> S;
     constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
     // arrays of their own, so that the compiler sees that loads into one
     // never meet reads of another
-    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * S::kTiles], sv0[S::kTileBytes * S::kTiles];
-    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16],
-        sv1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes], sk1[S::kTileBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sv0[S::kTileBytes], sv1[S::kTileBytes];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Place<kLayout> place(a, wave);
     const int head = place.head, kv = place.kv;
@@ -440,7 +393,6 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_W
     const int len = tile.len, window = kBand ? min(a.window, len) : -1;
     const int r0 = tile.first + (kLayout == kRowsOfOne ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
-    const int own = S::kSplit ? wave * S::kTileBytes : 0;  // this wave's tiles
     const Seen seen = seen_by(row, len, window);
     const LdsAddress at = lds_address();
 
@@ -456,13 +408,13 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_W
     float top = -INFINITY;  // the raised maximum, in powers of two
     float sum = 0.0f;       // of this half-wave's keys
 
-    const Loader<S::kPanels, S::kWaves> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
+    const Loader<S::kPanels> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
     auto load = [&](int k0, int n) __attribute__((always_inline)) {
-        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sk1 : sk0) + own);
-        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sv1 : sv0) + own);
+        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, n ? sk1 : sk0);
+        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, n ? sv1 : sv0);
     };
     auto step = [&](int k0, int n) __attribute__((always_inline)) {
-        const uint8_t *tk = (n ? sk1 : sk0) + own, *tv = (n ? sv1 : sv0) + own;
+        const uint8_t *tk = n ? sk1 : sk0, *tv = n ? sv1 : sv0;
         if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
         // with a band, 32 keys that no row sees are left out; without one
         // the two blocks are always taken together
@@ -530,37 +482,11 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_W
             }
         }
     };
-    over_keys<S>(lo, hi, wave, load, step);
+    over_keys(lo, hi, load, step);
 
     sum = sum_halves(sum);
-    float factor = 1.0f;
-    if constexpr (S::kSplit) {
-        // the waves' maxima and sums of the same rows
-        __shared__ float tops[4][32], sums[4][32];
-        if (lane < 32) {
-            tops[wave][lane] = top;
-            sums[wave][lane] = sum;
-        }
-        __syncthreads();
-        float all = -INFINITY, total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) all = fmaxf(all, tops[w][lane & 31]);
-        const float base = all == -INFINITY ? 0.0f : all;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) total += sums[w][lane & 31] * __builtin_amdgcn_exp2f(tops[w][lane & 31] - base);
-        factor = __builtin_amdgcn_exp2f(top - base);
-        top = all;
-        sum = total;
-    }
-    const float mul = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    if constexpr (S::kSplit) {
-        store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.out, tile.begin + r0, head, len - r0, a.head_dim, o, factor, mul,
-                                    wave);
-        if (wave > 0) return;
-    } else {
-        if (r0 >= len) return;
-        store_rows<kBlocks>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o, mul);
-    }
+    if (r0 >= len) return;
+    store_rows<kBlocks>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o, sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f);
     if (a.lse && lane < 32 && row < len)
         a.lse[int64_t(head) * a.rows + tile.begin + row] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
 }
@@ -577,13 +503,12 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? FWD_W
 constexpr int kFewKeys = 64;
 
 template <int kD, Layout kLayout>
-__global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WAVES : 1) void attention_dq_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kernel(AttentionArgs a) {
     typedef RowsShape<kD, kLayout> S;
     constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
-    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes * S::kTiles], sv0[S::kTileBytes * S::kTiles];
-    __shared__ __attribute__((aligned(16))) uint8_t sk1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16],
-        sv1[S::kBuffers == 2 ? S::kTileBytes * S::kTiles : 16];
-    __shared__ float part[4][32], whole[4];
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[S::kTileBytes], sk1[S::kTileBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sv0[S::kTileBytes], sv1[S::kTileBytes];
+    __shared__ float whole[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Place<kLayout> place(a, wave);
     const int head = place.head, kv = place.kv;
@@ -598,7 +523,6 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
     const int r0 = tile.first + (kLayout == kRowsOfOne ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
     const int64_t stat = int64_t(head) * a.rows + tile.begin + row;
-    const int own = S::kSplit ? wave * S::kTileBytes : 0;
     const Seen seen = seen_by(row, len, window);
     const LdsAddress at = lds_address();
 
@@ -616,10 +540,10 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
     for (int d = 0; d < kBlocks; ++d) dq[d] = f32x16{};
     float delta = 0.0f, pdp = 0.0f, p0 = 0.0f, p0dp0 = 0.0f;
 
-    const Loader<S::kPanels, S::kWaves> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
+    const Loader<S::kPanels> lk(a.k, wave, a.head_dim), lv(a.v, wave, a.head_dim);
     auto load = [&](int k0, int n) __attribute__((always_inline)) {
-        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sk1 : sk0) + own);
-        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, (n ? sv1 : sv0) + own);
+        lk.load(head_rsrc(a.k, tile.begin + k0, kv, len - k0, a.head_dim), wave, n ? sk1 : sk0);
+        lv.load(head_rsrc(a.v, tile.begin + k0, kv, len - k0, a.head_dim), wave, n ? sv1 : sv0);
     };
     // probabilities and dp of 32 keys
     auto block = [&](int k0, int b, const uint8_t *tk, const uint8_t *tv, bool all, f32x16 &s, f32x16 &dp) __attribute__((always_inline)) {
@@ -646,19 +570,14 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
             for (int b = 0; b < 2; ++b) {
                 if (!all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
                 f32x16 s, dp;
-                block(k0, b, (n ? sk1 : sk0) + own, (n ? sv1 : sv0) + own, all, s, dp);
+                block(k0, b, n ? sk1 : sk0, n ? sv1 : sv0, all, s, dp);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) delta = fmaf(s[r], dp[r], delta);
             }
         };
-        over_keys<S>(lo, hi, wave, load, sums);
+        over_keys(lo, hi, load, sums);
         delta = sum_halves(delta);
-        if constexpr (S::kSplit) {
-            if (lane < 32) part[wave][lane] = delta;
-            __syncthreads();
-            delta = (part[0][lane & 31] + part[1][lane & 31]) + (part[2][lane & 31] + part[3][lane & 31]);
-        }
-        __syncthreads();  // the tiles are read before the next pass loads them, and part before it is used again
+        __syncthreads();  // the tiles are read before the next pass loads them
     } else {
         bf16x8 o[kSteps];
         load_operand<kD>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o);
@@ -668,12 +587,12 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
             for (int e = 0; e < 8; ++e) delta = fmaf(float(o[i][e]), float(g[i][e]), delta);
         delta = sum_halves(delta);
     }
-    if (row < len && lane < 32 && (!S::kSplit || wave == 0)) {
+    if (row < len && lane < 32) {
         a.neg_lse[stat] = lse2 == INFINITY ? -INFINITY : -a.lse[stat] / a.scale;
         a.neg_delta[stat] = -delta;
     }
     auto step = [&](int k0, int n) __attribute__((always_inline)) {
-        const uint8_t *tk = (n ? sk1 : sk0) + own, *tv = (n ? sv1 : sv0) + own;
+        const uint8_t *tk = n ? sk1 : sk0, *tv = n ? sv1 : sv0;
         if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
         const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
@@ -699,22 +618,11 @@ __global__ __launch_bounds__(kThreads, kD == 64 && kLayout != kKeysOfOne ? DQ_WA
             }
         }
     };
-    over_keys<S>(lo, hi, wave, load, step);
+    over_keys(lo, hi, load, step);
 
-    if constexpr (S::kSplit)
-        store_rows_of_four<kBlocks>(reinterpret_cast<float *>(sk0), a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, 1.0f, a.scale,
-                                    wave);
-    else if (r0 < len)
-        store_rows<kBlocks>(a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, a.scale);
+    if (r0 < len) store_rows<kBlocks>(a.dq, tile.begin + r0, head, len - r0, a.head_dim, dq, a.scale);
     if (!dsink) return;
     pdp = sum_halves(pdp);
-    if constexpr (S::kSplit) {
-        // wave 0 has key 0 (where the tile sees it), all have a part of the sum
-        if (lane < 32) part[wave][lane] = pdp;
-        __syncthreads();
-        pdp = (part[0][lane & 31] + part[1][lane & 31]) + (part[2][lane & 31] + part[3][lane & 31]);
-        if (wave > 0) return;
-    }
     float v = lane < 32 && row < len ? p0dp0 - p0 * pdp : 0.0f;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
@@ -750,7 +658,7 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // row, so that the exponent and dp - delta need no further operation.  (Rows
 // behind the chunk read as zeros: their p is not, but q and do are.)
 template <int kD>
-__global__ __launch_bounds__(kThreads, kD == 64 ? DKDV_WAVES : 1) void attention_dkdv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, kD == 64 ? 2 : 1) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
     __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
@@ -786,7 +694,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? DKDV_WAVES : 1) void attention
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d) dk[d] = dv[d] = f32x16{};
 
-    const Loader<kPanels, 4> lq(a.q, wave, a.head_dim), lg(a.dout, wave, a.head_dim);
+    const Loader<kPanels> lq(a.q, wave, a.head_dim), lg(a.dout, wave, a.head_dim);
     auto load = [&](int head, int q0, int n) __attribute__((always_inline)) {
         lq.load(head_rsrc(a.q, tile.begin + q0, head, len - q0, a.head_dim), wave, n ? sq1 : sq0);
         lg.load(head_rsrc(a.dout, tile.begin + q0, head, len - q0, a.head_dim), wave, n ? sg1 : sg0);
@@ -859,14 +767,14 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? DKDV_WAVES : 1) void attention
         for (;;) {
             int h1 = h, q1 = q0;
             next(h1, q1);
-            tiles_ready<4>();
+            tiles_ready();
             if (left > 1) load(h1, q1, 1);
             step(h, q0, 0);
             if (left <= 1) break;
             h = h1;
             q0 = q1;
             next(h, q0);
-            tiles_ready<4>();
+            tiles_ready();
             if (left > 2) load(h, q0, 0);
             step(h1, q1, 1);
             left -= 2;
@@ -933,10 +841,6 @@ __global__ __launch_bounds__(kThreads) void attention_no_rows_kernel(AttentionAr
 }
 
 // Launch shapes, from sizes alone.
-#ifndef SPLIT_BELOW
-#define SPLIT_BELOW 512
-#define SLICE_TO 512
-#endif
 struct LaunchShape {
     Layout layout;    // of the kernels over query rows
     int32_t tiles, heads;  // their tiles, and heads (or groups of four) of the launch
@@ -944,26 +848,23 @@ struct LaunchShape {
 };
 LaunchShape launch_shape(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t chunks) {
     LaunchShape r;
+    const int32_t group = q_heads / kv_heads;
     r.key_tiles = int32_t(rows / kTileRows + chunks);
-    const int32_t row_tiles = int32_t(std::min<int64_t>(rows / kWaveRows + chunks, 0x7FFFFFFF));
-    r.heads = q_heads;
-    if (int64_t(r.key_tiles) * q_heads < SPLIT_BELOW) {
-        r.layout = kKeysOfOne;
-        r.tiles = row_tiles;
-    } else if (q_heads / kv_heads % 4 == 0) {
-        r.layout = kHeadsOfFour;
-        r.tiles = row_tiles;
-        r.heads = q_heads / 4;
-    } else {
-        r.layout = kRowsOfOne;
-        r.tiles = r.key_tiles;
-    }
-    const int64_t groups = int64_t(r.key_tiles) * kv_heads;
-    r.slices = groups >= SLICE_TO ? 1 : int32_t(std::min<int64_t>(8, (SLICE_TO + groups - 1) / std::max<int64_t>(groups, 1)));
+    r.layout = group % 4 == 0 ? kHeadsOfFour : kRowsOfOne;
+    r.tiles = r.layout == kRowsOfOne ? r.key_tiles : int32_t(std::min<int64_t>(rows / kWaveRows + chunks, 0x7FFFFFFF));
+    r.heads = r.layout == kRowsOfOne ? q_heads : q_heads / 4;
+    // dk's and dv's sums are split where there are fewer than two tiles a CU,
+    // into at most eight slices of at least four steps of the longest chunk
+    // there can be (16 heads on 8 of 4000 rows: two slices 268 us, one 298;
+    // 32 heads of 216 rows: eight slices 30 us, four 24)
+    const int64_t groups = std::max<int64_t>(int64_t(r.key_tiles) * kv_heads, 1);
+    const int64_t steps = int64_t(group) * ((rows + kStep - 1) / kStep);
+    r.slices = int32_t(std::max<int64_t>(1, std::min<int64_t>({8, (512 + groups - 1) / groups, steps / 4})));
     return r;
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxRowStride = int64_t(1) << 22;  // a 64-row tile's byte offsets stay below 2^31
 
 int check_heads(const mimo_heads &t, const char *who, const char *name, int64_t rows, int32_t heads, int32_t head_dim, bool written) {
@@ -1001,9 +902,10 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     a.window = p->window < 0 ? -1 : p->window;
     a.scale = p->scale;
     if (p->rows == 0 || p->chunks == 0) return MIMO_OK;
-    // (groups of four heads take at most as many workgroups as 128 rows do, and their empty tiles)
-    if ((p->rows / kTileRows + p->chunks) * p->q_heads > 0x7FFFFFFFll)
-        return set_error(MIMO_E_TOO_LARGE, w() + ": more than 2^31 - 1 tiles");
+    // a launch has fewer than 2^32 threads (groups of four heads take at most
+    // as many workgroups as 128 rows do; dsink takes one a head)
+    if ((p->rows / kTileRows + p->chunks) * p->q_heads + p->q_heads > kMaxGroups)
+        return set_error(MIMO_E_TOO_LARGE, w() + ": (rows / 128 + chunks + 1) * q_heads is above 2^24 - 1");
     if (!p->cu_seqlens || !check_ptr_align(p->cu_seqlens, 4) || !check_ptr_align(p->sink, 4))
         return set_error(MIMO_E_INVALID, w() + ": cu_seqlens must be non-null; it and sink 4-byte aligned");
     int st;
@@ -1041,10 +943,8 @@ void launch_forward_as(const LaunchShape &l, const AttentionArgs &a, hipStream_t
     const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
     if (l.layout == kRowsOfOne)
         hipLaunchKernelGGL((attention_forward_kernel<kD, kRowsOfOne, kBand>), grid, block, 0, s, a);
-    else if (l.layout == kHeadsOfFour)
-        hipLaunchKernelGGL((attention_forward_kernel<kD, kHeadsOfFour, kBand>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((attention_forward_kernel<kD, kKeysOfOne, kBand>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((attention_forward_kernel<kD, kHeadsOfFour, kBand>), grid, block, 0, s, a);
 }
 
 template <int kD>
@@ -1061,10 +961,8 @@ void launch_backward(const LaunchShape &l, const AttentionArgs &a, const Attenti
     const dim3 keys{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices) + unsigned(b.dsink ? b.q_heads : 0), 1, 1};
     if (l.layout == kRowsOfOne)
         hipLaunchKernelGGL((attention_dq_kernel<kD, kRowsOfOne>), grid, block, 0, s, a);
-    else if (l.layout == kHeadsOfFour)
-        hipLaunchKernelGGL((attention_dq_kernel<kD, kHeadsOfFour>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((attention_dq_kernel<kD, kKeysOfOne>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kHeadsOfFour>), grid, block, 0, s, a);
     hipLaunchKernelGGL(attention_dkdv_kernel<kD>, keys, block, 0, s, b);
 }
 
