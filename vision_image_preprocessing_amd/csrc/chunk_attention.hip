@@ -502,7 +502,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
 // is float32, always does, at the end of the one pass.
 constexpr int kFewKeys = 64;
 
-template <int kD, Layout kLayout>
+template <int kD, Layout kLayout, bool kBand>
 __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kernel(AttentionArgs a) {
     typedef RowsShape<kD, kLayout> S;
     constexpr int kSteps = S::kSteps, kBlocks = S::kBlocks;
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
         if (dsink && (kLayout == kHeadsOfFour ? lane == 0 : threadIdx.x == 0)) *dsink = 0.0f;
         return;
     }
-    const int len = tile.len, window = min(a.window, len);
+    const int len = tile.len, window = kBand ? min(a.window, len) : -1;
     const int r0 = tile.first + (kLayout == kRowsOfOne ? wave * kWaveRows : 0);
     const int row = r0 + (lane & 31);
     const int64_t stat = int64_t(head) * a.rows + tile.begin + row;
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
             const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                if (!all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
+                if (kBand && !all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
                 f32x16 s, dp;
                 block(k0, b, n ? sk1 : sk0, n ? sv1 : sv0, all, s, dp);
 #pragma unroll
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
         const bool all = all_visible(r0, k0, kStep, len, window);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            if (!all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
+            if (kBand && !all && (k0 + 32 * b >= len || !any_visible(r0, k0 + 32 * b, 32, window))) continue;
             f32x16 s, dp;
             block(k0, b, tk, tv, all, s, dp);
             if (a.sink) {
@@ -657,8 +657,8 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // The products' accumulators start from -lse / scale and -delta of their
 // row, so that the exponent and dp - delta need no further operation.  (Rows
 // behind the chunk read as zeros: their p is not, but q and do are.)
-template <int kD>
-__global__ __launch_bounds__(kThreads, kD == 64 ? 2 : 1) void attention_dkdv_kernel(AttentionArgs a) {
+template <int kD, bool kBand>
+__global__ __launch_bounds__(kThreads, kD == 128 ? 1 : 2) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
     __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
@@ -674,7 +674,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 2 : 1) void attention_dkdv_ker
     if (tile.len == 0) return;
     const int group = a.group;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int len = tile.len, window = min(a.window, len);
+    const int len = tile.len, window = kBand ? min(a.window, len) : -1;
     const int c0 = tile.first + wave * kWaveRows;  // this wave's keys
     const int key = c0 + (lane & 31);
     const Seen seen = seen_by(key, len, window);
@@ -712,7 +712,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 2 : 1) void attention_dkdv_ker
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int rb = q0 + 32 * b;
-            if (rb >= len || !any_visible(c0, rb, 32, window)) continue;
+            if (kBand && (rb >= len || !any_visible(c0, rb, 32, window))) continue;
             f32x16 s, dp;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -955,15 +955,23 @@ void launch_forward(const LaunchShape &l, const AttentionArgs &a, hipStream_t s)
         launch_forward_as<kD, true>(l, a, s);
 }
 
-template <int kD>
-void launch_backward(const LaunchShape &l, const AttentionArgs &a, const AttentionArgs &b, hipStream_t s) {
+template <int kD, bool kBand>
+void launch_backward_as(const LaunchShape &l, const AttentionArgs &a, const AttentionArgs &b, hipStream_t s) {
     const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
     const dim3 keys{unsigned(b.tiles) * unsigned(b.kv_heads) * unsigned(b.slices) + unsigned(b.dsink ? b.q_heads : 0), 1, 1};
     if (l.layout == kRowsOfOne)
-        hipLaunchKernelGGL((attention_dq_kernel<kD, kRowsOfOne>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kRowsOfOne, kBand>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((attention_dq_kernel<kD, kHeadsOfFour>), grid, block, 0, s, a);
-    hipLaunchKernelGGL(attention_dkdv_kernel<kD>, keys, block, 0, s, b);
+        hipLaunchKernelGGL((attention_dq_kernel<kD, kHeadsOfFour, kBand>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((attention_dkdv_kernel<kD, kBand>), keys, block, 0, s, b);
+}
+
+template <int kD>
+void launch_backward(const LaunchShape &l, const AttentionArgs &a, const AttentionArgs &b, hipStream_t s) {
+    if (a.window < 0)
+        launch_backward_as<kD, false>(l, a, b, s);
+    else
+        launch_backward_as<kD, true>(l, a, b, s);
 }
 
 }  // namespace
