@@ -26,7 +26,6 @@ from ._abi import MIMO_BF16, MIMO_E_INVALID, MIMO_F32, MimoError
 _F32, _BF16, _I8, _I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
 _TYPES = {"f32": _F32, "bf16": _BF16}
 _CODES = {_F32: MIMO_F32, _BF16: MIMO_BF16}
-_empty = torch.empty
 _device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
@@ -48,48 +47,30 @@ def _refuse(message):
     raise MimoError(MIMO_E_INVALID, message)
 
 
-def _one_device(what, tensors):
-    """The GPU every tensor is on (the first is not None)."""
-    index = tensors[0].get_device()
-    if index >= 0:
-        for t in tensors:
-            if t is not None and t.get_device() != index:
-                break
-        else:
-            return index
+def _check_devices(what, tensors):
+    """Refuses tensors that are not all on one GPU, as the binding does."""
     _abi._check_device(tensors, what)
-    return index
+    _refuse(f"{what}: every tensor must be on one GPU")  # not reached: the callers have seen a difference
 
 
 @contextlib.contextmanager
-def _entered(index, stream, tensors):
-    with contextlib.ExitStack() as stack:
-        if index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(index))
+def _entered(what, index, stream, tensors):
+    """The context of a call that is not where torch is: the tensors' device
+    made current, and the caller's stream, if one is given, current and known
+    to the allocator as a user of the tensors.  The entry points call
+    themselves again inside it, without the stream."""
+    if stream is not None and stream.device.index != index:
+        _refuse(f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
+    with torch.cuda.device(index), contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         if stream is not None:
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-            stack.enter_context(torch.cuda.stream(stream))
         yield
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(what, index, stream, tensors):
-    """The context a call runs in: the tensors' device current, and the
-    caller's stream, if one is given, current and known to the allocator as a
-    user of the tensors."""
-    if stream is None:
-        return _HERE if _device_now() == index else _entered(index, None, ())
-    if stream.device.index != index:
-        _refuse(f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
-    return _entered(index, stream, tensors)
-
-
 def _check_vector(what, name, t, n, dtype):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         _refuse(f"{what}: {name} must be contiguous {dtype} [{n}], got {tuple(t.shape)} {t.dtype}")
 
 
@@ -108,14 +89,21 @@ def _pointer(t):
     return None if t is None else t.data_ptr()
 
 
+def _dense_like(t):
+    """An uninitialised dense tensor of t's shape, type and device (the quickest of torch's ways)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 # ------------------------------------------------------------------ attention
 
 def _heads(what, name, t, shape):
     """(pointer, row stride, head stride) of a bf16 [rows, heads, head_dim] tensor."""
-    if t.dtype != _BF16 or t.shape != shape:
-        _refuse(f"{what}: {name} must be bfloat16 {tuple(shape)} ([rows, heads, head_dim]), got {tuple(t.shape)} {t.dtype}")
-    row, head, inner = t.stride()
     rows, heads, dim = shape
+    if t.dtype is not _BF16 or t.shape != shape:
+        _refuse(f"{what}: {name} must be bfloat16 {tuple(shape)} ([rows, heads, head_dim]), got {tuple(t.shape)} {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim, dim
+    row, head, inner = t.stride()
     if inner != 1 and dim != 1:
         _refuse(f"{what}: {name}'s innermost axis must be dense, got strides {t.stride()}")
     # torch leaves the stride of an axis of one free: the library asks for a valid one
@@ -173,18 +161,23 @@ def chunk_attention(q, k, v, cu_seqlens, window=-1, scale=None, sink=None, out=N
     """
     what = "chunk_attention"
     sizes = _check_qkv(what, q, k, v, cu_seqlens, sink, lse)
+    index = q.get_device()
+    if (index < 0 or k.get_device() != index or v.get_device() != index or cu_seqlens.get_device() != index
+            or (sink is not None and sink.get_device() != index) or (out is not None and out.get_device() != index)
+            or (lse is not None and lse.get_device() != index)):
+        _heads(what, "q", q, q.shape)
+        if out is not None:
+            _heads(what, "out", out, q.shape)
+        _check_devices(what, (q, k, v, cu_seqlens, sink, out, lse))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (q, k, v, cu_seqlens, sink, out, lse)):
+            return chunk_attention(q, k, v, cu_seqlens, window, scale, sink, out, lse, return_lse)
     if out is None:
-        _heads(what, "q", q, q.shape)  # before anything is allocated for it
-    else:
-        _heads(what, "out", out, q.shape)
-    index = _one_device(what, (q, k, v, cu_seqlens, sink, out, lse))
-    with _on(what, index, stream, (q, k, v, cu_seqlens, sink, out, lse)):
-        if out is None:
-            out = _empty(q.shape, dtype=_BF16, device=q.device)
-        if return_lse and lse is None:
-            lse = _empty((sizes[1], sizes[0]), dtype=_F32, device=q.device)
-        code = _library().mimo_chunk_attention(_pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse),
-                                               _raw_stream(index))
+        out = _dense_like(q)
+    if return_lse and lse is None:
+        lse = q.new_empty((sizes[1], sizes[0]), dtype=_F32)
+    code = _library().mimo_chunk_attention(_pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse),
+                                           _raw_stream(index))
     if code:
         _abi._check(code, what)
     return (out, lse) if return_lse else out
@@ -215,25 +208,30 @@ def chunk_attention_backward(dout, q, k, v, out, lse, cu_seqlens, window=-1, sca
         _abi._check_bytes(workspace, what + ": workspace")
     args = _pack(what, sizes, q, k, v, cu_seqlens, window, scale, sink, out, lse)
     dout_heads = _heads(what, "dout", dout, q.shape)
+    index = q.get_device()
     tensors = (q, k, v, out, lse, cu_seqlens, sink, dout, dq, dk, dv, dsink, workspace)
-    index = _one_device(what, tensors)
-    with _on(what, index, stream, tensors):
-        dev = q.device
-        if dq is None:
-            dq = _empty(q.shape, dtype=_BF16, device=dev)
-        if dk is None:
-            dk = _empty(k.shape, dtype=_BF16, device=dev)
-        if dv is None:
-            dv = _empty(v.shape, dtype=_BF16, device=dev)
-        if dsink is None and sink is not None:
-            dsink = _empty(sizes[1], dtype=_F32, device=dev)
-        lib = _library()
-        if workspace is None:
-            need = lib.mimo_chunk_attention_workspace_bytes(*sizes, cu_seqlens.shape[0] - 1)
-            workspace = _empty(max(need, 16), dtype=torch.uint8, device=dev)
-        grads = _GRADS.pack(*dout_heads, *_heads(what, "dq", dq, q.shape), *_heads(what, "dk", dk, k.shape),
-                            *_heads(what, "dv", dv, v.shape), 0 if dsink is None else dsink.data_ptr())
-        code = lib.mimo_chunk_attention_backward(args, grads, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _check_devices(what, tensors)
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, tensors):
+            return chunk_attention_backward(dout, q, k, v, out, lse, cu_seqlens, window, scale, sink, dq, dk, dv, dsink,
+                                            workspace)
+    if dq is None:
+        dq = _dense_like(q)
+    if dk is None:
+        dk = _dense_like(k)
+    if dv is None:
+        dv = _dense_like(v)
+    if dsink is None and sink is not None:
+        dsink = torch.empty_like(sink)
+    lib = _library()
+    if workspace is None:
+        need = lib.mimo_chunk_attention_workspace_bytes(*sizes, cu_seqlens.shape[0] - 1)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
+    grads = _GRADS.pack(*dout_heads, *_heads(what, "dq", dq, q.shape), *_heads(what, "dk", dk, k.shape),
+                        *_heads(what, "dv", dv, v.shape), 0 if dsink is None else dsink.data_ptr())
+    code = lib.mimo_chunk_attention_backward(args, grads, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
     if code:
         _abi._check(code, what)
     return dq, dk, dv, dsink
@@ -287,17 +285,23 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
         dtype = out.dtype
     else:
         dtype = x.dtype if out_dtype is None else _out_type(what, out_dtype)
-    index = _one_device(what, (x, weight, bias, out, mean, rstd))
-    with _on(what, index, stream, (x, weight, bias, out, mean, rstd)):
-        if out is None:
-            out = _empty((rows, width), dtype=dtype, device=x.device)
-        if return_stats:
-            if mean is None:
-                mean = _empty(rows, dtype=_F32, device=x.device)
-            if rstd is None:
-                rstd = _empty(rows, dtype=_F32, device=x.device)
-        code = _library().mimo_layer_norm(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(weight), _pointer(bias), eps,
-                                          _CODES[dtype], out.data_ptr(), _pointer(mean), _pointer(rstd), _raw_stream(index))
+    index = x.get_device()
+    if (index < 0 or (weight is not None and weight.get_device() != index) or (bias is not None and bias.get_device() != index)
+            or (out is not None and out.get_device() != index) or (mean is not None and mean.get_device() != index)
+            or (rstd is not None and rstd.get_device() != index)):
+        _check_devices(what, (x, weight, bias, out, mean, rstd))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (x, weight, bias, out, mean, rstd)):
+            return layer_norm(x, weight, bias, eps, out, out_dtype, return_stats, mean, rstd)
+    if out is None:
+        out = torch.empty_like(x, dtype=dtype)
+    if return_stats:
+        if mean is None:
+            mean = x.new_empty(rows, dtype=_F32)
+        if rstd is None:
+            rstd = x.new_empty(rows, dtype=_F32)
+    code = _library().mimo_layer_norm(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(weight), _pointer(bias), eps,
+                                      _CODES[dtype], out.data_ptr(), _pointer(mean), _pointer(rstd), _raw_stream(index))
     if code:
         _abi._check(code, what)
     return (out, mean, rstd) if return_stats else out
@@ -335,24 +339,28 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, dx=None, dweight=None,
         _check_shape(what, "dx", dx, x.shape)
     if workspace is not None:
         _abi._check_bytes(workspace, what + ": workspace")
+    index = x.get_device()
     tensors = (x, dout, mean, rstd, weight, dx, dweight, dbias, workspace)
-    index = _one_device(what, tensors)
-    with _on(what, index, stream, tensors):
-        dev = x.device
-        if dx is None:
-            dx = _empty((rows, width), dtype=x.dtype, device=dev)
-        if weight is not None if affine is None else affine:
-            if dweight is None:
-                dweight = _empty(width, dtype=_F32, device=dev)
-            if dbias is None:
-                dbias = _empty(width, dtype=_F32, device=dev)
-        lib = _library()
-        if workspace is None and (dweight is not None or dbias is not None):
-            workspace = _empty(max(lib.mimo_layer_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8, device=dev)
-        code = lib.mimo_layer_norm_backward(
-            rows, width, x.data_ptr(), _CODES[x.dtype], dout.data_ptr(), _CODES[dout.dtype], _pointer(weight),
-            mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _pointer(dweight), _pointer(dbias), _pointer(workspace),
-            0 if workspace is None else workspace.numel(), _raw_stream(index))
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _check_devices(what, tensors)
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, tensors):
+            return layer_norm_backward(dout, x, mean, rstd, weight, dx, dweight, dbias, affine, workspace)
+    if dx is None:
+        dx = torch.empty_like(x)
+    if weight is not None if affine is None else affine:
+        if dweight is None:
+            dweight = x.new_empty(width, dtype=_F32)
+        if dbias is None:
+            dbias = x.new_empty(width, dtype=_F32)
+    lib = _library()
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = x.new_empty(max(lib.mimo_layer_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8)
+    code = lib.mimo_layer_norm_backward(
+        rows, width, x.data_ptr(), _CODES[x.dtype], dout.data_ptr(), _CODES[dout.dtype], _pointer(weight),
+        mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _pointer(dweight), _pointer(dbias), _pointer(workspace),
+        0 if workspace is None else workspace.numel(), _raw_stream(index))
     if code:
         _abi._check(code, what)
     return dx, dweight, dbias
@@ -382,14 +390,18 @@ def quantize_rows(x, q=None, scale=None, stream=None):
         _check_shape(what, "q", q, (rows, padded))
     if scale is not None:
         _check_vector(what, "scale", scale, rows, _F32)
-    index = _one_device(what, (x, q, scale))
-    with _on(what, index, stream, (x, q, scale)):
-        if q is None:
-            q = _empty((rows, padded), dtype=_I8, device=x.device)
-        if scale is None:
-            scale = _empty(rows, dtype=_F32, device=x.device)
-        code = _library().mimo_quantize_rows(rows, width, x.data_ptr(), _CODES[x.dtype], q.data_ptr(), scale.data_ptr(),
-                                             _raw_stream(index))
+    index = x.get_device()
+    if index < 0 or (q is not None and q.get_device() != index) or (scale is not None and scale.get_device() != index):
+        _check_devices(what, (x, q, scale))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (x, q, scale)):
+            return quantize_rows(x, q, scale)
+    if q is None:
+        q = x.new_empty((rows, padded), dtype=_I8)
+    if scale is None:
+        scale = x.new_empty(rows, dtype=_F32)
+    code = _library().mimo_quantize_rows(rows, width, x.data_ptr(), _CODES[x.dtype], q.data_ptr(), scale.data_ptr(),
+                                         _raw_stream(index))
     if code:
         _abi._check(code, what)
     return q, scale
@@ -421,13 +433,17 @@ def quantized_linear(xq, x_scale, wq, w_scale, bias=None, out=None, out_dtype: s
         dtype = out.dtype
     else:
         dtype = _out_type(what, out_dtype)
-    index = _one_device(what, (xq, x_scale, wq, w_scale, bias, out))
-    with _on(what, index, stream, (xq, x_scale, wq, w_scale, bias, out)):
-        if out is None:
-            out = _empty((rows, n), dtype=dtype, device=xq.device)
-        code = _library().mimo_quantized_linear(rows, k, xq.data_ptr(), x_scale.data_ptr(), n, wq.data_ptr(),
-                                                w_scale.data_ptr(), _pointer(bias), _CODES[dtype], out.data_ptr(),
-                                                _raw_stream(index))
+    index = xq.get_device()
+    if (index < 0 or x_scale.get_device() != index or wq.get_device() != index or w_scale.get_device() != index
+            or (bias is not None and bias.get_device() != index) or (out is not None and out.get_device() != index)):
+        _check_devices(what, (xq, x_scale, wq, w_scale, bias, out))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (xq, x_scale, wq, w_scale, bias, out)):
+            return quantized_linear(xq, x_scale, wq, w_scale, bias, out, out_dtype)
+    if out is None:
+        out = xq.new_empty((rows, n), dtype=dtype)
+    code = _library().mimo_quantized_linear(rows, k, xq.data_ptr(), x_scale.data_ptr(), n, wq.data_ptr(), w_scale.data_ptr(),
+                                            _pointer(bias), _CODES[dtype], out.data_ptr(), _raw_stream(index))
     if code:
         _abi._check(code, what)
     return out
