@@ -657,7 +657,8 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
  *   embed_dim  in [1, 2^24].
  *   out      device [n_rows][embed_dim] of out_dtype (MIMO_F32 or MIMO_BF16,
  *            rounded to nearest even), 16-byte aligned.
- * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE (k, embed_dim, more than
+ * 2^31 - 1 rows, or of 2^24 - 1 tiles of 128 x 128) or MIMO_E_HIP.
  */
 int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float *x_scale, int32_t embed_dim, const void *wq,
                           const float *w_scale, const float *bias, int32_t out_dtype, void *out, void *stream);

@@ -57,8 +57,8 @@ template <typename TX, typename TO, bool kRagged, int kThreads, int kChunks>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_kernel(NormArgs a) {
     __shared__ float lds[2][4];
     const int tid = threadIdx.x % kThreads;
-    const int64_t row = int64_t(blockIdx.x) * (kRowWgThreads / kThreads) + threadIdx.x / kThreads;
-    if (row >= a.rows) return;  // whole waves, and only where a wave is a row
+    const int64_t row = row_group() * (kRowWgThreads / kThreads) + threadIdx.x / kThreads;
+    if (row >= a.rows) return;  // all of the threads that hold a row
     const TX *x = static_cast<const TX *>(a.x) + row * a.width;
     auto column = [&](int i) { return (i * kThreads + tid) * 8; };
     float v[kChunks][8];
@@ -108,7 +108,8 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_kernel(NormArgs a) {
 template <typename TX, typename TO>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_wide_kernel(NormArgs a) {
     __shared__ float lds[2][4];
-    const int64_t row = blockIdx.x;
+    const int64_t row = row_group();
+    if (row >= a.rows) return;
     const TX *x = static_cast<const TX *>(a.x) + row * a.width;
     float sum = 0.0f;
     for (int c = threadIdx.x; c < a.width; c += kRowWgThreads) sum += float(x[c]);
@@ -223,7 +224,8 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(Norm
 template <typename TX, typename TG>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_wide_kernel(NormArgs a) {
     __shared__ float lds[2][4];
-    const int64_t row = blockIdx.x;
+    const int64_t row = row_group();
+    if (row >= a.rows) return;
     const TX *x = static_cast<const TX *>(a.x) + row * a.width;
     const TG *dout = static_cast<const TG *>(a.dout) + row * a.width;
     const float mean = a.mean[row], rstd = a.rstd[row], inv_n = 1.0f / float(a.width);
@@ -330,7 +332,7 @@ bool is_dtype(int32_t d) { return d == MIMO_F32 || d == MIMO_BF16; }
 template <typename TX, typename TO>
 void launch_forward(const Shape &s, const NormArgs &a, hipStream_t stream) {
     const dim3 block{unsigned(kRowWgThreads), 1, 1};
-    const dim3 grid{unsigned(s.threads == 64 ? (a.rows + 3) / 4 : a.rows), 1, 1};
+    const dim3 grid = row_grid(s.threads == 64 ? (a.rows + 3) / 4 : a.rows);
 #define MIMO_NORM(R, T, C)  \
     if (s.ragged == R && s.threads == T && s.chunks == C) {  \
         hipLaunchKernelGGL((layer_norm_kernel<TX, TO, R, T, C>), grid, block, 0, stream, a);    \
@@ -365,7 +367,7 @@ void launch_backward(const Shape &s, const NormArgs &a, int32_t groups, hipStrea
     MIMO_NORM(true, 256, 3)
     MIMO_NORM(true, 256, 8)
 #undef MIMO_NORM
-    hipLaunchKernelGGL((layer_norm_backward_wide_kernel<TX, TG>), dim3(unsigned(a.rows), 1, 1), block, 0, stream, a);
+    hipLaunchKernelGGL((layer_norm_backward_wide_kernel<TX, TG>), row_grid(a.rows), block, 0, stream, a);
     if (a.part)
         hipLaunchKernelGGL((layer_norm_columns_kernel<TX, TG>),
                            dim3(unsigned((a.width + kRowWgThreads - 1) / kRowWgThreads), unsigned(groups), 1), block, 0, stream, a);

@@ -31,7 +31,7 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kPadK = 128;          // quantised rows are multiples of this
 constexpr int kMaxK = 130944;       // 2^14 kMaxK < 2^31: no overflow, values of -128 included
-constexpr int kThreads = 256;
+constexpr int kThreads = kRowWgThreads;
 constexpr int kFewThreads = 512;
 
 struct QuantizeArgs {
@@ -70,7 +70,7 @@ template <typename T, bool kRagged, int kThreadsRow, int kChunks>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a) {
     __shared__ uint32_t lds[4];
     const int tid = threadIdx.x % kThreadsRow;
-    const int64_t row = int64_t(blockIdx.x) * (kThreads / kThreadsRow) + threadIdx.x / kThreadsRow;
+    const int64_t row = row_group() * (kThreads / kThreadsRow) + threadIdx.x / kThreadsRow;
     if (row >= a.rows) return;
     const T *x = static_cast<const T *>(a.x) + row * a.width;
     int8_t *q = a.q + row * a.padded;
@@ -456,7 +456,7 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
     auto launch = [&](auto type, auto ragged) {
         typedef decltype(type) T;
         constexpr bool R = decltype(ragged)::value;
-        const dim3 waves{unsigned((rows + 3) / 4), 1, 1}, groups{unsigned(rows), 1, 1};
+        const dim3 waves = row_grid((rows + 3) / 4), groups = row_grid(rows);
         if (a.padded <= 64 * 8)
             hipLaunchKernelGGL((quantize_rows_kernel<T, R, 64, 1>), waves, block, 0, s, a);
         else if (a.padded <= 64 * 8 * 3)
@@ -519,7 +519,7 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
     const bool few = m32 == 1 || m32 * n32 <= 256, big = !few && m256 * n256 >= 1024;
     const int64_t tiles = few ? m32 * n32 : big ? m256 * n256 : m128 * n128;
     a.n_tiles = int32_t(few ? n32 : big ? n256 : n128);
-    if (tiles > 0x7FFFFFFFll) return set_error(MIMO_E_TOO_LARGE, "quantized_linear: more than 2^31 - 1 tiles");
+    if (tiles > (int64_t(1) << 24) - 1) return set_error(MIMO_E_TOO_LARGE, "quantized_linear: more than 2^24 - 1 tiles");
     hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 grid{unsigned(tiles), 1, 1}, block{unsigned(few ? kFewThreads : kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {

@@ -13,6 +13,14 @@ namespace rows {
 
 constexpr int kRowWgThreads = 256;
 
+// Workgroups of a launch over rows, and the number of one: in two dimensions,
+// since a dimension of a launch has fewer than 2^32 threads.
+inline dim3 row_grid(int64_t groups) {
+    constexpr int64_t kWide = int64_t(1) << 20;
+    return groups <= kWide ? dim3(unsigned(groups), 1, 1) : dim3(unsigned(kWide), unsigned((groups + kWide - 1) / kWide), 1);
+}
+__device__ __forceinline__ int64_t row_group() { return int64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 // Eight values of a row as float32, from one or two 16-byte accesses.
 // kRagged: rows of any width at any address of the type (the accesses are
 // then aligned to the values only, which the hardware takes), with n of the

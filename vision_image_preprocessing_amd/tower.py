@@ -10,8 +10,8 @@ graph: each backward pass is a call of its own.
 
 A small call is bound by the host, so the checks are written to cost a few
 hundred nanoseconds: attributes compared in place, messages formed on failure
-only (one small image's norm: 10.7 us a call with a message closure and a
-device object for every check, against the figure in the design notes).
+only (one small image's norm, issued back to back: 5.9 us a call, against 10.7
+with a message closure and a device object for every check).
 """
 from __future__ import annotations
 
