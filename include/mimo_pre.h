@@ -525,7 +525,7 @@ typedef struct mimo_heads {
 } mimo_heads;
 
 typedef struct mimo_attention {
-    int64_t rows;       /* rows of every tensor, at most 2^30 */
+    int64_t rows;       /* rows of every tensor, at most 2^29 */
     int32_t q_heads;    /* a multiple of kv_heads, at most 65536 */
     int32_t kv_heads;
     int32_t head_dim;   /* a multiple of 8 in [8, MIMO_HEAD_DIM_MAX] */
@@ -552,7 +552,7 @@ typedef struct mimo_attention_grads {
  * boundary outside [0, rows] or a descending pair makes its chunk empty;
  * boundaries that make chunks overlap give undefined values in out.
  * out must not overlap an input.  One kernel launch.  Returns MIMO_OK,
- * MIMO_E_INVALID, MIMO_E_TOO_LARGE (more than 2^30 rows or chunks, or
+ * MIMO_E_INVALID, MIMO_E_TOO_LARGE (more than 2^29 rows or chunks, or
  * (rows / 128 + chunks + 1) * q_heads above 2^24 - 1) or MIMO_E_HIP.
  */
 int mimo_chunk_attention(const mimo_attention *args, void *stream);

@@ -216,6 +216,24 @@ def test_rows_that_see_nothing(V):
             _within(got, r[name], bar, f"{name} window {window}")
 
 
+def test_sinks_of_any_size(V):
+    """Sinks that take a row for themselves, and sinks that vanish."""
+    _say("sinks of any size")
+    cu_host, n = [0, 70, 200], 200
+    q, k, v, do, _ = _inputs(n, 6, 2, 64, 25, False)
+    sink = torch.tensor([-200.0, -50.0, 30.0, 95.0, 130.0, 600.0])
+    r = tower.chunk_attention(_wide(q), _wide(k), _wide(v), cu_host, -1, None, _wide(sink), _wide(do))
+    cu = torch.tensor(cu_host, dtype=torch.int32, device="cuda")
+    out, lse = V.chunk_attention(q.cuda(), k.cuda(), v.cuda(), cu, sink=sink.cuda(), return_lse=True)
+    grads = V.chunk_attention_backward(do.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse, cu, sink=sink.cuda())
+    rel, out_bar, lse_bar = _forward_bars(r, 64)
+    _within(out, r["out"], out_bar, "out")
+    _within(lse, r["lse"], lse_bar, "lse")
+    bars = _backward_bars(_wide(q), _wide(k), _wide(v), _wide(do), r, 0.125, rel, out_bar, 64)
+    for got, name, bar in zip(grads, ("dq", "dk", "dv", "dsink"), bars):
+        _within(got, r[name], bar, name)
+
+
 def test_strides_and_slices(V):
     """Slices of one packed projection, head-major tensors, a shared key head
     by a stride of zero, and gradients into slices: the same bits as dense ones."""

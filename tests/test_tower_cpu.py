@@ -36,7 +36,8 @@ BAD_ATTENTION = [
     (dict(d=136), V.MIMO_E_INVALID), (dict(scale=0.0), V.MIMO_E_INVALID), (dict(scale=-1.0), V.MIMO_E_INVALID),
     (dict(scale=float("nan")), V.MIMO_E_INVALID), (dict(scale=float("inf")), V.MIMO_E_INVALID),
     (dict(cu=0), V.MIMO_E_INVALID), (dict(cu=P + 2), V.MIMO_E_INVALID), (dict(sink=P + 1), V.MIMO_E_INVALID),
-    (dict(rows=(1 << 30) + 1), V.MIMO_E_TOO_LARGE), (dict(rows=1 << 30, hq=65536, hk=1), V.MIMO_E_TOO_LARGE),
+    (dict(rows=(1 << 29) + 1), V.MIMO_E_TOO_LARGE), (dict(rows=1 << 29, hq=65536, hk=1), V.MIMO_E_TOO_LARGE),
+    (dict(chunks=(1 << 29) + 1), V.MIMO_E_TOO_LARGE), (dict(rows=1 << 20, chunks=1 << 22, hq=4), V.MIMO_E_TOO_LARGE),
     (dict(q=(0, 256, 64)), V.MIMO_E_INVALID), (dict(q=(P + 8, 256, 64)), V.MIMO_E_INVALID),
     (dict(k=(P, 132, 64)), V.MIMO_E_INVALID), (dict(k=(P, 128, 60)), V.MIMO_E_INVALID),
     (dict(v=(P, 56, 64)), V.MIMO_E_INVALID), (dict(v=(P, 0, 64)), V.MIMO_E_INVALID),

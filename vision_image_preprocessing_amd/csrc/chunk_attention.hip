@@ -130,22 +130,28 @@ __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t
 }
 
 // Staged tiles.  Panel rows are 128 bytes, eight 16-byte chunks; chunk v of
-// row r lies at position v ^ (r ^ r / 8) % 8, so that the same chunk of eight
-// rows (operand reads) and half rows of eight rows (transposed reads) cover
-// every bank.  The swizzle is an exclusive or, so a lane needs few distinct
-// addresses, formed once; everything else is a constant offset.
+// row r lies at position v ^ row_key(r % 8) ^ block_key(r / 8).  A cycle of
+// LDS serves 256 bytes, two panel rows' worth of banks: 16 lanes of an operand
+// read, whose rows then differ by row and block, and 32 lanes of a transposed
+// read, half rows of four rows, whose keys then have to differ in their
+// highest bit between rows two apart (hence the exchange of bits 1 and 2; a
+// plain r ^ r / 8 measured two conflict cycles a transposed read).  All is an
+// exclusive or, so a lane needs few distinct addresses, formed once;
+// everything else is a constant offset.
+__device__ __forceinline__ constexpr int row_key(int r) { return (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1); }
+__device__ __forceinline__ constexpr int block_key(int g) { return g ^ ((g & 3) >> 1); }
 struct LdsAddress {
     int row[4];  // operand reads: chunk 2 s + l / 32 of row l % 32, by s ^ 2 (block)
-    int col[8];  // transposed reads, by chunk ^ row / 8
+    int col[8];  // transposed reads, by chunk ^ block_key
 };
 __device__ __forceinline__ LdsAddress lds_address() {
     const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
     LdsAddress a;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a.row[j] = l * 128 + (((h ^ ((l ^ (l >> 3)) & 7)) ^ (2 * j)) << 4);
+    for (int j = 0; j < 4; ++j) a.row[j] = l * 128 + ((h ^ row_key(l & 7) ^ block_key(l >> 3) ^ (2 * j)) << 4);
     const int x = 4 * h + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a.col[j] = x * 128 + ((c ^ x ^ j) << 4) + (lane & 1) * 8;
+    for (int j = 0; j < 8; ++j) a.col[j] = x * 128 + ((c ^ row_key(x) ^ j) << 4) + (lane & 1) * 8;
     return a;
 }
 
@@ -157,14 +163,14 @@ __device__ __forceinline__ bf16x8 read_rows(const uint8_t *lds, const LdsAddress
 // First operand, transposed: 32-column block d as its rows, over the 16
 // staged rows from 16 s in the order the header gives.
 __device__ __forceinline__ bf16x8 read_columns(const uint8_t *lds, const LdsAddress &a, int d, int s) {
-    const int c = (4 * (d & 1)) ^ (2 * s);
+    const int c = (4 * (d & 1)) ^ block_key(2 * s), c8 = (4 * (d & 1)) ^ block_key(2 * s + 1);
     const uint8_t *p = lds + (d / 2) * kPanelBytes + s * 16 * 128;
     union {
         s16x4 h[2];
         bf16x8 f;
     } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + a.col[c]));
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + a.col[c ^ 1] + 8 * 128));
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + a.col[c8] + 8 * 128));
     return u.f;
 }
 
@@ -200,7 +206,7 @@ struct Loader {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int n = i * 4 + wave, g = n % 8;
-            const int v = (lane & 7) ^ ((lane >> 3) ^ g);
+            const int v = (lane & 7) ^ row_key(lane >> 3) ^ block_key(g);
             off[i] = head_offset(t, g * 8 + (lane >> 3), (n / 8) * 64 + v * 8, head_dim);
         }
     }
@@ -562,7 +568,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
             for (int r = 0; r < 16; ++r) s[r] = uint32_t(from + row_of(r)) < seen.count ? s[r] : 0.0f;
         }
     };
-    if (min(len, window < 0 ? len : 2 * window + 1) <= kFewKeys) {
+    if (len <= kFewKeys || (window >= 0 && window <= (kFewKeys - 1) / 2)) {
         auto sums = [&](int k0, int n) __attribute__((always_inline)) {
             if (r0 >= len || !any_visible(r0, k0, kStep, window)) return;
             const bool all = all_visible(r0, k0, kStep, len, window);
@@ -863,7 +869,7 @@ LaunchShape launch_shape(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_
     return r;
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxRows = int64_t(1) << 29;  // a row plus twice the window fits an int
 constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxRowStride = int64_t(1) << 22;  // a 64-row tile's byte offsets stay below 2^31
 
@@ -891,7 +897,7 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
         return set_error(MIMO_E_INVALID, w() + ": head_dim must be a multiple of 8 in [8, 128]");
     if (!(p->scale >= 1e-18f && p->scale <= 1e18f)) return set_error(MIMO_E_INVALID, w() + ": scale must be in [1e-18, 1e18]");
     if (p->rows > kMaxRows || p->chunks > kMaxRows)
-        return set_error(MIMO_E_TOO_LARGE, w() + ": more than 2^30 rows or chunks");
+        return set_error(MIMO_E_TOO_LARGE, w() + ": more than 2^29 rows or chunks");
     std::memset(&a, 0, sizeof(a));
     a.rows = p->rows;
     a.q_heads = p->q_heads;
