@@ -597,7 +597,8 @@ int mimo_chunk_attention_backward(const mimo_attention *args, const mimo_attenti
  *   weight, bias  device float32 [width], either may be NULL (ones, zeros).
  *   eps      finite, >= 0.  (A row of equal values has rstd = 1 / sqrt(eps).)
  *   out      device, out_dtype; may be x where the dtypes agree.
- *   mean, rstd    device float32 [rows], or NULL: the backward pass takes them.
+ *   mean, rstd    device float32 [rows], or NULL: the backward pass takes them;
+ *            not one array.
  * Pointers are aligned to their values.  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_TOO_LARGE (width, or more than 2^31 - 1 rows) or MIMO_E_HIP.
  */
@@ -612,12 +613,13 @@ size_t mimo_layer_norm_workspace_bytes(int64_t rows, int32_t width);
  *   dx = rstd (g - sum g / n - xh sum(g xh) / n)    (x's dtype)
  *   dweight = sum over rows of dout xh,  dbias = sum over rows of dout
  * dweight and dbias are device float32 [width], either may be NULL; they are
- * overwritten, and their sums have a fixed order.  dx must not be x or dout.
+ * overwritten, and their sums have a fixed order; not one array.  dx must not
+ * be x or dout.
  *   workspace  device, >= mimo_layer_norm_workspace_bytes(rows, width), 16-byte
  *              aligned, or NULL if both sums are; calls that may run at the
  *              same time need one each.
- * One kernel launch, and one for the sums (two for widths above 16384).  Returns MIMO_OK, MIMO_E_INVALID,
- * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ * One kernel launch, and one for the sums (two for widths above 16384).
+ * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
  */
 int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *dout, int32_t dout_dtype,
                              const float *weight, const float *mean, const float *rstd, void *dx, float *dweight,
@@ -639,7 +641,7 @@ int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t
  *   width    in [1, 130944].
  *   x        device, x_dtype (MIMO_F32 or MIMO_BF16), dense, aligned to its values.
  *   q        device int8 [rows][padded], padded = width rounded up to a
- *            multiple of 128 (the rest is set to zero), 16-byte aligned.
+ *            multiple of 128 (the rest is set to zero), 16-byte aligned, not x.
  *   scale    device float32 [rows].
  * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE (width, or more than
  * 2^31 - 1 rows) or MIMO_E_HIP.
@@ -656,7 +658,7 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
  *            [embed_dim] or NULL.
  *   embed_dim  in [1, 2^24].
  *   out      device [n_rows][embed_dim] of out_dtype (MIMO_F32 or MIMO_BF16,
- *            rounded to nearest even), 16-byte aligned.
+ *            rounded to nearest even), 16-byte aligned, not an input.
  * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE (k, embed_dim, more than
  * 2^31 - 1 rows, or of 2^24 - 1 tiles of 128 x 128) or MIMO_E_HIP.
  */

@@ -70,6 +70,11 @@ def test_attention_backward_refuses(bad):
     assert V.load().mimo_chunk_attention_backward(_attention(), _grads(**bad), P, 1 << 40, None) == V.MIMO_E_INVALID
 
 
+def test_attention_backward_refuses_the_sink_as_its_gradient():
+    # workgroups that read the sink run next to the ones that write dsink
+    assert V.load().mimo_chunk_attention_backward(_attention(sink=P), _grads(dsink=P), P, 1 << 40, None) == V.MIMO_E_INVALID
+
+
 def test_attention_backward_workspace_and_nulls():
     lib = V.load()
     need = V.chunk_attention_workspace_bytes(10, 4, 2, 64, 1)
@@ -94,12 +99,12 @@ def test_norm_refuses():
     lib = V.load()
     F, B = V.MIMO_F32, V.MIMO_BF16
 
-    def forward(rows=4, width=64, x=P, xd=F, w=P, b=P, eps=1e-6, od=F, out=2 * P, mean=P, rstd=P):
+    def forward(rows=4, width=64, x=P, xd=F, w=P, b=P, eps=1e-6, od=F, out=2 * P, mean=P, rstd=4 * P):
         return lib.mimo_layer_norm(rows, width, x, xd, w, b, eps, od, out, mean, rstd, None)
 
     for bad in (dict(rows=-1), dict(width=0), dict(xd=2), dict(od=-1), dict(eps=-1.0), dict(eps=float("nan")),
                 dict(eps=float("inf")), dict(x=None), dict(out=None), dict(x=P + 2), dict(xd=B, x=P + 1), dict(out=P + 2),
-                dict(w=P + 1), dict(b=P + 2), dict(mean=P + 1), dict(rstd=P + 2), dict(out=P, od=B)):
+                dict(w=P + 1), dict(b=P + 2), dict(mean=P + 1), dict(rstd=P + 2), dict(out=P, od=B), dict(rstd=P)):
         assert forward(**bad) == V.MIMO_E_INVALID, bad
     assert forward(width=65537) == V.MIMO_E_TOO_LARGE and forward(rows=1 << 31) == V.MIMO_E_TOO_LARGE
     assert forward(rows=0, x=None, out=None) == V.MIMO_OK
@@ -107,12 +112,13 @@ def test_norm_refuses():
     need = V.layer_norm_workspace_bytes(4, 64)
     assert need >= 2 * 64 * 4 and V.layer_norm_workspace_bytes(-1, 64) == 0 and V.layer_norm_workspace_bytes(4, 65537) == 0
 
-    def backward(rows=4, width=64, x=P, xd=F, g=2 * P, gd=F, w=P, mean=P, rstd=P, dx=3 * P, dw=P, db=P, ws=P, n=need):
+    def backward(rows=4, width=64, x=P, xd=F, g=2 * P, gd=F, w=P, mean=P, rstd=P, dx=3 * P, dw=P, db=4 * P, ws=P, n=need):
         return lib.mimo_layer_norm_backward(rows, width, x, xd, g, gd, w, mean, rstd, dx, dw, db, ws, n, None)
 
     for bad in (dict(rows=-1), dict(width=0), dict(xd=7), dict(gd=2), dict(x=None), dict(g=None), dict(mean=None),
                 dict(rstd=None), dict(dx=None), dict(dx=P), dict(dx=2 * P), dict(dw=P + 2), dict(db=P + 1), dict(ws=None),
-                dict(ws=P + 8), dict(x=P + 2), dict(gd=B, g=P + 1), dict(w=P + 2), dict(mean=P + 2)):
+                dict(ws=P + 8), dict(x=P + 2), dict(gd=B, g=P + 1), dict(w=P + 2), dict(mean=P + 2),
+                dict(db=P)):
         assert backward(**bad) == V.MIMO_E_INVALID, bad
     assert backward(n=need - 1) == V.MIMO_E_CAPACITY
     assert backward(width=65537) == V.MIMO_E_TOO_LARGE
@@ -122,21 +128,21 @@ def test_norm_refuses():
 def test_quantized_refuses():
     lib = V.load()
 
-    def quantize(rows=4, width=64, x=P, d=V.MIMO_F32, q=P, s=P):
+    def quantize(rows=4, width=64, x=P, d=V.MIMO_F32, q=2 * P, s=P):
         return lib.mimo_quantize_rows(rows, width, x, d, q, s, None)
 
     for bad in (dict(rows=-1), dict(width=0), dict(d=2), dict(x=None), dict(q=None), dict(s=None), dict(x=P + 2),
-                dict(x=P + 1, d=V.MIMO_BF16), dict(q=P + 8), dict(s=P + 2)):
+                dict(x=P + 1, d=V.MIMO_BF16), dict(q=P + 8), dict(s=P + 2), dict(q=P)):
         assert quantize(**bad) == V.MIMO_E_INVALID, bad
     assert quantize(width=130945) == V.MIMO_E_TOO_LARGE and quantize(rows=1 << 31) == V.MIMO_E_TOO_LARGE
     assert quantize(rows=0, x=None) == V.MIMO_OK
 
-    def linear(rows=4, k=128, x=P, xs=P, e=8, w=P, ws=P, b=P, d=V.MIMO_F32, out=P):
+    def linear(rows=4, k=128, x=P, xs=P, e=8, w=2 * P, ws=P, b=P, d=V.MIMO_F32, out=3 * P):
         return lib.mimo_quantized_linear(rows, k, x, xs, e, w, ws, b, d, out, None)
 
     for bad in (dict(rows=-1), dict(k=0), dict(k=64), dict(k=130), dict(e=0), dict(d=2), dict(x=None), dict(xs=None),
                 dict(w=None), dict(ws=None), dict(out=None), dict(x=P + 8), dict(w=P + 8), dict(out=P + 8), dict(b=P + 2),
-                dict(xs=P + 2), dict(ws=P + 1)):
+                dict(xs=P + 2), dict(ws=P + 1), dict(out=P), dict(out=2 * P)):
         assert linear(**bad) == V.MIMO_E_INVALID, bad
     assert linear(k=131072) == V.MIMO_E_TOO_LARGE and linear(e=(1 << 24) + 1) == V.MIMO_E_TOO_LARGE
     assert linear(rows=0, x=None, out=None) == V.MIMO_OK

@@ -661,8 +661,9 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // and the rows in the band, in a fixed order, into registers; or a slice of
 // them, as float32 partial sums, where there are too few tiles for the CUs.
 // The products' accumulators start from -lse / scale and -delta of their
-// row, so that the exponent and dp - delta need no further operation.  (Rows
-// behind the chunk read as zeros: their p is not, but q and do are.)
+// row, so that the exponent and dp - delta need no further operation.  Rows
+// behind the chunk read as zeros, and a block that holds any is masked, so
+// that their p is zero too, however large a sink makes it.
 template <int kD, bool kBand>
 __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : 2) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
@@ -1031,6 +1032,7 @@ int mimo_chunk_attention_backward(const mimo_attention *p, const mimo_attention_
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (g->dsink && (!p->sink && a.rows && a.chunks))
         return set_error(MIMO_E_INVALID, std::string(who) + ": dsink is given without sink");
+    if (g->dsink && g->dsink == p->sink) return set_error(MIMO_E_INVALID, std::string(who) + ": dsink must not be sink");
     if (a.rows && a.chunks) {
         if ((st = check_heads(p->out, who, "out", p->rows, p->q_heads, p->head_dim, false)) != MIMO_OK) return st;
         if ((st = check_heads(g->dout, who, "dout", p->rows, p->q_heads, p->head_dim, false)) != MIMO_OK) return st;

@@ -400,6 +400,7 @@ int mimo_layer_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype,
     if (!x || !out || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(out, out_dtype == MIMO_F32 ? 4 : 2) ||
         !check_ptr_align(weight, 4) || !check_ptr_align(bias, 4) || !check_ptr_align(mean, 4) || !check_ptr_align(rstd, 4))
         return set_error(MIMO_E_INVALID, "layer_norm: null or misaligned pointer (each aligned to its values)");
+    if (mean && mean == rstd) return set_error(MIMO_E_INVALID, "layer_norm: mean and rstd must not be one array");
     if (out == x && x_dtype != out_dtype)
         return set_error(MIMO_E_INVALID, "layer_norm: out may be x only in x's dtype");
     NormArgs a;
@@ -449,6 +450,7 @@ int mimo_layer_norm_backward(int64_t rows, int32_t width, const void *x, int32_t
     if (rows == 0 && !sums) return MIMO_OK;
     if (!check_ptr_align(dweight, 4) || !check_ptr_align(dbias, 4))
         return set_error(MIMO_E_INVALID, "layer_norm_backward: dweight and dbias must be 4-byte aligned");
+    if (dweight && dweight == dbias) return set_error(MIMO_E_INVALID, "layer_norm_backward: dweight and dbias must not be one array");
     if (rows > 0) {
         if (!x || !dout || !mean || !rstd || !dx || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) ||
             !check_ptr_align(dx, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(dout, dout_dtype == MIMO_F32 ? 4 : 2) ||

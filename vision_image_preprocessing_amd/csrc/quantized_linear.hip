@@ -459,6 +459,7 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
     if (rows == 0) return MIMO_OK;
     if (!x || !q || !scale || !check_ptr_align(x, x_dtype == MIMO_F32 ? 4 : 2) || !check_ptr_align(q, 16) || !check_ptr_align(scale, 4))
         return set_error(MIMO_E_INVALID, "quantize_rows: null or misaligned pointer (x to its values, q 16 bytes, scale 4)");
+    if (q == x) return set_error(MIMO_E_INVALID, "quantize_rows: q must not be x");
     QuantizeArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = x;
@@ -513,6 +514,7 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
     if (!xq || !x_scale || !wq || !w_scale || !out || !check_ptr_align(xq, 16) || !check_ptr_align(wq, 16) || !check_ptr_align(out, 16) ||
         !check_ptr_align(x_scale, 4) || !check_ptr_align(w_scale, 4) || !check_ptr_align(bias, 4))
         return set_error(MIMO_E_INVALID, "quantized_linear: null or misaligned pointer (xq, wq, out: 16 bytes; scales and bias: 4)");
+    if (out == xq || out == wq) return set_error(MIMO_E_INVALID, "quantized_linear: out must not be an input");
     LinearArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = static_cast<const int8_t *>(xq);
