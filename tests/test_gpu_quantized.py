@@ -2,7 +2,7 @@
 
 quantize_rows is defined by float32 operations, each rounded correctly, so its
 outputs are compared bit for bit.  The product's sum is exact; the result is
-float32(sum) * float32(s t) + bias: three roundings of e = 2^-24 of the
+(float32(sum) * s) * t + bias: at most three roundings of e = 2^-24 of the
 product, one of the sum with the bias, and the output's (u = 2^-8 for bf16, e
 for float32): bar = 3.01 e |sum s t| + e (|out| + |sum s t|) + u |out|.
 """
@@ -129,6 +129,37 @@ def test_longest_sums(V):
     out = V.quantized_linear(x.cuda(), one, w.cuda(), one, out_dtype="f32").cpu().double()
     want = torch.tensor([[127 * 127, -127 * 128], [-127 * 128, 128 * 128]], dtype=torch.float64) * k
     assert (out == want.float().double()).all()
+
+
+@pytest.mark.parametrize("out_kind", ["f32", "bf16"])
+def test_a_row_does_not_depend_on_the_others(V, out_kind):
+    """The same rows in calls of 1, 40, 300, 3000 and 70000 rows: the same bits."""
+    _say("rows alone and together", out_kind)
+    g = torch.Generator().manual_seed(7)
+    xq = torch.randint(-127, 128, (70000, 256), generator=g, dtype=torch.int8).cuda()
+    wq = torch.randint(-127, 128, (1283, 256), generator=g, dtype=torch.int8).cuda()
+    xs, ws, b = torch.rand(70000, generator=g).cuda(), torch.rand(1283, generator=g).cuda(), torch.randn(1283, generator=g).cuda()
+    whole = V.quantized_linear(xq, xs, wq, ws, b, out_dtype=out_kind)
+    for m in (1, 40, 300, 3000):
+        assert torch.equal(V.quantized_linear(xq[:m], xs[:m], wq, ws, b, out_dtype=out_kind), whole[:m]), m
+
+
+@pytest.mark.parametrize("m", [2, 2000])
+def test_scales_whose_product_leaves_the_range(V, m):
+    """2^-100 with 2^-40, and 2^60 with 2^80 on sums of zero: the product of the
+    scales alone is subnormal or infinite, the results are not.  Powers of two
+    and sums below 2^24: exact."""
+    _say("extreme scales", m)
+    g = torch.Generator().manual_seed(8)
+    xq = torch.randint(-127, 128, (m, 128), generator=g, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (300, 128), generator=g, dtype=torch.int8)
+    xq[1] = 0
+    xs, ws = torch.full((m,), 2.0 ** -100), torch.full((300,), 2.0 ** -40)
+    xs[1] = 2.0 ** 60
+    wq[5], ws[5], ws[6] = 0, 2.0 ** 80, 2.0 ** -30
+    want = (xq.double() @ wq.double().T) * xs.double()[:, None] * ws.double()
+    out = V.quantized_linear(xq.cuda(), xs.cuda(), wq.cuda(), ws.cuda(), out_dtype="f32").cpu()
+    assert torch.isfinite(want.float()).all() and torch.equal(out, want.float())
 
 
 def test_rows_that_are_not_finite(V):

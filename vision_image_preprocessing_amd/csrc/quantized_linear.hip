@@ -7,7 +7,11 @@
 // channels.  quantized_linear: with rows' scales s_r and channels' scales t_e,
 //   out[r][e] = (sum_k xq[r][k] wq[e][k]) s_r t_e + bias[e]
 // The sum is exact: products of 8-bit integers on v_mfma_i32_32x32x32_i8 into
-// 32-bit integers, which 2^17 of them cannot overflow.
+// 32-bit integers, which 2^17 of them cannot overflow.  It is rounded to
+// float32, multiplied by s_r, and then by t_e with the bias added in one
+// operation, in every kernel here: a row's result does not depend on how many
+// rows it comes with.  (The product of the two scales alone could leave
+// float32's range where the result does not.)
 //
 // Quantised rows are padded with zeros to a multiple of 128 bytes: rows of
 // whole 128-byte K steps, so the product needs no tail in K.
@@ -436,9 +440,7 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(LinearArgs a) {
         int32_t sum = 0;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) sum += part[i][r][l];
-        float v = float(sum) * (s * a.w_scale[e]);
-        if (a.bias) v += a.bias[e];
-        out[e] = OutT(v);
+        out[e] = OutT(fmaf(float(sum) * s, a.w_scale[e], a.bias ? a.bias[e] : 0.0f));
     }
 }
 
