@@ -262,40 +262,34 @@ __device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Values 8 g .. 8 g + 7 of a [32 columns][32 rows] block d, times mul, to
-// rows of a head: the halves exchange groups of four so that each lane
-// stores eight columns.
-__device__ __forceinline__ void store_columns(const Heads &t, int64_t row, int head, int left, int head_dim, int d, int g,
-                                              const float (&v)[8], float mul) {
-    const int lane = threadIdx.x & 63;
-    uint16_t *p = t.p + (row + (lane & 31)) * t.row + head * t.head;
-    union {
-        __bf16 h[8];
-        uint32_t w[4];
-    } a;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a.h[e] = __bf16(v[e] * mul);
-    // words 0, 1: columns 8 (2 g) + 4 (lane / 32) on; words 2, 3: eight
-    // further; the low half takes both parts of the first, the high half of
-    // the second
-    const auto x = __builtin_amdgcn_permlane32_swap(a.w[0], a.w[2], false, false);
-    const auto y = __builtin_amdgcn_permlane32_swap(a.w[1], a.w[3], false, false);
-    const u32x4 w = {x[0], y[0], x[1], y[1]};
-    const int col = d * 32 + 16 * g + 8 * (lane >> 5);
-    if ((lane & 31) < left && col < head_dim) *reinterpret_cast<u32x4 *>(p + col) = w;
-}
+// The lane's number, counted: behind a long loop that is cheaper than keeping
+// threadIdx.x through it, which has spilled a register.
+__device__ __forceinline__ int lane_again() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0)); }
 
+// [32 columns][32 rows] blocks, times mul, to rows of a head: the halves
+// exchange groups of four values so that each lane stores eight columns.
+// Stores past the chunk's rows or head_dim go past the resource, which drops
+// them.
 template <int kBlocks>
 __device__ __forceinline__ void store_rows(const Heads &t, int64_t row, int head, int left, int head_dim, const f32x16 (&o)[kBlocks],
                                            float mul) {
+    const int lane = lane_again();
+    const __amdgpu_buffer_rsrc_t rsrc = head_rsrc(t, row, head, left, head_dim);
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            float v[8];
+            bf16x8 v;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = o[d][8 * g + e];
-            store_columns(t, row, head, left, head_dim, d, g, v, mul);
+            for (int e = 0; e < 8; ++e) v[e] = __bf16(o[d][8 * g + e] * mul);
+            const u32x4 a = __builtin_bit_cast(u32x4, v);
+            // words 0, 1: columns 8 (2 g) + 4 (lane / 32) on; words 2, 3:
+            // eight further; the low half takes both parts of the first, the
+            // high half of the second
+            const auto x = __builtin_amdgcn_permlane32_swap(a[0], a[2], false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(a[1], a[3], false, false);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], y[0], x[1], y[1]}, rsrc,
+                                                   head_offset(t, lane & 31, d * 32 + 16 * g + 8 * (lane >> 5), head_dim), 0, 0);
         }
 }
 
@@ -322,16 +316,41 @@ __device__ __forceinline__ bool all_visible(int r, int k, int n, int len, int wi
 // rows that the upper half-wave is further down.
 __device__ __forceinline__ constexpr int row_of(int r) { return 8 * (r >> 2) + (r & 3); }
 
-// The keys a row sees (or rows that see a key), as first + [0, count): one
-// subtraction and one unsigned comparison tell whether another is in it.
+// The keys a row sees (or rows that see a key): [first, end).
 struct Seen {
-    int first;
-    uint32_t count;
+    int first, end;
 };
 __device__ __forceinline__ Seen seen_by(int row, int len, int window) {
     const int first = window < 0 ? 0 : max(0, row - window);
     const int end = window < 0 ? len : min(len, row + window + 1);
-    return Seen{first, uint32_t(max(end - first, 0))};
+    return Seen{first, max(first, end)};
+}
+
+// Which of a block's 32 keys from k on those are: bit row_of(r) for value r of
+// the lane.  A value is then masked by two operations without a condition
+// register: its bit, spread over a word, selects (three with one, and a wait
+// between them).
+__device__ __forceinline__ uint32_t seen_bits(const Seen &seen, int k) {
+    auto below = [](int n) { return uint32_t(1ull << max(0, min(32, n))); };  // 2^n, modulo 2^32
+    return (below(seen.end - k) - below(seen.first - k)) >> (4 * ((threadIdx.x & 63) >> 5));
+}
+__device__ __forceinline__ float seen_or_none(uint32_t bits, int r, float v) {
+    const uint32_t all = uint32_t(__builtin_amdgcn_sbfe(int(bits), row_of(r), 1));
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, v) & all) | (__builtin_bit_cast(uint32_t, -INFINITY) & ~all));
+}
+
+// A block's logits of keys that are not seen become -inf: the band's.
+__device__ __forceinline__ void mask_band(const Seen &seen, int k, f32x16 &s) {
+    const uint32_t bits = seen_bits(seen, k);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = seen_or_none(bits, r, s[r]);
+}
+// Values of keys behind the chunk become `other`: all there is to mask without
+// a band, and only at the chunk's end, where fewer registers count for more.
+__device__ __forceinline__ void mask_end(int len, int k, float other, f32x16 &s) {
+    const int left = len - k - 4 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = row_of(r) < left ? s[r] : other;
 }
 
 // How the kernels over query rows are laid out, four waves of 32 rows that
@@ -440,20 +459,13 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
             s[b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) s[b] = mfma(read_rows(tk, at, b, i), q[i], s[b]);
-            if (b == 0 && k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
-            if (kBand && !all_visible(r0, k0 + 32 * b, 32, len, window)) {
-                const int from = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = uint32_t(from + row_of(r)) < seen.count ? s[b][r] : -INFINITY;
-            }
+            if (kBand && !all_visible(r0, k0 + 32 * b, 32, len, window)) mask_band(seen, k0 + 32 * b, s[b]);
         }
         if (!kBand && k0 + kStep > len) {
-            const int left = len - k0 - 4 * (lane >> 5);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = 32 * b + row_of(r) < left ? s[b][r] : -INFINITY;
+            for (int b = 0; b < 2; ++b) mask_end(len, k0 + 32 * b, -INFINITY, s[b]);
         }
+        if (k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
         float m = s[0][0];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -493,8 +505,8 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
     sum = sum_halves(sum);
     if (r0 >= len) return;
     store_rows<kBlocks>(a.out, tile.begin + r0, head, len - r0, a.head_dim, o, sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f);
-    if (a.lse && lane < 32 && row < len)
-        a.lse[int64_t(head) * a.rows + tile.begin + row] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
+    if (a.lse && lane_again() < min(32, len - r0))
+        (a.lse + int64_t(head) * a.rows + tile.begin + r0)[lane_again()] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
 }
 
 // dq, delta and the sink's partial sums: the forward kernel's shape, with the
@@ -560,13 +572,11 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(tv, at, b, i), g[i], dp);
         if (b == 0 && k0 == 0 && a.sink) s[0] += lane < 32 ? sink : 0.0f;
+        const bool masked = !all && !all_visible(r0, k0 + 32 * b, 32, len, window);
+        if (kBand && masked) mask_band(seen, k0 + 32 * b, s);
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2));
-        if (!all && !all_visible(r0, k0 + 32 * b, 32, len, window)) {
-            const int from = k0 + 32 * b + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = uint32_t(from + row_of(r)) < seen.count ? s[r] : 0.0f;
-        }
+        if (!kBand && masked) mask_end(len, k0 + 32 * b, 0.0f, s);
     };
     if (len <= kFewKeys || (window >= 0 && window <= (kFewKeys - 1) / 2)) {
         auto sums = [&](int k0, int n) __attribute__((always_inline)) {
@@ -665,8 +675,13 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // behind the chunk read as zeros, and a block that holds any is masked, so
 // that their p is zero too, however large a sink makes it.
 template <int kD, bool kBand>
-__global__ __launch_bounds__(kThreads, kD == 128 ? 1 : 2) void attention_dkdv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, kD == 128 ? 1 : kD == 64 ? 3 : 2) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
+    // The chunk's end is masked in the logits, or, where the registers are
+    // full anyway, in the probabilities, as the compiler allots them better
+    // (8 of 4096 rows, 32 heads of 64: 2.00 ms against 2.04 with spills; both
+    // passes over 2 of 4096, 16 heads of 128: 0.94 ms against 1.01).
+    constexpr bool kMaskLast = kD == 128;
     __shared__ __attribute__((aligned(16))) uint8_t sq0[kPanels * kPanelBytes], sq1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) uint8_t sg0[kPanels * kPanelBytes], sg1[kPanels * kPanelBytes];
     __shared__ __attribute__((aligned(16))) float sl0[2][kStep], sl1[2][kStep];  // -lse / scale, -delta
@@ -736,13 +751,12 @@ __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : 2) void attention_dkdv_ke
             for (int i = 0; i < kSteps; ++i) s = mfma(read_rows(tq, at, b, i), k[i], s);
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) dp = mfma(read_rows(tg, at, b, i), v[i], dp);
+            const bool masked = !all_visible(c0, rb, 32, len, window);
+            if (kBand && masked) mask_band(seen, rb, s);
+            if (!kBand && !kMaskLast && masked) mask_end(len, rb, -INFINITY, s);
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, kb));
-            if (!all_visible(c0, rb, 32, len, window)) {
-                const int off = rb + 4 * (lane >> 5) - seen.first;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = uint32_t(off + row_of(r)) < seen.count ? s[r] : 0.0f;
-            }
+            if (!kBand && kMaskLast && masked) mask_end(len, rb, 0.0f, s);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bf16x8 p = pack(s, i);
@@ -794,14 +808,15 @@ __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : 2) void attention_dkdv_ke
         store_rows<kBlocks>(a.dv, tile.begin + c0, kv, len - c0, a.head_dim, dv, 1.0f);
         return;
     }
-    if (key >= len) return;
+    const int last_lane = lane_again(), r = last_lane & 31;
+    if (r >= len - c0) return;
     const int64_t plane = int64_t(a.kv_heads) * a.rows * a.head_dim;
-    float *p = a.part + 2 * slice * plane + (int64_t(kv) * a.rows + tile.begin + key) * a.head_dim;
+    float *p = a.part + 2 * slice * plane + (int64_t(kv) * a.rows + tile.begin + c0) * a.head_dim + r * a.head_dim;
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int col = d * 32 + 8 * g + 4 * (lane >> 5);
+            const int col = d * 32 + 8 * g + 4 * (last_lane >> 5);
             if (col >= a.head_dim) continue;
             *reinterpret_cast<f32x4 *>(p + col) = f32x4{dk[d][4 * g], dk[d][4 * g + 1], dk[d][4 * g + 2], dk[d][4 * g + 3]};
             *reinterpret_cast<f32x4 *>(p + plane + col) = f32x4{dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
