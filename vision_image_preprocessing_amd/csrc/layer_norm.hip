@@ -38,7 +38,6 @@ namespace {
 using namespace rows;
 
 constexpr int kMaxWidth = 65536;
-constexpr int kMaxGroups = 1024;   // workgroups of the backward pass, and partial sums of each column
 constexpr int kSumColumns = 32, kSumParts = 32;  // of the reduction kernel's workgroup
 
 struct NormArgs {
@@ -324,12 +323,18 @@ Shape backward_shape(int32_t width, bool aligned) {
 }
 
 // Workgroups of the backward kernel, each of which adds up every so many
-// rows: more of them hide memory better, but each writes partial sums
-// (131072 x 1280 bf16, sums included: 512 workgroups 365 us, 1024 222, 2048 249).
+// rows, and partial sums of each column: as many as the card holds at once by
+// their registers (four a CU with one chunk, three with three, one with eight).
+// Fewer leave memory waiting, more run in a second round and write more sums.
+// us, sums included, for 256, 512, 768, 1024 and 2048 of them: 131072 x 1280
+// bf16 663, 366, 270, 230, 249; 32768 x 5120 bf16 456, 302, 235, 313, 283;
+// 16384 x 12288 bf16 553, 572, 579, 596, 647; with rows in a wave, which end in
+// LDS, 262144 x 512 bf16 280, 168, 145, 154, 171.
 int32_t backward_groups(int64_t rows, int32_t width) {
     const int64_t per = width <= 64 * 8 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
-    return int32_t(groups < kMaxGroups ? groups : kMaxGroups);
+    const int64_t most = width <= 64 * 8 ? 768 : width <= 256 * 8 ? 1024 : width <= 256 * 8 * 3 ? 768 : 256;
+    return int32_t(groups < most ? groups : most);
 }
 
 bool is_dtype(int32_t d) { return d == MIMO_F32 || d == MIMO_BF16; }
