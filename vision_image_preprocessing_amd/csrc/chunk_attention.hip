@@ -360,8 +360,9 @@ __device__ __forceinline__ void mask_end(int len, int k, float other, f32x16 &s)
 //     the same keys, so a band costs them 32 + 2 window keys, not 128 + 2
 //     window (band of 64 over 32 x 3520 rows: 382 us against 471).
 // Sharing out a row's keys among waves, to be joined at the end, was measured
-// for calls that leave CUs idle, and gained nothing that a call shows (12
-// heads of 2000 rows: 33 us against 31; 32 heads of 216 rows: 7.8 against 8.2).
+// for calls that leave CUs idle, and gained nothing that a call shows (four
+// waves of a workgroup: 12 heads of 2000 rows 33 us against 31; eight waves and
+// three buffers: the same 28.2 against 29.5, 32 heads of 216 rows 7.8 against 7.4).
 enum Layout { kRowsOfOne, kHeadsOfFour };
 template <int kD, Layout kLayout>
 struct RowsShape {
