@@ -138,9 +138,9 @@ __global__ __launch_bounds__(kRowWgThreads) void layer_norm_wide_kernel(NormArgs
 // 131072 x 1280 bf16: 220 to 253 us, 1.0 GB at 4.0 to 4.6 TB/s; 4099 x 1283
 // float32: 14 to 18 us.
 template <typename TX, typename TG, bool kRagged, int kThreads, int kChunks>
-__global__ __launch_bounds__(kRowWgThreads) void layer_norm_backward_kernel(NormArgs a) {
-    constexpr int kRows = kRowWgThreads / kThreads;  // rows of the workgroup at a time
-    __shared__ float lds[4][4];
+__global__ __launch_bounds__(kThreads > kRowWgThreads ? kThreads : kRowWgThreads) void layer_norm_backward_kernel(NormArgs a) {
+    constexpr int kRows = kThreads < kRowWgThreads ? kRowWgThreads / kThreads : 1;  // rows of the workgroup at a time
+    __shared__ float lds[4][kThreads > kRowWgThreads ? kThreads / 64 : 4];
     const int tid = threadIdx.x % kThreads;
     const float inv_n = 1.0f / float(a.width);
     auto column = [&](int i) { return (i * kThreads + tid) * 8; };
@@ -312,24 +312,27 @@ Shape forward_shape(int32_t width, bool aligned) {
 }
 // Backward: a thread's columns cost five registers a value, so the workgroup
 // holds a row from one chunk of a wave on (131072 x 1280 bf16: 222 us against
-// 273; 4099 x 1283 float32: 21 against 26).
+// 273; 4099 x 1283 float32: 21 against 26), and rows of more than three chunks
+// go over 1024 threads (16384 x 12288 bf16: 246 us, 1.2 GB at 4.9 TB/s, against
+// 553 with eight chunks in 256 threads, one wave a SIMD).
 Shape backward_shape(int32_t width, bool aligned) {
     const bool ragged = !aligned || width % 8;
     if (width <= 64 * 8) return {ragged, 64, 1};
     if (width <= 256 * 8) return {ragged, 256, 1};
     if (width <= 256 * 8 * 3) return {ragged, 256, 3};
-    if (width <= 256 * 8 * 8) return {ragged, 256, 8};
+    if (width <= 1024 * 8 * 2) return {ragged, 1024, 2};
     return {ragged, 0, 0};
 }
 
 // Workgroups of the backward kernel, each of which adds up every so many
 // rows, and partial sums of each column: as many as the card holds at once by
-// their registers (four a CU with one chunk, three with three, one with eight).
+// their registers (four a CU with one chunk, three with three, one of 1024
+// threads).
 // Fewer leave memory waiting, more run in a second round and write more sums.
 // us, sums included, for 256, 512, 768, 1024 and 2048 of them: 131072 x 1280
 // bf16 663, 366, 270, 230, 249; 32768 x 5120 bf16 456, 302, 235, 313, 283;
-// 16384 x 12288 bf16 553, 572, 579, 596, 647; with rows in a wave, which end in
-// LDS, 262144 x 512 bf16 280, 168, 145, 154, 171.
+// 16384 x 12288 bf16 246 and 257 for 256 and 512; with rows in a wave, which end
+// in LDS, 262144 x 512 bf16 280, 168, 145, 154, 171.
 int32_t backward_groups(int64_t rows, int32_t width) {
     const int64_t per = width <= 64 * 8 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
@@ -363,19 +366,20 @@ void launch_forward(const Shape &s, const NormArgs &a, hipStream_t stream) {
 template <typename TX, typename TG>
 void launch_backward(const Shape &s, const NormArgs &a, int32_t groups, hipStream_t stream) {
     const dim3 block{unsigned(kRowWgThreads), 1, 1}, grid{unsigned(groups), 1, 1};
+    const dim3 row_block{unsigned(s.threads > kRowWgThreads ? s.threads : kRowWgThreads), 1, 1};
 #define MIMO_NORM(R, T, C)  \
     if (s.ragged == R && s.threads == T && s.chunks == C) {  \
-        hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TG, R, T, C>), grid, block, 0, stream, a);    \
-        return;                                                                                          \
+        hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TG, R, T, C>), grid, row_block, 0, stream, a);    \
+        return;                                                                                              \
     }
     MIMO_NORM(false, 64, 1)
     MIMO_NORM(false, 256, 1)
     MIMO_NORM(false, 256, 3)
-    MIMO_NORM(false, 256, 8)
+    MIMO_NORM(false, 1024, 2)
     MIMO_NORM(true, 64, 1)
     MIMO_NORM(true, 256, 1)
     MIMO_NORM(true, 256, 3)
-    MIMO_NORM(true, 256, 8)
+    MIMO_NORM(true, 1024, 2)
 #undef MIMO_NORM
     hipLaunchKernelGGL((layer_norm_backward_wide_kernel<TX, TG>), row_grid(a.rows), block, 0, stream, a);
     if (a.part)

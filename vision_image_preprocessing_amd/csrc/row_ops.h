@@ -105,17 +105,19 @@ __device__ __forceinline__ void store_values(__bf16 *p, int n, const float (&v)[
     }
 }
 
-// Sum over the kThreads (64: a wave, 256: the workgroup) threads of a row,
-// in a fixed order; every one of them gets it.  `lds`: 4 floats that no
-// other reduction in flight uses.
+// Sum over the kThreads (64: a wave, more: the workgroup) threads of a row,
+// in a fixed order; every one of them gets it.  `lds`: kThreads / 64 floats
+// that no other reduction in flight uses.
 template <int kThreads>
 __device__ __forceinline__ float row_sum(float v, float *lds) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    if constexpr (kThreads == 256) {
+    if constexpr (kThreads > 64) {
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
         __syncthreads();
         v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+#pragma unroll
+        for (int i = 4; i < kThreads / 64; i += 4) v += (lds[i] + lds[i + 1]) + (lds[i + 2] + lds[i + 3]);
     }
     return v;
 }
