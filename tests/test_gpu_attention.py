@@ -234,6 +234,26 @@ def test_sinks_of_any_size(V):
         _within(got, r[name], bar, name)
 
 
+def test_sinks_that_are_not_finite_stay_with_key_0(V):
+    """Rows whose band does not hold key 0 share its block, and have none of
+    its sink, whatever it is."""
+    _say("sinks that are not finite")
+    cu_host, n, window = [0, 40, 140], 140, 5
+    q, k, v, _, _ = _inputs(n, 4, 2, 64, 26, False)
+    cu = torch.tensor(cu_host, dtype=torch.int32, device="cuda")
+    dev = [t.cuda() for t in (q, k, v)]
+    sink = torch.tensor([float("inf"), float("nan"), -float("inf"), 2.0], device="cuda")
+    out, lse = V.chunk_attention(*dev, cu, window=window, sink=sink, return_lse=True)
+    plain, plain_lse = V.chunk_attention(*dev, cu, window=window, return_lse=True)
+    r = tower.chunk_attention(_wide(q), _wide(k), _wide(v), cu_host, window)
+    _, out_bar, lse_bar = _forward_bars(r, 64)
+    for a, b in zip(cu_host[:-1], cu_host[1:]):
+        away = slice(a + window + 1, b)
+        assert torch.equal(out[away], plain[away]) and torch.equal(lse[:, away], plain_lse[:, away])
+        _within(out[away], r["out"][away], out_bar[away], "out")
+        _within(lse[:, away], r["lse"][:, away], lse_bar[:, away], "lse")
+
+
 def test_strides_and_slices(V):
     """Slices of one packed projection, head-major tensors, a shared key head
     by a stride of zero, and gradients into slices: the same bits as dense ones."""

@@ -474,13 +474,14 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
             s[b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) s[b] = mfma(read_rows(tk, at, b, i), q[i], s[b]);
+            // before the mask: rows that do not see key 0 have none of its sink
+            if (b == 0 && k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
             if (kBand && !all_visible(r0, k0 + 32 * b, 32, len, window)) mask_band(seen, k0 + 32 * b, s[b]);
         }
         if (!kBand && k0 + kStep > len) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) mask_end(len, k0 + 32 * b, -INFINITY, s[b]);
         }
-        if (k0 == 0 && a.sink) s[0][0] += lane < 32 ? sink : 0.0f;
         float m = s[0][0];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
