@@ -509,10 +509,15 @@ int mimo_pixel_embed(int32_t n, const mimo_image_desc *desc, const uint8_t *src,
  * softmax statistics and sums are float32, the probabilities are rounded to
  * bf16 before their product.  Values of a chunk have to be finite: a NaN or
  * an infinity in it may reach any of the chunk's rows, but no other chunk's.
+ * A sink is any number but NaN.  It counts as at most MIMO_SINK_MAX and, -inf
+ * aside, as at least -MIMO_SINK_MAX, in lse too: there key 0 has all of a
+ * row's weight, or none where the row sees another key, as long as the row's
+ * other logits are less than 8000 apart.
  * Results do not depend on how calls run next to each other (no atomics).
  * ------------------------------------------------------------------------ */
 
 #define MIMO_HEAD_DIM_MAX 128
+#define MIMO_SINK_MAX 8192
 
 /* A bf16 tensor [rows][heads][head_dim] on the device, 16-byte aligned; the
  * innermost axis is dense, the strides (in values, multiples of 8) are free
@@ -533,7 +538,7 @@ typedef struct mimo_attention {
     int32_t window;     /* band half-width; negative: every row sees its whole chunk */
     float scale;        /* in [1e-18, 1e18]; 1 / sqrt(head_dim) in the tower */
     const int32_t *cu_seqlens; /* device [chunks + 1]: mimo_chunk_seqlens' boundaries */
-    const float *sink;  /* device [q_heads], or NULL */
+    const float *sink;  /* device [q_heads], or NULL; see MIMO_SINK_MAX */
     mimo_heads q, k, v; /* q: q_heads heads; k, v: kv_heads */
     mimo_heads out;     /* q_heads heads */
     float *lse;         /* device [q_heads][rows], or NULL (forward only) */

@@ -254,6 +254,35 @@ def test_sinks_that_are_not_finite_stay_with_key_0(V):
         _within(lse[:, away], r["lse"][:, away], lse_bar[:, away], "lse")
 
 
+@pytest.mark.parametrize("window", [-1, 0, 5])
+def test_sinks_beyond_the_range(V, window):
+    """The type's lowest and highest values and what lies before them: key 0
+    has nothing, or all, as by the definition in 64 bits.  lse and the bars are
+    those of the sink at the range's end, which is what it counts as."""
+    _say("sinks beyond the range, window", window)
+    big = float(torch.finfo(torch.float32).max)
+    cu_host, n = [0, 1, 71, 111], 111
+    sink = torch.tensor([-big, -1e30, -1e9, -1e5, 1e5, 1e9, big, float("inf")])
+    q, k, v, do, _ = _inputs(n, 8, 2, 64, 27, False)
+    wide = [_wide(t) for t in (q, k, v)]
+    by_definition = tower.chunk_attention(*wide, cu_host, window, None, _wide(sink.clamp(-big, big)), _wide(do))
+    r = tower.chunk_attention(*wide, cu_host, window, None, _wide(sink.clamp(-8192, 8192)), _wide(do))
+    for name in ("out", "dq", "dk", "dv", "dsink"):
+        np.testing.assert_allclose(r[name], by_definition[name], rtol=1e-9, atol=1e-9)
+    cu = torch.tensor(cu_host, dtype=torch.int32, device="cuda")
+    dev = [t.cuda() for t in (q, k, v)]
+    out, lse = V.chunk_attention(*dev, cu, window=window, sink=sink.cuda(), return_lse=True)
+    grads = V.chunk_attention_backward(do.cuda(), *dev, out, lse, cu, window=window, sink=sink.cuda())
+    rel, out_bar, lse_bar = _forward_bars(r, 64)
+    _within(out, by_definition["out"], out_bar, "out")
+    _within(lse, r["lse"], lse_bar, "lse")
+    bars = _backward_bars(_wide(q), _wide(k), _wide(v), _wide(do), r, 0.125, rel, out_bar, 64)
+    for got, name, bar in zip(grads, ("dq", "dk", "dv", "dsink"), bars):
+        _within(got, by_definition[name], bar, f"{name} window {window}")
+    clamped = V.chunk_attention(*dev, cu, window=window, sink=sink.clamp(-8192, 8192).cuda(), return_lse=True)
+    assert torch.equal(out, clamped[0]) and torch.equal(lse, clamped[1])
+
+
 def test_strides_and_slices(V):
     """Slices of one packed projection, head-major tensors, a shared key head
     by a stride of zero, and gradients into slices: the same bits as dense ones."""

@@ -61,6 +61,12 @@ constexpr float kLn2 = 0.693147180559945309417f;
 // powers of two: probabilities stay below 2^8 meanwhile, which float32 sums
 // and bf16 operands hold at full relative precision.
 constexpr float kRaise = 8.0f;
+// Sinks beyond this count as this.  lse is float32, and p = exp(s - lse) of
+// the backward pass is off by 2^-23 |s| or so: a sink of -1e9 on a key that a
+// row sees alone gave p0 = 2^30, and sinks above 3.4e38 scale became
+// infinite.  At the limit (and any further out) key 0 has all of a row's
+// weight or none, logits being less than some 8000 apart, and p keeps 10 bits.
+constexpr float kMaxSink = MIMO_SINK_MAX;
 
 // One [rows][heads][head_dim] bf16 tensor; strides in values.
 struct Heads {
@@ -312,6 +318,12 @@ __device__ __forceinline__ bool all_visible(int r, int k, int n, int len, int wi
     return k + n <= len && (window < 0 || (k + n - 1 - r <= window && r + 31 - k <= window));
 }
 
+// A head's sink as it counts: within kMaxSink, -inf (no key 0) and NaN as they are.
+__device__ __forceinline__ float head_sink(const float *sink, int head) {
+    const float v = sink[head];
+    return v > kMaxSink ? kMaxSink : v < -kMaxSink && v != -INFINITY ? -kMaxSink : v;
+}
+
 // Row of value r of a result block, without its 32-row block and the four
 // rows that the upper half-wave is further down.
 __device__ __forceinline__ constexpr int row_of(int r) { return 8 * (r >> 2) + (r & 3); }
@@ -441,7 +453,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
     int lo, hi;
     band(tile.first, S::kRows, len, window, lo, hi);
     const float c2 = a.scale * kLog2e;
-    const float sink = a.sink ? a.sink[head] / a.scale : 0.0f;  // in the unscaled logits' units
+    const float sink = a.sink ? head_sink(a.sink, head) / a.scale : 0.0f;  // in the unscaled logits' units
     f32x16 o[kBlocks];
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d) o[d] = f32x16{};
@@ -571,7 +583,7 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 3 : 1) void attention_dq_kerne
     int lo, hi;
     band(tile.first, S::kRows, len, window, lo, hi);
     const float c2 = a.scale * kLog2e;
-    const float sink = a.sink ? a.sink[head] / a.scale : 0.0f;
+    const float sink = a.sink ? head_sink(a.sink, head) / a.scale : 0.0f;
     float lse2 = row < len ? a.lse[stat] * kLog2e : 0.0f;
     if (lse2 == -INFINITY) lse2 = INFINITY;  // a row that saw nothing: every probability is zero
     f32x16 dq[kBlocks];
@@ -758,7 +770,7 @@ __global__ __launch_bounds__(kThreads, kD == 128 ? 1 : kD == 64 ? 3 : 2) void at
         const uint8_t *tq = n ? sq1 : sq0, *tg = n ? sg1 : sg0;
         const float *tl = n ? sl1[0] : sl0[0], *td = n ? sl1[1] : sl0[1];
         if (c0 >= len) return;
-        const float kb = a.sink && key == 0 ? a.sink[head] * kLog2e : 0.0f;
+        const float kb = a.sink && key == 0 ? head_sink(a.sink, head) * kLog2e : 0.0f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int rb = q0 + 32 * b;

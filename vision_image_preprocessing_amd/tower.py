@@ -151,8 +151,9 @@ def chunk_attention(q, k, v, cu_seqlens, window=-1, scale=None, sink=None, out=N
     of 8 values (slices of one projection's output are fine); cu_seqlens
     int32 [chunks + 1] on the same GPU (vit_tables' boundaries, moved there
     once).  window >= 0 limits a row to keys at most that far from it in its
-    chunk; sink (float32 [q_heads]) is added to each chunk's key 0's logit;
-    scale defaults to head_dim ** -0.5.
+    chunk; sink (float32 [q_heads]; beyond +-8192 it counts as that, -inf takes
+    key 0 away) is added to each chunk's key 0's logit; scale defaults to
+    head_dim ** -0.5.
 
     Returns out [rows, q_heads, head_dim], or with return_lse=True (out, lse)
     with lse float32 [q_heads, rows], which the backward pass takes.  Rows
