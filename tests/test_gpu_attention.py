@@ -340,6 +340,39 @@ def test_rows_behind_the_last_chunk(V):
         assert torch.equal(a[:n], b)
 
 
+@pytest.mark.parametrize("hq,hk", [(8, 2), (2, 2)])
+@pytest.mark.parametrize("window", [-1, 40])
+@pytest.mark.parametrize("first", [31, 32, 200, 1000])
+def test_rows_in_front_of_the_first_chunk(V, hq, hk, window, first):
+    """Boundaries that do not start at 0, by more than a tile: the rows in
+    front are neither read nor written, and the others have the values of a
+    call without them."""
+    _say("rows in front", (hq, hk), window, first)
+    n, d = 330, 64
+    rng = np.random.default_rng(first)
+    for lengths in ([130, 0, 200], [int(x) for x in rng.multinomial(n, [1 / 90] * 90)]):
+        q, k, v, do, s = (t.cuda() for t in _inputs(first + n, hq, hk, d, 29, True))
+        for t in (q, k, v, do):
+            t[:first] = float("nan")
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 3.0), torch.full((hq, first + n), 3.0, device="cuda")
+        V.chunk_attention(q, k, v, cu + first, window=window, sink=s, out=out, lse=lse)
+        grads = [torch.full_like(t, 3.0) for t in (q, k, v)]
+        _, _, _, dsink = V.chunk_attention_backward(do, q, k, v, out, lse, cu + first, window=window, sink=s, dq=grads[0],
+                                                    dk=grads[1], dv=grads[2])
+        for t in (out, *grads):
+            assert (t[:first] == 3).all()
+        assert (lse[:, :first] == 3).all()
+        x = [t[first:].double().cpu().numpy() for t in (q, k, v, do)]
+        r = tower.chunk_attention(*x[:3], cu.cpu().numpy(), window, None, _wide(s.cpu()), x[3])
+        rel, out_bar, lse_bar = _forward_bars(r, d)
+        _within(out[first:], r["out"], out_bar, "out")
+        _within(lse[:, first:], r["lse"], lse_bar, "lse")
+        bars = _backward_bars(*x, r, d ** -0.5, rel, out_bar, d)
+        for got, name, bar in zip([g[first:] for g in grads] + [dsink], ("dq", "dk", "dv", "dsink"), bars):
+            _within(got, r[name], bar, name)
+
+
 def test_other_chunks_are_not_touched(V):
     """What is not finite in one chunk reaches no other."""
     _say("chunks apart")

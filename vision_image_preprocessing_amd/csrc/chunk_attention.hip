@@ -120,7 +120,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t
         const int step = (hi - lo + 63) >> 6;
         const int idx = lo + lane * step;
         const bool le = idx < hi && int64_t(cu[idx] / kRows) + idx <= t;
-        const int k = max(__popcll(__ballot(le)) - 1, 0);
+        // in int: the count is unsigned, and less than one of it is not -1
+        // (none is at most t where rows lie in front of the first boundary)
+        const int k = max(int(__popcll(__ballot(le))) - 1, 0);
         lo += k * step;
         hi = min(lo + step, hi);
     }
