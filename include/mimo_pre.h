@@ -553,9 +553,10 @@ typedef struct mimo_attention_grads {
  * Forward: writes out, and lse unless it is NULL (the backward pass needs
  * it).  The boundaries are read on the device, so a call can be captured into
  * a graph and replayed for other boundaries of as many chunks.  Chunks may be
- * empty.  Rows behind the last boundary are neither read nor written.  A
- * boundary outside [0, rows] or a descending pair makes its chunk empty;
- * boundaries that make chunks overlap give undefined values in out.
+ * empty.  Rows in front of the first boundary and behind the last are neither
+ * read nor written.  Boundaries have to ascend within [0, rows]: where any do
+ * not, all that the outputs hold in rows [0, rows), here and in the backward
+ * pass (and dsink), is undefined, and nothing outside them is read or written.
  * out must not overlap an input.  One kernel launch.  Returns MIMO_OK,
  * MIMO_E_INVALID, MIMO_E_TOO_LARGE (more than 2^29 rows or chunks, or
  * (rows / 128 + chunks + 1) * q_heads above 2^24 - 1) or MIMO_E_HIP.

@@ -403,6 +403,46 @@ def test_bad_boundaries_stay_inside(V):
         assert torch.equal(out[:10], want[:10])
 
 
+@pytest.mark.parametrize("hq,hk", [(8, 2), (2, 2)])
+@pytest.mark.parametrize("window", [-1, 40])
+def test_boundaries_that_do_not_ascend(V, hq, hk, window):
+    """Chunks of several tiles, in any order, one over the other, or outside the
+    rows: nothing around the outputs and the workspace is written, and the next
+    call is right."""
+    _say("boundaries that do not ascend", (hq, hk), window)
+    n, d, guard = 600, 64, 3
+    q, k, v, do, s = (t.cuda() for t in _inputs(n, hq, hk, d, 28, True))
+    good = torch.tensor([0, 130, 130, 600], dtype=torch.int32, device="cuda")
+    want, lse = V.chunk_attention(q, k, v, good, window=window, sink=s, return_lse=True)
+    want = (want, lse, *V.chunk_attention_backward(do, q, k, v, want, lse, good, window=window, sink=s))
+
+    def guarded(shape, dtype, edge):
+        """A tensor of zeros in the middle of one that holds sevens."""
+        t = torch.full((edge * 2 + int(np.prod(shape)),), 7, dtype=dtype, device="cuda")
+        t[edge:-edge] = 0
+        return t, t[edge:-edge].view(shape)
+
+    for bad in ([500, 600, 0, 400], [0, 700, 300, 600], [-3, 200, 100, 2 ** 31 - 1, 0, 600], [600, 400, 200, 0],
+                [0, 600, 0, 600], [-(2 ** 31), 2 ** 31 - 1, -(2 ** 31)]):
+        _say(bad)
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        held = [guarded(shape, dtype, edge) for shape, dtype, edge in (
+            ((n, hq, d), torch.bfloat16, guard * hq * d), ((hq, n), torch.float32, 64), ((n, hq, d), torch.bfloat16, guard * hq * d),
+            ((n, hk, d), torch.bfloat16, guard * hk * d), ((n, hk, d), torch.bfloat16, guard * hk * d), ((hq,), torch.float32, 64),
+            ((V.chunk_attention_workspace_bytes(n, hq, hk, d, len(bad) - 1),), torch.uint8, 4096))]
+        out, l, dq, dk, dv, dsink, workspace = (inner for _, inner in held)
+        V.chunk_attention(q, k, v, cu, window=window, sink=s, out=out, lse=l)
+        V.chunk_attention_backward(do, q, k, v, out, l, cu, window=window, sink=s, dq=dq, dk=dk, dv=dv, dsink=dsink,
+                                   workspace=workspace)
+        torch.cuda.synchronize()
+        for whole, inner in held:
+            edge = (whole.numel() - inner.numel()) // 2
+            assert (whole[:edge] == 7).all() and (whole[-edge:] == 7).all()
+    again, lse = V.chunk_attention(q, k, v, good, window=window, sink=s, return_lse=True)
+    again = (again, lse, *V.chunk_attention_backward(do, q, k, v, again, lse, good, window=window, sink=s))
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
 def test_streams_and_graphs(V):
     """A stream of the caller's, and two captured calls that are replayed
     between eager ones with new inputs and boundaries, each with a workspace of

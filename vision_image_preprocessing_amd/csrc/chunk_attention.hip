@@ -110,8 +110,10 @@ __device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t grid) {
 // Tile t of the batch, kRows rows each: chunk c's tiles are numbered from
 // cu[c] / kRows + c, which leaves each chunk as many numbers as it needs or
 // one more, so that the grid is known from the row and chunk counts alone.
-// A boundary outside [0, rows] or a descending pair gives an empty tile:
-// nothing is read or written through it.
+// The search relies on ascending boundaries.  Where they do not ascend it may
+// take any chunk, so the chunk's own two are checked: one that is not inside
+// [0, rows], or that the tile is not a part of, gives an empty tile, through
+// which nothing is read or written.
 template <int kRows>
 __device__ __forceinline__ Tile find_tile(const int32_t *cu, int chunks, int64_t rows, int t) {
     const int lane = threadIdx.x & 63;
@@ -877,7 +879,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     const int kv = int(line / a.rows);
     const int64_t row = line - int64_t(kv) * a.rows;
     if (kv >= a.kv_heads) return;
-    // the row's chunk: the last one that starts at or before it
+    // the row's chunk: the last one that starts at or before it (checked, as find_tile's is)
     int lo = 0, hi = a.chunks;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

@@ -149,8 +149,9 @@ def chunk_attention(q, k, v, cu_seqlens, window=-1, scale=None, sink=None, out=N
     q bf16 [rows, q_heads, head_dim]; k, v bf16 [rows, kv_heads, head_dim],
     each with an innermost axis that is dense and other strides in multiples
     of 8 values (slices of one projection's output are fine); cu_seqlens
-    int32 [chunks + 1] on the same GPU (vit_tables' boundaries, moved there
-    once).  window >= 0 limits a row to keys at most that far from it in its
+    int32 [chunks + 1], ascending within [0, rows] (not checked: the outputs
+    are undefined where it is not), on the same GPU (vit_tables' boundaries,
+    moved there once).  window >= 0 limits a row to keys at most that far from it in its
     chunk; sink (float32 [q_heads]; beyond +-8192 it counts as that, -inf takes
     key 0 away) is added to each chunk's key 0's logit; scale defaults to
     head_dim ** -0.5.
