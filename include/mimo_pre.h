@@ -657,9 +657,10 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
 /*
  * out[r][e] = (sum_k xq[r][k] wq[e][k]) x_scale[r] w_scale[e] (+ bias[e]), one
  * kernel launch; the sum is exact (32-bit integers on the matrix cores), and
- * float32 from there on: the sum rounded, times x_scale, then times w_scale
- * and plus the bias with one rounding.  A row's values do not depend on the
- * rows next to it, nor on how many there are.
+ * float32 from there on: the sum rounded, times x_scale (which may pass
+ * float32's range), then times w_scale and plus the bias with one rounding.
+ * A row's values do not depend on the rows next to it, nor on how many there
+ * are.
  *   k        a multiple of 128, at most 130944.
  *   xq, wq   device int8 [n_rows][k], [embed_dim][k] (mimo_quantize_rows'
  *            padded rows), 16-byte aligned.

@@ -162,6 +162,43 @@ def test_scales_whose_product_leaves_the_range(V, m):
     assert torch.isfinite(want.float()).all() and torch.equal(out, want.float())
 
 
+@pytest.mark.parametrize("m", [3, 40, 300, 2000, 70000])
+@pytest.mark.parametrize("out_kind", ["f32", "bf16"])
+def test_row_scales_whose_product_with_a_sum_leaves_the_range(V, m, out_kind):
+    """2^100 and 2^127 with small channel scales, a subnormal one among them:
+    the sum times the row's scale is infinite alone, the result is not, unless
+    it has to be.  Powers of two and sums below 2^24: exact in float32."""
+    _say("large row scales", m, out_kind)
+    g = torch.Generator().manual_seed(9)
+    xq = torch.randint(-127, 128, (m, 128), generator=g, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (1030, 128), generator=g, dtype=torch.int8)
+    xs, ws = torch.full((m,), 0.125), torch.full((1030,), 2.0 ** -40)
+    xs[0], xs[1], xs[m - 1] = 2.0 ** 100, -2.0 ** 127, 2.0 ** 64
+    wq[5], ws[5], ws[7], ws[8] = 0, 2.0 ** 100, 2.0 ** 100, float("nan")
+    ws[6] = 2.0 ** -149 if out_kind == "f32" else 2.0 ** -120
+    want = ((xq.double() @ wq.double().T) * xs.double()[:, None] * ws.double()).float().to(KIND[out_kind])
+    out = V.quantized_linear(xq.cuda(), xs.cuda(), wq.cuda(), ws.cuda(), out_dtype=out_kind).cpu()
+    assert torch.isfinite(want[:, :5]).all() and (want[0, :3] != 0).all() and torch.isinf(want[0, 7])
+    assert (want[:, 5] == 0).all() and torch.isnan(out[:, 8]).all()
+    keep = torch.arange(1030) != 8
+    assert torch.equal(out[:, keep], want[:, keep])
+
+
+def test_rows_of_large_values(V):
+    """Rows up to 1e36 with weights up to 0.06, and with a bias."""
+    _say("rows of large values")
+    g = torch.Generator().manual_seed(10)
+    for m, n in ((4, 300), (600, 1283)):
+        x = (torch.rand((m, 1283), generator=g) * 2 - 0.5) * 1e36
+        w, b = torch.rand((n, 1283), generator=g) * 0.06, torch.randn(n, generator=g) * 1e36
+        (xq, xs), (wq, ws) = V.quantize_rows(x.cuda()), V.quantize_rows(w.cuda())
+        out = V.quantized_linear(xq, xs, wq, ws, b.cuda(), out_dtype="f32").double().cpu().numpy()
+        ref, mag = tower.quantized_linear(xq.cpu().numpy(), xs.cpu().numpy(), wq.cpu().numpy(), ws.cpu().numpy(), b.numpy())
+        assert np.abs(ref).max() < 3e38
+        bar = 3.01 * EPS * mag + EPS * (np.abs(ref) + mag) + EPS * np.abs(ref)
+        assert (np.abs(out - ref) <= 1.01 * bar).all()
+
+
 def test_rows_that_are_not_finite(V):
     _say("not finite")
     x = torch.randn(3, 300)
