@@ -563,7 +563,7 @@ typedef struct mimo_attention_grads {
  */
 int mimo_chunk_attention(const mimo_attention *args, void *stream);
 
-/* Device workspace bytes of the backward pass (0 for sizes it refuses). */
+/* Device workspace bytes of the backward pass (0 for sizes it refuses, or without rows or chunks). */
 size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                             int32_t chunks);
 

@@ -95,6 +95,27 @@ def test_attention_backward_workspace_and_nulls():
     assert lib.mimo_chunk_attention_backward(_attention(rows=0), _grads(), None, 0, None) == V.MIMO_OK
 
 
+def test_workspace_bytes_are_zero_from_the_first_refused_size_on():
+    lib = V.load()
+    sizes = lambda rows, chunks, hq, hk=1: (rows, hq, hk, 64, chunks)
+    refused = lambda rows, chunks, hq, hk=1: lib.mimo_chunk_attention_backward(
+        _attention(rows=rows, chunks=chunks, hq=hq, hk=hk), _grads(hq=hq, hk=hk), P, 0, None)
+    for last, first in (((32511, 1, 65536), (32512, 1, 65536)), ((10, (1 << 22) - 2, 4), (10, (1 << 22) - 1, 4)),
+                        (((1 << 29), 1, 1), ((1 << 29) + 1, 1, 1)), ((1 << 28, 8, 7), (1 << 29, 8, 7))):
+        assert V.chunk_attention_workspace_bytes(*sizes(*last)) > 0 and refused(*last) == V.MIMO_E_CAPACITY
+        assert V.chunk_attention_workspace_bytes(*sizes(*first)) == 0 and refused(*first) == V.MIMO_E_TOO_LARGE
+    # nothing to do, and so nothing to hold
+    assert V.chunk_attention_workspace_bytes(*sizes(0, 1 << 29, 65536)) == 0 and refused(0, 1 << 29, 65536) == V.MIMO_OK
+    assert V.chunk_attention_workspace_bytes(*sizes(1 << 29, 0, 65536)) == 0 and refused(1 << 29, 0, 65536) == V.MIMO_OK
+
+    def norm(rows, width):
+        return lib.mimo_layer_norm_backward(rows, width, P, V.MIMO_F32, 2 * P, V.MIMO_F32, P, P, P, 3 * P, P, 4 * P, P, 0, None)
+
+    for last, first in ((((1 << 31) - 1, 8), (1 << 31, 8)), ((5, 65536), (5, 65537))):
+        assert V.layer_norm_workspace_bytes(*last) > 0 and norm(*last) == V.MIMO_E_CAPACITY
+        assert V.layer_norm_workspace_bytes(*first) == 0 and norm(*first) == V.MIMO_E_TOO_LARGE
+
+
 def test_norm_refuses():
     lib = V.load()
     F, B = V.MIMO_F32, V.MIMO_BF16

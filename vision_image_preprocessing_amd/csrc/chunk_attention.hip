@@ -933,6 +933,11 @@ LaunchShape launch_shape(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_
 
 constexpr int64_t kMaxRows = int64_t(1) << 29;  // a row plus twice the window fits an int
 constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
+// A launch has fewer than 2^32 threads (groups of four heads take at most as
+// many workgroups as 128 rows do; dsink takes one a head).
+bool too_many_groups(int64_t rows, int32_t chunks, int32_t q_heads) {
+    return (rows / kTileRows + chunks) * q_heads + q_heads > kMaxGroups;
+}
 constexpr int64_t kMaxRowStride = int64_t(1) << 22;  // a 64-row tile's byte offsets stay below 2^31
 
 int check_heads(const mimo_heads &t, const char *who, const char *name, int64_t rows, int32_t heads, int32_t head_dim, bool written) {
@@ -970,9 +975,7 @@ int check_attention(const mimo_attention *p, const char *who, AttentionArgs &a) 
     a.window = p->window < 0 ? -1 : p->window;
     a.scale = p->scale;
     if (p->rows == 0 || p->chunks == 0) return MIMO_OK;
-    // a launch has fewer than 2^32 threads (groups of four heads take at most
-    // as many workgroups as 128 rows do; dsink takes one a head)
-    if ((p->rows / kTileRows + p->chunks) * p->q_heads + p->q_heads > kMaxGroups)
+    if (too_many_groups(p->rows, p->chunks, p->q_heads))
         return set_error(MIMO_E_TOO_LARGE, w() + ": (rows / 128 + chunks + 1) * q_heads is above 2^24 - 1");
     if (!p->cu_seqlens || !check_ptr_align(p->cu_seqlens, 4) || !check_ptr_align(p->sink, 4))
         return set_error(MIMO_E_INVALID, w() + ": cu_seqlens must be non-null; it and sink 4-byte aligned");
@@ -1079,6 +1082,7 @@ size_t mimo_chunk_attention_workspace_bytes(int64_t rows, int32_t q_heads, int32
     if (rows < 0 || rows > kMaxRows || chunks < 0 || chunks > kMaxRows || kv_heads < 1 || q_heads < kv_heads ||
         q_heads % kv_heads || q_heads > 65536 || head_dim < 8 || head_dim > MIMO_HEAD_DIM_MAX || head_dim % 8)
         return 0;
+    if (rows == 0 || chunks == 0 || too_many_groups(rows, chunks, q_heads)) return 0;
     return workspace_layout(launch_shape(rows, q_heads, kv_heads, chunks), rows, q_heads, kv_heads, head_dim).total;
 }
 

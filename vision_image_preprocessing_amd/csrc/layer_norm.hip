@@ -447,7 +447,7 @@ int mimo_layer_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype,
 }
 
 size_t mimo_layer_norm_workspace_bytes(int64_t rows, int32_t width) {
-    if (rows < 0 || width < 1 || width > kMaxWidth) return 0;
+    if (rows < 0 || rows > 0x7FFFFFFFll || width < 1 || width > kMaxWidth) return 0;
     return size_t(backward_groups(rows, width)) * 2 * size_t(width) * sizeof(float);
 }
 
