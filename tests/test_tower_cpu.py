@@ -218,6 +218,44 @@ def test_python_checks():
     assert "out_dtype" in lin(out_dtype="i8") and "out must be" in lin(out=torch.zeros(4, 5))
 
 
+def test_python_refuses_sizes_before_it_allocates():
+    """Outputs, gradients and workspaces of these would be terabytes."""
+    bf, meta = torch.bfloat16, dict(device="meta")
+
+    def too_large(f, *a, **k):
+        with pytest.raises(V.MimoError) as e:
+            f(*a, **k)
+        assert e.value.code == V.MIMO_E_TOO_LARGE and str(e.value)
+
+    def attention(rows, chunks, hq):
+        q = torch.zeros((rows, 1, 128), dtype=bf, **meta).expand(rows, hq, 128)
+        k, cu = torch.zeros((rows, 1, 128), dtype=bf, **meta), torch.zeros(chunks + 1, dtype=torch.int32, **meta)
+        return q, k, cu, torch.zeros((hq, rows), **meta)
+
+    for size in ((32512, 1, 65536), (1 << 28, 8, 8), ((1 << 29) + 1, 1, 1), (10, (1 << 22) - 1, 4)):
+        q, k, cu, lse = attention(*size)
+        too_large(V.chunk_attention, q, k, k, cu)
+        too_large(V.chunk_attention_backward, q, q, k, k, q, lse, cu)
+    # the last size below, and nothing to do, are refused for their device alone
+    for size in ((32511, 1, 65536), (0, 1 << 22, 65536), (1 << 29, 0, 8)):
+        q, k, cu, lse = attention(*size)
+        assert "one GPU" in _refused(V.chunk_attention, q, k, k, cu)
+        assert "one GPU" in _refused(V.chunk_attention_backward, q, q, k, k, q, lse, cu)
+    for rows, width, quantized in ((1 << 31, 1, True), (2, 65537, False), (2, 130945, True)):
+        x, m = torch.zeros((rows, width), **meta), torch.zeros(rows, **meta)
+        if not quantized or width == 1:
+            too_large(V.layer_norm, x)
+            too_large(V.layer_norm_backward, x, x, m, m)
+        if quantized:
+            too_large(V.quantize_rows, x)
+    x = torch.zeros((2, 130944), **meta)
+    assert "one GPU" in _refused(V.quantize_rows, x) and "one GPU" in _refused(V.layer_norm, x[:, :65536].contiguous())
+    i, m = torch.zeros((4, 131072), dtype=torch.int8, **meta), torch.zeros(4, **meta)
+    too_large(V.quantized_linear, i, m, i, m)
+    i, n = torch.zeros((4, 128), dtype=torch.int8, **meta), (1 << 24) + 1
+    too_large(V.quantized_linear, i, m, torch.zeros((n, 128), dtype=torch.int8, **meta), torch.zeros(n, **meta))
+
+
 def test_names_are_exported():
     for name in V._TOWER:
         assert callable(getattr(V, name)) and name in dir(V)

@@ -21,7 +21,7 @@ import struct
 import torch
 
 from . import _abi
-from ._abi import MIMO_BF16, MIMO_E_INVALID, MIMO_F32, MimoError
+from ._abi import MIMO_BF16, MIMO_E_INVALID, MIMO_E_TOO_LARGE, MIMO_F32, MimoError
 
 _F32, _BF16, _I8, _I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
 _TYPES = {"f32": _F32, "bf16": _BF16}
@@ -45,6 +45,12 @@ def _library():
 
 def _refuse(message):
     raise MimoError(MIMO_E_INVALID, message)
+
+
+def _refuse_size(message):
+    """The library's size limits, looked at before outputs are allocated: those
+    of a call that it would refuse might not fit the card."""
+    raise MimoError(MIMO_E_TOO_LARGE, message)
 
 
 def _check_devices(what, tensors):
@@ -123,6 +129,10 @@ def _check_qkv(what, q, k, v, cu_seqlens, sink, lse):
         _refuse(f"{what}: v must be of k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
     if cu_seqlens.dtype != _I32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
         _refuse(f"{what}: cu_seqlens must be contiguous int32 [chunks + 1], got {tuple(cu_seqlens.shape)} {cu_seqlens.dtype}")
+    chunks = cu_seqlens.shape[0] - 1
+    if rows > 0x20000000 or ((rows // 128 + chunks + 1) * q_heads > 0xFFFFFF and rows and chunks):
+        _refuse_size(f"{what}: more than 2^29 rows, or (rows / 128 + chunks + 1) * q_heads above 2^24 - 1: {rows} rows, "
+                     f"{chunks} chunks, {q_heads} heads")
     if sink is not None:
         _check_vector(what, "sink", sink, q_heads, _F32)
     if lse is not None and (lse.dtype != _F32 or lse.shape != (q_heads, rows) or not lse.is_contiguous()):
@@ -252,11 +262,13 @@ def _out_type(what, out_dtype):
     return _TYPES[out_dtype]
 
 
-def _rows_of(what, x):
+def _rows_of(what, x, widest):
     _check_matrix(what, "x", x)
     rows, width = x.shape
     if width < 1:
         _refuse(f"{what}: x has no columns")
+    if width > widest or rows > 0x7FFFFFFF:
+        _refuse_size(f"{what}: width above {widest} or more than 2^31 - 1 rows: {rows} x {width}")
     return rows, width
 
 
@@ -272,7 +284,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
     dtypes agree.
     """
     what = "layer_norm"
-    rows, width = _rows_of(what, x)
+    rows, width = _rows_of(what, x, 65536)
     if weight is not None:
         _check_vector(what, "weight", weight, width, _F32)
     if bias is not None:
@@ -323,7 +335,7 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, dx=None, dweight=None,
     same time need one each.
     """
     what = "layer_norm_backward"
-    rows, width = _rows_of(what, x)
+    rows, width = _rows_of(what, x, 65536)
     _check_matrix(what, "dout", dout)
     _check_shape(what, "dout", dout, x.shape)
     if mean is None or rstd is None:
@@ -385,7 +397,7 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     q[:, :width] * scale[:, None].
     """
     what = "quantize_rows"
-    rows, width = _rows_of(what, x)
+    rows, width = _rows_of(what, x, 130944)
     padded = (width + 127) & -128
     if q is not None:
         _check_matrix(what, "q", q, (_I8,))
@@ -425,6 +437,8 @@ def quantized_linear(xq, x_scale, wq, w_scale, bias=None, out=None, out_dtype: s
     n, wk = wq.shape
     if wk != k or k < 128 or k % 128 or n < 1:
         _refuse(f"{what}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must share a width that is a multiple of 128")
+    if k > 130944 or n > 0x1000000 or rows > 0x7FFFFFFF:
+        _refuse_size(f"{what}: width above 130944, more than 2^24 channels or 2^31 - 1 rows: xq {tuple(xq.shape)}, wq {tuple(wq.shape)}")
     _check_vector(what, "x_scale", x_scale, rows, _F32)
     _check_vector(what, "w_scale", w_scale, n, _F32)
     if bias is not None:
