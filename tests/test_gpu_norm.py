@@ -121,6 +121,44 @@ def test_rows(V, rows):
     _check(V, rows, 37, "f32", "f32", "f32", True, seed=rows + 1)
 
 
+def _sums_depth(V, rows, width):
+    """(workgroups, additions on a value's way into dweight or dbias): over the
+    rows of its workgroup (or of a wave, and then four waves), over the
+    workgroups' sums that one of the last launch's 32 threads a column takes,
+    and up their tree; and eight to spare."""
+    groups = V.layer_norm_workspace_bytes(rows, width) // (2 * 4 * width)
+    assert groups > 0
+    return groups, -(-rows // groups) + -(-groups // 32) + 8 + 2 + 5
+
+
+@pytest.mark.parametrize("rows,width", [(9001, 72), (9001, 509), (2500, 1280), (2500, 1283), (2500, 2041), (1700, 5120),
+                                        (1700, 5121), (700, 8192), (700, 8193), (700, 16384), (700, 16392), (600, 20001)])
+@pytest.mark.parametrize("x_kind,g_kind", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_workgroups_that_take_several_rows(V, rows, width, x_kind, g_kind):
+    """More than twice as many rows as workgroups, in every shape, aligned and
+    not: a sum has all of its rows, each once."""
+    _say("several rows a workgroup", (rows, width), x_kind, g_kind)
+    groups, depth = _sums_depth(V, rows, width)
+    assert rows > 2 * groups
+    x, dout, w, b = _inputs(rows, width, x_kind, g_kind, True, rows + width)
+    wide = [_wide(t) for t in (x, dout, w, b)]
+    r = tower.layer_norm(wide[0], wide[2], wide[3], NORM_EPS, wide[1])
+    mean_bar, rel, _, dx_bar, _, _ = _bars(*wide, r)
+    dev = [t.cuda() for t in (x, dout, w, b)]
+    _, mean, rstd = V.layer_norm(dev[0], dev[2], dev[3], eps=NORM_EPS, return_stats=True)
+    dx, dw, db = V.layer_norm_backward(dev[1], dev[0], mean, rstd, dev[2])
+    _within(dx, r["dx"], dx_bar + ROUND[dx.dtype] * np.abs(r["dx"]), "dx")
+    hat = r["rstd"][:, None] * (mean_bar[:, None] + 2 * EPS * np.abs(wide[0] - r["mean"][:, None])) + np.abs(r["hat"]) * rel[:, None]
+    dw_bar = (np.abs(wide[1]) * hat).sum(axis=0) + depth * EPS * np.abs(wide[1] * r["hat"]).sum(axis=0)
+    db_bar = depth * EPS * np.abs(wide[1]).sum(axis=0)
+    # no row's part of a sum is lost in the bar
+    assert np.median(dw_bar) < np.median(np.abs(wide[1] * r["hat"])) / 4 and np.median(db_bar) < np.median(np.abs(wide[1])) / 4
+    _within(dw, r["dweight"], dw_bar + EPS * np.abs(r["dweight"]), "dweight")
+    _within(db, r["dbias"], db_bar + EPS * np.abs(r["dbias"]), "dbias")
+    again = V.layer_norm_backward(dev[1], dev[0], mean, rstd, dev[2])
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dw, db)))
+
+
 def test_large_mean(V):
     """A mean a thousand times the spread: the variance is taken from the
     distances, not from a difference of large numbers."""

@@ -158,6 +158,43 @@ def test_norm_and_product_past_32_bits(V):
     assert ((db.double() - want).abs() <= n * 2.0 ** -24 * mag).all() and torch.isfinite(dw).all()
 
 
+def test_norm_sums_and_product_rows_past_32_bits(V):
+    """The weight's and bias's sums over 1.7 million rows against sums in
+    float64, with a bar for the additions that there are, and the product's rows
+    bit for bit the same from every kernel: blocks of 32 x 32, tiles of 128 and
+    of 256."""
+    _say("norm's sums and the product's rows, 1.7 million rows")
+    n, width, e = 1_700_003, 1280, 1280
+    x, do = _fill((n, width), 5), _fill((n, width), 6)
+    w = torch.rand(width, generator=torch.Generator().manual_seed(7)).cuda()
+    _, mean, rstd = V.layer_norm(x, w, w, return_stats=True)
+    _, dw, db = V.layer_norm_backward(do, x, mean, rstd, w)
+    _, depth = N._sums_depth(V, n, width)
+    zero = lambda: torch.zeros(width, dtype=torch.float64, device="cuda")
+    want_w, want_b, mag_w, mag_b, hat_bar = zero(), zero(), zero(), zero(), zero()
+    rel = (width / 64 + 28 + 4 + 2) * A.EPS  # of rstd and of the distance; N._bars
+    for i in range(0, n, 1 << 16):
+        xx, g = x[i:i + (1 << 16)].double(), do[i:i + (1 << 16)].double()
+        var, mu = torch.var_mean(xx, dim=1, unbiased=False, keepdim=True)
+        hat = (xx - mu) / torch.sqrt(var + 1e-6)
+        want_w += (g * hat).sum(0)
+        want_b += g.sum(0)
+        mag_w += (g * hat).abs().sum(0)
+        mag_b += g.abs().sum(0)
+        # the mean's own error, D e mean|x| with mean|x| below the spread
+        hat_bar += (g.abs() * (rel * hat.abs() + (width / 64 + 20) * A.EPS)).sum(0)
+    for got, want, bar in ((dw, want_w, hat_bar + depth * A.EPS * mag_w), (db, want_b, depth * A.EPS * mag_b)):
+        bar = bar + A.EPS * want.abs()
+        assert bar.max() < want.abs().median()  # zeros would not pass
+        assert ((got.double() - want).abs() <= 1.01 * bar).all()
+    del do
+    wq, ws = V.quantize_rows(torch.randn((e, width), generator=torch.Generator().manual_seed(8)).cuda())
+    xq, xs = V.quantize_rows(x)
+    y = V.quantized_linear(xq, xs, wq, ws)
+    for at in (slice(0, 300), slice(n // 2, n // 2 + 32), slice(n // 2, n // 2 + 5000), slice(n - 17, n), slice(n - 300, n)):
+        assert torch.equal(V.quantized_linear(xq[at], xs[at], wq, ws), y[at])
+
+
 def test_more_rows_than_a_launch_dimension_holds(V):
     """17 million rows of a width that a workgroup takes: 2^32 threads and more."""
     _say("17 million rows")
