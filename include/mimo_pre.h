@@ -509,6 +509,9 @@ int mimo_pixel_embed(int32_t n, const mimo_image_desc *desc, const uint8_t *src,
  * softmax statistics and sums are float32, the probabilities are rounded to
  * bf16 before their product.  Values of a chunk have to be finite: a NaN or
  * an infinity in it may reach any of the chunk's rows, but no other chunk's.
+ * Logits have to stay below 2^28 in magnitude: a row with a larger one may
+ * hold anything.  In the backward pass p is off by the relative 2^-22 |s_ij|,
+ * the roundings of s and lse.
  * A sink is any number but NaN.  It counts as at most MIMO_SINK_MAX and, -inf
  * aside, as at least -MIMO_SINK_MAX, in lse too: there key 0 has all of a
  * row's weight, or none where the row sees another key, as long as the row's

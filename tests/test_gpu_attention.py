@@ -174,6 +174,26 @@ def test_scales(V, scale, spread):
     _check(V, [100, 300], 4, 2, 64, -1, True, seed=15, scale=scale, spread=spread)
 
 
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8])
+def test_large_logits(V, size):
+    """Logits of up to 10^8: one key takes each row, whichever has the largest
+    logit by more than float32's spacing there."""
+    _say("large logits", size)
+    n, d = 300, 64
+    g = torch.Generator().manual_seed(33)
+    k = torch.nn.functional.one_hot(torch.arange(n) % d, d).to(torch.bfloat16)[:, None]
+    k[64:] *= 0.5  # shorter copies of the first 64
+    q = (torch.nn.functional.one_hot(torch.randint(0, d, (n,), generator=g), d) * size).to(torch.bfloat16)[:, None]
+    v = torch.randn((n, 1, d), generator=g).to(torch.bfloat16)
+    r = tower.chunk_attention(_wide(q), _wide(k), _wide(v), [0, n], -1, 1.0)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse = V.chunk_attention(q.cuda(), k.cuda(), v.cuda(), cu, scale=1.0, return_lse=True)
+    # one probability, rounded to bf16, over itself; lse by way of powers of
+    # two: two constants, their products, the maximum, and the sum with its log
+    _within(out, r["out"], 2 * U * np.abs(r["out"]), "out")
+    _within(lse, r["lse"], 6 * EPS * np.abs(r["lse"]), "lse")
+
+
 def test_rising_logits(V):
     """Every step's maximum outgrows the last one's: keys grow along the chunk."""
     _say("rising logits")
