@@ -130,6 +130,24 @@ def test_attention_past_32_bits(V):
             assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
 
 
+def test_key_gradients_past_32_bits(V):
+    """dk and dv of chunks of a call of 1.1 million rows, bit for bit those of a
+    call of three chunks: enough of them that neither call's sums are sliced."""
+    _say("key gradients of 1.1 million rows")
+    length, chunks, hq, hk, d = 3520, 312, 32, 8, 64
+    n = length * chunks
+    q, k, v, do = _fill((n, hq, d), 11), _fill((n, hk, d), 12), _fill((n, hk, d), 13), _fill((n, hq, d), 14)
+    sink = torch.randn(hq, generator=torch.Generator().manual_seed(15)).cuda()
+    cu = torch.arange(chunks + 1, dtype=torch.int32, device="cuda") * length
+    out, lse = V.chunk_attention(q, k, v, cu, window=64, sink=sink, return_lse=True)
+    _, dk, dv, _ = V.chunk_attention_backward(do, q, k, v, out, lse, cu, window=64, sink=sink)
+    for c in (0, chunks // 2, chunks - 3):
+        at = slice(c * length, (c + 3) * length)
+        o, l = V.chunk_attention(q[at], k[at], v[at], cu[:4], window=64, sink=sink, return_lse=True)
+        g = V.chunk_attention_backward(do[at], q[at], k[at], v[at], o, l, cu[:4], window=64, sink=sink)
+        assert torch.equal(g[1], dk[at]) and torch.equal(g[2], dv[at])
+
+
 def test_norm_and_product_past_32_bits(V):
     _say("norm and product of 1.7 million rows")
     n, width, e = 1_700_003, 1280, 1280
