@@ -546,10 +546,13 @@ __global__ __launch_bounds__(kThreads, kD == 64 ? 4 : 1) void attention_forward_
 //
 // delta is do . out, which has out's rounding; the rounding of one row's
 // delta moves all of its ds alike, and where few keys share the probability
-// it is as large as the roundings of ds itself.  So rows that see at most
-// kFewKeys keys take delta = sum_j p_ij dp_ij, the same number, from a pass
-// over their keys of its own (two products more on a few keys); dsink, which
-// is float32, always does, at the end of the one pass.
+// it is as large as the roundings of ds itself.  So where no row sees more
+// than kFewKeys keys (the chunk is as short, or the band as narrow: a window
+// of 31 or less), delta = sum_j p_ij dp_ij, the same number, from a pass over
+// the keys of its own (two products more on a few keys).  Rows at a chunk's
+// ends see as few keys with a window of up to 63; they take do . out like the
+// others of their launch.  dsink, which is float32, always takes the sum, at
+// the end of the one pass.
 //
 // Three products a pair of row and key: 32 heads of 64 over 8 of 4096 rows
 // 1.53 ms, 1.08 PFLOP/s (VALU 67% of its cycles, matrix cores 60%).  With a
@@ -713,8 +716,11 @@ __device__ __forceinline__ void sum_dsink(const AttentionArgs &a, int head, doub
 // that their p is zero too, however large a sink makes it.
 //
 // Four products a pair: 32 heads of 64 over 8 of 4096 rows 1.98 ms, 1.11
-// PFLOP/s; matrix cores 57% of the cycles, LDS 43%, at the clock that the
-// card's power leaves (1.7 GHz).  With a band of 64, 16 x 3520 rows: 221 us,
+// PFLOP/s.  No unit is full there (matrix cores 57% of the cycles, VALU 45%,
+// LDS 43%): a wave's products, exponentials, packing and next products follow
+// from each other, and three waves a SIMD do not cover that.  16 heads of 128
+// over 2 of 4096 rows, both passes: 0.94 to 0.97 ms, 0.99 PFLOP/s, one wave a
+// SIMD.  With a band of 64, 16 x 3520 rows: 221 us,
 // 0.69 GB at 3.1 TB/s; its waves' keys see 160 of the 256 rows that the
 // workgroup's do (32 keys a workgroup, which read the rows 2.5 times as often,
 // gained nothing).
@@ -1008,7 +1014,10 @@ Workspace workspace_layout(const LaunchShape &l, int64_t rows, int32_t q_heads, 
     return w;
 }
 
-// The narrowest instance that holds head_dim: 64, 96 or 128 columns.
+// The narrowest instance that holds head_dim: 64, 96 or 128 columns.  What it
+// has beyond head_dim is multiplied as zeros: 32 heads on 8 over 8 of 4096 rows,
+// forward, 32 columns 1.02 ms and 64 1.14; 72, 80 and 96 columns 1.6 to 1.7; 128
+// 2.0 (backward 3.1 and 3.5; 4.8 to 5.1; 7.2).
 template <int kD, bool kBand>
 void launch_forward_as(const LaunchShape &l, const AttentionArgs &a, hipStream_t s) {
     const dim3 grid{unsigned(l.tiles) * unsigned(l.heads), 1, 1}, block{unsigned(kThreads), 1, 1};
