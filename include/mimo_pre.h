@@ -678,6 +678,99 @@ int mimo_quantize_rows(int64_t rows, int32_t width, const void *x, int32_t x_dty
 int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float *x_scale, int32_t embed_dim, const void *wq,
                           const float *w_scale, const float *bias, int32_t out_dtype, void *out, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows of embeddings with the residual's addition
+ * (NeMo Automodel "mimo_v2_flash.vision", MiMoVisionBlock: a norm before the
+ * attention and one before the feed-forward block, over the stream that the
+ * branch before it is added to), with its backward pass.  For a row of n values:
+ *   h = x + residual, rounded to the residual's type (h = x without one)
+ *   rstd = 1 / sqrt(sum h^2 / n + eps),  y = h rstd weight
+ * The norm is that of the rounded h, which the backward pass is given.  Rows
+ * are dense [rows][width]; those of a width that is a multiple of 8 at 16-byte
+ * aligned addresses run fastest.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Forward, one kernel launch; float32 inside, out rounded once.
+ *   width    in [1, 65536].
+ *   x        device, x_dtype (MIMO_F32 or MIMO_BF16).
+ *   residual device, residual_dtype (x_dtype or MIMO_F32), or NULL.
+ *   weight   device float32 [width], or NULL (ones).
+ *   eps      finite, >= 0.
+ *   residual_out  device, residual_dtype: h.  Not NULL with a residual (without
+ *            one it is not written); may be the residual, or x where the
+ *            dtypes agree.
+ *   out      device, out_dtype: y; may be x or the residual where the dtypes
+ *            agree, but not residual_out.
+ *   rstd     device float32 [rows], or NULL: the backward pass takes it.
+ * Pointers are aligned to their values.  Returns MIMO_OK, MIMO_E_INVALID,
+ * MIMO_E_TOO_LARGE (width, or more than 2^31 - 1 rows) or MIMO_E_HIP.
+ */
+int mimo_rms_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *residual, int32_t residual_dtype,
+                  const float *weight, double eps, void *residual_out, int32_t out_dtype, void *out, float *rstd,
+                  void *stream);
+
+/*
+ * The same to 8-bit rows as mimo_quantize_rows makes them, for
+ * mimo_quantized_linear: y in float32 (h * rstd rounded, times the weight
+ * rounded), scale[r] = max |y| / 127, q = y / scale rounded to nearest, ties to
+ * even (both float32 divisions); rstd is the float32 of a float64 sum's, so
+ * that the integers do not depend on an order of addition.  A row of zeros has
+ * the scale 0; a row whose y holds a NaN or an infinity has the scale NaN, and
+ * zeros.
+ *   q        device int8 [rows][padded], padded = width rounded up to a
+ *            multiple of 128 (the rest is set to zero), 16-byte aligned, not
+ *            an input.
+ *   scale    device float32 [rows].
+ * Other arguments and results as for mimo_rms_norm.
+ */
+int mimo_rms_norm_quantized(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *residual,
+                            int32_t residual_dtype, const float *weight, double eps, void *residual_out, void *q, float *scale,
+                            void *stream);
+
+/* Device workspace bytes of the backward pass (0 for sizes it refuses). */
+size_t mimo_rms_norm_workspace_bytes(int64_t rows, int32_t width);
+
+/*
+ * Backward, for h (residual_out, or x where there was no residual) and dout of
+ * dout_dtype: with g = dout weight, hh = h rstd and dresidual, the gradient
+ * that reaches h by the residual stream,
+ *   dx = dresidual + rstd (g - hh sum(g hh) / n)
+ *   dweight = sum over rows of dout hh
+ * dx is the gradient of x and of the residual alike.
+ *   dresidual  device, h_dtype, or NULL (zeros).
+ *   dx       device, h_dtype; may be dresidual, but not h or dout.
+ *   dweight  device float32 [width], or NULL; overwritten, its sum has a fixed
+ *            order; not an input.
+ *   workspace  device, >= mimo_rms_norm_workspace_bytes(rows, width), 16-byte
+ *            aligned, or NULL if dweight is; calls that may run at the same
+ *            time need one each.
+ * One kernel launch, and one for dweight (two for widths above 16384).
+ * Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h_dtype, const void *dout, int32_t dout_dtype,
+                           const float *weight, const float *rstd, const void *dresidual, void *dx, float *dweight,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotates the heads of every row by the tables of mimo_rotary_tables (NeMo
+ * Automodel "mimo_v2_flash.vision", _apply_rotary_pos_emb, _rotate_half):
+ * with half = head_dim / 2, for i < half and the row's c_i, s_i,
+ *   out_i = x_i c_i - x_{i+half} s_i,  out_{i+half} = x_{i+half} c_i + x_i s_i
+ * or with inverse != 0 by -s: the gradient of x is the inverse rotation of
+ * out's.  Float32 inside, rounded once.  Query and key heads that lie side by
+ * side (a slice of one projection's output) are one call.
+ *   rows     at most 2^29.
+ *   heads    in [1, 65536].
+ *   head_dim a multiple of 8 in [8, 2 * MIMO_ROPE_DIM_MAX].
+ *   x, out   bf16, as mimo_chunk_attention takes them; out may be x with x's
+ *            strides, and otherwise must not overlap it.
+ *   cos, sin device float32 [rows][half], 16-byte aligned.
+ * One kernel launch.  Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_rotate_heads(int64_t rows, int32_t heads, int32_t head_dim, const mimo_heads *x, const float *cos, const float *sin,
+                      int32_t inverse, const mimo_heads *out, void *stream);
+
 /*
  * Instrumentation.  When start and stop are non-null hipEvent_t handles
  * (passed as void*), every later kernel launch that the library makes on the

@@ -105,3 +105,52 @@ def quantized_linear(xq, x_scale, wq, w_scale, bias=None):
     s = np.asarray(x_scale, dtype=np.float64)[:, None] * np.asarray(w_scale, dtype=np.float64)[None, :]
     out = total * s
     return (out if bias is None else out + np.asarray(bias, dtype=np.float64)), np.abs(total * s)
+
+
+def _rounded(a, kind):
+    """float64 values to float32 ("f32") or bf16 ("bf16"), nearest even, as float64."""
+    f = np.asarray(a, dtype=np.float32)
+    if kind == "f32":
+        return f.astype(np.float64)
+    bits = f.view(np.uint32).astype(np.uint64)
+    bits = (bits + 0x7FFF + ((bits >> 16) & 1)) & 0xFFFF0000
+    return bits.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def residual_sum(x, residual, kind):
+    """The stream: a float32 sum, rounded to the residual's type."""
+    return _rounded(np.asarray(x, dtype=np.float32) + np.asarray(residual, dtype=np.float32), kind)
+
+
+def rms_norm(h, weight, eps, dout=None, dresidual=None):
+    """h [rows, n] (float64), weight [n] or None.
+
+    Returns a dict: out, rstd, hat, and with dout dx, dweight, g, s."""
+    n = h.shape[1]
+    rstd = 1.0 / np.sqrt((h * h).sum(axis=1) / n + eps)
+    hat = h * rstd[:, None]
+    w = np.ones(n) if weight is None else weight
+    r = {"out": hat * w, "rstd": rstd, "hat": hat}
+    if dout is not None:
+        g = dout * w
+        s = (g * hat).sum(axis=1) / n
+        dx = rstd[:, None] * (g - hat * s[:, None])
+        r.update(dx=dx if dresidual is None else dx + dresidual, dweight=(dout * hat).sum(axis=0), g=g, s=s)
+    return r
+
+
+def rms_norm_quantized(h, weight, eps):
+    """(q, scale) by the definition: y in float32 from the float32 of rstd."""
+    rstd = (1.0 / np.sqrt((h * h).sum(axis=1) / h.shape[1] + eps)).astype(np.float32)
+    y = h.astype(np.float32) * rstd[:, None]
+    if weight is not None:
+        y = y * np.asarray(weight, dtype=np.float32)
+    return quantize_rows(y)
+
+
+def rotate_heads(x, cos, sin, inverse=False):
+    """x [rows, heads, d], cos and sin [rows, d / 2] (float64); (out, sum of magnitudes)."""
+    half = x.shape[2] // 2
+    a, b, c, s = x[..., :half], x[..., half:], cos[:, None], sin[:, None] * (-1.0 if inverse else 1.0)
+    out = np.concatenate((a * c - b * s, b * c + a * s), axis=2)
+    return out, np.concatenate((abs(a * c) + abs(b * s), abs(b * c) + abs(a * s)), axis=2)

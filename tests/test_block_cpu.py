@@ -1,0 +1,90 @@
+"""What the block's operators refuse, and with which code: in the C entry
+points, before anything touches a GPU, and in the Python functions."""
+import struct
+
+import pytest
+
+import vision_image_preprocessing_amd as V
+
+torch = pytest.importorskip("torch")
+
+P = 1 << 20  # an address that is never used: every call here is refused (or has nothing to do) before a launch
+F, B = V.MIMO_F32, V.MIMO_BF16
+
+
+def _forward(rows=4, width=64, x=P, xd=F, r=2 * P, rd=F, w=3 * P, eps=1e-6, h=4 * P, od=F, out=5 * P, rstd=6 * P):
+    return V.load().mimo_rms_norm(rows, width, x, xd, r, rd, w, eps, h, od, out, rstd, None)
+
+
+def _quantized(rows=4, width=64, x=P, xd=F, r=2 * P, rd=F, w=3 * P, eps=1e-6, h=4 * P, q=5 * P, s=6 * P):
+    return V.load().mimo_rms_norm_quantized(rows, width, x, xd, r, rd, w, eps, h, q, s, None)
+
+
+BOTH = [dict(rows=-1), dict(width=0), dict(xd=2), dict(xd=-1), dict(rd=3), dict(rd=B), dict(eps=-1.0), dict(eps=float("nan")),
+        dict(eps=float("inf")), dict(x=None), dict(x=P + 2), dict(xd=B, x=P + 1), dict(r=2 * P + 2), dict(xd=B, rd=B, r=P + 1),
+        dict(h=None), dict(h=4 * P + 1), dict(w=P + 2), dict(xd=B, h=P), dict(h=5 * P)]
+
+
+@pytest.mark.parametrize("bad", BOTH + [dict(od=2), dict(od=-1), dict(out=None), dict(out=P + 2), dict(rstd=P + 1),
+                                        dict(out=P, od=B), dict(out=2 * P, od=B)])
+def test_norm_refuses(bad):
+    before = V.dispatch_count()
+    assert _forward(**bad) == V.MIMO_E_INVALID
+    assert V.last_error().startswith("rms_norm:") and V.dispatch_count() == before
+
+
+@pytest.mark.parametrize("bad", BOTH + [dict(q=None), dict(q=P + 8), dict(q=P), dict(q=2 * P), dict(s=None), dict(s=P + 2)])
+def test_quantized_norm_refuses(bad):
+    assert _quantized(**bad) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm_quantized:")
+
+
+def test_norm_sizes():
+    for call in (_forward, _quantized):
+        assert call(width=65537) == V.MIMO_E_TOO_LARGE and call(rows=1 << 31) == V.MIMO_E_TOO_LARGE
+        assert call(rows=0, x=None, r=None, h=None) == V.MIMO_OK
+
+
+def test_norm_backward_refuses():
+    lib = V.load()
+    need = V.rms_norm_workspace_bytes(4, 64)
+    assert need >= 64 * 4 and V.rms_norm_workspace_bytes(-1, 64) == 0
+    assert V.rms_norm_workspace_bytes(4, 65537) == 0 and V.rms_norm_workspace_bytes(1 << 31, 4) == 0
+
+    def backward(rows=4, width=64, h=P, hd=F, g=2 * P, gd=F, w=3 * P, rstd=4 * P, dr=5 * P, dx=6 * P, dw=7 * P, ws=P, n=need):
+        return lib.mimo_rms_norm_backward(rows, width, h, hd, g, gd, w, rstd, dr, dx, dw, ws, n, None)
+
+    for bad in (dict(rows=-1), dict(width=0), dict(hd=7), dict(gd=2), dict(h=None), dict(g=None), dict(rstd=None), dict(dx=None),
+                dict(dx=P), dict(dx=2 * P), dict(dw=P + 2), dict(ws=None), dict(ws=P + 8), dict(h=P + 2), dict(gd=B, g=P + 1),
+                dict(w=P + 2), dict(rstd=P + 2), dict(dr=P + 2), dict(dw=3 * P), dict(dw=4 * P)):
+        assert backward(**bad) == V.MIMO_E_INVALID, bad
+    assert backward(n=need - 1) == V.MIMO_E_CAPACITY
+    assert backward(width=65537) == V.MIMO_E_TOO_LARGE and backward(rows=1 << 31) == V.MIMO_E_TOO_LARGE
+    assert backward(rows=0, dw=None, h=None, dx=None) == V.MIMO_OK
+
+
+def test_rotation_refuses():
+    lib = V.load()
+    heads = lambda p=P, row=256, head=64: struct.pack("<Qqq", p, row, head)
+
+    def rotate(rows=10, n=4, d=64, x=heads(), cos=2 * P, sin=3 * P, out=heads(4 * P)):
+        return lib.mimo_rotate_heads(rows, n, d, x, cos, sin, 0, out, None)
+
+    before = V.dispatch_count()
+    for bad in (dict(rows=-1), dict(n=0), dict(n=65537), dict(d=0), dict(d=4), dict(d=60), dict(d=520), dict(x=None), dict(out=None),
+                dict(x=heads(0)), dict(x=heads(P + 8)), dict(x=heads(P, 252)), dict(x=heads(P, 56)), dict(x=heads(P, 256, 60)),
+                dict(x=heads(P, 256, -64)), dict(x=heads(P, (1 << 22) + 8)), dict(out=heads(0)), dict(out=heads(4 * P, 64)),
+                dict(out=heads(4 * P, 256, 0)), dict(out=heads(4 * P, 192)), dict(out=heads(P, 512)), dict(out=heads(P, 264, 64)),
+                dict(out=heads(4 * P, 64, 576)), dict(cos=None), dict(sin=None), dict(cos=P + 4), dict(sin=P + 8)):
+        assert rotate(**bad) == V.MIMO_E_INVALID, bad
+        assert V.last_error().startswith("rotate_heads:")
+    assert rotate(rows=(1 << 29) + 1) == V.MIMO_E_TOO_LARGE
+    assert rotate(rows=0, x=heads(0), cos=None) == V.MIMO_OK and V.dispatch_count() == before
+
+
+def test_functions_refuse_what_is_not_on_a_gpu():
+    x, w = torch.zeros((4, 64)), torch.ones(64)
+    for call in (lambda: V.rms_norm(x, w), lambda: V.rms_norm(x, w, x), lambda: V.rms_norm_quantized(x, w),
+                 lambda: V.rms_norm_backward(x, x, torch.ones(4), w),
+                 lambda: V.rotate_heads(torch.zeros((4, 2, 32), dtype=torch.bfloat16), torch.zeros((4, 16)), torch.zeros((4, 16)))):
+        with pytest.raises(Exception):
+            call()

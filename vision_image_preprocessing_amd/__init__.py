@@ -34,7 +34,8 @@ from .processor import (  # noqa: F401
 # The tower's operators work on torch tensors throughout: their module, and
 # torch with it, is imported when the first of them is asked for.
 _TOWER = ("chunk_attention", "chunk_attention_backward", "chunk_attention_workspace_bytes", "layer_norm",
-          "layer_norm_backward", "layer_norm_workspace_bytes", "quantize_rows", "quantized_linear")
+          "layer_norm_backward", "layer_norm_workspace_bytes", "quantize_rows", "quantized_linear", "rms_norm",
+          "rms_norm_quantized", "rms_norm_backward", "rms_norm_workspace_bytes", "rotate_heads")
 
 
 def __getattr__(name):

@@ -113,6 +113,11 @@ SIGNATURES = {
     "mimo_layer_norm_backward": ([_I64, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "mimo_quantize_rows": ([_I64, _I32, _P, _I32, _P, _P, _P], ctypes.c_int),
     "mimo_quantized_linear": ([_I64, _I32, _P, _P, _I32, _P, _P, _P, _I32, _P, _P], ctypes.c_int),
+    "mimo_rms_norm": ([_I64, _I32, _P, _I32, _P, _I32, _P, ctypes.c_double, _P, _I32, _P, _P, _P], ctypes.c_int),
+    "mimo_rms_norm_quantized": ([_I64, _I32, _P, _I32, _P, _I32, _P, ctypes.c_double, _P, _P, _P, _P], ctypes.c_int),
+    "mimo_rms_norm_workspace_bytes": ([_I64, _I32], _SZ),
+    "mimo_rms_norm_backward": ([_I64, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "mimo_rotate_heads": ([_I64, _I32, _I32, _P, _P, _P, _I32, _P, _P], ctypes.c_int),
 }
 
 _lock = threading.Lock()

@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmimopre.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["plan.cpp", "runtime.hip", "preprocess.hip", "vit_tables.hip", "patch_embed.hip", "hf_resize.hip",
-           "pixel_embed.hip", "chunk_attention.hip", "layer_norm.hip", "quantized_linear.hip"]
+           "pixel_embed.hip", "chunk_attention.hip", "layer_norm.hip", "quantized_linear.hip",
+           "rms_norm.hip", "rotate_heads.hip"]
 # Code-generation options of one source only.  The contrast kernel's
 # matrix-core products chain through VALU shifts, so their accumulators
 # belong in ordinary VGPRs, as do the attention kernels', which the softmax

@@ -48,50 +48,6 @@ struct QuantizeArgs {
     int32_t width, padded;
 };
 
-// |v| as an unsigned integer: the order of the magnitudes, NaN above all.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
-
-template <int kThreadsRow>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *lds) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = max(v, uint32_t(__shfl_xor(int(v), m)));
-    if constexpr (kThreadsRow == 256) {
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = max(max(lds[0], lds[1]), max(lds[2], lds[3]));
-    }
-    return v;
-}
-
-// Eight quotients as bytes.  The definition divides in float32 (rounded
-// correctly) and takes the nearest integer, ties to even.  A product with the
-// reciprocal is within 2^-15 of the quotient (|quotient| <= 128, two
-// roundings of 2^-24 and the quotient's own), so where it is further than
-// kNear from the middle of two integers it rounds to the same one; only where
-// one of the eight is not are they divided, which costs three times as much
-// (131072 x 1536 bf16: 137 us, 116% of the VALU's cycles, with divisions
-// throughout).  Scales below kSmall hold few bits or have no reciprocal: they
-// are divided too, and their quotients may pass 127.
-constexpr float kNear = 1e-3f, kSmall = 1e-30f;
-__device__ __forceinline__ u32x2 quantize(const float (&v)[8], float scale, float inv) {
-    float r[8];
-    float off = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float y = v[j] * inv;
-        r[j] = __builtin_rintf(y);
-        off = fmaxf(off, fabsf(y - r[j]));
-    }
-    if (off > 0.5f - kNear || scale < kSmall) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = fminf(fmaxf(__builtin_rintf(v[j] / scale), -127.0f), 127.0f);
-    }
-    u32x2 p = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t(int(r[j])) & 0xFFu) << (8 * (j % 4));
-    return p;
-}
-
 // One row by a wave (kThreadsRow = 64) or the workgroup, held in registers
 // (kChunks chunks of eight values a thread), or read twice (kChunks = 0).
 // 131072 x 1536 bf16: 107 to 119 us, 0.60 GB at 5.1 to 5.6 TB/s, with the VALU

@@ -1,5 +1,6 @@
 // row_ops.h -- what the kernels over rows of embeddings share: eight values
-// of a row in registers, and sums over the threads that hold one row.
+// of a row in registers, sums and maxima over the threads that hold one row,
+// and its values as 8-bit integers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -106,10 +107,10 @@ __device__ __forceinline__ void store_values(__bf16 *p, int n, const float (&v)[
 }
 
 // Sum over the kThreads (64: a wave, more: the workgroup) threads of a row,
-// in a fixed order; every one of them gets it.  `lds`: kThreads / 64 floats
+// in a fixed order; every one of them gets it.  `lds`: kThreads / 64 values
 // that no other reduction in flight uses.
-template <int kThreads>
-__device__ __forceinline__ float row_sum(float v, float *lds) {
+template <int kThreads, typename T>
+__device__ __forceinline__ T row_sum(T v, T *lds) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
     if constexpr (kThreads > 64) {
@@ -120,6 +121,50 @@ __device__ __forceinline__ float row_sum(float v, float *lds) {
         for (int i = 4; i < kThreads / 64; i += 4) v += (lds[i] + lds[i + 1]) + (lds[i + 2] + lds[i + 3]);
     }
     return v;
+}
+
+// |v| as an unsigned integer: the order of the magnitudes, NaN above all.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+template <int kThreadsRow>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *lds) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v = max(v, uint32_t(__shfl_xor(int(v), m)));
+    if constexpr (kThreadsRow == 256) {
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = max(max(lds[0], lds[1]), max(lds[2], lds[3]));
+    }
+    return v;
+}
+
+// Eight quotients as bytes.  The definition divides in float32 (rounded
+// correctly) and takes the nearest integer, ties to even.  A product with the
+// reciprocal is within 2^-15 of the quotient (|quotient| <= 128, two
+// roundings of 2^-24 and the quotient's own), so where it is further than
+// kNear from the middle of two integers it rounds to the same one; only where
+// one of the eight is not are they divided, which costs three times as much
+// (131072 x 1536 bf16: 137 us, 116% of the VALU's cycles, with divisions
+// throughout).  Scales below kSmall hold few bits or have no reciprocal: they
+// are divided too, and their quotients may pass 127.
+constexpr float kNear = 1e-3f, kSmall = 1e-30f;
+__device__ __forceinline__ u32x2 quantize(const float (&v)[8], float scale, float inv) {
+    float r[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float y = v[j] * inv;
+        r[j] = __builtin_rintf(y);
+        off = fmaxf(off, fabsf(y - r[j]));
+    }
+    if (off > 0.5f - kNear || scale < kSmall) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = fminf(fmaxf(__builtin_rintf(v[j] / scale), -127.0f), 127.0f);
+    }
+    u32x2 p = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t(int(r[j])) & 0xFFu) << (8 * (j % 4));
+    return p;
 }
 
 }  // namespace rows

@@ -1,6 +1,7 @@
 """The vision tower's operators over patch embeddings, on torch tensors:
-attention over the plan's chunks and layer norm, each with its backward pass,
-and the matrix product in 8-bit integers.
+attention over the plan's chunks, the rotation of its heads, layer norm and
+root-mean-square norm with the residual, each with its backward pass, and the
+matrix product in 8-bit integers.
 
 Argument checks and allocation only: the work runs in the HIP library
 (``include/mimo_pre.h``), on the tensors' device and on ``stream`` (default:
@@ -32,6 +33,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 # mimo_attention and mimo_attention_grads (include/mimo_pre.h)
 _ATTENTION = struct.Struct("<q5if2Q" + "Qqq" * 4 + "Q")
 _GRADS = struct.Struct("<" + "Qqq" * 4 + "Q")
+_HEADS = struct.Struct("<Qqq")  # mimo_heads
 
 _lib = None
 
@@ -383,6 +385,211 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, dx=None, dweight=None,
 def layer_norm_workspace_bytes(rows: int, width: int) -> int:
     """mimo_layer_norm_workspace_bytes."""
     return int(_library().mimo_layer_norm_workspace_bytes(int(rows), int(width)))
+
+
+# ------------------------------------------------------ root-mean-square norm
+
+def _check_stream(what, x, weight, residual, residual_out):
+    """The arguments that both forms of the norm share; (rows, width)."""
+    rows, width = _rows_of(what, x, 65536)
+    if weight is not None:
+        _check_vector(what, "weight", weight, width, _F32)
+    if residual is not None:
+        _check_matrix(what, "residual", residual)
+        _check_shape(what, "residual", residual, x.shape)
+        if residual.dtype is not x.dtype and residual.dtype is not _F32:
+            _refuse(f"{what}: residual must be of x's dtype or float32, got {residual.dtype} with x {x.dtype}")
+        if residual_out is not None:
+            _check_matrix(what, "residual_out", residual_out, (residual.dtype,))
+            _check_shape(what, "residual_out", residual_out, x.shape)
+    elif residual_out is not None:
+        _refuse(f"{what}: residual_out is given without residual")
+    return rows, width
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None, out_dtype=None, residual_out=None,
+             return_rstd: bool = False, rstd=None, stream=None):
+    """mimo_rms_norm: h * rstd * weight of each row of h = x + residual, rounded
+    to the residual's dtype (h = x without one), rstd = 1 / sqrt(mean(h ** 2) +
+    eps).
+
+    x [rows, width] (float32 or bf16, contiguous); residual of x's shape, its
+    dtype or float32; weight float32 [width] or None.  Returns out [rows, width]
+    of out_dtype ("f32" or "bf16"; x's by default), followed by h with a
+    residual, and by rstd (float32 [rows], which the backward pass takes) with
+    return_rstd=True.  residual_out (where h goes) may be the residual itself,
+    or x where the dtypes agree; out may be x or the residual where the dtypes
+    agree, but not residual_out.
+    """
+    what = "rms_norm"
+    rows, _ = _check_stream(what, x, weight, residual, residual_out)
+    if rstd is not None:
+        _check_vector(what, "rstd", rstd, rows, _F32)
+    if out is not None:
+        _check_matrix(what, "out", out)
+        _check_shape(what, "out", out, x.shape)
+        dtype = out.dtype
+    else:
+        dtype = x.dtype if out_dtype is None else _out_type(what, out_dtype)
+    index = x.get_device()
+    if (index < 0 or (weight is not None and weight.get_device() != index) or (residual is not None and residual.get_device() != index)
+            or (out is not None and out.get_device() != index) or (residual_out is not None and residual_out.get_device() != index)
+            or (rstd is not None and rstd.get_device() != index)):
+        _check_devices(what, (x, weight, residual, out, residual_out, rstd))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (x, weight, residual, out, residual_out, rstd)):
+            return rms_norm(x, weight, residual, eps, out, out_dtype, residual_out, return_rstd, rstd)
+    if out is None:
+        out = torch.empty_like(x, dtype=dtype)
+    if return_rstd and rstd is None:
+        rstd = x.new_empty(rows, dtype=_F32)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    code = _library().mimo_rms_norm(rows, x.shape[1], x.data_ptr(), _CODES[x.dtype], _pointer(residual),
+                                    0 if residual is None else _CODES[residual.dtype], _pointer(weight), eps,
+                                    _pointer(residual_out), _CODES[dtype], out.data_ptr(), _pointer(rstd), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    if residual is None:
+        return (out, rstd) if return_rstd else out
+    return (out, residual_out, rstd) if return_rstd else (out, residual_out)
+
+
+def rms_norm_quantized(x, weight=None, residual=None, eps: float = 1e-6, q=None, scale=None, residual_out=None, stream=None):
+    """mimo_rms_norm_quantized: rms_norm's rows as 8-bit integers with a scale
+    for each, as quantize_rows makes them, for quantized_linear.
+
+    Arguments as for rms_norm.  Returns (q, scale), or with a residual (q,
+    scale, h): int8 [rows, padded], padded = width rounded up to a multiple of
+    128 (zeros behind width), and float32 [rows].
+    """
+    what = "rms_norm_quantized"
+    rows, width = _check_stream(what, x, weight, residual, residual_out)
+    padded = (width + 127) & -128
+    if q is not None:
+        _check_matrix(what, "q", q, (_I8,))
+        _check_shape(what, "q", q, (rows, padded))
+    if scale is not None:
+        _check_vector(what, "scale", scale, rows, _F32)
+    index = x.get_device()
+    if (index < 0 or (weight is not None and weight.get_device() != index) or (residual is not None and residual.get_device() != index)
+            or (q is not None and q.get_device() != index) or (scale is not None and scale.get_device() != index)
+            or (residual_out is not None and residual_out.get_device() != index)):
+        _check_devices(what, (x, weight, residual, q, scale, residual_out))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (x, weight, residual, q, scale, residual_out)):
+            return rms_norm_quantized(x, weight, residual, eps, q, scale, residual_out)
+    if q is None:
+        q = x.new_empty((rows, padded), dtype=_I8)
+    if scale is None:
+        scale = x.new_empty(rows, dtype=_F32)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    code = _library().mimo_rms_norm_quantized(rows, width, x.data_ptr(), _CODES[x.dtype], _pointer(residual),
+                                              0 if residual is None else _CODES[residual.dtype], _pointer(weight), eps,
+                                              _pointer(residual_out), q.data_ptr(), scale.data_ptr(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    return (q, scale) if residual is None else (q, scale, residual_out)
+
+
+def rms_norm_backward(dout, h, rstd, weight=None, dresidual=None, dx=None, dweight=None, affine=None, workspace=None,
+                      stream=None):
+    """mimo_rms_norm_backward: the gradients of rms_norm's x (and of its
+    residual: they are the same) and weight for dout [rows, width] (float32 or
+    bf16), given what was normed (h of the forward call, or x where it had no
+    residual) and its rstd.  dresidual, of h's shape and dtype, is the gradient
+    that reaches h by the residual stream; it is added.
+
+    Returns (dx, dweight): h's dtype, and float32 [width].  dweight is made
+    where weight or dweight is given, or with affine=True, and is None
+    otherwise.  dx may be dresidual.  ``workspace``: uint8, at least
+    rms_norm_workspace_bytes(rows, width) bytes; calls that may run at the same
+    time need one each.
+    """
+    what = "rms_norm_backward"
+    _check_matrix(what, "h", h)
+    rows, width = _rows_of(what, h, 65536)
+    _check_matrix(what, "dout", dout)
+    _check_shape(what, "dout", dout, h.shape)
+    if rstd is None:
+        _refuse(f"{what}: rstd is needed (rms_norm returns it with return_rstd=True)")
+    _check_vector(what, "rstd", rstd, rows, _F32)
+    if weight is not None:
+        _check_vector(what, "weight", weight, width, _F32)
+    if dweight is not None:
+        _check_vector(what, "dweight", dweight, width, _F32)
+    for name, t in (("dresidual", dresidual), ("dx", dx)):
+        if t is not None:
+            _check_matrix(what, name, t, (h.dtype,))
+            _check_shape(what, name, t, h.shape)
+    if workspace is not None:
+        _abi._check_bytes(workspace, what + ": workspace")
+    index = h.get_device()
+    tensors = (h, dout, rstd, weight, dresidual, dx, dweight, workspace)
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _check_devices(what, tensors)
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, tensors):
+            return rms_norm_backward(dout, h, rstd, weight, dresidual, dx, dweight, affine, workspace)
+    if dx is None:
+        dx = torch.empty_like(h)
+    if dweight is None and (weight is not None if affine is None else affine):
+        dweight = h.new_empty(width, dtype=_F32)
+    lib = _library()
+    if workspace is None and dweight is not None:
+        workspace = h.new_empty(max(lib.mimo_rms_norm_workspace_bytes(rows, width), 16), dtype=torch.uint8)
+    code = lib.mimo_rms_norm_backward(rows, width, h.data_ptr(), _CODES[h.dtype], dout.data_ptr(), _CODES[dout.dtype],
+                                      _pointer(weight), rstd.data_ptr(), _pointer(dresidual), dx.data_ptr(), _pointer(dweight),
+                                      _pointer(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    return dx, dweight
+
+
+def rms_norm_workspace_bytes(rows: int, width: int) -> int:
+    """mimo_rms_norm_workspace_bytes."""
+    return int(_library().mimo_rms_norm_workspace_bytes(int(rows), int(width)))
+
+
+# ------------------------------------------------------ rotation of the heads
+
+def rotate_heads(x, cos, sin, inverse: bool = False, out=None, stream=None):
+    """mimo_rotate_heads: the rotary embedding of query and key heads (vision
+    page, _apply_rotary_pos_emb, _rotate_half) by vit_tables' rope_cos and
+    rope_sin, float32 [rows, head_dim / 2]; with inverse=True the inverse
+    rotation, which takes the gradient of the output to that of x.
+
+    x bf16 [rows, heads, head_dim], head_dim a multiple of 8, strides as
+    chunk_attention takes them: query and key heads that are one slice of a
+    projection's output are one call.  Returns out, of x's shape; it may be x.
+    """
+    what = "rotate_heads"
+    if x.dim() != 3:
+        _refuse(f"{what}: x must be [rows, heads, head_dim], got {tuple(x.shape)}")
+    rows, heads, dim = x.shape
+    if heads < 1 or dim < 8 or dim % 8:
+        _refuse(f"{what}: x must have heads of a multiple of 8 columns, got {tuple(x.shape)}")
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t.dtype is not _F32 or t.shape != (rows, dim // 2) or not t.is_contiguous():
+            _refuse(f"{what}: {name} must be contiguous float32 [{rows}, {dim // 2}], got {tuple(t.shape)} {t.dtype}")
+    if rows > 0x20000000:
+        _refuse_size(f"{what}: more than 2^29 rows: {rows}")
+    index = x.get_device()
+    if index < 0 or cos.get_device() != index or sin.get_device() != index or (out is not None and out.get_device() != index):
+        _check_devices(what, (x, cos, sin, out))
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, (x, cos, sin, out)):
+            return rotate_heads(x, cos, sin, inverse, out)
+    source = _HEADS.pack(*_heads(what, "x", x, x.shape))
+    if out is None:
+        out = _dense_like(x)
+    code = _library().mimo_rotate_heads(rows, heads, dim, source, cos.data_ptr(), sin.data_ptr(), 1 if inverse else 0,
+                                        _HEADS.pack(*_heads(what, "out", out, x.shape)), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    return out
 
 
 # ------------------------------------------------------ 8-bit matrix product
