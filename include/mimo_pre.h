@@ -771,6 +771,79 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
 int mimo_rotate_heads(int64_t rows, int32_t heads, int32_t head_dim, const mimo_heads *x, const float *cos, const float *sin,
                       int32_t inverse, const mimo_heads *out, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block (NeMo Automodel "mimo_v2_flash.vision", the SwiGLU
+ * MLP of MiMoVisionBlock), forward and backward.  For rows x of `width` values
+ * and `hidden_width` hidden ones, with weights as a checkpoint has them, by
+ * output channels:
+ *   g = x Wg' + bg,  u = x Wu' + bu,  h = silu(g) u,  out = h Wd' + bd
+ * Runs on the matrix cores in bf16; sums are float32, h and the gradients dg
+ * and du are rounded to bf16 as operands of the next product, outputs once.
+ * Results do not depend on how calls run next to each other (no atomics); how
+ * sums are split depends on the sizes alone.
+ * ------------------------------------------------------------------------ */
+
+/* Matrices are dense, on the device, 16-byte aligned, bf16 unless said.  Widths
+ * that are multiples of 8 run fastest; operands of others are first copied into
+ * the workspace, padded. */
+typedef struct mimo_mlp {
+    int64_t rows;          /* at most 2^31 - 1 */
+    int32_t width;         /* both in [1, 65536] */
+    int32_t hidden_width;
+    const void *x;         /* [rows][width] */
+    const void *w_gate;    /* [hidden_width][width] */
+    const void *w_up;      /* [hidden_width][width] */
+    const void *w_down;    /* [width][hidden_width] */
+    const float *b_gate;   /* float32 [hidden_width], or NULL (forward only) */
+    const float *b_up;     /* the same */
+    const float *b_down;   /* float32 [width], or NULL (forward only) */
+    float *gate_up;        /* float32 [2][rows][padded]: g and u, padded = hidden_width rounded up to a multiple of 64 */
+    void *hidden;          /* [rows][padded]: h; both have zeros behind hidden_width */
+} mimo_mlp;
+
+typedef struct mimo_mlp_grads {
+    const void *dout;      /* [rows][width] */
+    void *dx;              /* [rows][width], or NULL */
+    void *dw_gate, *dw_up; /* [hidden_width][width], or NULL */
+    void *dw_down;         /* [width][hidden_width], or NULL */
+    float *db_gate, *db_up; /* float32 [hidden_width], or NULL */
+    float *db_down;        /* float32 [width], or NULL */
+} mimo_mlp_grads;
+
+/* Device workspace bytes of the forward pass (0 for sizes it refuses). */
+size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidden_width);
+
+/*
+ * Forward: writes out, bf16 [rows][width], and gate_up and hidden unless both
+ * are NULL (the backward pass needs them).  out must not be an input.
+ *   workspace  device, >= mimo_gated_mlp_workspace_bytes(...), 16-byte
+ *              aligned; calls that may run at the same time need one each.
+ * Two kernel launches; one more where K of the second is split (few rows), and
+ * one for each operand that is copied.  Returns MIMO_OK, MIMO_E_INVALID,
+ * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE (rows or widths, or more than 2^24 - 1
+ * tiles) or MIMO_E_HIP.
+ */
+int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace bytes of the backward pass (0 for sizes it refuses). */
+size_t mimo_gated_mlp_backward_workspace_bytes(int64_t rows, int32_t width, int32_t hidden_width);
+
+/*
+ * Backward: args as the forward call's, with the gate_up and hidden that it
+ * wrote (biases are not read).  With s = 1 / (1 + exp -g):
+ *   dh = dout Wd,  dg = dh u s (1 + g (1 - s)),  du = dh g s
+ *   dx = dg Wg + du Wu,  dWg = dg' x,  dWu = du' x,  dWd = dout' h
+ * and the biases' gradients are the sums over rows of dg, du (before they are
+ * rounded) and dout.  Gradients are overwritten; those that are NULL are not
+ * made.  None may be an input or another one.
+ *   workspace  device, >= mimo_gated_mlp_backward_workspace_bytes(...), 16-byte
+ *              aligned; calls that may run at the same time need one each.
+ * Three kernel launches, one or two more for each bias, and as above.  Returns
+ * MIMO_OK, MIMO_E_INVALID, MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ */
+int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
 /*
  * Instrumentation.  When start and stop are non-null hipEvent_t handles
  * (passed as void*), every later kernel launch that the library makes on the

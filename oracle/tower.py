@@ -154,3 +154,23 @@ def rotate_heads(x, cos, sin, inverse=False):
     a, b, c, s = x[..., :half], x[..., half:], cos[:, None], sin[:, None] * (-1.0 if inverse else 1.0)
     out = np.concatenate((a * c - b * s, b * c + a * s), axis=2)
     return out, np.concatenate((abs(a * c) + abs(b * s), abs(b * c) + abs(a * s)), axis=2)
+
+
+def gated_mlp(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, dout=None):
+    """All float64; a dict: gate, up, silu, hidden, out, and with dout dhidden,
+    slope (of silu), dgate, dup, dx, dw_gate, dw_up, dw_down, db_gate, db_up,
+    db_down."""
+    zero = lambda b: 0.0 if b is None else b
+    g, u = x @ w_gate.T + zero(b_gate), x @ w_up.T + zero(b_up)
+    with np.errstate(over="ignore"):
+        s = 1.0 / (1.0 + np.exp(-g))
+    silu = g * s
+    h = silu * u
+    r = {"gate": g, "up": u, "silu": silu, "hidden": h, "out": h @ w_down.T + zero(b_down)}
+    if dout is not None:
+        dh = dout @ w_down
+        slope = s * (1.0 + g * (1.0 - s))
+        dg, du = dh * u * slope, dh * silu
+        r.update(dhidden=dh, slope=slope, dgate=dg, dup=du, dx=dg @ w_gate + du @ w_up, dw_gate=dg.T @ x, dw_up=du.T @ x,
+                 dw_down=dout.T @ h, db_gate=dg.sum(axis=0), db_up=du.sum(axis=0), db_down=dout.sum(axis=0))
+    return r

@@ -88,3 +88,60 @@ def test_functions_refuse_what_is_not_on_a_gpu():
                  lambda: V.rotate_heads(torch.zeros((4, 2, 32), dtype=torch.bfloat16), torch.zeros((4, 16)), torch.zeros((4, 16)))):
         with pytest.raises(Exception):
             call()
+
+
+def _mlp(rows=4, width=64, hidden=72, x=P, wg=2 * P, wu=3 * P, wd=4 * P, bg=5 * P, bu=6 * P, bd=7 * P, gu=8 * P, h=9 * P):
+    return V.tower._MLP.pack(rows, width, hidden, x, wg, wu, wd, bg, bu, bd, gu, h)
+
+
+def _mlp_grads(dout=11 * P, dx=12 * P, dwg=13 * P, dwu=14 * P, dwd=15 * P, dbg=16 * P, dbu=17 * P, dbd=18 * P):
+    return V.tower._MLP_GRADS.pack(dout, dx, dwg, dwu, dwd, dbg, dbu, dbd)
+
+
+def test_mlp_refuses():
+    lib = V.load()
+    need = V.gated_mlp_workspace_bytes(4, 64, 72)
+    assert need >= 4 * 128 * 2
+
+    def forward(out=10 * P, ws=20 * P, n=need, **kw):
+        return lib.mimo_gated_mlp(_mlp(**kw), out, ws, n, None)
+
+    before = V.dispatch_count()
+    for bad in (dict(rows=-1), dict(width=0), dict(hidden=0), dict(x=0), dict(wg=0), dict(wu=0), dict(wd=0), dict(out=None), dict(x=P + 8),
+                dict(wg=P + 2), dict(wu=P + 4), dict(wd=P + 8), dict(out=P + 8), dict(bg=P + 2), dict(bu=P + 1), dict(bd=P + 2), dict(gu=0),
+                dict(h=0), dict(gu=P + 8), dict(h=P + 8), dict(out=P), dict(out=2 * P), dict(out=3 * P), dict(out=4 * P), dict(out=8 * P),
+                dict(out=9 * P), dict(ws=None), dict(ws=P + 8)):
+        assert forward(**bad) == V.MIMO_E_INVALID, bad
+        assert V.last_error().startswith("gated_mlp:")
+    assert forward(n=need - 1) == V.MIMO_E_CAPACITY and lib.mimo_gated_mlp(None, P, P, need, None) == V.MIMO_E_INVALID
+    for bad in (dict(rows=1 << 31), dict(width=65537), dict(hidden=65537), dict(rows=1 << 30, hidden=65536)):
+        assert forward(**bad) == V.MIMO_E_TOO_LARGE, bad
+    assert forward(rows=0, x=0, out=None, ws=None) == V.MIMO_OK and V.dispatch_count() == before
+    for sizes in ((-1, 64, 72), (4, 0, 72), (4, 64, 0), (1 << 31, 64, 72), (4, 65537, 72), (4, 64, 65537), (1 << 30, 64, 65536)):
+        assert V.gated_mlp_workspace_bytes(*sizes) == 0 and V.gated_mlp_backward_workspace_bytes(*sizes) == 0
+
+
+def test_mlp_backward_refuses():
+    lib = V.load()
+    need = V.gated_mlp_backward_workspace_bytes(4, 64, 72)
+    assert need >= 2 * 4 * 128 * 2
+
+    def backward(args=None, ws=20 * P, n=need, **kw):
+        return lib.mimo_gated_mlp_backward(_mlp(**(args or {})), _mlp_grads(**kw), ws, n, None)
+
+    for bad in (dict(rows=-1), dict(width=0), dict(x=0), dict(wg=0), dict(wu=0), dict(wd=0), dict(gu=0), dict(h=0), dict(x=P + 8), dict(h=P + 8)):
+        assert backward(args=bad) == V.MIMO_E_INVALID, bad
+        assert V.last_error().startswith("gated_mlp_backward:")
+    for bad in (dict(dout=0), dict(dout=P + 8), dict(dx=P + 8), dict(dwg=P + 2), dict(dwu=P + 4), dict(dwd=P + 8), dict(dbg=P + 2), dict(dbu=P + 1),
+                dict(dbd=P + 2), dict(dx=P), dict(dx=11 * P), dict(dwg=2 * P), dict(dwd=9 * P), dict(dx=8 * P), dict(dwg=14 * P), dict(dbg=17 * P),
+                dict(dx=15 * P), dict(ws=None), dict(ws=P + 8)):
+        assert backward(**bad) == V.MIMO_E_INVALID, bad
+    assert backward(n=need - 1) == V.MIMO_E_CAPACITY
+    assert lib.mimo_gated_mlp_backward(_mlp(), None, P, need, None) == V.MIMO_E_INVALID
+    assert lib.mimo_gated_mlp_backward(None, _mlp_grads(), P, need, None) == V.MIMO_E_INVALID
+    assert backward(args=dict(width=65537)) == V.MIMO_E_TOO_LARGE
+    assert backward(args=dict(rows=0), dwg=0, dwu=0, dwd=0, dbg=0, dbu=0, dbd=0, ws=None) == V.MIMO_OK
+
+
+def test_mlp_structs_are_as_the_header_lays_them_out():
+    assert V.tower._MLP.size == 16 + 9 * 8 and V.tower._MLP_GRADS.size == 8 * 8

@@ -35,7 +35,8 @@ from .processor import (  # noqa: F401
 # torch with it, is imported when the first of them is asked for.
 _TOWER = ("chunk_attention", "chunk_attention_backward", "chunk_attention_workspace_bytes", "layer_norm",
           "layer_norm_backward", "layer_norm_workspace_bytes", "quantize_rows", "quantized_linear", "rms_norm",
-          "rms_norm_quantized", "rms_norm_backward", "rms_norm_workspace_bytes", "rotate_heads")
+          "rms_norm_quantized", "rms_norm_backward", "rms_norm_workspace_bytes", "rotate_heads", "gated_mlp",
+          "gated_mlp_backward", "gated_mlp_workspace_bytes", "gated_mlp_backward_workspace_bytes")
 
 
 def __getattr__(name):

@@ -118,6 +118,10 @@ SIGNATURES = {
     "mimo_rms_norm_workspace_bytes": ([_I64, _I32], _SZ),
     "mimo_rms_norm_backward": ([_I64, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "mimo_rotate_heads": ([_I64, _I32, _I32, _P, _P, _P, _I32, _P, _P], ctypes.c_int),
+    "mimo_gated_mlp_workspace_bytes": ([_I64, _I32, _I32], _SZ),
+    "mimo_gated_mlp": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
+    "mimo_gated_mlp_backward_workspace_bytes": ([_I64, _I32, _I32], _SZ),
+    "mimo_gated_mlp_backward": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
 }
 
 _lock = threading.Lock()

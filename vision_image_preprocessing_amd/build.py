@@ -15,7 +15,7 @@ LIB_NAME = "libmimopre.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["plan.cpp", "runtime.hip", "preprocess.hip", "vit_tables.hip", "patch_embed.hip", "hf_resize.hip",
            "pixel_embed.hip", "chunk_attention.hip", "layer_norm.hip", "quantized_linear.hip",
-           "rms_norm.hip", "rotate_heads.hip"]
+           "rms_norm.hip", "rotate_heads.hip", "gated_mlp.hip"]
 # Code-generation options of one source only.  The contrast kernel's
 # matrix-core products chain through VALU shifts, so their accumulators
 # belong in ordinary VGPRs, as do the attention kernels', which the softmax

@@ -1,0 +1,700 @@
+// gated_mlp.hip -- the gated feed-forward block and its backward pass on the
+// bf16 matrix cores of AMD Instinct MI355X (gfx950, CDNA4).
+//
+// What is computed (NeMo Automodel "mimo_v2_flash.vision": the SwiGLU MLP of
+// MiMoVisionBlock), for rows x of D values and H hidden ones:
+//   g = x Wg' + bg,  u = x Wu' + bu,  h = silu(g) u,  out = h Wd' + bd
+// with silu(g) = g s, s = 1 / (1 + exp -g); and for dout:
+//   dh = dout Wd,  dg = dh u s (1 + g (1 - s)),  du = dh g s
+//   dx = dg Wg + du Wu,  dWg = dg' x,  dWu = du' x,  dWd = dout' h
+//   dbg = sum over rows of dg, and so on
+//
+// Launches.  Forward: both projections, the activation and the product are one
+// kernel, whose tiles hold gate and up of the same channels, so h is formed
+// from the accumulators and g, u need not be written; then the projection back.
+// Backward: dh's product, whose epilogue forms dg and du; dx over both halves
+// of its K; the three weights' gradients in one launch.
+//
+// Roundings: sums are float32 on the matrix cores; h, dg and du are rounded to
+// bf16, once, as operands of the next product, as x, dout and the weights come
+// in; outputs are rounded once.  For the backward pass g and u are kept in
+// float32: in bf16 their rounding would add half as much again to the error of
+// dx and the weights' gradients as the operands' own (relative to them 1.85
+// roundings instead of 1.41), and to the biases' gradients, which are float32
+// sums of unrounded dg and du, all of theirs.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "column_sums.h"
+#include "device_util.h"
+#include "gemm_tile.h"
+#include "internal.h"
+#include "row_ops.h"
+#include "runtime.h"
+
+namespace mimo {
+namespace {
+
+using namespace gemm;
+using rows::row_grid;
+using rows::row_group;
+
+constexpr int kMaxWidth = 65536;
+constexpr int kMaxTiles = (1 << 24) - 1;
+constexpr int kPad = 64;  // rows of hidden values, and copied operands, are multiples of this
+
+struct MlpArgs {
+    Product p[3];
+    uint16_t *out[3];            // bf16 [m][ldo]
+    int64_t ldo[3];
+    int32_t products, tiles;
+    const float *bias0, *bias1;  // or null
+    float *gate_up;              // [2][rows][ldh], or null
+    uint16_t *hidden;            // [rows][ldh]
+    uint16_t *dgate, *dup;       // [rows][ldh]
+    float *part;                 // partial sums: of split products, or of dg and du over rows; or null
+    int64_t ldh;
+    int32_t part_stride;         // of split products' rows
+};
+
+// Eight channels to bf16, at any address of the type; `left` of them inside.
+__device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[8], int left) {
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    bf16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
+    if (left >= 8) {
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<any_u32x4 *>(p));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < left) reinterpret_cast<__bf16 *>(p)[j] = h[j];
+    }
+}
+// The same where the next kernel reads it: kept in cache.
+__device__ __forceinline__ void keep_bf16(uint16_t *p, const float (&v)[8]) {
+    bf16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
+    *reinterpret_cast<bf16x8 *>(p) = h;
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+// Biases of eight channels from c on, of n.
+__device__ __forceinline__ void load_bias(const float *bias, int c, int n, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = bias ? bias[min(c + j, n - 1)] : 0.0f;
+}
+
+// s = 1 / (1 + exp -g): the hardware's exponential and reciprocal, each to
+// about a unit in the last place of float32.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// The tile's five buffers: 160 KB, one workgroup a CU, with 256; 80 KB, two, with 128.
+#define MIMO_TILE_BUFFERS(kTile)                                                                  \
+    __shared__ __attribute__((aligned(16))) uint8_t sx0[kTile * 128], sx1[kTile * 128], sx2[kTile * 128]; \
+    __shared__ __attribute__((aligned(16))) uint8_t sw0[kTile * 128], sw1[kTile * 128];           \
+    const Buffers<kTile> lds{{sx0, sx1, sx2}, {sw0, sw1}}
+
+// Stages of a split of a product.
+__device__ __forceinline__ void part_of(const Product &p, int split, int &begin, int &end) {
+    const int stages = (p.k + kStageK - 1) / kStageK * p.segments;
+    begin = int(int64_t(stages) * split / p.splits);
+    end = int(int64_t(stages) * (split + 1) / p.splits);
+}
+
+// h = silu(x Wg' + bg) (x Wu' + bu).
+template <int kTile>
+__global__ __launch_bounds__(kThreads) void mlp_gate_kernel(MlpArgs a) {
+    MIMO_TILE_BUFFERS(kTile);
+    constexpr int kWave = kTile / 2, kHalf = kWave / 2, kBlocks = kWave / 32;
+    const Product &p = a.p[0];
+    const Place at(p, int(xcd_contiguous_tile(blockIdx.x, gridDim.x)));
+    const int64_t m0 = at.mt * kTile;
+    const int n0 = at.nt * (kTile / 2);
+    f32x16 acc[kBlocks][kBlocks];
+    multiply<kTile, false, false, true>(p, m0, n0, 0, (p.k + kStageK - 1) / kStageK, lds, acc);
+    const Turned<kTile> turned(lds);
+    constexpr int kLanes = kHalf / 8, kPass = 64 / kLanes;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kHalf + piece;
+    float bg[8], bu[8];
+    load_bias(a.bias0, col, p.n, bg);
+    load_bias(a.bias1, col, p.n, bu);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+        turned.put(acc[i]);
+#pragma unroll
+        for (int t = 0; t < 32 / kPass; ++t) {
+            const int r = t * kPass + lane / kLanes;
+            float g[8], u[8], h[8];
+            turned.template get<8>(r, piece, g);
+            turned.template get<8>(r, kHalf + piece, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool in = col + j < p.n;
+                g[j] = in ? g[j] + bg[j] : 0.0f;
+                u[j] = in ? u[j] + bu[j] : 0.0f;
+                h[j] = g[j] * sigmoid(g[j]) * u[j];
+            }
+            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            if (row >= p.m || col >= a.ldh) continue;
+            keep_bf16(a.hidden + row * a.ldh + col, h);
+            if (a.gate_up) {
+                store8(a.gate_up + row * a.ldh + col, g);
+                store8(a.gate_up + (p.m + row) * a.ldh + col, u);
+            }
+        }
+    }
+}
+
+// dg and du from dh = dout Wd and the saved g, u; partial sums of both over
+// the rows of each half of the tile.
+template <int kTile>
+__global__ __launch_bounds__(kThreads) void mlp_dhidden_kernel(MlpArgs a) {
+    MIMO_TILE_BUFFERS(kTile);
+    constexpr int kWave = kTile / 2, kBlocks = kWave / 32;
+    const Product &p = a.p[0];
+    const Place at(p, int(xcd_contiguous_tile(blockIdx.x, gridDim.x)));
+    const int64_t m0 = at.mt * kTile;
+    const int n0 = at.nt * kTile;
+    f32x16 acc[kBlocks][kBlocks];
+    multiply<kTile, false, true, false>(p, m0, n0, 0, (p.k + kStageK - 1) / kStageK, lds, acc);
+    const Turned<kTile> turned(lds);
+    constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kWave + piece;
+    float sg[8] = {}, su[8] = {};
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+        turned.put(acc[i]);
+#pragma unroll
+        for (int t = 0; t < 32 / kPass; ++t) {
+            const int r = t * kPass + lane / kLanes;
+            float dh[8], g[8], u[8];
+            turned.template get<8>(r, piece, dh);
+            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            if (row >= p.m || col >= a.ldh) continue;
+            load8(a.gate_up + row * a.ldh + col, g);
+            load8(a.gate_up + (p.m + row) * a.ldh + col, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float s = sigmoid(g[j]), d = col + j < p.n ? dh[j] : 0.0f;
+                dh[j] = d * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
+                u[j] = d * (g[j] * s);
+                sg[j] += dh[j];
+                su[j] += u[j];
+            }
+            keep_bf16(a.dgate + row * a.ldh + col, dh);
+            keep_bf16(a.dup + row * a.ldh + col, u);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int m = kLanes; m < 64; m <<= 1) {
+            sg[j] += __shfl_xor(sg[j], m);
+            su[j] += __shfl_xor(su[j], m);
+        }
+    if (lane < kLanes && col < a.ldh) {
+        float *part = a.part + (2 * at.mt + (wave >> 1)) * 2 * a.ldh + col;
+        store8(part, sg);
+        store8(part + a.ldh, su);
+    }
+}
+
+// Products whose sums are the output: out = h Wd' + bd (kWAcross false), dx
+// (kWAcross), the weights' gradients (both across), or a split's partial sums.
+template <int kTile, bool kXAcross, bool kWAcross>
+__global__ __launch_bounds__(kThreads) void mlp_product_kernel(MlpArgs a) {
+    MIMO_TILE_BUFFERS(kTile);
+    constexpr int kWave = kTile / 2, kBlocks = kWave / 32;
+    const int tile = int(xcd_contiguous_tile(blockIdx.x, gridDim.x));
+    int n = 0;
+    if constexpr (kXAcross) n = a.products > 2 && tile >= a.p[2].first ? 2 : a.products > 1 && tile >= a.p[1].first ? 1 : 0;
+    const Product &p = a.p[n];
+    const Place at(p, tile - p.first);
+    const int64_t m0 = at.mt * kTile;
+    const int n0 = at.nt * kTile;
+    int begin, end;
+    part_of(p, at.split, begin, end);
+    f32x16 acc[kBlocks][kBlocks];
+    multiply<kTile, kXAcross, kWAcross, false>(p, m0, n0, begin, end, lds, acc);
+    const Turned<kTile> turned(lds);
+    constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kWave + piece, left = p.n - col;
+    float bias[8];
+    load_bias(p.splits > 1 ? nullptr : a.bias0, col, p.n, bias);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+        turned.put(acc[i]);
+#pragma unroll
+        for (int t = 0; t < 32 / kPass; ++t) {
+            const int r = t * kPass + lane / kLanes;
+            float v[8];
+            turned.template get<8>(r, piece, v);
+            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            if (row >= p.m || left <= 0) continue;
+            if (p.splits > 1) {
+                store8(a.part + (at.split * p.m + row) * a.part_stride + col, v);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += bias[j];
+            store_bf16(a.out[n] + row * a.ldo[n] + col, v, left);
+        }
+    }
+}
+
+// out = the sum of the splits' parts, in their order, + bias.
+__global__ __launch_bounds__(256) void mlp_join_kernel(const float *part, int32_t splits, int64_t m, int32_t n, int32_t stride,
+                                                       const float *bias, uint16_t *out, int64_t ldo) {
+    const int pieces = (n + 7) / 8;
+    const int64_t id = row_group() * 256 + threadIdx.x, row = id / pieces;
+    if (row >= m) return;
+    const int col = int(id - row * pieces) * 8;
+    float v[8];
+    load8(part + row * stride + col, v);
+    for (int s = 1; s < splits; ++s) {
+        float w[8];
+        load8(part + (s * m + row) * stride + col, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += w[j];
+    }
+    float b[8];
+    load_bias(bias, col, n, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+    store_bf16(out + row * ldo + col, v, n - col);
+}
+
+// Rows of any width to rows of a multiple of kPad values, zeros behind: the
+// products read 16 bytes at a time.
+__global__ __launch_bounds__(256) void mlp_pad_kernel(const uint16_t *x, int64_t rows, int32_t width, uint16_t *out, int32_t padded) {
+    const int pieces = padded / 8;
+    const int64_t id = row_group() * 256 + threadIdx.x, row = id / pieces;
+    if (row >= rows) return;
+    const int col = int(id - row * pieces) * 8, left = width - col;
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    const uint16_t *p = x + row * width + col;
+    u32x4 v;
+    if (left >= 8) {
+        v = *reinterpret_cast<const any_u32x4 *>(p);
+    } else {
+        u16x8 h;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = j < left ? p[j] : uint16_t(0);
+        v = __builtin_bit_cast(u32x4, h);
+    }
+    *reinterpret_cast<u32x4 *>(out + row * padded + col) = v;
+}
+
+// Partial sums over every gridDim.y-th group of eight rows of 256 columns.
+__global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int64_t rows, int64_t stride, int32_t columns, float *part) {
+    __shared__ float lds[8][256 + 8];
+    const int lane = threadIdx.x % 32, first = threadIdx.x / 32;
+    const int col = blockIdx.x * 256 + lane * 8;
+    float v[8] = {};
+    if (col < columns) {
+        for (int64_t row = int64_t(blockIdx.y) * 8 + first; row < rows; row += int64_t(gridDim.y) * 8) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(x + row * stride + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] += __builtin_bit_cast(float, w[j] << 16);
+                v[2 * j + 1] += __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lds[first][lane * 8 + j] = v[j];
+    __syncthreads();
+    float sum = lds[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += lds[i][threadIdx.x];
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c < columns) part[int64_t(blockIdx.y) * columns + c] = sum;
+}
+
+int64_t pad_to(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
+int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// How a product is cut into tiles: 256 x 256 where there are enough of them
+// for the card, else 128 x 128, and K into parts where there are few.
+struct Cut {
+    int tile;
+    int64_t m_tiles, n_tiles;
+    int splits;
+    int64_t tiles() const { return m_tiles * n_tiles * splits; }
+};
+constexpr int kCus = 256;
+Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable) {
+    const int64_t big = ceil_div(m, 256) * ceil_div(n, 256);
+    if (big >= kCus) return {256, ceil_div(m, 256), ceil_div(n, 256), 1};
+    Cut c{128, ceil_div(m, 128), ceil_div(n, 128), 1};
+    const int64_t tiles = c.m_tiles * c.n_tiles;
+    // two workgroups a CU, at least six stages each
+    if (splittable && tiles > 0) {
+        const int64_t most = stages / 6, wanted = 2 * kCus / tiles;
+        c.splits = int(wanted < most ? wanted : most);
+        if (c.splits < 1) c.splits = 1;
+    }
+    return c;
+}
+
+struct Sizes {
+    int64_t rows, d, h;
+    bool pad_d, pad_h;   // rows of d (h) values are copied to padded ones
+    int64_t dp, hp;      // strides of such copies; hp of hidden values too
+    Sizes(int64_t rows, int64_t d, int64_t h)
+        : rows(rows), d(d), h(h), pad_d(d % 8 != 0), pad_h(h % 8 != 0), dp(pad_to(d, kPad)), hp(pad_to(h, kPad)) {}
+    int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
+    int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
+    // gate and up of a channel lie in one tile
+    Cut gate() const {
+        Cut c = cut(rows, 2 * h, ceil_div(d, kStageK), false);
+        c.n_tiles = ceil_div(h, c.tile / 2);
+        return c;
+    }
+    Cut down() const { return cut(rows, d, ceil_div(h, kStageK), true); }
+    Cut dhidden() const { return cut(rows, h, ceil_div(d, kStageK), false); }
+    Cut dx() const { return cut(rows, d, 2 * ceil_div(h, kStageK), true); }
+};
+
+// Takes aligned parts of a workspace, or measures them.
+struct Carver {
+    uint8_t *base;
+    size_t used = 0;
+    template <typename T>
+    T *take(int64_t values) {
+        T *p = reinterpret_cast<T *>(base + used);
+        used += align256(size_t(values) * sizeof(T));
+        return p;
+    }
+};
+
+struct ForwardSpace {
+    uint16_t *hidden, *x, *wg, *wu, *wd;
+    float *part;
+    size_t bytes;
+    ForwardSpace(const Sizes &s, void *base) {
+        Carver c{static_cast<uint8_t *>(base)};
+        hidden = c.take<uint16_t>(s.rows * s.hp);
+        x = c.take<uint16_t>(s.pad_d ? s.rows * s.dp : 0);
+        wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
+        wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
+        wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
+        const Cut k = s.down();
+        part = c.take<float>(k.splits > 1 ? k.splits * s.rows * pad_to(s.d, 8) : 0);
+        bytes = c.used;
+    }
+};
+
+constexpr int kColumnGroups = 128;  // workgroups along the rows of mlp_columns_kernel
+struct BackwardSpace {
+    uint16_t *dgate, *dup, *x, *dout, *wg, *wu, *wd;
+    float *part, *sums, *columns;
+    size_t bytes;
+    BackwardSpace(const Sizes &s, void *base) {
+        Carver c{static_cast<uint8_t *>(base)};
+        dgate = c.take<uint16_t>(s.rows * s.hp);
+        dup = c.take<uint16_t>(s.rows * s.hp);
+        x = c.take<uint16_t>(s.pad_d ? s.rows * s.dp : 0);
+        dout = c.take<uint16_t>(s.pad_d ? s.rows * s.dp : 0);
+        wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
+        wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
+        wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
+        const Cut k = s.dx();
+        part = c.take<float>(k.splits > 1 ? k.splits * s.rows * pad_to(s.d, 8) : 0);
+        sums = c.take<float>(2 * s.dhidden().m_tiles * 2 * s.hp);
+        columns = c.take<float>(kColumnGroups * s.d);
+        bytes = c.used;
+    }
+};
+
+Matrix matrix(const void *p, int64_t stride) { return Matrix{static_cast<const uint16_t *>(p), stride}; }
+
+Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t k, const Cut &c) {
+    Product p;
+    std::memset(&p, 0, sizeof(p));
+    p.x[0] = p.x[1] = x;
+    p.w[0] = p.w[1] = w;
+    p.m = m;
+    p.n = int32_t(n);
+    p.k = int32_t(k);
+    p.segments = 1;
+    p.splits = c.splits;
+    p.m_tiles = int32_t(c.m_tiles);
+    p.n_tiles = int32_t(c.n_tiles);
+    return p;
+}
+
+void pad(const void *x, int64_t rows, int64_t width, uint16_t *out, int64_t padded, hipStream_t s) {
+    const int64_t blocks = ceil_div(rows * (padded / 8), 256);
+    if (blocks)
+        hipLaunchKernelGGL(mlp_pad_kernel, row_grid(blocks), dim3(256, 1, 1), 0, s, static_cast<const uint16_t *>(x), rows,
+                           int32_t(width), out, int32_t(padded));
+}
+
+void join(const MlpArgs &a, hipStream_t s) {
+    const Product &p = a.p[0];
+    const int64_t blocks = ceil_div(p.m * ceil_div(p.n, 8), 256);
+    hipLaunchKernelGGL(mlp_join_kernel, row_grid(blocks), dim3(256, 1, 1), 0, s, a.part, p.splits, p.m, p.n, a.part_stride,
+                       a.bias0, a.out[0], a.ldo[0]);
+}
+
+int check_mlp(const mimo_mlp *p, const char *who) {
+    const std::string w(who);
+    if (!p) return set_error(MIMO_E_INVALID, w + ": null arguments");
+    if (p->rows < 0 || p->width < 1 || p->hidden_width < 1)
+        return set_error(MIMO_E_INVALID, w + ": rows must be >= 0, width and hidden_width >= 1");
+    if (p->rows > 0x7FFFFFFFll || p->width > kMaxWidth || p->hidden_width > kMaxWidth)
+        return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 rows, or a width above 65536");
+    const Sizes s(p->rows, p->width, p->hidden_width);
+    for (const Cut &c : {s.gate(), s.down(), s.dhidden(), s.dx()})
+        if (c.tiles() > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
+    return MIMO_OK;
+}
+
+bool is_aligned(const void *p) { return p && check_ptr_align(p, 16); }
+
+}  // namespace
+}  // namespace mimo
+
+using namespace mimo;
+
+extern "C" {
+
+size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidden_width) {
+    const mimo_mlp p{rows, width, hidden_width, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    if (check_mlp(&p, "gated_mlp") != MIMO_OK) {
+        clear_error();
+        return 0;
+    }
+    return ForwardSpace(Sizes(rows, width, hidden_width), nullptr).bytes;
+}
+
+int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t workspace_bytes, void *stream) {
+    clear_error();
+    const char *who = "gated_mlp";
+    int st = check_mlp(args, who);
+    if (st != MIMO_OK) return st;
+    if (args->rows == 0) return MIMO_OK;
+    if (!is_aligned(args->x) || !is_aligned(args->w_gate) || !is_aligned(args->w_up) || !is_aligned(args->w_down) || !is_aligned(out))
+        return set_error(MIMO_E_INVALID, "gated_mlp: x, the weights and out must be non-null and 16-byte aligned");
+    if (!check_ptr_align(args->b_gate, 4) || !check_ptr_align(args->b_up, 4) || !check_ptr_align(args->b_down, 4))
+        return set_error(MIMO_E_INVALID, "gated_mlp: biases must be 4-byte aligned");
+    if ((args->gate_up != nullptr) != (args->hidden != nullptr) || !check_ptr_align(args->gate_up, 16) || !check_ptr_align(args->hidden, 16))
+        return set_error(MIMO_E_INVALID, "gated_mlp: gate_up and hidden are given together, 16-byte aligned, or neither is");
+    if (out == args->x || out == args->w_gate || out == args->w_up || out == args->w_down || out == args->hidden || out == args->gate_up)
+        return set_error(MIMO_E_INVALID, "gated_mlp: out must not be an input or a saved tensor");
+    if (!is_aligned(workspace)) return set_error(MIMO_E_INVALID, "gated_mlp: workspace must be non-null and 16-byte aligned");
+    const Sizes z(args->rows, args->width, args->hidden_width);
+    const ForwardSpace space(z, workspace);
+    if (workspace_bytes < space.bytes)
+        return set_error(MIMO_E_CAPACITY, "gated_mlp: workspace smaller than mimo_gated_mlp_workspace_bytes");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int launches = 2;
+    const void *x = args->x, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
+    uint16_t *hidden = args->hidden ? static_cast<uint16_t *>(args->hidden) : space.hidden;
+    const Cut gate = z.gate(), down = z.down();
+    const hipError_t e = timed_launch(s, [&] {
+        if (z.pad_d) {
+            pad(x, z.rows, z.d, space.x, z.dp, s);
+            pad(wg, z.h, z.d, space.wg, z.dp, s);
+            pad(wu, z.h, z.d, space.wu, z.dp, s);
+            x = space.x;
+            wg = space.wg;
+            wu = space.wu;
+            launches += 3;
+        }
+        if (z.pad_h) {
+            pad(wd, z.d, z.h, space.wd, z.hp, s);
+            wd = space.wd;
+            ++launches;
+        }
+        MlpArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.p[0] = product(matrix(x, z.ld()), matrix(wg, z.ld()), z.rows, z.h, z.d, gate);
+        a.p[0].w[1] = matrix(wu, z.ld());
+        a.bias0 = args->b_gate;
+        a.bias1 = args->b_up;
+        a.gate_up = args->gate_up;
+        a.hidden = hidden;
+        a.ldh = z.hp;
+        const dim3 block{unsigned(kThreads), 1, 1};
+        if (gate.tile == 256)
+            hipLaunchKernelGGL(mlp_gate_kernel<256>, dim3(unsigned(gate.tiles()), 1, 1), block, 0, s, a);
+        else
+            hipLaunchKernelGGL(mlp_gate_kernel<128>, dim3(unsigned(gate.tiles()), 1, 1), block, 0, s, a);
+        a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down);
+        a.out[0] = static_cast<uint16_t *>(out);
+        a.ldo[0] = z.d;
+        a.bias0 = args->b_down;
+        a.part = space.part;
+        a.part_stride = int32_t(pad_to(z.d, 8));
+        a.products = 1;
+        if (down.tile == 256)
+            hipLaunchKernelGGL((mlp_product_kernel<256, false, false>), dim3(unsigned(down.tiles()), 1, 1), block, 0, s, a);
+        else
+            hipLaunchKernelGGL((mlp_product_kernel<128, false, false>), dim3(unsigned(down.tiles()), 1, 1), block, 0, s, a);
+        if (down.splits > 1) {
+            join(a, s);
+            ++launches;
+        }
+    });
+    if (e != hipSuccess) return hip_error(e, "gated_mlp: kernel launch");
+    g_dispatches.fetch_add(launches);
+    return MIMO_OK;
+}
+
+size_t mimo_gated_mlp_backward_workspace_bytes(int64_t rows, int32_t width, int32_t hidden_width) {
+    const mimo_mlp p{rows, width, hidden_width, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    if (check_mlp(&p, "gated_mlp_backward") != MIMO_OK) {
+        clear_error();
+        return 0;
+    }
+    return BackwardSpace(Sizes(rows, width, hidden_width), nullptr).bytes;
+}
+
+int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    clear_error();
+    const char *who = "gated_mlp_backward";
+    int st = check_mlp(args, who);
+    if (st != MIMO_OK) return st;
+    if (!grads) return set_error(MIMO_E_INVALID, "gated_mlp_backward: null gradients");
+    void *const made[] = {grads->dx, grads->dw_gate, grads->dw_up, grads->dw_down, grads->db_gate, grads->db_up, grads->db_down};
+    const bool any_weight = grads->dw_gate || grads->dw_up || grads->dw_down;
+    const bool any_bias = grads->db_gate || grads->db_up || grads->db_down;
+    if (!check_ptr_align(grads->dx, 16) || !check_ptr_align(grads->dw_gate, 16) || !check_ptr_align(grads->dw_up, 16) ||
+        !check_ptr_align(grads->dw_down, 16) || !check_ptr_align(grads->db_gate, 4) || !check_ptr_align(grads->db_up, 4) ||
+        !check_ptr_align(grads->db_down, 4))
+        return set_error(MIMO_E_INVALID, "gated_mlp_backward: dx and the weights' gradients must be 16-byte aligned, the biases' 4-byte");
+    if (args->rows == 0 && !any_weight && !any_bias) return MIMO_OK;
+    if (args->rows > 0) {
+        if (!is_aligned(args->x) || !is_aligned(args->w_gate) || !is_aligned(args->w_up) || !is_aligned(args->w_down) ||
+            !is_aligned(grads->dout) || !is_aligned(args->gate_up) || !is_aligned(args->hidden))
+            return set_error(MIMO_E_INVALID, "gated_mlp_backward: x, the weights, dout, gate_up and hidden must be non-null and 16-byte aligned");
+        const void *const inputs[] = {args->x, args->w_gate, args->w_up, args->w_down, grads->dout, args->gate_up, args->hidden};
+        for (const void *m : made)
+            for (const void *i : inputs)
+                if (m && m == i) return set_error(MIMO_E_INVALID, "gated_mlp_backward: a gradient must not be an input");
+    }
+    for (int i = 0; i < 7; ++i)
+        for (int j = 0; j < i; ++j)
+            if (made[i] && made[i] == made[j]) return set_error(MIMO_E_INVALID, "gated_mlp_backward: gradients must not be one array");
+    if (!is_aligned(workspace)) return set_error(MIMO_E_INVALID, "gated_mlp_backward: workspace must be non-null and 16-byte aligned");
+    const Sizes z(args->rows, args->width, args->hidden_width);
+    const BackwardSpace space(z, workspace);
+    if (workspace_bytes < space.bytes)
+        return set_error(MIMO_E_CAPACITY, "gated_mlp_backward: workspace smaller than mimo_gated_mlp_backward_workspace_bytes");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int launches = 0;
+    const void *x = args->x, *dout = grads->dout, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
+    const Cut dhidden = z.dhidden(), dx = z.dx();
+    const dim3 block{unsigned(kThreads), 1, 1};
+    const hipError_t e = timed_launch(s, [&] {
+        if (z.rows > 0 && z.pad_d) {
+            pad(x, z.rows, z.d, space.x, z.dp, s);
+            pad(dout, z.rows, z.d, space.dout, z.dp, s);
+            pad(wg, z.h, z.d, space.wg, z.dp, s);
+            pad(wu, z.h, z.d, space.wu, z.dp, s);
+            x = space.x;
+            dout = space.dout;
+            wg = space.wg;
+            wu = space.wu;
+            launches += 4;
+        }
+        if (z.rows > 0 && z.pad_h) {
+            pad(wd, z.d, z.h, space.wd, z.hp, s);
+            wd = space.wd;
+            ++launches;
+        }
+        MlpArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.gate_up = args->gate_up;
+        a.ldh = z.hp;
+        if (z.rows > 0) {
+            a.p[0] = product(matrix(dout, z.ld()), matrix(wd, z.lh()), z.rows, z.h, z.d, dhidden);
+            a.dgate = space.dgate;
+            a.dup = space.dup;
+            a.part = grads->db_gate || grads->db_up ? space.sums : nullptr;
+            if (dhidden.tile == 256)
+                hipLaunchKernelGGL(mlp_dhidden_kernel<256>, dim3(unsigned(dhidden.tiles()), 1, 1), block, 0, s, a);
+            else
+                hipLaunchKernelGGL(mlp_dhidden_kernel<128>, dim3(unsigned(dhidden.tiles()), 1, 1), block, 0, s, a);
+            ++launches;
+        }
+        const int32_t halves = z.rows > 0 ? int32_t(2 * dhidden.m_tiles) : 0;
+        if (grads->db_gate) launch_column_sums(space.sums, halves, 2 * z.hp, z.h, grads->db_gate, s), ++launches;
+        if (grads->db_up) launch_column_sums(space.sums + z.hp, halves, 2 * z.hp, z.h, grads->db_up, s), ++launches;
+        if (grads->db_down) {
+            const int64_t groups = z.rows == 0 ? 0 : ceil_div(z.rows, 8) < kColumnGroups ? ceil_div(z.rows, 8) : kColumnGroups;
+            if (groups)
+                hipLaunchKernelGGL(mlp_columns_kernel, dim3(unsigned(ceil_div(z.d, 256)), unsigned(groups), 1), dim3(256, 1, 1), 0, s,
+                                   static_cast<const uint16_t *>(dout), z.rows, z.ld(), int32_t(z.d), space.columns);
+            launch_column_sums(space.columns, int32_t(groups), z.d, z.d, grads->db_down, s);
+            launches += groups ? 2 : 1;
+        }
+        if (z.rows > 0 && grads->dx) {
+            a.p[0] = product(matrix(space.dgate, z.hp), matrix(wg, z.ld()), z.rows, z.d, z.h, dx);
+            a.p[0].x[1] = matrix(space.dup, z.hp);
+            a.p[0].w[1] = matrix(wu, z.ld());
+            a.p[0].segments = 2;
+            a.products = 1;
+            a.out[0] = static_cast<uint16_t *>(grads->dx);
+            a.ldo[0] = z.d;
+            a.part = space.part;
+            a.part_stride = int32_t(pad_to(z.d, 8));
+            if (dx.tile == 256)
+                hipLaunchKernelGGL((mlp_product_kernel<256, false, true>), dim3(unsigned(dx.tiles()), 1, 1), block, 0, s, a);
+            else
+                hipLaunchKernelGGL((mlp_product_kernel<128, false, true>), dim3(unsigned(dx.tiles()), 1, 1), block, 0, s, a);
+            if (dx.splits > 1) join(a, s), ++launches;
+            ++launches;
+        }
+        if (any_weight) {
+            const Cut wide = cut(z.h, z.d, 0, false), back = cut(z.d, z.h, 0, false);
+            int n = 0, tiles = 0;
+            auto add = [&](void *out, const Matrix &left, const Matrix &right, int64_t m, int64_t columns, const Cut &c) {
+                if (!out) return;
+                a.p[n] = product(left, right, m, columns, z.rows, c);
+                a.p[n].first = tiles;
+                a.out[n] = static_cast<uint16_t *>(out);
+                a.ldo[n] = columns;
+                tiles += int(c.tiles());
+                ++n;
+            };
+            add(grads->dw_gate, matrix(space.dgate, z.hp), matrix(x, z.ld()), z.h, z.d, wide);
+            add(grads->dw_up, matrix(space.dup, z.hp), matrix(x, z.ld()), z.h, z.d, wide);
+            add(grads->dw_down, matrix(dout, z.ld()), matrix(args->hidden, z.hp), z.d, z.h, back);
+            a.products = n;
+            if (wide.tile == 256)
+                hipLaunchKernelGGL((mlp_product_kernel<256, true, true>), dim3(unsigned(tiles), 1, 1), block, 0, s, a);
+            else
+                hipLaunchKernelGGL((mlp_product_kernel<128, true, true>), dim3(unsigned(tiles), 1, 1), block, 0, s, a);
+            ++launches;
+        }
+    });
+    if (e != hipSuccess) return hip_error(e, "gated_mlp_backward: kernel launch");
+    g_dispatches.fetch_add(launches);
+    return MIMO_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,356 @@
+// gemm_tile.h -- one tile of a bf16 matrix product on the matrix cores of AMD
+// Instinct MI355X (gfx950, CDNA4), for operands in either order in memory:
+//   sum over k of X[m][k] W[n][k]
+// where a matrix is stored along k ([rows][k], the summed axis innermost) or
+// across it ([k][rows]).  Forward products are along, along; a gradient of the
+// input is along, across; a gradient of a weight, whose summed axis is the
+// rows of both operands, is across, across.
+//
+// A workgroup of four waves makes a kTile x kTile tile, a quarter each: 256 x
+// 256 (256 accumulators a lane, one workgroup a CU), or 128 x 128 (two
+// workgroups a CU).  K advances 64 values a stage.  Operands go from memory
+// straight into LDS (buffer_load ... lds), x two stages ahead of the products
+// (three buffers), w one (two buffers).  The five buffers are arrays of their
+// own, so that the compiler sees that loads into one never meet reads of
+// another, and the stage loop is unrolled six times, after which both rings
+// are back where they were.  Stages past the end are loaded through an empty
+// resource: zeros, without memory traffic.
+//
+// In LDS a matrix stored along k lies as kTile rows of 64 values, read 16
+// bytes a lane; one stored across as panels of 64 columns, 64 rows of k each,
+// read by ds_read_b64_tr_b16, which hands a lane four rows of one column.
+// Either way lane l of an operand holds row l % 32, k = 8 (l / 32) .. + 7 of
+// the 16 that a product takes.  16-byte chunks are XOR-swizzled by the row so
+// that neither kind of read meets a bank twice.
+//
+// Products are v_mfma_f32_32x32x16_bf16 with w as the first operand: a lane of
+// the result holds one row of x (lane % 32) and channels 8 (r / 4) + 4 (lane /
+// 32) + r % 4, so that it can stage and store neighbouring channels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "device_util.h"
+
+namespace mimo {
+namespace gemm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_ptr;
+typedef __attribute__((address_space(3))) void *lds_void_ptr;
+
+constexpr int kThreads = 256;
+constexpr int kStageK = 64;
+constexpr int kWord3 = 0x00020000;          // raw buffer resource word 3
+constexpr int kRecords = 0x7FFFFFF0;        // the largest size of a resource
+constexpr uint32_t kOutside = 0x7FFFFFF8u;  // a byte offset past every resource: reads zeros
+constexpr int kWaitAll = 0;                 // s_waitcnt: every counter at zero
+constexpr int kGroupM = 8;                  // tiles of rows that share a run of channel tiles
+
+// One bf16 matrix; stride in values, a multiple of 8, as is the innermost
+// axis; 16-byte aligned.
+struct Matrix {
+    const uint16_t *p;
+    int64_t stride;
+};
+
+// One product of a launch.  With two segments K runs over both pairs of
+// matrices, k of each; with kGate the two matrices of w are the gate's and the
+// up projection's rows, and k is of one segment.
+struct Product {
+    Matrix x[2], w[2];
+    int64_t m;
+    int32_t n, k, segments;
+    int32_t splits;       // parts of K, each a tile of its own
+    int32_t m_tiles, n_tiles;
+    int32_t first;        // of its tiles in the launch
+};
+
+__device__ __forceinline__ int row_key(int r) { return (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1); }
+__device__ __forceinline__ int block_key(int g) { return g ^ ((g & 3) >> 1); }
+
+__device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f32x16 &c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Where a tile is: its part of K and its place.  Runs of kGroupM tiles of rows
+// go by channels together, so that the tiles an XCD works on at one time share
+// rows and channels in its L2 (a run of one row of tiles reads every channel).
+struct Place {
+    int64_t mt;
+    int nt, split;
+    __device__ __forceinline__ Place(const Product &p, int t) {
+        const int tiles = p.m_tiles * p.n_tiles;
+        split = t / tiles;
+        t -= split * tiles;
+        const int group = t / (kGroupM * p.n_tiles), first = group * kGroupM;
+        const int rows = min(p.m_tiles - first, kGroupM);
+        t -= first * p.n_tiles;
+        nt = t / rows;
+        mt = first + t - nt * rows;
+    }
+};
+
+// A stage's buffers of both operands.
+template <int kTile>
+struct Buffers {
+    uint8_t *x[3], *w[2];
+};
+
+// One operand's loads by a wave, kGroups of 1 KB a stage, and its operands.
+// kAcross: stored across k.  kTile rows (columns, if across) from `first` on, of
+// `count`.
+template <int kTile, bool kAcross>
+struct Operand {
+    static constexpr int kGroups = kTile / 8 / 4;
+    uint32_t off[kGroups];
+    int chunk;      // along: the first group's chunk of the lane's row; group i's is chunk ^ i
+    int base;       // across: the lane's part of a transposed read's address
+    int lane, wave;
+
+    // Group i of wave w is number n = w * kGroups + i: along, rows 8 n .. + 7;
+    // across, rows 8 (n % 8) .. + 7 of k in panel n / 8.  Lane l lands at row l /
+    // 8, chunk l % 8 of it, so it fetches the chunk that the swizzle puts there.
+    // `rows_from`: what row of the matrix the wave's first row of the tile is
+    // (along); rows past the last one read the last one, and are not stored.
+    __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int l8 = lane >> 3;
+        if constexpr (kAcross) {
+            chunk = 0;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int n = wave * kGroups + i, g = n % 8;
+                const int col = (n / 8) * 64 + (((lane & 7) ^ row_key(l8) ^ block_key(g)) << 3);
+                off[i] = first + col < count ? uint32_t((8 * g + l8) * int(stride) + col) * 2 : kOutside;
+            }
+            const int x = 8 * (lane >> 5) + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+            // row x of the 16 of a step, whose block of eight is 2 s + lane / 32:
+            // block_key of it is (lane / 32) ^ the step's own part
+            base = x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
+        } else {
+            base = 0;
+            chunk = ((lane & 7) ^ l8 ^ (wave * kGroups)) & 7;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+                off[i] = uint32_t(int(min(rows_from + i * 8 + l8, count - 1) - first) * int(stride) + ((chunk ^ i) & 7) * 8) * 2;
+        }
+    }
+
+    // Group i of stage ks of a segment of k values, from the tile's base (row
+    // `first`, or column `first`, of the matrix).
+    __device__ __forceinline__ void load(const Matrix &t, int64_t first, int64_t count, int i, int ks, int k, bool live, uint8_t *d) const {
+        uint8_t *to = d + (wave * kGroups + i) * 1024;
+        const int left = k - ks * kStageK;  // values of k from the stage on
+        if constexpr (kAcross) {
+            // to the end of the last row's last chunk: a size that cuts a word
+            // would cut the value in its lower half too
+            const int64_t bytes = ((left - 1) * t.stride + ((count + 7) & ~int64_t(7)) - first) * 2;
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint16_t *>(t.p) + int64_t(ks) * kStageK * t.stride + first, 0,
+                live && left > 0 ? int(min(bytes, int64_t(kRecords))) : 0, kWord3);
+            send(r, to, off[i], 0);
+        } else {
+            const __amdgpu_buffer_rsrc_t r =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(t.p) + first * t.stride, 0, live ? kRecords : 0, kWord3);
+            send(r, to, ((chunk ^ i) & 7) * 8 < left ? off[i] : kOutside, live ? ks * (kStageK * 2) : 0);
+        }
+    }
+    // The host's pass over this file does not know the size (and would drop
+    // every kernel that contains it), so it does not see the call.
+    static __device__ __forceinline__ void send(const __amdgpu_buffer_rsrc_t &r, uint8_t *to, uint32_t off, int at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)to, 16, off, at, 0, 0);
+#endif
+    }
+
+    // Rows (columns) c0 .. c0 + 31 of the tile, step s of the stage.
+    __device__ __forceinline__ bf16x8 read(const uint8_t *t, int c0, int s) const {
+        if constexpr (kAcross) {
+            const int d = c0 / 32, flip = ((4 * (d & 1)) ^ (2 * s) ^ (s & 1)) << 4;
+            const uint8_t *p = t + (d / 2) * (kStageK * 128) + s * 16 * 128;
+            union {
+                s16x4 h[2];
+                bf16x8 f;
+            } u;
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + (base ^ flip)));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + (base ^ flip ^ (2 << 4)) + 4 * 128));
+            return u.f;
+        } else {
+            const int r = c0 + (lane & 31);
+            return *reinterpret_cast<const bf16x8 *>(t + r * 128 + (((2 * s + (lane >> 5)) ^ ((r ^ (r >> 3)) & 7)) << 4));
+        }
+    }
+};
+
+// The sums of stages [begin, end) of a tile into acc ([blocks of rows][blocks
+// of channels]); every load has landed and every wave has read its operands
+// when it returns.
+template <int kTile, bool kXAcross, bool kWAcross, bool kGate>
+__device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, int begin, int end, const Buffers<kTile> &lds,
+                                         f32x16 (&acc)[kTile / 64][kTile / 64]) {
+    static_assert(!(kGate && kWAcross), "gate and up are stored along k");
+    typedef Operand<kTile, kXAcross> X;
+    typedef Operand<kTile, kWAcross> W;
+    constexpr int kWave = kTile / 2, kBlocks = kWave / 32, kGroups = X::kGroups, kSteps = 4;
+    constexpr int kWaitVmemButX = 0x0F70 | kGroups;     // vmcnt: one stage of x may stay in flight
+    constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;  // the same, and lgkmcnt(0)
+    // two loads go out after each row of products, w's first: all of them
+    // before the stage's wait, which counts on x's being the newest
+    static_assert(kGroups <= 15 && kGroups <= (kSteps - 1) * kBlocks, "every load is issued before the last step");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int seg = (p.k + kStageK - 1) / kStageK;  // stages of a segment
+    const X x(p.x[0].stride, m0, p.m, m0 + wave * (kTile / 4));
+    // gate's rows are those of even waves, up's of odd ones: a quarter of the
+    // tile holds both projections of the same kWave / 2 channels
+    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kTile / 4) : n0 + wave * (kTile / 4));
+    auto load_x = [&](int i, int s, uint8_t *d) {
+        const int q = s >= seg ? 1 : 0;
+        x.load(p.x[q], m0, p.m, i, s - q * seg, p.k, s < end, d);
+    };
+    auto load_w = [&](int i, int s, uint8_t *d) {
+        const int q = s >= seg ? 1 : 0;
+        w.load(p.w[kGate ? wave & 1 : q], n0, p.n, i, s - q * seg, p.k, s < end, d);
+    };
+    // between stages: each wave has waited for its own loads and reads
+    auto barrier = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) acc[i][j] = f32x16{};
+    bf16x8 fx[2][kBlocks], fw[2][kBlocks];
+    auto read = [&](const uint8_t *tx, const uint8_t *tw, int s, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) a[i] = x.read(tx, wm * kWave + i * 32, s);
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) b[i] = w.read(tw, wn * kWave + i * 32, s);
+    };
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_x(i, begin, lds.x[0]);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_w(i, begin, lds.w[0]);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_x(i, begin + 1, lds.x[1]);
+    __builtin_amdgcn_s_waitcnt(kWaitVmemButX);
+    barrier();
+    read(lds.x[0], lds.w[0], 0, fx[0], fw[0]);
+    // One stage: the next step's operands are read while this one's products
+    // run; the loads go out in its first half, two after each row of
+    // products; before the last step's products, whose operands are in
+    // registers, the waves meet and read the next stage's first operands.
+    auto stage = [&](int s, const uint8_t *tx, const uint8_t *tw, uint8_t *nw, uint8_t *nx2, const uint8_t *nx,
+                     const uint8_t *nwr) __attribute__((always_inline)) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+            if (ks + 1 < kSteps) {
+                read(tx, tw, ks + 1, fx[(ks + 1) & 1], fw[(ks + 1) & 1]);
+            } else {
+                __builtin_amdgcn_s_waitcnt(kWaitLdsVmemButX);
+                barrier();
+                read(nx, nwr, 0, fx[0], fw[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+#pragma unroll
+                for (int j = 0; j < kBlocks; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
+                const int slot = ks * kBlocks + i;
+#pragma unroll
+                for (int n = 2 * slot; n < 2 * slot + 2; ++n) {
+                    if (n < kGroups)
+                        load_w(n, s + 1, nw);
+                    else if (n < 2 * kGroups)
+                        load_x(n - kGroups, s + 2, nx2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    // stage u of a group of six
+    auto ring = [&](int s, auto number) __attribute__((always_inline)) {
+        constexpr int u = decltype(number)::value;
+        stage(s, lds.x[u % 3], lds.w[u % 2], lds.w[(u + 1) % 2], lds.x[(u + 2) % 3], lds.x[(u + 1) % 3], lds.w[(u + 1) % 2]);
+    };
+    typedef std::integral_constant<int, 0> U0;
+    typedef std::integral_constant<int, 1> U1;
+    typedef std::integral_constant<int, 2> U2;
+    typedef std::integral_constant<int, 3> U3;
+    typedef std::integral_constant<int, 4> U4;
+    typedef std::integral_constant<int, 5> U5;
+    int s = begin;
+    for (; s + 6 <= end; s += 6) {
+        ring(s, U0());
+        ring(s + 1, U1());
+        ring(s + 2, U2());
+        ring(s + 3, U3());
+        ring(s + 4, U4());
+        ring(s + 5, U5());
+    }
+    // the rest, nested: where two paths met, the compiler could not tell which
+    // loads are in flight and would wait for all of them before the next read
+    const int rest = end - s;
+    if (rest > 0) {
+        ring(s, U0());
+        if (rest > 1) {
+            ring(s + 1, U1());
+            if (rest > 2) {
+                ring(s + 2, U2());
+                if (rest > 3) {
+                    ring(s + 3, U3());
+                    if (rest > 4) ring(s + 4, U4());
+                }
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    barrier();
+}
+
+// A wave's block of 32 rows and kTile / 2 channels, turned in LDS (float32,
+// 16-byte chunks XOR-swizzled by the row): a lane then reads whole pieces of
+// rows.
+template <int kTile>
+struct Turned {
+    static constexpr int kWave = kTile / 2, kBlocks = kWave / 32, kRowBytes = kWave * 4, kChunks = kRowBytes / 16;
+    uint8_t *region;
+    __device__ __forceinline__ explicit Turned(const Buffers<kTile> &lds) {
+        static_assert(2 * 32 * kRowBytes <= kTile * 128, "two waves share a buffer");
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        region = (wave < 2 ? lds.x[0] : lds.x[1]) + (wave & 1) * (32 * kRowBytes);
+    }
+    __device__ __forceinline__ void put(const f32x16 (&acc)[kBlocks]) const {
+        const int lane = threadIdx.x & 63, r = lane & 31;
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = j * 8 + 2 * g + (lane >> 5);
+                const f32x4 v = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+                *reinterpret_cast<f32x4 *>(region + r * kRowBytes + ((c ^ r) % kChunks) * 16) = v;
+            }
+    }
+    // kN channels from c0 on (multiples of 4) of row r.
+    template <int kN>
+    __device__ __forceinline__ void get(int r, int c0, float (&v)[kN]) const {
+#pragma unroll
+        for (int k = 0; k < kN / 4; ++k) {
+            const f32x4 w = *reinterpret_cast<const f32x4 *>(region + r * kRowBytes + (((c0 / 4 + k) ^ r) % kChunks) * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * k + j] = w[j];
+        }
+    }
+};
+
+}  // namespace gemm
+}  // namespace mimo

@@ -1,7 +1,7 @@
 """The vision tower's operators over patch embeddings, on torch tensors:
 attention over the plan's chunks, the rotation of its heads, layer norm and
-root-mean-square norm with the residual, each with its backward pass, and the
-matrix product in 8-bit integers.
+root-mean-square norm with the residual, and the gated feed-forward block, each
+with its backward pass, and the matrix product in 8-bit integers.
 
 Argument checks and allocation only: the work runs in the HIP library
 (``include/mimo_pre.h``), on the tensors' device and on ``stream`` (default:
@@ -34,6 +34,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 _ATTENTION = struct.Struct("<q5if2Q" + "Qqq" * 4 + "Q")
 _GRADS = struct.Struct("<" + "Qqq" * 4 + "Q")
 _HEADS = struct.Struct("<Qqq")  # mimo_heads
+_MLP = struct.Struct("<qii9Q")  # mimo_mlp, mimo_mlp_grads
+_MLP_GRADS = struct.Struct("<8Q")
 
 _lib = None
 
@@ -590,6 +592,158 @@ def rotate_heads(x, cos, sin, inverse: bool = False, out=None, stream=None):
     if code:
         _abi._check(code, what)
     return out
+
+
+# ------------------------------------------------------ gated feed-forward block
+
+def _check_bf16(what, name, t, shape):
+    if t.dtype is not _BF16 or t.shape != shape or not t.is_contiguous():
+        _refuse(f"{what}: {name} must be contiguous bfloat16 {tuple(shape)}, got {tuple(t.shape)} {t.dtype}"
+                + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+def _check_mlp(what, x, w_gate, w_up, w_down, gate_up, hidden):
+    """(rows, width, hidden width, its padded form) of a block's tensors."""
+    if x.dim() != 2 or w_gate.dim() != 2:
+        _refuse(f"{what}: x must be [rows, width] and w_gate [hidden width, width], got {tuple(x.shape)} and {tuple(w_gate.shape)}")
+    rows, width = x.shape
+    inner = w_gate.shape[0]
+    if width < 1 or inner < 1:
+        _refuse(f"{what}: x and w_gate must have columns and w_gate rows, got {tuple(x.shape)} and {tuple(w_gate.shape)}")
+    if width > 65536 or inner > 65536 or rows > 0x7FFFFFFF:
+        _refuse_size(f"{what}: a width above 65536 or more than 2^31 - 1 rows: {rows} x {width}, hidden {inner}")
+    _check_bf16(what, "x", x, (rows, width))
+    _check_bf16(what, "w_gate", w_gate, (inner, width))
+    _check_bf16(what, "w_up", w_up, (inner, width))
+    _check_bf16(what, "w_down", w_down, (width, inner))
+    padded = (inner + 63) & -64
+    if gate_up is not None and (gate_up.dtype is not _F32 or gate_up.shape != (2, rows, padded) or not gate_up.is_contiguous()):
+        _refuse(f"{what}: gate_up must be contiguous float32 {(2, rows, padded)}, got {tuple(gate_up.shape)} {gate_up.dtype}")
+    if hidden is not None:
+        _check_bf16(what, "hidden", hidden, (rows, padded))
+    return rows, width, inner, padded
+
+
+def gated_mlp(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, out=None, return_saved: bool = False, gate_up=None,
+              hidden=None, workspace=None, stream=None):
+    """mimo_gated_mlp: the gated feed-forward block (vision page, the SwiGLU
+    MLP of MiMoVisionBlock), (silu(x @ w_gate.T + b_gate) * (x @ w_up.T + b_up))
+    @ w_down.T + b_down.
+
+    x bf16 [rows, width]; w_gate, w_up bf16 [hidden, width] and w_down bf16
+    [width, hidden], as a checkpoint has them; biases float32 or None; all
+    contiguous.  Returns out bf16 [rows, width], or with return_saved=True (out,
+    gate_up, hidden), which the backward pass takes: float32 [2, rows, padded]
+    and bf16 [rows, padded], padded = hidden rounded up to a multiple of 64.
+    ``workspace``: uint8, at least gated_mlp_workspace_bytes(rows, width, hidden)
+    bytes; calls that may run at the same time need one each.
+    """
+    what = "gated_mlp"
+    rows, width, inner, padded = _check_mlp(what, x, w_gate, w_up, w_down, gate_up, hidden)
+    if b_gate is not None:
+        _check_vector(what, "b_gate", b_gate, inner, _F32)
+    if b_up is not None:
+        _check_vector(what, "b_up", b_up, inner, _F32)
+    if b_down is not None:
+        _check_vector(what, "b_down", b_down, width, _F32)
+    if out is not None:
+        _check_bf16(what, "out", out, x.shape)
+    if workspace is not None:
+        _abi._check_bytes(workspace, what + ": workspace")
+    if not return_saved and (gate_up is not None or hidden is not None):
+        _refuse(f"{what}: gate_up and hidden are written with return_saved=True only")
+    index = x.get_device()
+    tensors = (x, w_gate, w_up, w_down, b_gate, b_up, b_down, out, gate_up, hidden, workspace)
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _check_devices(what, tensors)
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, tensors):
+            return gated_mlp(x, w_gate, w_up, w_down, b_gate, b_up, b_down, out, return_saved, gate_up, hidden, workspace)
+    lib = _library()
+    if workspace is None:
+        workspace = x.new_empty(max(lib.mimo_gated_mlp_workspace_bytes(rows, width, inner), 16), dtype=torch.uint8)
+    if out is None:
+        out = torch.empty_like(x)
+    if return_saved:
+        if gate_up is None:
+            gate_up = x.new_empty((2, rows, padded), dtype=_F32)
+        if hidden is None:
+            hidden = x.new_empty((rows, padded))
+    args = _MLP.pack(rows, width, inner, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _pointer(b_gate) or 0,
+                     _pointer(b_up) or 0, _pointer(b_down) or 0, _pointer(gate_up) or 0, _pointer(hidden) or 0)
+    code = lib.mimo_gated_mlp(args, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    return (out, gate_up, hidden) if return_saved else out
+
+
+def gated_mlp_backward(dout, x, w_gate, w_up, w_down, gate_up, hidden, bias_grads: bool = False, dx=None, dw_gate=None, dw_up=None,
+                       dw_down=None, db_gate=None, db_up=None, db_down=None, weight_grads: bool = True, workspace=None, stream=None):
+    """mimo_gated_mlp_backward: the gradients of gated_mlp's inputs for dout
+    bf16 [rows, width], given its gate_up and hidden.
+
+    Returns (dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down): bf16 of x's
+    and the weights' shapes, and float32 of the biases'.  The weights' gradients
+    are made unless weight_grads is False, the biases' with bias_grads=True;
+    apart from that, those that are passed in are made and the others are None.
+    Gradients are overwritten.  ``workspace``: uint8, at least
+    gated_mlp_backward_workspace_bytes(rows, width, hidden) bytes; calls that
+    may run at the same time need one each.
+    """
+    what = "gated_mlp_backward"
+    if gate_up is None or hidden is None:
+        _refuse(f"{what}: gate_up and hidden are needed (gated_mlp returns them with return_saved=True)")
+    rows, width, inner, _ = _check_mlp(what, x, w_gate, w_up, w_down, gate_up, hidden)
+    _check_bf16(what, "dout", dout, x.shape)
+    for name, t, like in (("dx", dx, x), ("dw_gate", dw_gate, w_gate), ("dw_up", dw_up, w_up), ("dw_down", dw_down, w_down)):
+        if t is not None:
+            _check_bf16(what, name, t, like.shape)
+    for name, t, n in (("db_gate", db_gate, inner), ("db_up", db_up, inner), ("db_down", db_down, width)):
+        if t is not None:
+            _check_vector(what, name, t, n, _F32)
+    if workspace is not None:
+        _abi._check_bytes(workspace, what + ": workspace")
+    index = x.get_device()
+    tensors = (x, w_gate, w_up, w_down, gate_up, hidden, dout, dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down, workspace)
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _check_devices(what, tensors)
+    if stream is not None or _device_now() != index:
+        with _entered(what, index, stream, tensors):
+            return gated_mlp_backward(dout, x, w_gate, w_up, w_down, gate_up, hidden, bias_grads, dx, dw_gate, dw_up, dw_down, db_gate,
+                                      db_up, db_down, weight_grads, workspace)
+    if dx is None:
+        dx = torch.empty_like(x)
+    if weight_grads:
+        dw_gate = torch.empty_like(w_gate) if dw_gate is None else dw_gate
+        dw_up = torch.empty_like(w_up) if dw_up is None else dw_up
+        dw_down = torch.empty_like(w_down) if dw_down is None else dw_down
+    if bias_grads:
+        db_gate = x.new_empty(inner, dtype=_F32) if db_gate is None else db_gate
+        db_up = x.new_empty(inner, dtype=_F32) if db_up is None else db_up
+        db_down = x.new_empty(width, dtype=_F32) if db_down is None else db_down
+    lib = _library()
+    if workspace is None:
+        workspace = x.new_empty(max(lib.mimo_gated_mlp_backward_workspace_bytes(rows, width, inner), 16), dtype=torch.uint8)
+    args = _MLP.pack(rows, width, inner, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), 0, 0, 0,
+                     gate_up.data_ptr(), hidden.data_ptr())
+    made = (dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down)
+    grads = _MLP_GRADS.pack(dout.data_ptr(), *[_pointer(t) or 0 for t in made])
+    code = lib.mimo_gated_mlp_backward(args, grads, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    if code:
+        _abi._check(code, what)
+    return made
+
+
+def gated_mlp_workspace_bytes(rows: int, width: int, hidden: int) -> int:
+    """mimo_gated_mlp_workspace_bytes."""
+    return int(_library().mimo_gated_mlp_workspace_bytes(int(rows), int(width), int(hidden)))
+
+
+def gated_mlp_backward_workspace_bytes(rows: int, width: int, hidden: int) -> int:
+    """mimo_gated_mlp_backward_workspace_bytes."""
+    return int(_library().mimo_gated_mlp_backward_workspace_bytes(int(rows), int(width), int(hidden)))
 
 
 # ------------------------------------------------------ 8-bit matrix product
