@@ -107,13 +107,12 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
 #define MIMO_TILE_BUFFERS(kTile)                                                                  \
     __shared__ __attribute__((aligned(16))) uint8_t sx0[kTile * 128], sx1[kTile * 128], sx2[kTile * 128]; \
     __shared__ __attribute__((aligned(16))) uint8_t sw0[kTile * 128], sw1[kTile * 128];           \
-    const Buffers<kTile> lds{{sx0, sx1, sx2}, {sw0, sw1}}
+    const Buffers<kTile> lds{{(lds_ptr)sx0, (lds_ptr)sx1, (lds_ptr)sx2}, {(lds_ptr)sw0, (lds_ptr)sw1}}
 
 // Stages of a split of a product.
 __device__ __forceinline__ void part_of(const Product &p, int split, int &begin, int &end) {
-    const int stages = (p.k + kStageK - 1) / kStageK * p.segments;
-    begin = int(int64_t(stages) * split / p.splits);
-    end = int(int64_t(stages) * (split + 1) / p.splits);
+    begin = int(int64_t(p.stages) * split / p.splits);
+    end = int(int64_t(p.stages) * (split + 1) / p.splits);
 }
 
 // h = silu(x Wg' + bg) (x Wu' + bu).
@@ -126,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void mlp_gate_kernel(MlpArgs a) {
     const int64_t m0 = at.mt * kTile;
     const int n0 = at.nt * (kTile / 2);
     f32x16 acc[kBlocks][kBlocks];
-    multiply<kTile, false, false, true>(p, m0, n0, 0, (p.k + kStageK - 1) / kStageK, lds, acc);
+    multiply<kTile, false, false, kGateUp>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
     constexpr int kLanes = kHalf / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void mlp_dhidden_kernel(MlpArgs a) {
     const int64_t m0 = at.mt * kTile;
     const int n0 = at.nt * kTile;
     f32x16 acc[kBlocks][kBlocks];
-    multiply<kTile, false, true, false>(p, m0, n0, 0, (p.k + kStageK - 1) / kStageK, lds, acc);
+    multiply<kTile, false, true, kOnce>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
     constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void mlp_product_kernel(MlpArgs a) {
     int begin, end;
     part_of(p, at.split, begin, end);
     f32x16 acc[kBlocks][kBlocks];
-    multiply<kTile, kXAcross, kWAcross, false>(p, m0, n0, begin, end, lds, acc);
+    multiply<kTile, kXAcross, kWAcross, kWAcross && !kXAcross ? kTwice : kOnce>(p, m0, n0, begin, end, lds, acc);
     const Turned<kTile> turned(lds);
     constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -437,7 +436,7 @@ Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t 
     p.m = m;
     p.n = int32_t(n);
     p.k = int32_t(k);
-    p.segments = 1;
+    p.stages = int32_t(ceil_div(k, kStageK));
     p.splits = c.splits;
     p.m_tiles = int32_t(c.m_tiles);
     p.n_tiles = int32_t(c.n_tiles);
@@ -656,7 +655,7 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             a.p[0] = product(matrix(space.dgate, z.hp), matrix(wg, z.ld()), z.rows, z.d, z.h, dx);
             a.p[0].x[1] = matrix(space.dup, z.hp);
             a.p[0].w[1] = matrix(wu, z.ld());
-            a.p[0].segments = 2;
+            a.p[0].stages *= 2;
             a.products = 1;
             a.out[0] = static_cast<uint16_t *>(grads->dx);
             a.ldo[0] = z.d;

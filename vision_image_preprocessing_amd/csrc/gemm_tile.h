@@ -42,7 +42,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_ptr;
-typedef __attribute__((address_space(3))) void *lds_void_ptr;
+typedef __attribute__((address_space(3))) bf16x8 *lds_bf16x8_ptr;
+typedef __attribute__((address_space(3))) f32x4 *lds_f32x4_ptr;
+typedef __attribute__((address_space(3))) uint8_t *lds_ptr;
 
 constexpr int kThreads = 256;
 constexpr int kStageK = 64;
@@ -59,13 +61,12 @@ struct Matrix {
     int64_t stride;
 };
 
-// One product of a launch.  With two segments K runs over both pairs of
-// matrices, k of each; with kGate the two matrices of w are the gate's and the
-// up projection's rows, and k is of one segment.
+// One product of a launch; k is that of one pair of matrices.
 struct Product {
     Matrix x[2], w[2];
     int64_t m;
-    int32_t n, k, segments;
+    int32_t n, k;
+    int32_t stages;       // of all of K
     int32_t splits;       // parts of K, each a tile of its own
     int32_t m_tiles, n_tiles;
     int32_t first;        // of its tiles in the launch
@@ -96,10 +97,12 @@ struct Place {
     }
 };
 
-// A stage's buffers of both operands.
+// The tile's buffers.  Every address in them is one of these plus a lane's
+// offset and a constant: through longer chains the compiler no longer sees
+// which array a read is of, and waits for all loads in flight.
 template <int kTile>
 struct Buffers {
-    uint8_t *x[3], *w[2];
+    lds_ptr x[3], w[2];
 };
 
 // One operand's loads by a wave, kGroups of 1 KB a stage, and its operands.
@@ -109,19 +112,19 @@ template <int kTile, bool kAcross>
 struct Operand {
     static constexpr int kGroups = kTile / 8 / 4;
     uint32_t off[kGroups];
-    int chunk;      // along: the first group's chunk of the lane's row; group i's is chunk ^ i
-    int base;       // across: the lane's part of a transposed read's address
-    int lane, wave;
+    int chunk;  // along: the first group's chunk of the lane's row; group i's is chunk ^ i
+    int base;   // the lane's part of an operand read's address
+    int wave;
 
     // Group i of wave w is number n = w * kGroups + i: along, rows 8 n .. + 7;
     // across, rows 8 (n % 8) .. + 7 of k in panel n / 8.  Lane l lands at row l /
     // 8, chunk l % 8 of it, so it fetches the chunk that the swizzle puts there.
     // `rows_from`: what row of the matrix the wave's first row of the tile is
     // (along); rows past the last one read the last one, and are not stored.
-    __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from) {
-        lane = threadIdx.x & 63;
+    // `half`: which half of the tile the wave's operands are of.
+    __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from, int half) {
+        const int lane = threadIdx.x & 63, l8 = lane >> 3;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int l8 = lane >> 3;
         if constexpr (kAcross) {
             chunk = 0;
 #pragma unroll
@@ -133,9 +136,10 @@ struct Operand {
             const int x = 8 * (lane >> 5) + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
             // row x of the 16 of a step, whose block of eight is 2 s + lane / 32:
             // block_key of it is (lane / 32) ^ the step's own part
-            base = x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
+            base = half * (kTile / 128) * (kStageK * 128) + x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
         } else {
-            base = 0;
+            const int r = lane & 31;
+            base = (half * (kTile / 2) + r) * 128 + (((lane >> 5) ^ ((r ^ (r >> 3)) & 7)) << 4);
             chunk = ((lane & 7) ^ l8 ^ (wave * kGroups)) & 7;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
@@ -145,16 +149,16 @@ struct Operand {
 
     // Group i of stage ks of a segment of k values, from the tile's base (row
     // `first`, or column `first`, of the matrix).
-    __device__ __forceinline__ void load(const Matrix &t, int64_t first, int64_t count, int i, int ks, int k, bool live, uint8_t *d) const {
-        uint8_t *to = d + (wave * kGroups + i) * 1024;
+    __device__ __forceinline__ void load(const Matrix &t, int64_t first, int64_t count, int i, int ks, int k, bool live, lds_ptr d) const {
+        const lds_ptr to = d + (wave * kGroups + i) * 1024;
         const int left = k - ks * kStageK;  // values of k from the stage on
         if constexpr (kAcross) {
-            // to the end of the last row's last chunk: a size that cuts a word
-            // would cut the value in its lower half too
-            const int64_t bytes = ((left - 1) * t.stride + ((count + 7) & ~int64_t(7)) - first) * 2;
+            // its rows of the stage to the end of the last one's last chunk (a
+            // size that cuts a word would cut the value in its lower half too);
+            // 32 bits hold them, and no branch is needed
+            const int bytes = ((min(left, kStageK) - 1) * int(t.stride) + int(((count + 7) & ~int64_t(7)) - first)) * 2;
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<uint16_t *>(t.p) + int64_t(ks) * kStageK * t.stride + first, 0,
-                live && left > 0 ? int(min(bytes, int64_t(kRecords))) : 0, kWord3);
+                const_cast<uint16_t *>(t.p) + int64_t(ks) * kStageK * t.stride + first, 0, live && left > 0 ? bytes : 0, kWord3);
             send(r, to, off[i], 0);
         } else {
             const __amdgpu_buffer_rsrc_t r =
@@ -164,27 +168,25 @@ struct Operand {
     }
     // The host's pass over this file does not know the size (and would drop
     // every kernel that contains it), so it does not see the call.
-    static __device__ __forceinline__ void send(const __amdgpu_buffer_rsrc_t &r, uint8_t *to, uint32_t off, int at) {
+    static __device__ __forceinline__ void send(const __amdgpu_buffer_rsrc_t &r, lds_ptr to, uint32_t off, int at) {
 #if defined(__HIP_DEVICE_COMPILE__)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)to, 16, off, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, off, at, 0, 0);
 #endif
     }
 
-    // Rows (columns) c0 .. c0 + 31 of the tile, step s of the stage.
-    __device__ __forceinline__ bf16x8 read(const uint8_t *t, int c0, int s) const {
+    // Rows (columns) 32 i .. + 31 of the wave's half, step s of the stage.
+    __device__ __forceinline__ bf16x8 read(lds_ptr t, int i, int s) const {
         if constexpr (kAcross) {
-            const int d = c0 / 32, flip = ((4 * (d & 1)) ^ (2 * s) ^ (s & 1)) << 4;
-            const uint8_t *p = t + (d / 2) * (kStageK * 128) + s * 16 * 128;
+            const int flip = ((4 * (i & 1)) ^ (2 * s) ^ (s & 1)) << 4, at = (i / 2) * (kStageK * 128) + s * 16 * 128;
             union {
                 s16x4 h[2];
                 bf16x8 f;
             } u;
-            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + (base ^ flip)));
-            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(p + (base ^ flip ^ (2 << 4)) + 4 * 128));
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(t + ((base ^ flip) + at)));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(t + ((base ^ flip ^ (2 << 4)) + (at + 4 * 128))));
             return u.f;
         } else {
-            const int r = c0 + (lane & 31);
-            return *reinterpret_cast<const bf16x8 *>(t + r * 128 + (((2 * s + (lane >> 5)) ^ ((r ^ (r >> 3)) & 7)) << 4));
+            return *(lds_bf16x8_ptr)(t + ((base ^ (((2 * s) ^ (4 * (i & 1))) << 4)) + i * 32 * 128));
         }
     }
 };
@@ -192,13 +194,19 @@ struct Operand {
 // The sums of stages [begin, end) of a tile into acc ([blocks of rows][blocks
 // of channels]); every load has landed and every wave has read its operands
 // when it returns.
-template <int kTile, bool kXAcross, bool kWAcross, bool kGate>
+//
+// kOver: what K runs over.  kOnce: the first pair of matrices; kTwice: both
+// pairs, one after the other; kGateUp: the first x, with w the gate's rows and
+// the up projection's.
+enum Over { kOnce, kTwice, kGateUp };
+template <int kTile, bool kXAcross, bool kWAcross, Over kOver>
 __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, int begin, int end, const Buffers<kTile> &lds,
                                          f32x16 (&acc)[kTile / 64][kTile / 64]) {
+    constexpr bool kGate = kOver == kGateUp;
     static_assert(!(kGate && kWAcross), "gate and up are stored along k");
     typedef Operand<kTile, kXAcross> X;
     typedef Operand<kTile, kWAcross> W;
-    constexpr int kWave = kTile / 2, kBlocks = kWave / 32, kGroups = X::kGroups, kSteps = 4;
+    constexpr int kBlocks = kTile / 64, kGroups = X::kGroups, kSteps = 4;
     constexpr int kWaitVmemButX = 0x0F70 | kGroups;     // vmcnt: one stage of x may stay in flight
     constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;  // the same, and lgkmcnt(0)
     // two loads go out after each row of products, w's first: all of them
@@ -207,17 +215,23 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int seg = (p.k + kStageK - 1) / kStageK;  // stages of a segment
-    const X x(p.x[0].stride, m0, p.m, m0 + wave * (kTile / 4));
+    const X x(p.x[0].stride, m0, p.m, m0 + wave * (kTile / 4), wm);
     // gate's rows are those of even waves, up's of odd ones: a quarter of the
     // tile holds both projections of the same kWave / 2 channels
-    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kTile / 4) : n0 + wave * (kTile / 4));
-    auto load_x = [&](int i, int s, uint8_t *d) {
-        const int q = s >= seg ? 1 : 0;
-        x.load(p.x[q], m0, p.m, i, s - q * seg, p.k, s < end, d);
+    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kTile / 4) : n0 + wave * (kTile / 4), wn);
+    // in registers from here on: a scalar load in the loop would make every
+    // wait for LDS a wait for all of it
+    const Matrix x0 = p.x[0], w0 = kGate ? p.w[wave & 1] : p.w[0];
+    const Matrix x1 = kOver == kTwice ? p.x[1] : x0, w1 = kOver == kTwice ? p.w[1] : w0;
+    const int64_t rows = p.m;
+    const int channels = p.n, k = p.k;
+    auto load_x = [&](int i, int s, lds_ptr d) {
+        const bool second = kOver == kTwice && s >= seg;
+        x.load(second ? x1 : x0, m0, rows, i, second ? s - seg : s, k, s < end, d);
     };
-    auto load_w = [&](int i, int s, uint8_t *d) {
-        const int q = s >= seg ? 1 : 0;
-        w.load(p.w[kGate ? wave & 1 : q], n0, p.n, i, s - q * seg, p.k, s < end, d);
+    auto load_w = [&](int i, int s, lds_ptr d) {
+        const bool second = kOver == kTwice && s >= seg;
+        w.load(second ? w1 : w0, n0, channels, i, second ? s - seg : s, k, s < end, d);
     };
     // between stages: each wave has waited for its own loads and reads
     auto barrier = [] {
@@ -230,11 +244,11 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) acc[i][j] = f32x16{};
     bf16x8 fx[2][kBlocks], fw[2][kBlocks];
-    auto read = [&](const uint8_t *tx, const uint8_t *tw, int s, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
+    auto read = [&](lds_ptr tx, lds_ptr tw, int s, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) a[i] = x.read(tx, wm * kWave + i * 32, s);
+        for (int i = 0; i < kBlocks; ++i) a[i] = x.read(tx, i, s);
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) b[i] = w.read(tw, wn * kWave + i * 32, s);
+        for (int i = 0; i < kBlocks; ++i) b[i] = w.read(tw, i, s);
     };
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin, lds.x[0]);
@@ -249,8 +263,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     // run; the loads go out in its first half, two after each row of
     // products; before the last step's products, whose operands are in
     // registers, the waves meet and read the next stage's first operands.
-    auto stage = [&](int s, const uint8_t *tx, const uint8_t *tw, uint8_t *nw, uint8_t *nx2, const uint8_t *nx,
-                     const uint8_t *nwr) __attribute__((always_inline)) {
+    auto stage = [&](int s, lds_ptr tx, lds_ptr tw, lds_ptr nw, lds_ptr nx2, lds_ptr nx) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
             if (ks + 1 < kSteps) {
@@ -258,7 +271,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
             } else {
                 __builtin_amdgcn_s_waitcnt(kWaitLdsVmemButX);
                 barrier();
-                read(nx, nwr, 0, fx[0], fw[0]);
+                read(nx, nw, 0, fx[0], fw[0]);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -280,7 +293,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     // stage u of a group of six
     auto ring = [&](int s, auto number) __attribute__((always_inline)) {
         constexpr int u = decltype(number)::value;
-        stage(s, lds.x[u % 3], lds.w[u % 2], lds.w[(u + 1) % 2], lds.x[(u + 2) % 3], lds.x[(u + 1) % 3], lds.w[(u + 1) % 2]);
+        stage(s, lds.x[u % 3], lds.w[u % 2], lds.w[(u + 1) % 2], lds.x[(u + 2) % 3], lds.x[(u + 1) % 3]);
     };
     typedef std::integral_constant<int, 0> U0;
     typedef std::integral_constant<int, 1> U1;
@@ -323,7 +336,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 template <int kTile>
 struct Turned {
     static constexpr int kWave = kTile / 2, kBlocks = kWave / 32, kRowBytes = kWave * 4, kChunks = kRowBytes / 16;
-    uint8_t *region;
+    lds_ptr region;
     __device__ __forceinline__ explicit Turned(const Buffers<kTile> &lds) {
         static_assert(2 * 32 * kRowBytes <= kTile * 128, "two waves share a buffer");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -337,7 +350,7 @@ struct Turned {
             for (int g = 0; g < 4; ++g) {
                 const int c = j * 8 + 2 * g + (lane >> 5);
                 const f32x4 v = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
-                *reinterpret_cast<f32x4 *>(region + r * kRowBytes + ((c ^ r) % kChunks) * 16) = v;
+                *(lds_f32x4_ptr)(region + r * kRowBytes + ((c ^ r) % kChunks) * 16) = v;
             }
     }
     // kN channels from c0 on (multiples of 4) of row r.
@@ -345,7 +358,7 @@ struct Turned {
     __device__ __forceinline__ void get(int r, int c0, float (&v)[kN]) const {
 #pragma unroll
         for (int k = 0; k < kN / 4; ++k) {
-            const f32x4 w = *reinterpret_cast<const f32x4 *>(region + r * kRowBytes + (((c0 / 4 + k) ^ r) % kChunks) * 16);
+            const f32x4 w = *(lds_f32x4_ptr)(region + r * kRowBytes + (((c0 / 4 + k) ^ r) % kChunks) * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[4 * k + j] = w[j];
         }
