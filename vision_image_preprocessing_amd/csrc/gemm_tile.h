@@ -9,8 +9,8 @@
 // A workgroup of four waves makes a kTile x kTile tile, a quarter each: 256 x
 // 256 (256 accumulators a lane, one workgroup a CU), or 128 x 128 (two
 // workgroups a CU).  K advances 64 values a stage.  Operands go from memory
-// straight into LDS (buffer_load ... lds), x two stages ahead of the products
-// (three buffers), w one (two buffers).  The five buffers are arrays of their
+// straight into LDS (buffer_load ... lds), two stages ahead of the products; x
+// has three buffers, w two, which are filled again as soon as they are read.  The five buffers are arrays of their
 // own, so that the compiler sees that loads into one never meet reads of
 // another, and the stage loop is unrolled six times, after which both rings
 // are back where they were.  Stages past the end are loaded through an empty
@@ -207,11 +207,12 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     typedef Operand<kTile, kXAcross> X;
     typedef Operand<kTile, kWAcross> W;
     constexpr int kBlocks = kTile / 64, kGroups = X::kGroups, kSteps = 4;
-    constexpr int kWaitVmemButX = 0x0F70 | kGroups;     // vmcnt: one stage of x may stay in flight
-    constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;  // the same, and lgkmcnt(0)
-    // two loads go out after each row of products, w's first: all of them
-    // before the stage's wait, which counts on x's being the newest
-    static_assert(kGroups <= 15 && kGroups <= (kSteps - 1) * kBlocks, "every load is issued before the last step");
+    // vmcnt (bits 3:0 and 15:14) and lgkmcnt: one stage of both operands may stay
+    // in flight; one of x, and lgkmcnt(0)
+    constexpr int kWaitVmemButBoth = 0x0F70 | ((2 * kGroups) & 15) | ((2 * kGroups) >> 4 << 14);
+    constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;
+    // a stage's wait counts on x's loads being the newest
+    static_assert(kGroups <= 15 && kGroups == 2 * kBlocks, "two loads after each row of products fill a step");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int seg = (p.k + kStageK - 1) / kStageK;  // stages of a segment
@@ -244,11 +245,12 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) acc[i][j] = f32x16{};
     bf16x8 fx[2][kBlocks], fw[2][kBlocks];
-    auto read = [&](lds_ptr tx, lds_ptr tw, int s, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i) a[i] = x.read(tx, i, s);
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i) b[i] = w.read(tw, i, s);
+    // operand n of a step, w's first
+    auto read = [&](lds_ptr tx, lds_ptr tw, int s, int n, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
+        if (n < kBlocks)
+            b[n] = w.read(tw, n, s);
+        else if (n < 2 * kBlocks)
+            a[n - kBlocks] = x.read(tx, n - kBlocks, s);
     };
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin, lds.x[0]);
@@ -256,35 +258,44 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     for (int i = 0; i < kGroups; ++i) load_w(i, begin, lds.w[0]);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin + 1, lds.x[1]);
-    __builtin_amdgcn_s_waitcnt(kWaitVmemButX);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) load_w(i, begin + 1, lds.w[1]);
+    __builtin_amdgcn_s_waitcnt(kWaitVmemButBoth);
     barrier();
-    read(lds.x[0], lds.w[0], 0, fx[0], fw[0]);
-    // One stage: the next step's operands are read while this one's products
-    // run; the loads go out in its first half, two after each row of
-    // products; before the last step's products, whose operands are in
-    // registers, the waves meet and read the next stage's first operands.
+#pragma unroll
+    for (int n = 0; n < 2 * kBlocks; ++n) read(lds.x[0], lds.w[0], 0, n, fx[0], fw[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    // One stage.  The next step's operands are read between this one's rows of
+    // products, three at a time (all eight at once, by four waves, keep LDS
+    // busy for half a step and hold the products at issue).  Before the last
+    // step's products, whose operands are in registers, the waves meet, and read
+    // the next stage's first operands between them.  Loads go out two after each
+    // row of products: x's in the first step, w's in the last, as soon as their
+    // buffers are free.  (Both in the first half, w then one stage ahead, left
+    // it 8 rows of products before it was waited for, not 12.)
     auto stage = [&](int s, lds_ptr tx, lds_ptr tw, lds_ptr nw, lds_ptr nx2, lds_ptr nx) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
-            if (ks + 1 < kSteps) {
-                read(tx, tw, ks + 1, fx[(ks + 1) & 1], fw[(ks + 1) & 1]);
-            } else {
+            if (ks + 1 == kSteps) {
                 __builtin_amdgcn_s_waitcnt(kWaitLdsVmemButX);
                 barrier();
-                read(nx, nw, 0, fx[0], fw[0]);
             }
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-                for (int j = 0; j < kBlocks; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
-                const int slot = ks * kBlocks + i;
+                for (int n = 3 * i; n < 3 * i + 3; ++n) {
+                    if (ks + 1 < kSteps)
+                        read(tx, tw, ks + 1, n, fx[(ks + 1) & 1], fw[(ks + 1) & 1]);
+                    else
+                        read(nx, nw, 0, n, fx[0], fw[0]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 2 * slot; n < 2 * slot + 2; ++n) {
-                    if (n < kGroups)
-                        load_w(n, s + 1, nw);
-                    else if (n < 2 * kGroups)
-                        load_x(n - kGroups, s + 2, nx2);
+                for (int j = 0; j < kBlocks; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
+#pragma unroll
+                for (int n = 2 * i; n < 2 * i + 2; ++n) {
+                    if (ks == 0) load_x(n, s + 2, nx2);
+                    if (ks + 1 == kSteps) load_w(n, s + 2, tw);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
