@@ -117,24 +117,25 @@ __device__ __forceinline__ void part_of(const Product &p, int split, int &begin,
 
 // h = silu(x Wg' + bg) (x Wu' + bu).
 template <int kTile>
-__global__ __launch_bounds__(kThreads) void mlp_gate_kernel(MlpArgs a) {
+__global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
-    constexpr int kWave = kTile / 2, kHalf = kWave / 2, kBlocks = kWave / 32;
+    typedef Tile<kTile> T;
+    constexpr int kHalf = T::kWaveN / 2;
     const Product &p = a.p[0];
     const Place at(p, int(xcd_contiguous_tile(blockIdx.x, gridDim.x)));
     const int64_t m0 = at.mt * kTile;
     const int n0 = at.nt * (kTile / 2);
-    f32x16 acc[kBlocks][kBlocks];
+    Sums<kTile> acc;
     multiply<kTile, false, false, kGateUp>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
     constexpr int kLanes = kHalf / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kHalf + piece;
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * kHalf + piece;
     float bg[8], bu[8];
     load_bias(a.bias0, col, p.n, bg);
     load_bias(a.bias1, col, p.n, bu);
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
+    for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void mlp_gate_kernel(MlpArgs a) {
                 u[j] = in ? u[j] + bu[j] : 0.0f;
                 h[j] = g[j] * sigmoid(g[j]) * u[j];
             }
-            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
             if (row >= p.m || col >= a.ldh) continue;
             keep_bf16(a.hidden + row * a.ldh + col, h);
             if (a.gate_up) {
@@ -163,29 +164,29 @@ __global__ __launch_bounds__(kThreads) void mlp_gate_kernel(MlpArgs a) {
 // dg and du from dh = dout Wd and the saved g, u; partial sums of both over
 // the rows of each half of the tile.
 template <int kTile>
-__global__ __launch_bounds__(kThreads) void mlp_dhidden_kernel(MlpArgs a) {
+__global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
-    constexpr int kWave = kTile / 2, kBlocks = kWave / 32;
+    typedef Tile<kTile> T;
     const Product &p = a.p[0];
     const Place at(p, int(xcd_contiguous_tile(blockIdx.x, gridDim.x)));
     const int64_t m0 = at.mt * kTile;
     const int n0 = at.nt * kTile;
-    f32x16 acc[kBlocks][kBlocks];
+    Sums<kTile> acc;
     multiply<kTile, false, true, kOnce>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
-    constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
+    constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kWave + piece;
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece;
     float sg[8] = {}, su[8] = {};
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
+    for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
             const int r = t * kPass + lane / kLanes;
             float dh[8], g[8], u[8];
             turned.template get<8>(r, piece, dh);
-            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
             if (row >= p.m || col >= a.ldh) continue;
             load8(a.gate_up + row * a.ldh + col, g);
             load8(a.gate_up + (p.m + row) * a.ldh + col, u);
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void mlp_dhidden_kernel(MlpArgs a) {
             su[j] += __shfl_xor(su[j], m);
         }
     if (lane < kLanes && col < a.ldh) {
-        float *part = a.part + (2 * at.mt + (wave >> 1)) * 2 * a.ldh + col;
+        float *part = a.part + (2 * at.mt + wave / T::kWavesN) * 2 * a.ldh + col;
         store8(part, sg);
         store8(part + a.ldh, su);
     }
@@ -219,9 +220,9 @@ __global__ __launch_bounds__(kThreads) void mlp_dhidden_kernel(MlpArgs a) {
 // Products whose sums are the output: out = h Wd' + bd (kWAcross false), dx
 // (kWAcross), the weights' gradients (both across), or a split's partial sums.
 template <int kTile, bool kXAcross, bool kWAcross>
-__global__ __launch_bounds__(kThreads) void mlp_product_kernel(MlpArgs a) {
+__global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
-    constexpr int kWave = kTile / 2, kBlocks = kWave / 32;
+    typedef Tile<kTile> T;
     const int tile = int(xcd_contiguous_tile(blockIdx.x, gridDim.x));
     int n = 0;
     if constexpr (kXAcross) n = a.products > 2 && tile >= a.p[2].first ? 2 : a.products > 1 && tile >= a.p[1].first ? 1 : 0;
@@ -231,23 +232,23 @@ __global__ __launch_bounds__(kThreads) void mlp_product_kernel(MlpArgs a) {
     const int n0 = at.nt * kTile;
     int begin, end;
     part_of(p, at.split, begin, end);
-    f32x16 acc[kBlocks][kBlocks];
+    Sums<kTile> acc;
     multiply<kTile, kXAcross, kWAcross, kWAcross && !kXAcross ? kTwice : kOnce>(p, m0, n0, begin, end, lds, acc);
     const Turned<kTile> turned(lds);
-    constexpr int kLanes = kWave / 8, kPass = 64 / kLanes;
+    constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave & 1) * kWave + piece, left = p.n - col;
+    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece, left = p.n - col;
     float bias[8];
     load_bias(p.splits > 1 ? nullptr : a.bias0, col, p.n, bias);
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
+    for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
             const int r = t * kPass + lane / kLanes;
             float v[8];
             turned.template get<8>(r, piece, v);
-            const int64_t row = m0 + (wave >> 1) * kWave + i * 32 + r;
+            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
             if (row >= p.m || left <= 0) continue;
             if (p.splits > 1) {
                 store8(a.part + (at.split * p.m + row) * a.part_stride + col, v);
@@ -536,11 +537,10 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         a.gate_up = args->gate_up;
         a.hidden = hidden;
         a.ldh = z.hp;
-        const dim3 block{unsigned(kThreads), 1, 1};
         if (gate.tile == 256)
-            hipLaunchKernelGGL(mlp_gate_kernel<256>, dim3(unsigned(gate.tiles()), 1, 1), block, 0, s, a);
+            hipLaunchKernelGGL(mlp_gate_kernel<256>, dim3(unsigned(gate.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
         else
-            hipLaunchKernelGGL(mlp_gate_kernel<128>, dim3(unsigned(gate.tiles()), 1, 1), block, 0, s, a);
+            hipLaunchKernelGGL(mlp_gate_kernel<128>, dim3(unsigned(gate.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
         a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down);
         a.out[0] = static_cast<uint16_t *>(out);
         a.ldo[0] = z.d;
@@ -549,9 +549,9 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         a.part_stride = int32_t(pad_to(z.d, 8));
         a.products = 1;
         if (down.tile == 256)
-            hipLaunchKernelGGL((mlp_product_kernel<256, false, false>), dim3(unsigned(down.tiles()), 1, 1), block, 0, s, a);
+            hipLaunchKernelGGL((mlp_product_kernel<256, false, false>), dim3(unsigned(down.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
         else
-            hipLaunchKernelGGL((mlp_product_kernel<128, false, false>), dim3(unsigned(down.tiles()), 1, 1), block, 0, s, a);
+            hipLaunchKernelGGL((mlp_product_kernel<128, false, false>), dim3(unsigned(down.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
         if (down.splits > 1) {
             join(a, s);
             ++launches;
@@ -607,7 +607,6 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
     int launches = 0;
     const void *x = args->x, *dout = grads->dout, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
     const Cut dhidden = z.dhidden(), dx = z.dx();
-    const dim3 block{unsigned(kThreads), 1, 1};
     const hipError_t e = timed_launch(s, [&] {
         if (z.rows > 0 && z.pad_d) {
             pad(x, z.rows, z.d, space.x, z.dp, s);
@@ -635,9 +634,9 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             a.dup = space.dup;
             a.part = grads->db_gate || grads->db_up ? space.sums : nullptr;
             if (dhidden.tile == 256)
-                hipLaunchKernelGGL(mlp_dhidden_kernel<256>, dim3(unsigned(dhidden.tiles()), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL(mlp_dhidden_kernel<256>, dim3(unsigned(dhidden.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
             else
-                hipLaunchKernelGGL(mlp_dhidden_kernel<128>, dim3(unsigned(dhidden.tiles()), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL(mlp_dhidden_kernel<128>, dim3(unsigned(dhidden.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
             ++launches;
         }
         const int32_t halves = z.rows > 0 ? int32_t(2 * dhidden.m_tiles) : 0;
@@ -662,9 +661,9 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             a.part = space.part;
             a.part_stride = int32_t(pad_to(z.d, 8));
             if (dx.tile == 256)
-                hipLaunchKernelGGL((mlp_product_kernel<256, false, true>), dim3(unsigned(dx.tiles()), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL((mlp_product_kernel<256, false, true>), dim3(unsigned(dx.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
             else
-                hipLaunchKernelGGL((mlp_product_kernel<128, false, true>), dim3(unsigned(dx.tiles()), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL((mlp_product_kernel<128, false, true>), dim3(unsigned(dx.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
             if (dx.splits > 1) join(a, s), ++launches;
             ++launches;
         }
@@ -685,9 +684,9 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             add(grads->dw_down, matrix(dout, z.ld()), matrix(args->hidden, z.hp), z.d, z.h, back);
             a.products = n;
             if (wide.tile == 256)
-                hipLaunchKernelGGL((mlp_product_kernel<256, true, true>), dim3(unsigned(tiles), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL((mlp_product_kernel<256, true, true>), dim3(unsigned(tiles), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
             else
-                hipLaunchKernelGGL((mlp_product_kernel<128, true, true>), dim3(unsigned(tiles), 1, 1), block, 0, s, a);
+                hipLaunchKernelGGL((mlp_product_kernel<128, true, true>), dim3(unsigned(tiles), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
             ++launches;
         }
     });

@@ -46,13 +46,12 @@ typedef __attribute__((address_space(3))) bf16x8 *lds_bf16x8_ptr;
 typedef __attribute__((address_space(3))) f32x4 *lds_f32x4_ptr;
 typedef __attribute__((address_space(3))) uint8_t *lds_ptr;
 
-constexpr int kThreads = 256;
 constexpr int kStageK = 64;
 constexpr int kWord3 = 0x00020000;          // raw buffer resource word 3
 constexpr int kRecords = 0x7FFFFFF0;        // the largest size of a resource
 constexpr uint32_t kOutside = 0x7FFFFFF8u;  // a byte offset past every resource: reads zeros
 constexpr int kWaitAll = 0;                 // s_waitcnt: every counter at zero
-constexpr int kGroupM = 8;                  // tiles of rows that share a run of channel tiles
+constexpr int kGroupM = 4;                  // tiles of rows that share a run of channel tiles
 
 // One bf16 matrix; stride in values, a multiple of 8, as is the innermost
 // axis; 16-byte aligned.
@@ -71,6 +70,24 @@ struct Product {
     int32_t m_tiles, n_tiles;
     int32_t first;        // of its tiles in the launch
 };
+
+// How a tile is cut among its waves: two along the rows, the others along the
+// channels, each kWaveM x kWaveN in blocks of 32 x 32.
+template <int kTile_>
+struct Tile {
+    static constexpr int kTile = kTile_;
+#ifdef W4
+    static constexpr int kWaves = 4;
+#else
+    static constexpr int kWaves = kTile == 256 ? 8 : 4;
+#endif
+    static constexpr int kThreads = kWaves * 64, kWavesN = kWaves / 2;
+    static constexpr int kWaveM = kTile / 2, kWaveN = kTile / kWavesN;
+    static constexpr int kBlocksM = kWaveM / 32, kBlocksN = kWaveN / 32;
+    static constexpr int kGroups = kTile / 8 / kWaves;  // 1 KB loads a wave makes of each operand a stage
+};
+template <int kTile>
+using Sums = f32x16[Tile<kTile>::kBlocksM][Tile<kTile>::kBlocksN];
 
 __device__ __forceinline__ int row_key(int r) { return (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1); }
 __device__ __forceinline__ int block_key(int g) { return g ^ ((g & 3) >> 1); }
@@ -110,7 +127,7 @@ struct Buffers {
 // `count`.
 template <int kTile, bool kAcross>
 struct Operand {
-    static constexpr int kGroups = kTile / 8 / 4;
+    static constexpr int kGroups = Tile<kTile>::kGroups;
     uint32_t off[kGroups];
     int chunk;  // along: the first group's chunk of the lane's row; group i's is chunk ^ i
     int base;   // the lane's part of an operand read's address
@@ -121,8 +138,8 @@ struct Operand {
     // 8, chunk l % 8 of it, so it fetches the chunk that the swizzle puts there.
     // `rows_from`: what row of the matrix the wave's first row of the tile is
     // (along); rows past the last one read the last one, and are not stored.
-    // `half`: which half of the tile the wave's operands are of.
-    __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from, int half) {
+    // `at`: the first row (column) of the tile that the wave's operands are of.
+    __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from, int at) {
         const int lane = threadIdx.x & 63, l8 = lane >> 3;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         if constexpr (kAcross) {
@@ -136,10 +153,10 @@ struct Operand {
             const int x = 8 * (lane >> 5) + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
             // row x of the 16 of a step, whose block of eight is 2 s + lane / 32:
             // block_key of it is (lane / 32) ^ the step's own part
-            base = half * (kTile / 128) * (kStageK * 128) + x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
+            base = at / 64 * (kStageK * 128) + x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
         } else {
             const int r = lane & 31;
-            base = (half * (kTile / 2) + r) * 128 + (((lane >> 5) ^ ((r ^ (r >> 3)) & 7)) << 4);
+            base = (at + r) * 128 + (((lane >> 5) ^ ((r ^ (r >> 3)) & 7)) << 4);
             chunk = ((lane & 7) ^ l8 ^ (wave * kGroups)) & 7;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
@@ -174,7 +191,7 @@ struct Operand {
 #endif
     }
 
-    // Rows (columns) 32 i .. + 31 of the wave's half, step s of the stage.
+    // Rows (columns) 32 i .. + 31 of the wave's, step s of the stage.
     __device__ __forceinline__ bf16x8 read(lds_ptr t, int i, int s) const {
         if constexpr (kAcross) {
             const int flip = ((4 * (i & 1)) ^ (2 * s) ^ (s & 1)) << 4, at = (i / 2) * (kStageK * 128) + s * 16 * 128;
@@ -201,25 +218,32 @@ struct Operand {
 enum Over { kOnce, kTwice, kGateUp };
 template <int kTile, bool kXAcross, bool kWAcross, Over kOver>
 __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, int begin, int end, const Buffers<kTile> &lds,
-                                         f32x16 (&acc)[kTile / 64][kTile / 64]) {
+                                         Sums<kTile> &acc) {
     constexpr bool kGate = kOver == kGateUp;
     static_assert(!(kGate && kWAcross), "gate and up are stored along k");
     typedef Operand<kTile, kXAcross> X;
     typedef Operand<kTile, kWAcross> W;
-    constexpr int kBlocks = kTile / 64, kGroups = X::kGroups, kSteps = 4;
-    // vmcnt (bits 3:0 and 15:14) and lgkmcnt: one stage of both operands may stay
-    // in flight; one of x, and lgkmcnt(0)
-    constexpr int kWaitVmemButBoth = 0x0F70 | ((2 * kGroups) & 15) | ((2 * kGroups) >> 4 << 14);
-    constexpr int kWaitLdsVmemButX = 0x0070 | kGroups;
-    // a stage's wait counts on x's loads being the newest
-    static_assert(kGroups <= 15 && kGroups == 2 * kBlocks, "two loads after each row of products fill a step");
+    typedef Tile<kTile> T;
+    constexpr int kM = T::kBlocksM, kN = T::kBlocksN, kGroups = T::kGroups, kSteps = 4;
+    // Loads go out one after each row of products: first w's of two stages on,
+    // from the last step on, when their buffer is free, then x's.  kEarly of
+    // w's are sent before the next stage begins.
+    constexpr int kEarly = kGroups < kM ? kGroups : kM;
+    static_assert(kGroups <= 15 && 2 * kGroups <= kSteps * kM, "a stage's loads fit its rows of products");
+    // vmcnt (bits 3:0 and 15:14) and lgkmcnt: one stage of x and w's early loads
+    // may stay in flight; one of x, and lgkmcnt(0)
+    constexpr int kFlight = kGroups + kEarly;
+    constexpr int kWaitFirst = 0x0F70 | (kFlight & 15) | (kFlight >> 4 << 14);
+    constexpr int kWaitStage = 0x0070 | kGroups;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / T::kWavesN, wn = wave % T::kWavesN;
     const int seg = (p.k + kStageK - 1) / kStageK;  // stages of a segment
-    const X x(p.x[0].stride, m0, p.m, m0 + wave * (kTile / 4), wm);
-    // gate's rows are those of even waves, up's of odd ones: a quarter of the
-    // tile holds both projections of the same kWave / 2 channels
-    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kTile / 4) : n0 + wave * (kTile / 4), wn);
+    const X x(p.x[0].stride, m0, p.m, m0 + wave * (kGroups * 8), wm * T::kWaveM);
+    // of a wave's channels the first half is gate's and the second up's, of the
+    // same rows of the two weights; so the rows that a wave loads are of one of
+    // them, gate's in even ones
+    static_assert(!kGate || kGroups * 8 == T::kWaveN / 2, "a wave loads rows of one of the two");
+    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kGroups * 8) : n0 + wave * (kGroups * 8), wn * T::kWaveN);
     // in registers from here on: a scalar load in the loop would make every
     // wait for LDS a wait for all of it
     const Matrix x0 = p.x[0], w0 = kGate ? p.w[wave & 1] : p.w[0];
@@ -241,16 +265,16 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i)
+    for (int i = 0; i < kM; ++i)
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) acc[i][j] = f32x16{};
-    bf16x8 fx[2][kBlocks], fw[2][kBlocks];
+        for (int j = 0; j < kN; ++j) acc[i][j] = f32x16{};
+    bf16x8 fx[2][kM], fw[2][kN];
     // operand n of a step, w's first
-    auto read = [&](lds_ptr tx, lds_ptr tw, int s, int n, bf16x8 (&a)[kBlocks], bf16x8 (&b)[kBlocks]) __attribute__((always_inline)) {
-        if (n < kBlocks)
+    auto read = [&](lds_ptr tx, lds_ptr tw, int s, int n, bf16x8 (&a)[kM], bf16x8 (&b)[kN]) __attribute__((always_inline)) {
+        if (n < kN)
             b[n] = w.read(tw, n, s);
-        else if (n < 2 * kBlocks)
-            a[n - kBlocks] = x.read(tx, n - kBlocks, s);
+        else if (n < kN + kM)
+            a[n - kN] = x.read(tx, n - kN, s);
     };
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin, lds.x[0]);
@@ -259,29 +283,26 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin + 1, lds.x[1]);
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) load_w(i, begin + 1, lds.w[1]);
-    __builtin_amdgcn_s_waitcnt(kWaitVmemButBoth);
+    for (int i = 0; i < kEarly; ++i) load_w(i, begin + 1, lds.w[1]);
+    __builtin_amdgcn_s_waitcnt(kWaitFirst);
     barrier();
 #pragma unroll
-    for (int n = 0; n < 2 * kBlocks; ++n) read(lds.x[0], lds.w[0], 0, n, fx[0], fw[0]);
+    for (int n = 0; n < kM + kN; ++n) read(lds.x[0], lds.w[0], 0, n, fx[0], fw[0]);
     __builtin_amdgcn_sched_barrier(0);
     // One stage.  The next step's operands are read between this one's rows of
-    // products, three at a time (all eight at once, by four waves, keep LDS
-    // busy for half a step and hold the products at issue).  Before the last
-    // step's products, whose operands are in registers, the waves meet, and read
-    // the next stage's first operands between them.  Loads go out two after each
-    // row of products: x's in the first step, w's in the last, as soon as their
-    // buffers are free.  (Both in the first half, w then one stage ahead, left
-    // it 8 rows of products before it was waited for, not 12.)
+    // products, three at a time (all at once, by every wave, keep LDS busy for
+    // half a step and hold the products at issue).  Before the last step's
+    // products, whose operands are in registers, the waves meet, and read the
+    // next stage's first operands between them.
     auto stage = [&](int s, lds_ptr tx, lds_ptr tw, lds_ptr nw, lds_ptr nx2, lds_ptr nx) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
             if (ks + 1 == kSteps) {
-                __builtin_amdgcn_s_waitcnt(kWaitLdsVmemButX);
+                __builtin_amdgcn_s_waitcnt(kWaitStage);
                 barrier();
             }
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
+            for (int i = 0; i < kM; ++i) {
 #pragma unroll
                 for (int n = 3 * i; n < 3 * i + 3; ++n) {
                     if (ks + 1 < kSteps)
@@ -291,12 +312,12 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < kBlocks; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
-#pragma unroll
-                for (int n = 2 * i; n < 2 * i + 2; ++n) {
-                    if (ks == 0) load_x(n, s + 2, nx2);
-                    if (ks + 1 == kSteps) load_w(n, s + 2, tw);
-                }
+                for (int j = 0; j < kN; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
+                const int q = (ks + 1) % kSteps * kM + i;
+                if (q < kGroups)
+                    load_w(q, ks + 1 == kSteps ? s + 2 : s + 1, ks + 1 == kSteps ? tw : nw);
+                else if (q < 2 * kGroups)
+                    load_x(q - kGroups, s + 2, nx2);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -341,22 +362,23 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     barrier();
 }
 
-// A wave's block of 32 rows and kTile / 2 channels, turned in LDS (float32,
-// 16-byte chunks XOR-swizzled by the row): a lane then reads whole pieces of
-// rows.
+// A wave's block of 32 rows and its channels, turned in LDS (float32, 16-byte
+// chunks XOR-swizzled by the row): a lane then reads whole pieces of rows.
 template <int kTile>
 struct Turned {
-    static constexpr int kWave = kTile / 2, kBlocks = kWave / 32, kRowBytes = kWave * 4, kChunks = kRowBytes / 16;
+    typedef Tile<kTile> T;
+    static constexpr int kRowBytes = T::kWaveN * 4, kChunks = kRowBytes / 16;
     lds_ptr region;
     __device__ __forceinline__ explicit Turned(const Buffers<kTile> &lds) {
-        static_assert(2 * 32 * kRowBytes <= kTile * 128, "two waves share a buffer");
+        constexpr int kHalf = T::kWaves / 2;
+        static_assert(kHalf * 32 * kRowBytes <= kTile * 128, "half the waves share a buffer");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        region = (wave < 2 ? lds.x[0] : lds.x[1]) + (wave & 1) * (32 * kRowBytes);
+        region = (wave < kHalf ? lds.x[0] : lds.x[1]) + (wave % kHalf) * (32 * kRowBytes);
     }
-    __device__ __forceinline__ void put(const f32x16 (&acc)[kBlocks]) const {
+    __device__ __forceinline__ void put(const f32x16 (&acc)[T::kBlocksN]) const {
         const int lane = threadIdx.x & 63, r = lane & 31;
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j)
+        for (int j = 0; j < T::kBlocksN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int c = j * 8 + 2 * g + (lane >> 5);
