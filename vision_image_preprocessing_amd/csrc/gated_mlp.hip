@@ -50,14 +50,14 @@ struct MlpArgs {
     Product p[3];
     uint16_t *out[3];            // bf16 [m][ldo]
     int64_t ldo[3];
-    int32_t products, tiles;
+    int32_t products;
+    Units units;
     const float *bias0, *bias1;  // or null
     float *gate_up;              // [2][rows][ldh], or null
     uint16_t *hidden;            // [rows][ldh]
     uint16_t *dgate, *dup;       // [rows][ldh]
-    float *part;                 // partial sums: of split products, or of dg and du over rows; or null
+    float *part;                 // partial sums: [slot][tile][tile] of tiles in parts, or of dg and du over rows; or null
     int64_t ldh;
-    int32_t part_stride;         // of split products' rows
 };
 
 // Eight channels to bf16, at any address of the type; `left` of them inside.
@@ -109,10 +109,9 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
     __shared__ __attribute__((aligned(16))) uint8_t sw0[kTile * 128], sw1[kTile * 128];           \
     const Buffers<kTile> lds{{(lds_ptr)sx0, (lds_ptr)sx1, (lds_ptr)sx2}, {(lds_ptr)sw0, (lds_ptr)sw1}}
 
-// Stages of a split of a product.
-__device__ __forceinline__ void part_of(const Product &p, int split, int &begin, int &end) {
-    begin = int(int64_t(p.stages) * split / p.splits);
-    end = int(int64_t(p.stages) * (split + 1) / p.splits);
+// Which product of a launch a tile is of.
+__device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
+    return a.products > 2 && tile >= a.p[2].first ? 2 : a.products > 1 && tile >= a.p[1].first ? 1 : 0;
 }
 
 // h = silu(x Wg' + bg) (x Wu' + bu).
@@ -223,64 +222,72 @@ template <int kTile, bool kXAcross, bool kWAcross>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
     typedef Tile<kTile> T;
-    const int tile = int(xcd_contiguous_tile(blockIdx.x, gridDim.x));
-    int n = 0;
-    if constexpr (kXAcross) n = a.products > 2 && tile >= a.p[2].first ? 2 : a.products > 1 && tile >= a.p[1].first ? 1 : 0;
+    const Unit unit(a.units);
+    const int n = kXAcross ? product_of(a, unit.tile) : 0;
     const Product &p = a.p[n];
-    const Place at(p, tile - p.first);
+    const Place at(p, unit.tile - p.first);
     const int64_t m0 = at.mt * kTile;
     const int n0 = at.nt * kTile;
-    int begin, end;
-    part_of(p, at.split, begin, end);
+    const bool part = unit.split >= 0;
+    const int begin = part ? int(int64_t(p.stages) * unit.split / a.units.splits) : 0;
+    const int end = part ? int(int64_t(p.stages) * (unit.split + 1) / a.units.splits) : p.stages;
     Sums<kTile> acc;
     multiply<kTile, kXAcross, kWAcross, kWAcross && !kXAcross ? kTwice : kOnce>(p, m0, n0, begin, end, lds, acc);
     const Turned<kTile> turned(lds);
     constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece, left = p.n - col;
+    const int piece = (lane % kLanes) * 8, c0 = (wave % T::kWavesN) * T::kWaveN + piece, col = n0 + c0, left = p.n - col;
     float bias[8];
-    load_bias(p.splits > 1 ? nullptr : a.bias0, col, p.n, bias);
+    load_bias(part ? nullptr : a.bias0, col, p.n, bias);
+    float *sums = part ? a.part + int64_t(unit.slot) * (kTile * kTile) + c0 : nullptr;
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
-            const int r = t * kPass + lane / kLanes;
+            const int r = t * kPass + lane / kLanes, r0 = (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
             float v[8];
             turned.template get<8>(r, piece, v);
-            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
-            if (row >= p.m || left <= 0) continue;
-            if (p.splits > 1) {
-                store8(a.part + (at.split * p.m + row) * a.part_stride + col, v);
+            if (m0 + r0 >= p.m || left <= 0) continue;
+            if (part) {
+                store8(sums + r0 * kTile, v);
                 continue;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += bias[j];
-            store_bf16(a.out[n] + row * a.ldo[n] + col, v, left);
+            store_bf16(a.out[n] + (m0 + r0) * a.ldo[n] + col, v, left);
         }
     }
 }
 
-// out = the sum of the splits' parts, in their order, + bias.
-__global__ __launch_bounds__(256) void mlp_join_kernel(const float *part, int32_t splits, int64_t m, int32_t n, int32_t stride,
-                                                       const float *bias, uint16_t *out, int64_t ldo) {
-    const int pieces = (n + 7) / 8;
-    const int64_t id = row_group() * 256 + threadIdx.x, row = id / pieces;
-    if (row >= m) return;
-    const int col = int(id - row * pieces) * 8;
+// The tiles in parts: their sums in the parts' order, + bias.  32 (8, of 128 x
+// 128) workgroups a tile, eight channels a thread.
+template <int kTile>
+__global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
+    constexpr int kPieces = kTile / 8, kWgs = kTile * kPieces / 256;
+    const int t = int(blockIdx.x) / kWgs, tile = a.units.full + t;
+    const int n = product_of(a, tile);
+    const Product &p = a.p[n];
+    const Place at(p, tile - p.first);
+    const int id = (int(blockIdx.x) - t * kWgs) * 256 + int(threadIdx.x), r = id / kPieces, c = id % kPieces * 8;
+    const int64_t row = at.mt * kTile + r;
+    const int col = at.nt * kTile + c, left = p.n - col;
+    if (row >= p.m || left <= 0) return;
+    const float *part = a.part + int64_t(t) * (kTile * kTile) + r * kTile + c;
     float v[8];
-    load8(part + row * stride + col, v);
-    for (int s = 1; s < splits; ++s) {
+    load8(part, v);
+#pragma unroll 4
+    for (int s = 1; s < a.units.splits; ++s) {
         float w[8];
-        load8(part + (s * m + row) * stride + col, w);
+        load8(part + int64_t(s) * a.units.tail * (kTile * kTile), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += w[j];
     }
     float b[8];
-    load_bias(bias, col, n, b);
+    load_bias(a.bias0, col, p.n, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += b[j];
-    store_bf16(out + row * ldo + col, v, n - col);
+    store_bf16(a.out[n] + row * a.ldo[n] + col, v, left);
 }
 
 // Rows of any width to rows of a multiple of kPad values, zeros behind: the
@@ -334,27 +341,61 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
 int64_t pad_to(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
 int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// How a product is cut into tiles: 256 x 256 where there are enough of them
-// for the card, else 128 x 128, and K into parts where there are few.
+// How a launch's products are cut into tiles and these into parts of K.
 struct Cut {
     int tile;
-    int64_t m_tiles, n_tiles;
-    int splits;
-    int64_t tiles() const { return m_tiles * n_tiles * splits; }
+    Units units;
+    int64_t tiles;
+    int64_t part_values() const { return units.splits > 1 ? int64_t(units.tail) * units.splits * tile * tile : 0; }
 };
 constexpr int kCus = 256;
-Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable) {
-    const int64_t big = ceil_div(m, 256) * ceil_div(n, 256);
-    if (big >= kCus) return {256, ceil_div(m, 256), ceil_div(n, 256), 1};
-    Cut c{128, ceil_div(m, 128), ceil_div(n, 128), 1};
-    const int64_t tiles = c.m_tiles * c.n_tiles;
-    // two workgroups a CU, at least six stages each
-    if (splittable && tiles > 0) {
-        const int64_t most = stages / 6, wanted = 2 * kCus / tiles;
-        c.splits = int(wanted < most ? wanted : most);
-        if (c.splits < 1) c.splits = 1;
+constexpr int kMinStages = 6;  // of a part
+
+// Tiles of one size: a round of the card is a tile a CU of 256 x 256, two of
+// 128 x 128.  What is left over after whole rounds would keep some CUs busy for
+// all of K and leave the others idle; its K is cut into parts where that saves
+// enough stages to pay for writing and joining them.
+// Weighs in units of a 256 x 256 stage, about 1.7 us; 128 x 128 tiles take 0.68
+// of it for half the products.
+Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, double *cost) {
+    Cut c{tile, {int32_t(tiles), 0, 1}, tiles};
+    const int64_t slots = tile == 256 ? kCus : 2 * kCus, full = tiles / slots * slots, tail = tiles - full;
+    const double stage = tile == 256 ? 1.0 : 0.68;
+    double rest = tail ? double(stages) : 0.0, extra = 0.0;
+    if (splittable && tail) {
+        const int64_t most = stages / kMinStages, wanted = slots / tail, splits = wanted < most ? wanted : most;
+        const double joined = double(ceil_div(stages, splits > 0 ? splits : 1)), cost_of = 8.0 + 8.0 * double(tail * splits) / double(slots);
+        if (splits > 1 && (rest - joined) * stage > cost_of) {
+            c.units = {int32_t(full), int32_t(tail), int32_t(splits)};
+            rest = joined;
+            extra = cost_of;
+        }
     }
+    // a round's first loads and its store are about four stages
+    if (cost) *cost = (double(full / slots) * (double(stages) + 4.0) + (tail ? rest + 4.0 : 0.0)) * stage + extra;
     return c;
+}
+
+// One or more products [m][n] of as many stages each.
+struct Extent {
+    int64_t m, n;
+};
+int64_t tiles_of(const Extent *e, int count, int tile, int columns) {
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) tiles += ceil_div(e[i].m, tile) * ceil_div(e[i].n, columns);
+    return tiles;
+}
+// gate: both projections of a channel lie in one tile, which then has half as
+// many.
+Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool gate) {
+    double big, small;
+    const Cut c256 = cut_tiles(256, tiles_of(e, count, 256, gate ? 128 : 256), stages, splittable, &big);
+    const Cut c128 = cut_tiles(128, tiles_of(e, count, 128, gate ? 64 : 128), stages, splittable, &small);
+    return big <= small ? c256 : c128;
+}
+Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable, bool gate = false) {
+    const Extent e{m, n};
+    return cut(&e, 1, stages, splittable, gate);
 }
 
 struct Sizes {
@@ -365,15 +406,19 @@ struct Sizes {
         : rows(rows), d(d), h(h), pad_d(d % 8 != 0), pad_h(h % 8 != 0), dp(pad_to(d, kPad)), hp(pad_to(h, kPad)) {}
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
-    // gate and up of a channel lie in one tile
-    Cut gate() const {
-        Cut c = cut(rows, 2 * h, ceil_div(d, kStageK), false);
-        c.n_tiles = ceil_div(h, c.tile / 2);
-        return c;
-    }
+    Cut gate() const { return cut(rows, h, ceil_div(d, kStageK), false, true); }
     Cut down() const { return cut(rows, d, ceil_div(h, kStageK), true); }
     Cut dhidden() const { return cut(rows, h, ceil_div(d, kStageK), false); }
     Cut dx() const { return cut(rows, d, 2 * ceil_div(h, kStageK), true); }
+    // of the weights' gradients that are made
+    Cut dweights(bool gate, bool up, bool down) const {
+        Extent e[3];
+        int n = 0;
+        if (gate) e[n++] = {h, d};
+        if (up) e[n++] = {h, d};
+        if (down) e[n++] = {d, h};
+        return cut(e, n, ceil_div(rows, kStageK), true, false);
+    }
 };
 
 // Takes aligned parts of a workspace, or measures them.
@@ -399,8 +444,7 @@ struct ForwardSpace {
         wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
-        const Cut k = s.down();
-        part = c.take<float>(k.splits > 1 ? k.splits * s.rows * pad_to(s.d, 8) : 0);
+        part = c.take<float>(s.down().part_values());
         bytes = c.used;
     }
 };
@@ -419,9 +463,13 @@ struct BackwardSpace {
         wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
-        const Cut k = s.dx();
-        part = c.take<float>(k.splits > 1 ? k.splits * s.rows * pad_to(s.d, 8) : 0);
-        sums = c.take<float>(2 * s.dhidden().m_tiles * 2 * s.hp);
+        int64_t values = s.dx().part_values();
+        for (int made = 1; made < 8; ++made) {  // gate's and up's alone are alike
+            const int64_t w = made == 2 || made == 6 ? 0 : s.dweights(made & 1, made & 2, made & 4).part_values();
+            if (w > values) values = w;
+        }
+        part = c.take<float>(values);
+        sums = c.take<float>(2 * ceil_div(s.rows, s.dhidden().tile) * 2 * s.hp);
         columns = c.take<float>(kColumnGroups * s.d);
         bytes = c.used;
     }
@@ -429,7 +477,7 @@ struct BackwardSpace {
 
 Matrix matrix(const void *p, int64_t stride) { return Matrix{static_cast<const uint16_t *>(p), stride}; }
 
-Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t k, const Cut &c) {
+Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t k, int tile, int columns) {
     Product p;
     std::memset(&p, 0, sizeof(p));
     p.x[0] = p.x[1] = x;
@@ -438,9 +486,8 @@ Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t 
     p.n = int32_t(n);
     p.k = int32_t(k);
     p.stages = int32_t(ceil_div(k, kStageK));
-    p.splits = c.splits;
-    p.m_tiles = int32_t(c.m_tiles);
-    p.n_tiles = int32_t(c.n_tiles);
+    p.m_tiles = int32_t(ceil_div(m, tile));
+    p.n_tiles = int32_t(ceil_div(n, columns));
     return p;
 }
 
@@ -451,11 +498,21 @@ void pad(const void *x, int64_t rows, int64_t width, uint16_t *out, int64_t padd
                            int32_t(width), out, int32_t(padded));
 }
 
-void join(const MlpArgs &a, hipStream_t s) {
-    const Product &p = a.p[0];
-    const int64_t blocks = ceil_div(p.m * ceil_div(p.n, 8), 256);
-    hipLaunchKernelGGL(mlp_join_kernel, row_grid(blocks), dim3(256, 1, 1), 0, s, a.part, p.splits, p.m, p.n, a.part_stride,
-                       a.bias0, a.out[0], a.ldo[0]);
+// A launch of mlp_product_kernel, and its join; the launches made.
+template <bool kXAcross, bool kWAcross>
+int launch_products(MlpArgs &a, const Cut &c, float *part, hipStream_t s) {
+    a.units = c.units;
+    a.part = part;
+    const dim3 grid(unsigned(c.units.count()), 1, 1);
+    const bool joined = c.units.splits > 1;
+    if (c.tile == 256) {
+        hipLaunchKernelGGL((mlp_product_kernel<256, kXAcross, kWAcross>), grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
+        if (joined) hipLaunchKernelGGL(mlp_join_kernel<256>, dim3(unsigned(c.units.tail) * 32, 1, 1), dim3(256, 1, 1), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((mlp_product_kernel<128, kXAcross, kWAcross>), grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+        if (joined) hipLaunchKernelGGL(mlp_join_kernel<128>, dim3(unsigned(c.units.tail) * 8, 1, 1), dim3(256, 1, 1), 0, s, a);
+    }
+    return joined ? 2 : 1;
 }
 
 int check_mlp(const mimo_mlp *p, const char *who) {
@@ -467,7 +524,7 @@ int check_mlp(const mimo_mlp *p, const char *who) {
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 rows, or a width above 65536");
     const Sizes s(p->rows, p->width, p->hidden_width);
     for (const Cut &c : {s.gate(), s.down(), s.dhidden(), s.dx()})
-        if (c.tiles() > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
+        if (c.tiles > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
     return MIMO_OK;
 }
 
@@ -509,7 +566,7 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
     if (workspace_bytes < space.bytes)
         return set_error(MIMO_E_CAPACITY, "gated_mlp: workspace smaller than mimo_gated_mlp_workspace_bytes");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    int launches = 2;
+    int launches = 0;
     const void *x = args->x, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
     uint16_t *hidden = args->hidden ? static_cast<uint16_t *>(args->hidden) : space.hidden;
     const Cut gate = z.gate(), down = z.down();
@@ -530,32 +587,24 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         }
         MlpArgs a;
         std::memset(&a, 0, sizeof(a));
-        a.p[0] = product(matrix(x, z.ld()), matrix(wg, z.ld()), z.rows, z.h, z.d, gate);
+        a.p[0] = product(matrix(x, z.ld()), matrix(wg, z.ld()), z.rows, z.h, z.d, gate.tile, gate.tile / 2);
         a.p[0].w[1] = matrix(wu, z.ld());
+        a.products = 1;
         a.bias0 = args->b_gate;
         a.bias1 = args->b_up;
         a.gate_up = args->gate_up;
         a.hidden = hidden;
         a.ldh = z.hp;
+        const dim3 grid(unsigned(gate.tiles), 1, 1);
         if (gate.tile == 256)
-            hipLaunchKernelGGL(mlp_gate_kernel<256>, dim3(unsigned(gate.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
+            hipLaunchKernelGGL(mlp_gate_kernel<256>, grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
         else
-            hipLaunchKernelGGL(mlp_gate_kernel<128>, dim3(unsigned(gate.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
-        a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down);
+            hipLaunchKernelGGL(mlp_gate_kernel<128>, grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+        a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down.tile, down.tile);
         a.out[0] = static_cast<uint16_t *>(out);
         a.ldo[0] = z.d;
         a.bias0 = args->b_down;
-        a.part = space.part;
-        a.part_stride = int32_t(pad_to(z.d, 8));
-        a.products = 1;
-        if (down.tile == 256)
-            hipLaunchKernelGGL((mlp_product_kernel<256, false, false>), dim3(unsigned(down.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
-        else
-            hipLaunchKernelGGL((mlp_product_kernel<128, false, false>), dim3(unsigned(down.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
-        if (down.splits > 1) {
-            join(a, s);
-            ++launches;
-        }
+        launches += 1 + launch_products<false, false>(a, down, space.part, s);
     });
     if (e != hipSuccess) return hip_error(e, "gated_mlp: kernel launch");
     g_dispatches.fetch_add(launches);
@@ -629,17 +678,19 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
         a.gate_up = args->gate_up;
         a.ldh = z.hp;
         if (z.rows > 0) {
-            a.p[0] = product(matrix(dout, z.ld()), matrix(wd, z.lh()), z.rows, z.h, z.d, dhidden);
+            a.p[0] = product(matrix(dout, z.ld()), matrix(wd, z.lh()), z.rows, z.h, z.d, dhidden.tile, dhidden.tile);
+            a.products = 1;
             a.dgate = space.dgate;
             a.dup = space.dup;
             a.part = grads->db_gate || grads->db_up ? space.sums : nullptr;
+            const dim3 grid(unsigned(dhidden.tiles), 1, 1);
             if (dhidden.tile == 256)
-                hipLaunchKernelGGL(mlp_dhidden_kernel<256>, dim3(unsigned(dhidden.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
+                hipLaunchKernelGGL(mlp_dhidden_kernel<256>, grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
             else
-                hipLaunchKernelGGL(mlp_dhidden_kernel<128>, dim3(unsigned(dhidden.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+                hipLaunchKernelGGL(mlp_dhidden_kernel<128>, grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
             ++launches;
         }
-        const int32_t halves = z.rows > 0 ? int32_t(2 * dhidden.m_tiles) : 0;
+        const int32_t halves = int32_t(2 * ceil_div(z.rows, dhidden.tile));
         if (grads->db_gate) launch_column_sums(space.sums, halves, 2 * z.hp, z.h, grads->db_gate, s), ++launches;
         if (grads->db_up) launch_column_sums(space.sums + z.hp, halves, 2 * z.hp, z.h, grads->db_up, s), ++launches;
         if (grads->db_down) {
@@ -651,43 +702,32 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             launches += groups ? 2 : 1;
         }
         if (z.rows > 0 && grads->dx) {
-            a.p[0] = product(matrix(space.dgate, z.hp), matrix(wg, z.ld()), z.rows, z.d, z.h, dx);
+            a.p[0] = product(matrix(space.dgate, z.hp), matrix(wg, z.ld()), z.rows, z.d, z.h, dx.tile, dx.tile);
             a.p[0].x[1] = matrix(space.dup, z.hp);
             a.p[0].w[1] = matrix(wu, z.ld());
             a.p[0].stages *= 2;
             a.products = 1;
             a.out[0] = static_cast<uint16_t *>(grads->dx);
             a.ldo[0] = z.d;
-            a.part = space.part;
-            a.part_stride = int32_t(pad_to(z.d, 8));
-            if (dx.tile == 256)
-                hipLaunchKernelGGL((mlp_product_kernel<256, false, true>), dim3(unsigned(dx.tiles()), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
-            else
-                hipLaunchKernelGGL((mlp_product_kernel<128, false, true>), dim3(unsigned(dx.tiles()), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
-            if (dx.splits > 1) join(a, s), ++launches;
-            ++launches;
+            launches += launch_products<false, true>(a, dx, space.part, s);
         }
         if (any_weight) {
-            const Cut wide = cut(z.h, z.d, 0, false), back = cut(z.d, z.h, 0, false);
+            const Cut c = z.dweights(grads->dw_gate, grads->dw_up, grads->dw_down);
             int n = 0, tiles = 0;
-            auto add = [&](void *out, const Matrix &left, const Matrix &right, int64_t m, int64_t columns, const Cut &c) {
+            auto add = [&](void *out, const Matrix &left, const Matrix &right, int64_t m, int64_t columns) {
                 if (!out) return;
-                a.p[n] = product(left, right, m, columns, z.rows, c);
+                a.p[n] = product(left, right, m, columns, z.rows, c.tile, c.tile);
                 a.p[n].first = tiles;
                 a.out[n] = static_cast<uint16_t *>(out);
                 a.ldo[n] = columns;
-                tiles += int(c.tiles());
+                tiles += a.p[n].m_tiles * a.p[n].n_tiles;
                 ++n;
             };
-            add(grads->dw_gate, matrix(space.dgate, z.hp), matrix(x, z.ld()), z.h, z.d, wide);
-            add(grads->dw_up, matrix(space.dup, z.hp), matrix(x, z.ld()), z.h, z.d, wide);
-            add(grads->dw_down, matrix(dout, z.ld()), matrix(args->hidden, z.hp), z.d, z.h, back);
+            add(grads->dw_gate, matrix(space.dgate, z.hp), matrix(x, z.ld()), z.h, z.d);
+            add(grads->dw_up, matrix(space.dup, z.hp), matrix(x, z.ld()), z.h, z.d);
+            add(grads->dw_down, matrix(dout, z.ld()), matrix(args->hidden, z.hp), z.d, z.h);
             a.products = n;
-            if (wide.tile == 256)
-                hipLaunchKernelGGL((mlp_product_kernel<256, true, true>), dim3(unsigned(tiles), 1, 1), dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
-            else
-                hipLaunchKernelGGL((mlp_product_kernel<128, true, true>), dim3(unsigned(tiles), 1, 1), dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
-            ++launches;
+            launches += launch_products<true, true>(a, c, space.part, s);
         }
     });
     if (e != hipSuccess) return hip_error(e, "gated_mlp_backward: kernel launch");

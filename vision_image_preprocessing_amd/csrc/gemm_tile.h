@@ -66,9 +66,30 @@ struct Product {
     int64_t m;
     int32_t n, k;
     int32_t stages;       // of all of K
-    int32_t splits;       // parts of K, each a tile of its own
     int32_t m_tiles, n_tiles;
     int32_t first;        // of its tiles in the launch
+};
+
+// How a launch's tiles are worked on: the first `full` by a workgroup each, the
+// `tail` behind them by `splits` each, over as many parts of K.  Each of the
+// two ranges goes to the XCDs in contiguous runs.
+struct Units {
+    int32_t full, tail, splits;
+    __host__ __device__ int32_t count() const { return full + tail * splits; }
+};
+struct Unit {
+    int tile, split, slot;  // split < 0: all of K; else the part's place in the workspace
+    __device__ __forceinline__ explicit Unit(const Units &u) {
+        const int b = int(blockIdx.x);
+        if (b < u.full) {
+            tile = int(xcd_contiguous_tile(b, u.full));
+            split = slot = -1;
+        } else {
+            slot = int(xcd_contiguous_tile(b - u.full, u.tail * u.splits));
+            split = slot / u.tail;
+            tile = u.full + slot - split * u.tail;
+        }
+    }
 };
 
 // How a tile is cut among its waves: two along the rows, the others along the
@@ -96,16 +117,13 @@ __device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Where a tile is: its part of K and its place.  Runs of kGroupM tiles of rows
+// Where a tile is.  Runs of kGroupM tiles of rows
 // go by channels together, so that the tiles an XCD works on at one time share
 // rows and channels in its L2 (a run of one row of tiles reads every channel).
 struct Place {
     int64_t mt;
-    int nt, split;
+    int nt;
     __device__ __forceinline__ Place(const Product &p, int t) {
-        const int tiles = p.m_tiles * p.n_tiles;
-        split = t / tiles;
-        t -= split * tiles;
         const int group = t / (kGroupM * p.n_tiles), first = group * kGroupM;
         const int rows = min(p.m_tiles - first, kGroupM);
         t -= first * p.n_tiles;
