@@ -74,29 +74,44 @@ __device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[8], int
             if (j < left) reinterpret_cast<__bf16 *>(p)[j] = h[j];
     }
 }
-// The same where the next kernel reads it: kept in cache.
-__device__ __forceinline__ void keep_bf16(uint16_t *p, const float (&v)[8]) {
-    bf16x8 h;
+// Biases of n channels from c on, of `count`.
+template <int kN>
+__device__ __forceinline__ void load_bias(const float *bias, int c, int count, float (&v)[kN]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = __bf16(v[j]);
-    *reinterpret_cast<bf16x8 *>(p) = h;
+    for (int j = 0; j < kN; ++j) v[j] = bias ? bias[min(c + j, count - 1)] : 0.0f;
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = a[j];
-        v[4 + j] = b[j];
+
+// The tile's rows of a matrix of padded rows ([rows][ldh]), which the
+// epilogues read and write four channels a lane, so that every access of a
+// wave is whole lines.  What is past the rows or the columns reads as zeros and
+// is not written; no branch keeps one access apart from the next.
+template <typename T>
+struct Panel {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t off;  // the lane's column
+    int ldh;
+    __device__ __forceinline__ Panel(const T *p, int64_t m0, int64_t m, int tile, int64_t ldh_, int col) : ldh(int(ldh_)) {
+        const int rows = int(min(m - m0, int64_t(tile)));
+        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p + m0 * ldh_), 0, rows * ldh * int(sizeof(T)), kWord3);
+        off = col < ldh ? uint32_t(col) * sizeof(T) : kOutside;
     }
-}
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-}
-// Biases of eight channels from c on, of n.
-__device__ __forceinline__ void load_bias(const float *bias, int c, int n, float (&v)[8]) {
+    // past the rows, or from kOutside, an offset is outside the resource; it
+    // must not wrap back into it
+    __device__ __forceinline__ uint32_t at(int row) const { return off == kOutside ? kOutside : off + uint32_t(row * ldh) * uint32_t(sizeof(T)); }
+};
+constexpr int kStream = 2;  // non-temporal: what is not read again soon
+__device__ __forceinline__ void load4(const Panel<float> &p, int row, float (&v)[4]) {
+    const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.r, p.at(row), 0, kStream));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = bias ? bias[min(c + j, n - 1)] : 0.0f;
+    for (int j = 0; j < 4; ++j) v[j] = w[j];
+}
+__device__ __forceinline__ void store4(const Panel<float> &p, int row, const float (&v)[4]) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), p.r, p.at(row), 0, kStream);
+}
+__device__ __forceinline__ void store4(const Panel<uint16_t> &p, int row, const float (&v)[4]) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const bf16x4 h = {__bf16(v[0]), __bf16(v[1]), __bf16(v[2]), __bf16(v[3])};
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), p.r, p.at(row), 0, 0);
 }
 
 // s = 1 / (1 + exp -g): the hardware's exponential and reciprocal, each to
@@ -127,34 +142,34 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
     Sums<kTile> acc;
     multiply<kTile, false, false, kGateUp>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
-    constexpr int kLanes = kHalf / 8, kPass = 64 / kLanes;
+    constexpr int kLanes = kHalf / 4, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * kHalf + piece;
-    float bg[8], bu[8];
+    const int piece = (lane % kLanes) * 4, col = n0 + (wave % T::kWavesN) * kHalf + piece;
+    float bg[4], bu[4];
     load_bias(a.bias0, col, p.n, bg);
     load_bias(a.bias1, col, p.n, bu);
+    const Panel<uint16_t> hidden(a.hidden, m0, p.m, kTile, a.ldh, col);
+    const Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, col);
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
-            const int r = t * kPass + lane / kLanes;
-            float g[8], u[8], h[8];
-            turned.template get<8>(r, piece, g);
-            turned.template get<8>(r, kHalf + piece, u);
+            const int r = t * kPass + lane / kLanes, row = (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
+            float g[4], u[4], h[4];
+            turned.get(r, piece, g);
+            turned.get(r, kHalf + piece, u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const bool in = col + j < p.n;
                 g[j] = in ? g[j] + bg[j] : 0.0f;
                 u[j] = in ? u[j] + bu[j] : 0.0f;
                 h[j] = g[j] * sigmoid(g[j]) * u[j];
             }
-            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
-            if (row >= p.m || col >= a.ldh) continue;
-            keep_bf16(a.hidden + row * a.ldh + col, h);
+            store4(hidden, row, h);
             if (a.gate_up) {
-                store8(a.gate_up + row * a.ldh + col, g);
-                store8(a.gate_up + (p.m + row) * a.ldh + col, u);
+                store4(gate, row, g);
+                store4(up, row, u);
             }
         }
     }
@@ -173,37 +188,43 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
     Sums<kTile> acc;
     multiply<kTile, false, true, kOnce>(p, m0, n0, 0, p.stages, lds, acc);
     const Turned<kTile> turned(lds);
-    constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
+    constexpr int kLanes = T::kWaveN / 4, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece;
-    float sg[8] = {}, su[8] = {};
+    const int piece = (lane % kLanes) * 4, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece;
+    const Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, col);
+    const Panel<uint16_t> dgate(a.dgate, m0, p.m, kTile, a.ldh, col), dup(a.dup, m0, p.m, kTile, a.ldh, col);
+    float sg[4] = {}, su[4] = {};
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
+        const int first = (wave / T::kWavesN) * T::kWaveM + i * 32 + lane / kLanes;
+        float g[32 / kPass][4], u[32 / kPass][4];
+#pragma unroll
+        for (int t = 0; t < 32 / kPass; ++t) {
+            load4(gate, first + t * kPass, g[t]);
+            load4(up, first + t * kPass, u[t]);
+        }
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
-            const int r = t * kPass + lane / kLanes;
-            float dh[8], g[8], u[8];
-            turned.template get<8>(r, piece, dh);
-            const int64_t row = m0 + (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
-            if (row >= p.m || col >= a.ldh) continue;
-            load8(a.gate_up + row * a.ldh + col, g);
-            load8(a.gate_up + (p.m + row) * a.ldh + col, u);
+            float dh[4];
+            turned.get(t * kPass + lane / kLanes, piece, dh);
+            // past the columns dh is any value, and has to be zero for the
+            // padding; past the rows g and u read as zeros, and with them dg and du
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = sigmoid(g[j]), d = col + j < p.n ? dh[j] : 0.0f;
-                dh[j] = d * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
-                u[j] = d * (g[j] * s);
+            for (int j = 0; j < 4; ++j) {
+                const float s = sigmoid(g[t][j]), d = col + j < p.n ? dh[j] : 0.0f;
+                dh[j] = d * u[t][j] * (s * (1.0f + g[t][j] * (1.0f - s)));
+                u[t][j] = d * (g[t][j] * s);
                 sg[j] += dh[j];
-                su[j] += u[j];
+                su[j] += u[t][j];
             }
-            keep_bf16(a.dgate + row * a.ldh + col, dh);
-            keep_bf16(a.dup + row * a.ldh + col, u);
+            store4(dgate, first + t * kPass, dh);
+            store4(dup, first + t * kPass, u[t]);
         }
     }
     if (!a.part) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int m = kLanes; m < 64; m <<= 1) {
             sg[j] += __shfl_xor(sg[j], m);
@@ -211,8 +232,8 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
         }
     if (lane < kLanes && col < a.ldh) {
         float *part = a.part + (2 * at.mt + wave / T::kWavesN) * 2 * a.ldh + col;
-        store8(part, sg);
-        store8(part + a.ldh, su);
+        *reinterpret_cast<f32x4 *>(part) = f32x4{sg[0], sg[1], sg[2], sg[3]};
+        *reinterpret_cast<f32x4 *>(part + a.ldh) = f32x4{su[0], su[1], su[2], su[3]};
     }
 }
 
@@ -234,28 +255,43 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpA
     Sums<kTile> acc;
     multiply<kTile, kXAcross, kWAcross, kWAcross && !kXAcross ? kTwice : kOnce>(p, m0, n0, begin, end, lds, acc);
     const Turned<kTile> turned(lds);
-    constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int piece = (lane % kLanes) * 8, c0 = (wave % T::kWavesN) * T::kWaveN + piece, col = n0 + c0, left = p.n - col;
+    const int wave_row = (wave / T::kWavesN) * T::kWaveM, wave_col = (wave % T::kWavesN) * T::kWaveN;
+    if (part) {
+        // the whole of the part's tile, four channels a lane
+        constexpr int kLanes = T::kWaveN / 4, kPass = 64 / kLanes;
+        const int piece = (lane % kLanes) * 4;
+        float *sums = a.part + int64_t(unit.slot) * (kTile * kTile) + wave_col + piece;
+#pragma unroll
+        for (int i = 0; i < T::kBlocksM; ++i) {
+            turned.put(acc[i]);
+#pragma unroll
+            for (int t = 0; t < 32 / kPass; ++t) {
+                const int r = t * kPass + lane / kLanes;
+                float v[4];
+                turned.get(r, piece, v);
+                *reinterpret_cast<f32x4 *>(sums + (wave_row + i * 32 + r) * kTile) = f32x4{v[0], v[1], v[2], v[3]};
+            }
+        }
+        return;
+    }
+    constexpr int kLanes = T::kWaveN / 8, kPass = 64 / kLanes;
+    const int piece = (lane % kLanes) * 8, col = n0 + wave_col + piece, left = p.n - col;
     float bias[8];
-    load_bias(part ? nullptr : a.bias0, col, p.n, bias);
-    float *sums = part ? a.part + int64_t(unit.slot) * (kTile * kTile) + c0 : nullptr;
+    load_bias(a.bias0, col, p.n, bias);
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
-            const int r = t * kPass + lane / kLanes, r0 = (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
+            const int r = t * kPass + lane / kLanes;
             float v[8];
-            turned.template get<8>(r, piece, v);
-            if (m0 + r0 >= p.m || left <= 0) continue;
-            if (part) {
-                store8(sums + r0 * kTile, v);
-                continue;
-            }
+            turned.get(r, piece, v);
+            const int64_t row = m0 + wave_row + i * 32 + r;
+            if (row >= p.m || left <= 0) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += bias[j];
-            store_bf16(a.out[n] + (m0 + r0) * a.ldo[n] + col, v, left);
+            store_bf16(a.out[n] + row * a.ldo[n] + col, v, left);
         }
     }
 }
@@ -275,11 +311,19 @@ __global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
     if (row >= p.m || left <= 0) return;
     const float *part = a.part + int64_t(t) * (kTile * kTile) + r * kTile + c;
     float v[8];
-    load8(part, v);
+    auto load = [&](const float *q, float (&w)[8]) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(q), y = *reinterpret_cast<const f32x4 *>(q + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = x[j];
+            w[4 + j] = y[j];
+        }
+    };
+    load(part, v);
 #pragma unroll 4
     for (int s = 1; s < a.units.splits; ++s) {
         float w[8];
-        load8(part + int64_t(s) * a.units.tail * (kTile * kTile), w);
+        load(part + int64_t(s) * a.units.tail * (kTile * kTile), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += w[j];
     }
