@@ -58,6 +58,8 @@ struct MlpArgs {
     uint16_t *dgate, *dup;       // [rows][ldh]
     float *part;                 // partial sums: [slot][tile][tile] of tiles in parts, or of dg and du over rows; or null
     int64_t ldh;
+    int32_t channels;            // mlp_few_kernel: of a workgroup
+    int32_t all_channels;        // and those that are written, n or the padded n
 };
 
 // Eight channels to bf16, at any address of the type; `left` of them inside.
@@ -112,6 +114,18 @@ __device__ __forceinline__ void store4(const Panel<uint16_t> &p, int row, const 
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const bf16x4 h = {__bf16(v[0]), __bf16(v[1]), __bf16(v[2]), __bf16(v[3])};
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), p.r, p.at(row), 0, 0);
+}
+
+// Eight bf16 values from any address of the type, `left` of them inside (any
+// number, none among them); zeros behind.
+__device__ __forceinline__ u32x4 load_ragged(const uint16_t *p, int left) {
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    if (left >= 8) return *reinterpret_cast<const any_u32x4 *>(p);
+    u16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = j < left ? p[j] : uint16_t(0);
+    return __builtin_bit_cast(u32x4, h);
 }
 
 // s = 1 / (1 + exp -g): the hardware's exponential and reciprocal, each to
@@ -197,15 +211,19 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
         const int first = (wave / T::kWavesN) * T::kWaveM + i * 32 + lane / kLanes;
+        constexpr int kAhead = 2;  // passes whose g and u are on the way; more need registers that there are not
         float g[32 / kPass][4], u[32 / kPass][4];
-#pragma unroll
-        for (int t = 0; t < 32 / kPass; ++t) {
+        auto load = [&](int t) __attribute__((always_inline)) {
+            if (t >= 32 / kPass) return;
             load4(gate, first + t * kPass, g[t]);
             load4(up, first + t * kPass, u[t]);
-        }
+        };
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) load(t);
         turned.put(acc[i]);
 #pragma unroll
         for (int t = 0; t < 32 / kPass; ++t) {
+            load(t + kAhead);
             float dh[4];
             turned.get(t * kPass + lane / kLanes, piece, dh);
             // past the columns dh is any value, and has to be zero for the
@@ -335,25 +353,25 @@ __global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
 }
 
 // Rows of any width to rows of a multiple of kPad values, zeros behind: the
-// products read 16 bytes at a time.
-__global__ __launch_bounds__(256) void mlp_pad_kernel(const uint16_t *x, int64_t rows, int32_t width, uint16_t *out, int32_t padded) {
-    const int pieces = padded / 8;
-    const int64_t id = row_group() * 256 + threadIdx.x, row = id / pieces;
-    if (row >= rows) return;
-    const int col = int(id - row * pieces) * 8, left = width - col;
-    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-    const uint16_t *p = x + row * width + col;
-    u32x4 v;
-    if (left >= 8) {
-        v = *reinterpret_cast<const any_u32x4 *>(p);
-    } else {
-        u16x8 h;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = j < left ? p[j] : uint16_t(0);
-        v = __builtin_bit_cast(u32x4, h);
-    }
-    *reinterpret_cast<u32x4 *>(out + row * padded + col) = v;
+// products read 16 bytes at a time.  A wave takes a row; all of a call's
+// operands are one launch.
+struct PadArgs {
+    const uint16_t *from[5];
+    uint16_t *to[5];
+    int32_t width[5], padded[5];
+    int64_t first[6];  // of each operand's rows
+    int32_t count;
+};
+__global__ __launch_bounds__(256) void mlp_pad_kernel(PadArgs a) {
+    int64_t row = row_group() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (row >= a.first[a.count]) return;
+    int n = 0;
+    while (n + 1 < a.count && row >= a.first[n + 1]) ++n;
+    row -= a.first[n];
+    const uint16_t *from = a.from[n] + row * a.width[n];
+    uint16_t *to = a.to[n] + row * a.padded[n];
+    for (int col = int(threadIdx.x & 63) * 8; col < a.padded[n]; col += 64 * 8)
+        *reinterpret_cast<u32x4 *>(to + col) = load_ragged(from + col, a.width[n] - col);
 }
 
 // Partial sums over every gridDim.y-th group of eight rows of 256 columns.
@@ -382,6 +400,78 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
     if (c < columns) part[int64_t(blockIdx.y) * columns + c] = sum;
 }
 
+// Up to 16 rows: the weights are read once, and that is what such a call waits
+// for.  A workgroup takes up to 16 channels (with kGate of both projections);
+// its waves share K, 32 values a product, and each has the operands of kDeep
+// products on the way from memory at once; their sums meet in LDS.  Operands
+// come straight from memory, at any address of the type where kRagged, so
+// nothing is copied first.
+//
+// A CU takes in about 25 GB/s of them, whatever waves and loads it has (80
+// workgroups of 16 channels: 4.2, 5.6, 9.0, 15.6 us for K 1280, 2560, 5120,
+// 10240), so what counts is that all CUs have as many channels.
+//
+// v_mfma_f32_16x16x32_bf16, weights first: lane l holds row l % 16 and k = 8 (l /
+// 16) .. + 7 of an operand, and channels 4 (l / 16) + r of x's row l % 16 of the
+// result.
+template <bool kGate, bool kRagged, int kWaves, int kDeep>
+__global__ __launch_bounds__(kWaves * 64) void mlp_few_kernel(MlpArgs a) {
+    constexpr int kParts = kGate ? 2 : 1;
+    __shared__ f32x4 sums[kWaves][kParts][64];
+    const Product &p = a.p[0];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = int(blockIdx.x) * a.channels, l16 = lane & 15, at = 8 * (lane >> 4);
+    const uint16_t *w[kParts], *x = p.x[0].p + min(int64_t(l16), p.m - 1) * p.x[0].stride + at;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) w[i] = p.w[i].p + int64_t(min(n0 + l16, p.n - 1)) * p.w[i].stride + at;
+    // lanes of other channels and of no row ask for nothing
+    const int k_w = l16 < a.channels ? p.k - at : 0, k_x = l16 < p.m ? p.k - at : 0;
+    auto load = [&](const uint16_t *q, int k, int end) -> bf16x8 {
+        if constexpr (kRagged) return __builtin_bit_cast(bf16x8, load_ragged(q + k, end - k));
+        return k < end ? *reinterpret_cast<const bf16x8 *>(q + k) : bf16x8{};
+    };
+    f32x4 acc[kParts] = {};
+    for (int k0 = 32 * wave; k0 < p.k; k0 += 32 * kWaves * kDeep) {
+        bf16x8 fw[kDeep][kParts], fx[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int k = k0 + 32 * kWaves * d;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) fw[d][i] = load(w[i], k, k_w);
+            fx[d] = load(x, k, k_x);
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[d][i], fx[d], acc[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    // one value a thread: a channel of a row
+    const int c = threadIdx.x % 16, r = threadIdx.x / 16, col = n0 + c;
+    if (r >= p.m || c >= a.channels || col >= a.all_channels) return;
+    float v[kParts];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        v[i] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kWaves; ++s) v[i] += sums[s][i][(c / 4) * 16 + r][c % 4];
+    }
+    if constexpr (kGate) {
+        const bool in = col < p.n;
+        const float g = in ? v[0] + (a.bias0 ? a.bias0[col] : 0.0f) : 0.0f, u = in ? v[1] + (a.bias1 ? a.bias1[col] : 0.0f) : 0.0f;
+        const int64_t to = r * a.ldh + col;
+        reinterpret_cast<__bf16 *>(a.hidden)[to] = __bf16(g * sigmoid(g) * u);
+        if (a.gate_up) {
+            a.gate_up[to] = g;
+            a.gate_up[p.m * a.ldh + to] = u;
+        }
+    } else if (col < p.n) {
+        reinterpret_cast<__bf16 *>(a.out[0])[r * a.ldo[0] + col] = __bf16(v[0] + (a.bias0 ? a.bias0[col] : 0.0f));
+    }
+}
+
 int64_t pad_to(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
 int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
@@ -394,29 +484,37 @@ struct Cut {
 };
 constexpr int kCus = 256;
 constexpr int kMinStages = 6;  // of a part
+constexpr int kFewRows = 16;
 
 // Tiles of one size: a round of the card is a tile a CU of 256 x 256, two of
 // 128 x 128.  What is left over after whole rounds would keep some CUs busy for
 // all of K and leave the others idle; its K is cut into parts where that saves
-// enough stages to pay for writing and joining them.
-// Weighs in units of a 256 x 256 stage, about 1.7 us; 128 x 128 tiles take 0.68
-// of it for half the products.
-Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, double *cost) {
+// more than writing and joining them costs.
+// cost: microseconds by what was measured of 1960 and 32768 rows (width 1280,
+// hidden 5120).  A stage takes 1.5 in a round of 256 x 256, 1.07 in one of 128 x
+// 128 (half the products), 0.6 where a CU has one of those; a round's first
+// loads and its store 11 and 4, or 20 and 6 where g and u are read or written
+// (wide_ends); parts, which are float32, 7 and 3 more, and
+// their join 12 and 6.  So 1960 rows run on 128 x 128 tiles: dW 84 us against 95
+// with the join, out 40 against 49, dg and du 48 against 57; 32768 on the
+// others: dW 980 against 1620, out 358 against 520.
+Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, bool wide_ends, double *cost) {
+    const bool big = tile == 256;
     Cut c{tile, {int32_t(tiles), 0, 1}, tiles};
-    const int64_t slots = tile == 256 ? kCus : 2 * kCus, full = tiles / slots * slots, tail = tiles - full;
-    const double stage = tile == 256 ? 1.0 : 0.68;
-    double rest = tail ? double(stages) : 0.0, extra = 0.0;
+    const int64_t slots = big ? kCus : 2 * kCus, full = tiles / slots * slots, tail = tiles - full;
+    const double stage = big ? 1.5 : 1.07, ends = big ? (wide_ends ? 20.0 : 11.0) : (wide_ends ? 6.0 : 4.0), extra = big ? 19.0 : 9.0;
+    double rest = tail ? double(stages) * (!big && tail <= kCus ? 0.6 : stage) + ends : 0.0;
     if (splittable && tail) {
         const int64_t most = stages / kMinStages, wanted = slots / tail, splits = wanted < most ? wanted : most;
-        const double joined = double(ceil_div(stages, splits > 0 ? splits : 1)), cost_of = 8.0 + 8.0 * double(tail * splits) / double(slots);
-        if (splits > 1 && (rest - joined) * stage > cost_of) {
-            c.units = {int32_t(full), int32_t(tail), int32_t(splits)};
-            rest = joined;
-            extra = cost_of;
+        if (splits > 1) {
+            const double parts = double(ceil_div(stages, splits)) * (!big && tail * splits <= kCus ? 0.6 : stage) + ends + extra;
+            if (parts < rest) {
+                c.units = {int32_t(full), int32_t(tail), int32_t(splits)};
+                rest = parts;
+            }
         }
     }
-    // a round's first loads and its store are about four stages
-    if (cost) *cost = (double(full / slots) * (double(stages) + 4.0) + (tail ? rest + 4.0 : 0.0)) * stage + extra;
+    if (cost) *cost = double(full / slots) * (double(stages) * stage + ends) + rest;
     return c;
 }
 
@@ -431,15 +529,15 @@ int64_t tiles_of(const Extent *e, int count, int tile, int columns) {
 }
 // gate: both projections of a channel lie in one tile, which then has half as
 // many.
-Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool gate) {
+Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool wide_ends, bool gate) {
     double big, small;
-    const Cut c256 = cut_tiles(256, tiles_of(e, count, 256, gate ? 128 : 256), stages, splittable, &big);
-    const Cut c128 = cut_tiles(128, tiles_of(e, count, 128, gate ? 64 : 128), stages, splittable, &small);
+    const Cut c256 = cut_tiles(256, tiles_of(e, count, 256, gate ? 128 : 256), stages, splittable, wide_ends, &big);
+    const Cut c128 = cut_tiles(128, tiles_of(e, count, 128, gate ? 64 : 128), stages, splittable, wide_ends, &small);
     return big <= small ? c256 : c128;
 }
-Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable, bool gate = false) {
+Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable, bool wide_ends, bool gate = false) {
     const Extent e{m, n};
-    return cut(&e, 1, stages, splittable, gate);
+    return cut(&e, 1, stages, splittable, wide_ends, gate);
 }
 
 struct Sizes {
@@ -448,12 +546,13 @@ struct Sizes {
     int64_t dp, hp;      // strides of such copies; hp of hidden values too
     Sizes(int64_t rows, int64_t d, int64_t h)
         : rows(rows), d(d), h(h), pad_d(d % 8 != 0), pad_h(h % 8 != 0), dp(pad_to(d, kPad)), hp(pad_to(h, kPad)) {}
+    bool few() const { return rows <= kFewRows; }  // the forward pass's other kernels
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
-    Cut gate() const { return cut(rows, h, ceil_div(d, kStageK), false, true); }
-    Cut down() const { return cut(rows, d, ceil_div(h, kStageK), true); }
-    Cut dhidden() const { return cut(rows, h, ceil_div(d, kStageK), false); }
-    Cut dx() const { return cut(rows, d, 2 * ceil_div(h, kStageK), true); }
+    Cut gate(bool saved) const { return cut(rows, h, ceil_div(d, kStageK), false, saved, true); }
+    Cut down() const { return cut(rows, d, ceil_div(h, kStageK), true, false); }
+    Cut dhidden() const { return cut(rows, h, ceil_div(d, kStageK), false, true); }
+    Cut dx() const { return cut(rows, d, 2 * ceil_div(h, kStageK), true, false); }
     // of the weights' gradients that are made
     Cut dweights(bool gate, bool up, bool down) const {
         Extent e[3];
@@ -461,7 +560,7 @@ struct Sizes {
         if (gate) e[n++] = {h, d};
         if (up) e[n++] = {h, d};
         if (down) e[n++] = {d, h};
-        return cut(e, n, ceil_div(rows, kStageK), true, false);
+        return cut(e, n, ceil_div(rows, kStageK), true, false, false);
     }
 };
 
@@ -483,12 +582,13 @@ struct ForwardSpace {
     size_t bytes;
     ForwardSpace(const Sizes &s, void *base) {
         Carver c{static_cast<uint8_t *>(base)};
+        const bool copy_d = s.pad_d && !s.few(), copy_h = s.pad_h && !s.few();
         hidden = c.take<uint16_t>(s.rows * s.hp);
-        x = c.take<uint16_t>(s.pad_d ? s.rows * s.dp : 0);
-        wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
-        wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
-        wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
-        part = c.take<float>(s.down().part_values());
+        x = c.take<uint16_t>(copy_d ? s.rows * s.dp : 0);
+        wg = c.take<uint16_t>(copy_d ? s.h * s.dp : 0);
+        wu = c.take<uint16_t>(copy_d ? s.h * s.dp : 0);
+        wd = c.take<uint16_t>(copy_h ? s.d * s.hp : 0);
+        part = c.take<float>(s.few() ? 0 : s.down().part_values());
         bytes = c.used;
     }
 };
@@ -535,12 +635,26 @@ Product product(const Matrix &x, const Matrix &w, int64_t m, int64_t n, int64_t 
     return p;
 }
 
-void pad(const void *x, int64_t rows, int64_t width, uint16_t *out, int64_t padded, hipStream_t s) {
-    const int64_t blocks = ceil_div(rows * (padded / 8), 256);
-    if (blocks)
-        hipLaunchKernelGGL(mlp_pad_kernel, row_grid(blocks), dim3(256, 1, 1), 0, s, static_cast<const uint16_t *>(x), rows,
-                           int32_t(width), out, int32_t(padded));
-}
+// Operands to copy, and their launch; the launches made.
+struct Padding {
+    PadArgs a;
+    Padding() { std::memset(&a, 0, sizeof(a)); }
+    // `p` becomes the copy.
+    void add(const void *&p, int64_t rows, int64_t width, uint16_t *to, int64_t padded) {
+        const int n = a.count++;
+        a.from[n] = static_cast<const uint16_t *>(p);
+        a.to[n] = to;
+        a.width[n] = int32_t(width);
+        a.padded[n] = int32_t(padded);
+        a.first[n + 1] = a.first[n] + rows;
+        p = to;
+    }
+    int launch(hipStream_t s) const {
+        if (!a.count) return 0;
+        hipLaunchKernelGGL(mlp_pad_kernel, row_grid(ceil_div(a.first[a.count], 4)), dim3(256, 1, 1), 0, s, a);
+        return 1;
+    }
+};
 
 // A launch of mlp_product_kernel, and its join; the launches made.
 template <bool kXAcross, bool kWAcross>
@@ -559,6 +673,38 @@ int launch_products(MlpArgs &a, const Cut &c, float *part, hipStream_t s) {
     return joined ? 2 : 1;
 }
 
+// As many workgroups as CUs, or a multiple of that, of as many channels each.
+template <bool kGate, int kWaves, int kDeep>
+void launch_few_kernel(MlpArgs &a, int64_t channels, bool ragged, hipStream_t s) {
+    const int64_t groups = kCus * ceil_div(channels, kCus * 16);
+    a.channels = int32_t(ceil_div(channels, groups));
+    a.all_channels = int32_t(channels);
+    const dim3 grid(unsigned(ceil_div(channels, a.channels)), 1, 1), block(kWaves * 64, 1, 1);
+    if (ragged)
+        hipLaunchKernelGGL((mlp_few_kernel<kGate, true, kWaves, kDeep>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((mlp_few_kernel<kGate, false, kWaves, kDeep>), grid, block, 0, s, a);
+}
+
+// The forward pass of few rows, operands as they are.
+void launch_few(const Sizes &z, const mimo_mlp &args, uint16_t *hidden, uint16_t *out, hipStream_t s) {
+    MlpArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.p[0] = product(matrix(args.x, z.d), matrix(args.w_gate, z.d), z.rows, z.h, z.d, 128, 128);
+    a.p[0].w[1] = matrix(args.w_up, z.d);
+    a.bias0 = args.b_gate;
+    a.bias1 = args.b_up;
+    a.gate_up = args.gate_up;
+    a.hidden = hidden;
+    a.ldh = z.hp;
+        launch_few_kernel<true, 8, 5>(a, z.hp, z.pad_d, s);
+    a.p[0] = product(matrix(hidden, z.hp), matrix(args.w_down, z.h), z.rows, z.d, z.h, 128, 128);
+    a.bias0 = args.b_down;
+    a.out[0] = out;
+    a.ldo[0] = z.d;
+    launch_few_kernel<false, 16, 10>(a, z.d, z.pad_h, s);
+}
+
 int check_mlp(const mimo_mlp *p, const char *who) {
     const std::string w(who);
     if (!p) return set_error(MIMO_E_INVALID, w + ": null arguments");
@@ -567,7 +713,7 @@ int check_mlp(const mimo_mlp *p, const char *who) {
     if (p->rows > 0x7FFFFFFFll || p->width > kMaxWidth || p->hidden_width > kMaxWidth)
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 rows, or a width above 65536");
     const Sizes s(p->rows, p->width, p->hidden_width);
-    for (const Cut &c : {s.gate(), s.down(), s.dhidden(), s.dx()})
+    for (const Cut &c : {s.gate(false), s.gate(true), s.down(), s.dhidden(), s.dx()})
         if (c.tiles > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
     return MIMO_OK;
 }
@@ -613,22 +759,21 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
     int launches = 0;
     const void *x = args->x, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
     uint16_t *hidden = args->hidden ? static_cast<uint16_t *>(args->hidden) : space.hidden;
-    const Cut gate = z.gate(), down = z.down();
+    const Cut gate = z.gate(args->gate_up != nullptr), down = z.down();
     const hipError_t e = timed_launch(s, [&] {
+        if (z.few()) {
+            launches = 2;
+            launch_few(z, *args, hidden, static_cast<uint16_t *>(out), s);
+            return;
+        }
+        Padding padding;
         if (z.pad_d) {
-            pad(x, z.rows, z.d, space.x, z.dp, s);
-            pad(wg, z.h, z.d, space.wg, z.dp, s);
-            pad(wu, z.h, z.d, space.wu, z.dp, s);
-            x = space.x;
-            wg = space.wg;
-            wu = space.wu;
-            launches += 3;
+            padding.add(x, z.rows, z.d, space.x, z.dp);
+            padding.add(wg, z.h, z.d, space.wg, z.dp);
+            padding.add(wu, z.h, z.d, space.wu, z.dp);
         }
-        if (z.pad_h) {
-            pad(wd, z.d, z.h, space.wd, z.hp, s);
-            wd = space.wd;
-            ++launches;
-        }
+        if (z.pad_h) padding.add(wd, z.d, z.h, space.wd, z.hp);
+        launches += padding.launch(s);
         MlpArgs a;
         std::memset(&a, 0, sizeof(a));
         a.p[0] = product(matrix(x, z.ld()), matrix(wg, z.ld()), z.rows, z.h, z.d, gate.tile, gate.tile / 2);
@@ -701,22 +846,15 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
     const void *x = args->x, *dout = grads->dout, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
     const Cut dhidden = z.dhidden(), dx = z.dx();
     const hipError_t e = timed_launch(s, [&] {
+        Padding padding;
         if (z.rows > 0 && z.pad_d) {
-            pad(x, z.rows, z.d, space.x, z.dp, s);
-            pad(dout, z.rows, z.d, space.dout, z.dp, s);
-            pad(wg, z.h, z.d, space.wg, z.dp, s);
-            pad(wu, z.h, z.d, space.wu, z.dp, s);
-            x = space.x;
-            dout = space.dout;
-            wg = space.wg;
-            wu = space.wu;
-            launches += 4;
+            padding.add(x, z.rows, z.d, space.x, z.dp);
+            padding.add(dout, z.rows, z.d, space.dout, z.dp);
+            padding.add(wg, z.h, z.d, space.wg, z.dp);
+            padding.add(wu, z.h, z.d, space.wu, z.dp);
         }
-        if (z.rows > 0 && z.pad_h) {
-            pad(wd, z.d, z.h, space.wd, z.hp, s);
-            wd = space.wd;
-            ++launches;
-        }
+        if (z.rows > 0 && z.pad_h) padding.add(wd, z.d, z.h, space.wd, z.hp);
+        launches += padding.launch(s);
         MlpArgs a;
         std::memset(&a, 0, sizeof(a));
         a.gate_up = args->gate_up;
