@@ -270,6 +270,67 @@ def test_streams_graphs_and_workspaces(V):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows,d,h", [(1, 72, 136), (16, 72, 136), (17, 1280, 2048), (200, 1280, 640), (1500, 264, 4096), (2600, 640, 640),
+                                      (4099, 72, 264), (20000, 128, 200)])
+def test_the_same_bits_again(V, rows, d, h):
+    """Few rows, split sums and whole tiles, from the same inputs next to other
+    work on the card: bit for bit the same."""
+    _say("again", (rows, d, h))
+    x, w, b, dout = _inputs(rows, d, h, True, 9)
+    xd, wd, bd, gd = _dev(x), [_dev(t) for t in w], [_dev(t) for t in b], _dev(dout)
+
+    def step():
+        out, gate_up, hidden = V.gated_mlp(xd, *wd, *bd, return_saved=True)
+        return (out, gate_up, hidden, *V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, bias_grads=True))
+
+    want = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        other = [V.gated_mlp(xd, *wd, *bd) for _ in range(3)]
+    got = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(want, got)) and all(torch.equal(o, want[0]) for o in other)
+
+
+def test_past_32_bits(V):
+    """A million rows of 2304 hidden values: rows of a large call against the
+    float64 form, and the sums over all rows against sums in float64."""
+    _say("a million rows")
+    rows, d, h = 1_000_003, 64, 2304
+    assert rows * h > 1 << 31
+    x, w, b, _ = _inputs(64, d, h, True, 31)
+    wd, bd = [_dev(t) for t in w], [_dev(t) for t in b]
+    g = torch.Generator(device="cuda").manual_seed(32)
+    x, dout = (torch.randn((rows, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    out, gate_up, hidden = V.gated_mlp(x, *wd, *bd, return_saved=True)
+    got = V.gated_mlp_backward(dout, x, *wd, gate_up, hidden, bias_grads=True)
+    for first in (0, rows // 2, rows - 64):
+        at = slice(first, first + 64)
+        wide = _wide(x[at]), [_wide(t) for t in w], [_wide(t) for t in b], _wide(dout[at])
+        r = tower.gated_mlp(wide[0], *wide[1], *wide[2], wide[3])
+        bars = _bars(*wide, r)
+        _within(out[at], r["out"], bars["out"], "out")
+        _within(got[0][at], r["dx"], bars["dx"], "dx")
+        _within(gate_up[1, at], r["up"], bars["up"] + EPS * np.abs(r["up"]), "up")
+    # the sums over all rows, from their operands as the kernels hold them: h and g, u as saved
+    db, mag_b = (torch.zeros(d, dtype=torch.float64, device="cuda") for _ in range(2))
+    dw, mag = (torch.zeros((d, h), dtype=torch.float64, device="cuda") for _ in range(2))
+    for i in range(0, rows, 1 << 16):
+        dd, hh = dout[i:i + (1 << 16)].double(), hidden[i:i + (1 << 16)].double()
+        db += dd.sum(0)
+        mag_b += dd.abs().sum(0)
+        dw += dd.T @ hh
+        mag += dd.abs().T @ hh.abs()
+    # additions on a value's way: over the rows of one of 128 x 8 row groups (or of a split), over those, and over a product's 16
+    depth = rows / 1024 + 200
+    assert ((got[6].double() - db).abs() <= depth * EPS * mag_b + EPS * db.abs()).all()
+    assert ((got[3].double() - dw).abs() <= (rows + 8) * EPS * mag + U8 * dw.abs()).all()
+    # a part of 64 rows left out, or taken twice, would show
+    part = (dout[:64].double().T @ hidden[:64].double()).abs()
+    assert (U8 * dw.abs()).median() < part.median()
+
+
 def test_refusals(V):
     _say("refusals")
     x, w, b, dout = _inputs(4, 64, 72, True, 5)
