@@ -687,11 +687,12 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
  *   rstd = 1 / sqrt(sum h^2 / n + eps),  y = h rstd weight
  * The norm is that of the rounded h, which the backward pass is given.  Rows
  * are dense [rows][width]; those of a width that is a multiple of 8 at 16-byte
- * aligned addresses run fastest.
+ * aligned addresses run fastest.  No output may be the weight.
  * ------------------------------------------------------------------------ */
 
 /*
- * Forward, one kernel launch; float32 inside, out rounded once.
+ * Forward, one kernel launch; float32 inside, out rounded once.  Where a row's
+ * sum of squares passes float32's range (no values below 2^56 do) rstd is 0.
  *   width    in [1, 65536].
  *   x        device, x_dtype (MIMO_F32 or MIMO_BF16).
  *   residual device, residual_dtype (x_dtype or MIMO_F32), or NULL.
@@ -815,7 +816,8 @@ size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidde
 
 /*
  * Forward: writes out, bf16 [rows][width], and gate_up and hidden unless both
- * are NULL (the backward pass needs them).  out must not be an input.
+ * are NULL (the backward pass needs them).  None of these may be an input or
+ * another one.
  *   workspace  device, >= mimo_gated_mlp_workspace_bytes(...), 16-byte
  *              aligned; calls that may run at the same time need one each.
  * Two kernel launches; one more where K of the second is split (few rows), and

@@ -26,14 +26,15 @@ BOTH = [dict(rows=-1), dict(width=0), dict(xd=2), dict(xd=-1), dict(rd=3), dict(
 
 
 @pytest.mark.parametrize("bad", BOTH + [dict(od=2), dict(od=-1), dict(out=None), dict(out=P + 2), dict(rstd=P + 1),
-                                        dict(out=P, od=B), dict(out=2 * P, od=B)])
+                                        dict(out=P, od=B), dict(out=2 * P, od=B), dict(out=3 * P), dict(rstd=3 * P), dict(h=3 * P)])
 def test_norm_refuses(bad):
     before = V.dispatch_count()
     assert _forward(**bad) == V.MIMO_E_INVALID
     assert V.last_error().startswith("rms_norm:") and V.dispatch_count() == before
 
 
-@pytest.mark.parametrize("bad", BOTH + [dict(q=None), dict(q=P + 8), dict(q=P), dict(q=2 * P), dict(s=None), dict(s=P + 2)])
+@pytest.mark.parametrize("bad", BOTH + [dict(q=None), dict(q=P + 8), dict(q=P), dict(q=2 * P), dict(s=None), dict(s=P + 2), dict(q=3 * P), dict(s=3 * P),
+                                        dict(h=3 * P)])
 def test_quantized_norm_refuses(bad):
     assert _quantized(**bad) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm_quantized:")
 
@@ -55,7 +56,7 @@ def test_norm_backward_refuses():
 
     for bad in (dict(rows=-1), dict(width=0), dict(hd=7), dict(gd=2), dict(h=None), dict(g=None), dict(rstd=None), dict(dx=None),
                 dict(dx=P), dict(dx=2 * P), dict(dw=P + 2), dict(ws=None), dict(ws=P + 8), dict(h=P + 2), dict(gd=B, g=P + 1),
-                dict(w=P + 2), dict(rstd=P + 2), dict(dr=P + 2), dict(dw=3 * P), dict(dw=4 * P)):
+                dict(w=P + 2), dict(rstd=P + 2), dict(dr=P + 2), dict(dw=3 * P), dict(dw=4 * P), dict(dx=3 * P), dict(dx=4 * P)):
         assert backward(**bad) == V.MIMO_E_INVALID, bad
     assert backward(n=need - 1) == V.MIMO_E_CAPACITY
     assert backward(width=65537) == V.MIMO_E_TOO_LARGE and backward(rows=1 << 31) == V.MIMO_E_TOO_LARGE
@@ -110,7 +111,7 @@ def test_mlp_refuses():
     for bad in (dict(rows=-1), dict(width=0), dict(hidden=0), dict(x=0), dict(wg=0), dict(wu=0), dict(wd=0), dict(out=None), dict(x=P + 8),
                 dict(wg=P + 2), dict(wu=P + 4), dict(wd=P + 8), dict(out=P + 8), dict(bg=P + 2), dict(bu=P + 1), dict(bd=P + 2), dict(gu=0),
                 dict(h=0), dict(gu=P + 8), dict(h=P + 8), dict(out=P), dict(out=2 * P), dict(out=3 * P), dict(out=4 * P), dict(out=8 * P),
-                dict(out=9 * P), dict(ws=None), dict(ws=P + 8)):
+                dict(out=9 * P), dict(ws=None), dict(ws=P + 8), dict(h=P), dict(h=8 * P), dict(gu=4 * P), dict(out=7 * P), dict(h=5 * P)):
         assert forward(**bad) == V.MIMO_E_INVALID, bad
         assert V.last_error().startswith("gated_mlp:")
     assert forward(n=need - 1) == V.MIMO_E_CAPACITY and lib.mimo_gated_mlp(None, P, P, need, None) == V.MIMO_E_INVALID

@@ -748,8 +748,13 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         return set_error(MIMO_E_INVALID, "gated_mlp: biases must be 4-byte aligned");
     if ((args->gate_up != nullptr) != (args->hidden != nullptr) || !check_ptr_align(args->gate_up, 16) || !check_ptr_align(args->hidden, 16))
         return set_error(MIMO_E_INVALID, "gated_mlp: gate_up and hidden are given together, 16-byte aligned, or neither is");
-    if (out == args->x || out == args->w_gate || out == args->w_up || out == args->w_down || out == args->hidden || out == args->gate_up)
-        return set_error(MIMO_E_INVALID, "gated_mlp: out must not be an input or a saved tensor");
+    const void *const inputs[] = {args->x, args->w_gate, args->w_up, args->w_down, args->b_gate, args->b_up, args->b_down};
+    const void *const written[] = {out, args->gate_up, args->hidden};
+    for (const void *w : written)
+        for (const void *i : inputs)
+            if (w && w == i) return set_error(MIMO_E_INVALID, "gated_mlp: out, gate_up and hidden must not be inputs");
+    if (out == args->gate_up || out == args->hidden || (args->hidden && args->hidden == args->gate_up))
+        return set_error(MIMO_E_INVALID, "gated_mlp: out, gate_up and hidden must not be one array");
     if (!is_aligned(workspace)) return set_error(MIMO_E_INVALID, "gated_mlp: workspace must be non-null and 16-byte aligned");
     const Sizes z(args->rows, args->width, args->hidden_width);
     const ForwardSpace space(z, workspace);

@@ -494,6 +494,9 @@ int mimo_rms_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, c
     int st = check_forward("rms_norm", rows, width, x, x_dtype, residual, residual_dtype, weight, eps, residual_out, out, size_of(out_dtype));
     if (st != MIMO_OK || rows == 0) return st;
     if (!check_ptr_align(rstd, 4)) return set_error(MIMO_E_INVALID, "rms_norm: rstd must be 4-byte aligned");
+    // workgroups that still read the weight run next to the ones that write
+    if (weight && (rstd == weight || out == weight || residual_out == weight))
+        return set_error(MIMO_E_INVALID, "rms_norm: no output may be the weight");
     if ((out == x && out_dtype != x_dtype) || (residual && out == residual && out_dtype != residual_dtype))
         return set_error(MIMO_E_INVALID, "rms_norm: out may be x or the residual only in its dtype");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, out);
@@ -521,6 +524,8 @@ int mimo_rms_norm_quantized(int64_t rows, int32_t width, const void *x, int32_t 
     if (!scale || !check_ptr_align(scale, 4))
         return set_error(MIMO_E_INVALID, "rms_norm_quantized: scale must be non-null and 4-byte aligned");
     if (q == x || (residual && q == residual)) return set_error(MIMO_E_INVALID, "rms_norm_quantized: q must not be an input");
+    if (weight && (scale == weight || q == weight || residual_out == weight))
+        return set_error(MIMO_E_INVALID, "rms_norm_quantized: no output may be the weight");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, q);
     a.scale = scale;
     const Shape shape = forward_shape(width, all_aligned(a));
@@ -559,6 +564,7 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
         if (dx == h || dx == dout) return set_error(MIMO_E_INVALID, "rms_norm_backward: dx must not be h or dout");
         if (dweight && (dweight == weight || dweight == rstd))
             return set_error(MIMO_E_INVALID, "rms_norm_backward: dweight must not be an input");
+        if (dx == weight || dx == rstd) return set_error(MIMO_E_INVALID, "rms_norm_backward: dx must not be the weight or rstd");
     }
     RmsArgs a;
     std::memset(&a, 0, sizeof(a));
