@@ -823,7 +823,7 @@ size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidde
  * Two kernel launches; one more where K of the second is split (few rows), and
  * one for each operand that is copied.  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE (rows or widths, or more than 2^24 - 1
- * tiles) or MIMO_E_HIP.
+ * tiles of 256 x 256, of both products together) or MIMO_E_HIP.
  */
 int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -486,35 +486,39 @@ constexpr int kCus = 256;
 constexpr int kMinStages = 6;  // of a part
 constexpr int kFewRows = 16;
 
-// Tiles of one size: a round of the card is a tile a CU of 256 x 256, two of
-// 128 x 128.  What is left over after whole rounds would keep some CUs busy for
-// all of K and leave the others idle; its K is cut into parts where that saves
-// more than writing and joining them costs.
-// cost: microseconds by what was measured of 1960 and 32768 rows (width 1280,
-// hidden 5120).  A stage takes 1.5 in a round of 256 x 256, 1.07 in one of 128 x
-// 128 (half the products), 0.6 where a CU has one of those; a round's first
-// loads and its store 11 and 4, or 20 and 6 where g and u are read or written
-// (wide_ends); parts, which are float32, 7 and 3 more, and
-// their join 12 and 6.  So 1960 rows run on 128 x 128 tiles: dW 84 us against 95
-// with the join, out 40 against 49, dg and du 48 against 57; 32768 on the
-// others: dW 980 against 1620, out 358 against 520.
-Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, bool wide_ends, double *cost) {
-    const bool big = tile == 256;
+// What a round of the card's tiles takes, in microseconds, fitted to 17 to 32768
+// rows of widths 264 to 2048 and 520 to 5120 hidden values: a stage of the
+// tiles that the CUs have at once (one of 256 x 256, two of 128 x 128, four of 64
+// x 64), by how many there are; a tile's first loads and its store (more where g
+// and u are read or written); and what parts cost, which are written in
+// float32 and joined.
+double stage_us(int tile, int64_t units) {
+    if (tile == 256) return 1.5;
+    if (tile == 128) return units <= kCus ? 0.6 : 1.07;
+    return units <= kCus ? 0.33 : units <= 2 * kCus ? 0.42 : units <= 3 * kCus ? 0.55 : 0.7;
+}
+double ends_us(int tile, bool wide) { return tile == 256 ? (wide ? 20.0 : 11.0) : tile == 128 ? (wide ? 6.0 : 4.0) : (wide ? 4.0 : 3.0); }
+double parts_us(int tile) { return tile == 256 ? 19.0 : 6.0; }
+
+// Tiles of one size.  What is left over after whole rounds would keep some CUs
+// busy for all of K and leave the others idle; its K is cut into parts where
+// that is quicker.
+Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, bool wide, double *cost) {
     Cut c{tile, {int32_t(tiles), 0, 1}, tiles};
-    const int64_t slots = big ? kCus : 2 * kCus, full = tiles / slots * slots, tail = tiles - full;
-    const double stage = big ? 1.5 : 1.07, ends = big ? (wide_ends ? 20.0 : 11.0) : (wide_ends ? 6.0 : 4.0), extra = big ? 19.0 : 9.0;
-    double rest = tail ? double(stages) * (!big && tail <= kCus ? 0.6 : stage) + ends : 0.0;
+    const int64_t slots = int64_t(kCus) * (tile == 256 ? 1 : tile == 128 ? 2 : 4), full = tiles / slots * slots, tail = tiles - full;
+    const double ends = ends_us(tile, wide);
+    double rest = tail ? double(stages) * stage_us(tile, tail) + ends : 0.0;
     if (splittable && tail) {
-        const int64_t most = stages / kMinStages, wanted = slots / tail, splits = wanted < most ? wanted : most;
-        if (splits > 1) {
-            const double parts = double(ceil_div(stages, splits)) * (!big && tail * splits <= kCus ? 0.6 : stage) + ends + extra;
+        const int64_t most = stages / kMinStages < slots / tail ? stages / kMinStages : slots / tail;
+        for (int64_t splits = 2; splits <= most; ++splits) {
+            const double parts = double(ceil_div(stages, splits)) * stage_us(tile, tail * splits) + ends + parts_us(tile);
             if (parts < rest) {
                 c.units = {int32_t(full), int32_t(tail), int32_t(splits)};
                 rest = parts;
             }
         }
     }
-    if (cost) *cost = double(full / slots) * (double(stages) * stage + ends) + rest;
+    *cost = double(full / slots) * (double(stages) * stage_us(tile, slots) + ends) + rest;
     return c;
 }
 
@@ -527,17 +531,31 @@ int64_t tiles_of(const Extent *e, int count, int tile, int columns) {
     for (int i = 0; i < count; ++i) tiles += ceil_div(e[i].m, tile) * ceil_div(e[i].n, columns);
     return tiles;
 }
+// The quickest of the three sizes by that.  us of the forward and the backward
+// pass on 64, 128 and 256, width 1280, hidden 5120: 64 rows 23, 27, 47 and 47, 53,
+// 76; 512 rows 50, 49, 54 and 98, 79, 114; 1960 rows 135, 94, 107 and 278, 200, 202;
+// 4096 rows 257, 172, 171 and 564, 378, 355; width 640, hidden 1000: 1024 rows 14,
+// 20, 41 and 39, 44, 76; 4096 rows 34, 32, 46 and 80, 69, 104.
 // gate: both projections of a channel lie in one tile, which then has half as
 // many.
-Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool wide_ends, bool gate) {
-    double big, small;
-    const Cut c256 = cut_tiles(256, tiles_of(e, count, 256, gate ? 128 : 256), stages, splittable, wide_ends, &big);
-    const Cut c128 = cut_tiles(128, tiles_of(e, count, 128, gate ? 64 : 128), stages, splittable, wide_ends, &small);
-    return big <= small ? c256 : c128;
+Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool wide, bool gate) {
+    Cut best{};
+    double least = 0.0;
+    for (int tile = 256; tile >= 64; tile /= 2) {
+        const int64_t tiles = tiles_of(e, count, tile, gate ? tile / 2 : tile);
+        if (tile < 256 && tiles > kMaxTiles) break;  // a launch of fewer, larger ones
+        double cost;
+        const Cut c = cut_tiles(tile, tiles, stages, splittable, wide, &cost);
+        if (tile == 256 || cost < least) {
+            best = c;
+            least = cost;
+        }
+    }
+    return best;
 }
-Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable, bool wide_ends, bool gate = false) {
+Cut cut(int64_t m, int64_t n, int64_t stages, bool splittable, bool wide, bool gate = false) {
     const Extent e{m, n};
-    return cut(&e, 1, stages, splittable, wide_ends, gate);
+    return cut(&e, 1, stages, splittable, wide, gate);
 }
 
 struct Sizes {
@@ -549,8 +567,8 @@ struct Sizes {
     bool few() const { return rows <= kFewRows; }  // the forward pass's other kernels
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
-    Cut gate(bool saved) const { return cut(rows, h, ceil_div(d, kStageK), false, saved, true); }
-    Cut down() const { return cut(rows, d, ceil_div(h, kStageK), true, false); }
+    Cut gate(bool saved) const { return few() ? Cut{} : cut(rows, hp, ceil_div(d, kStageK), false, saved, true); }  // the padding is written too
+    Cut down() const { return few() ? Cut{} : cut(rows, d, ceil_div(h, kStageK), true, false); }
     Cut dhidden() const { return cut(rows, h, ceil_div(d, kStageK), false, true); }
     Cut dx() const { return cut(rows, d, 2 * ceil_div(h, kStageK), true, false); }
     // of the weights' gradients that are made
@@ -580,7 +598,7 @@ struct ForwardSpace {
     uint16_t *hidden, *x, *wg, *wu, *wd;
     float *part;
     size_t bytes;
-    ForwardSpace(const Sizes &s, void *base) {
+    ForwardSpace(const Sizes &s, const Cut &down, void *base) {
         Carver c{static_cast<uint8_t *>(base)};
         const bool copy_d = s.pad_d && !s.few(), copy_h = s.pad_h && !s.few();
         hidden = c.take<uint16_t>(s.rows * s.hp);
@@ -588,7 +606,7 @@ struct ForwardSpace {
         wg = c.take<uint16_t>(copy_d ? s.h * s.dp : 0);
         wu = c.take<uint16_t>(copy_d ? s.h * s.dp : 0);
         wd = c.take<uint16_t>(copy_h ? s.d * s.hp : 0);
-        part = c.take<float>(s.few() ? 0 : s.down().part_values());
+        part = c.take<float>(s.few() ? 0 : down.part_values());
         bytes = c.used;
     }
 };
@@ -598,7 +616,7 @@ struct BackwardSpace {
     uint16_t *dgate, *dup, *x, *dout, *wg, *wu, *wd;
     float *part, *sums, *columns;
     size_t bytes;
-    BackwardSpace(const Sizes &s, void *base) {
+    BackwardSpace(const Sizes &s, const Cut &dhidden, const Cut &dx, void *base) {
         Carver c{static_cast<uint8_t *>(base)};
         dgate = c.take<uint16_t>(s.rows * s.hp);
         dup = c.take<uint16_t>(s.rows * s.hp);
@@ -607,13 +625,15 @@ struct BackwardSpace {
         wg = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wu = c.take<uint16_t>(s.pad_d ? s.h * s.dp : 0);
         wd = c.take<uint16_t>(s.pad_h ? s.d * s.hp : 0);
-        int64_t values = s.dx().part_values();
-        for (int made = 1; made < 8; ++made) {  // gate's and up's alone are alike
+        int64_t values = dx.part_values();
+        // whichever of the weights' gradients are made (gate's and up's alone are
+        // alike); few rows are not cut into parts
+        for (int made = 1; made < 8 && s.rows >= 2 * kMinStages * kStageK - kStageK; ++made) {
             const int64_t w = made == 2 || made == 6 ? 0 : s.dweights(made & 1, made & 2, made & 4).part_values();
             if (w > values) values = w;
         }
         part = c.take<float>(values);
-        sums = c.take<float>(2 * ceil_div(s.rows, s.dhidden().tile) * 2 * s.hp);
+        sums = c.take<float>(2 * ceil_div(s.rows, dhidden.tile) * 2 * s.hp);
         columns = c.take<float>(kColumnGroups * s.d);
         bytes = c.used;
     }
@@ -666,9 +686,12 @@ int launch_products(MlpArgs &a, const Cut &c, float *part, hipStream_t s) {
     if (c.tile == 256) {
         hipLaunchKernelGGL((mlp_product_kernel<256, kXAcross, kWAcross>), grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
         if (joined) hipLaunchKernelGGL(mlp_join_kernel<256>, dim3(unsigned(c.units.tail) * 32, 1, 1), dim3(256, 1, 1), 0, s, a);
-    } else {
+    } else if (c.tile == 128) {
         hipLaunchKernelGGL((mlp_product_kernel<128, kXAcross, kWAcross>), grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
         if (joined) hipLaunchKernelGGL(mlp_join_kernel<128>, dim3(unsigned(c.units.tail) * 8, 1, 1), dim3(256, 1, 1), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((mlp_product_kernel<64, kXAcross, kWAcross>), grid, dim3(Tile<64>::kThreads, 1, 1), 0, s, a);
+        if (joined) hipLaunchKernelGGL(mlp_join_kernel<64>, dim3(unsigned(c.units.tail) * 2, 1, 1), dim3(256, 1, 1), 0, s, a);
     }
     return joined ? 2 : 1;
 }
@@ -712,9 +735,9 @@ int check_mlp(const mimo_mlp *p, const char *who) {
         return set_error(MIMO_E_INVALID, w + ": rows must be >= 0, width and hidden_width >= 1");
     if (p->rows > 0x7FFFFFFFll || p->width > kMaxWidth || p->hidden_width > kMaxWidth)
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 rows, or a width above 65536");
-    const Sizes s(p->rows, p->width, p->hidden_width);
-    for (const Cut &c : {s.gate(false), s.gate(true), s.down(), s.dhidden(), s.dx()})
-        if (c.tiles > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
+    // of 256 x 256; cut() takes no smaller ones where there would be more
+    const int64_t m = ceil_div(p->rows, 256), n = ceil_div(p->hidden_width, 128) + ceil_div(p->width, 256);
+    if (m * n > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
     return MIMO_OK;
 }
 
@@ -733,7 +756,8 @@ size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidde
         clear_error();
         return 0;
     }
-    return ForwardSpace(Sizes(rows, width, hidden_width), nullptr).bytes;
+    const Sizes s(rows, width, hidden_width);
+    return ForwardSpace(s, s.down(), nullptr).bytes;
 }
 
 int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t workspace_bytes, void *stream) {
@@ -757,14 +781,14 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         return set_error(MIMO_E_INVALID, "gated_mlp: out, gate_up and hidden must not be one array");
     if (!is_aligned(workspace)) return set_error(MIMO_E_INVALID, "gated_mlp: workspace must be non-null and 16-byte aligned");
     const Sizes z(args->rows, args->width, args->hidden_width);
-    const ForwardSpace space(z, workspace);
+    const Cut gate = z.gate(args->gate_up != nullptr), down = z.down();
+    const ForwardSpace space(z, down, workspace);
     if (workspace_bytes < space.bytes)
         return set_error(MIMO_E_CAPACITY, "gated_mlp: workspace smaller than mimo_gated_mlp_workspace_bytes");
     hipStream_t s = static_cast<hipStream_t>(stream);
     int launches = 0;
     const void *x = args->x, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
     uint16_t *hidden = args->hidden ? static_cast<uint16_t *>(args->hidden) : space.hidden;
-    const Cut gate = z.gate(args->gate_up != nullptr), down = z.down();
     const hipError_t e = timed_launch(s, [&] {
         if (z.few()) {
             launches = 2;
@@ -783,6 +807,7 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         std::memset(&a, 0, sizeof(a));
         a.p[0] = product(matrix(x, z.ld()), matrix(wg, z.ld()), z.rows, z.h, z.d, gate.tile, gate.tile / 2);
         a.p[0].w[1] = matrix(wu, z.ld());
+        a.p[0].n_tiles = int32_t(ceil_div(z.hp, gate.tile / 2));
         a.products = 1;
         a.bias0 = args->b_gate;
         a.bias1 = args->b_up;
@@ -792,8 +817,10 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         const dim3 grid(unsigned(gate.tiles), 1, 1);
         if (gate.tile == 256)
             hipLaunchKernelGGL(mlp_gate_kernel<256>, grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
-        else
+        else if (gate.tile == 128)
             hipLaunchKernelGGL(mlp_gate_kernel<128>, grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+        else
+            hipLaunchKernelGGL(mlp_gate_kernel<64>, grid, dim3(Tile<64>::kThreads, 1, 1), 0, s, a);
         a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down.tile, down.tile);
         a.out[0] = static_cast<uint16_t *>(out);
         a.ldo[0] = z.d;
@@ -811,7 +838,8 @@ size_t mimo_gated_mlp_backward_workspace_bytes(int64_t rows, int32_t width, int3
         clear_error();
         return 0;
     }
-    return BackwardSpace(Sizes(rows, width, hidden_width), nullptr).bytes;
+    const Sizes s(rows, width, hidden_width);
+    return BackwardSpace(s, s.dhidden(), s.dx(), nullptr).bytes;
 }
 
 int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, void *workspace, size_t workspace_bytes,
@@ -843,13 +871,13 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             if (made[i] && made[i] == made[j]) return set_error(MIMO_E_INVALID, "gated_mlp_backward: gradients must not be one array");
     if (!is_aligned(workspace)) return set_error(MIMO_E_INVALID, "gated_mlp_backward: workspace must be non-null and 16-byte aligned");
     const Sizes z(args->rows, args->width, args->hidden_width);
-    const BackwardSpace space(z, workspace);
+    const Cut dhidden = z.dhidden(), dx = z.dx();
+    const BackwardSpace space(z, dhidden, dx, workspace);
     if (workspace_bytes < space.bytes)
         return set_error(MIMO_E_CAPACITY, "gated_mlp_backward: workspace smaller than mimo_gated_mlp_backward_workspace_bytes");
     hipStream_t s = static_cast<hipStream_t>(stream);
     int launches = 0;
     const void *x = args->x, *dout = grads->dout, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
-    const Cut dhidden = z.dhidden(), dx = z.dx();
     const hipError_t e = timed_launch(s, [&] {
         Padding padding;
         if (z.rows > 0 && z.pad_d) {
@@ -873,8 +901,10 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
             const dim3 grid(unsigned(dhidden.tiles), 1, 1);
             if (dhidden.tile == 256)
                 hipLaunchKernelGGL(mlp_dhidden_kernel<256>, grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
-            else
+            else if (dhidden.tile == 128)
                 hipLaunchKernelGGL(mlp_dhidden_kernel<128>, grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+            else
+                hipLaunchKernelGGL(mlp_dhidden_kernel<64>, grid, dim3(Tile<64>::kThreads, 1, 1), 0, s, a);
             ++launches;
         }
         const int32_t halves = int32_t(2 * ceil_div(z.rows, dhidden.tile));

@@ -6,15 +6,25 @@
 // input is along, across; a gradient of a weight, whose summed axis is the
 // rows of both operands, is across, across.
 //
-// A workgroup of four waves makes a kTile x kTile tile, a quarter each: 256 x
-// 256 (256 accumulators a lane, one workgroup a CU), or 128 x 128 (two
-// workgroups a CU).  K advances 64 values a stage.  Operands go from memory
-// straight into LDS (buffer_load ... lds), two stages ahead of the products; x
-// has three buffers, w two, which are filled again as soon as they are read.  The five buffers are arrays of their
-// own, so that the compiler sees that loads into one never meet reads of
-// another, and the stage loop is unrolled six times, after which both rings
-// are back where they were.  Stages past the end are loaded through an empty
-// resource: zeros, without memory traffic.
+// A workgroup makes a kTile x kTile tile: 256 x 256 (eight waves of 128 x 64, 128
+// accumulators a lane, one workgroup a CU), 128 x 128 (four of 64 x 64, two
+// workgroups a CU) or 64 x 64 (four of 32 x 32, four workgroups a CU).  K
+// advances 64 values a stage.  Operands go from memory straight into LDS
+// (buffer_load ... lds), two stages ahead of the products; x has three buffers,
+// w two, which are filled again as soon as they are read.  The five buffers are
+// arrays of their own, so that the compiler sees that loads into one never meet
+// reads of another, and the stage loop is unrolled six times, after which both
+// rings are back where they were.  Stages past the end are loaded through an
+// empty resource: zeros, without memory traffic.
+//
+// 256 x 256, K 5120: 131072 x 1280 in 1.25 to 1.31 ms, 1.31 to 1.37 PFLOP/s, next
+// to 1.43 of a large library product; a stage takes 1.5 us, a tile's first
+// loads and its store about 8.  The card's power bounds that (the clock falls
+// to 1.6 to 1.7 GHz; on zeros 1.2 ms), and at smaller sizes what a CU takes in,
+// some 60 GB/s.  Four waves of 128 x 128 took 2 to 7% longer, all of a stage's
+// loads in its first half 4%, all of a step's reads at once 2%, and tiles in
+// runs of eight rows up to 6%; raised wave priority, tiles turned in two
+// regions and workgroups that start staggered made no difference.
 //
 // In LDS a matrix stored along k lies as kTile rows of 64 values, read 16
 // bytes a lane; one stored across as panels of 64 columns, 64 rows of k each,
@@ -97,11 +107,7 @@ struct Unit {
 template <int kTile_>
 struct Tile {
     static constexpr int kTile = kTile_;
-#ifdef W4
-    static constexpr int kWaves = 4;
-#else
     static constexpr int kWaves = kTile == 256 ? 8 : 4;
-#endif
     static constexpr int kThreads = kWaves * 64, kWavesN = kWaves / 2;
     static constexpr int kWaveM = kTile / 2, kWaveN = kTile / kWavesN;
     static constexpr int kBlocksM = kWaveM / 32, kBlocksN = kWaveN / 32;
@@ -171,10 +177,10 @@ struct Operand {
             const int x = 8 * (lane >> 5) + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
             // row x of the 16 of a step, whose block of eight is 2 s + lane / 32:
             // block_key of it is (lane / 32) ^ the step's own part
-            base = at / 64 * (kStageK * 128) + x * 128 + ((c ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
+            base = at / 64 * (kStageK * 128) + x * 128 + ((c ^ (4 * (at / 32 & 1)) ^ row_key(x & 7) ^ (lane >> 5)) << 4) + (lane & 1) * 8;
         } else {
             const int r = lane & 31;
-            base = (at + r) * 128 + (((lane >> 5) ^ ((r ^ (r >> 3)) & 7)) << 4);
+            base = (at + r) * 128 + (((lane >> 5) ^ ((r ^ ((at + r) >> 3)) & 7)) << 4);
             chunk = ((lane & 7) ^ l8 ^ (wave * kGroups)) & 7;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
@@ -261,7 +267,9 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     // same rows of the two weights; so the rows that a wave loads are of one of
     // them, gate's in even ones
     static_assert(!kGate || kGroups * 8 == T::kWaveN / 2, "a wave loads rows of one of the two");
-    const W w(p.w[0].stride, n0, p.n, kGate ? n0 + (wave >> 1) * (kGroups * 8) : n0 + wave * (kGroups * 8), wn * T::kWaveN);
+    // (a tile may lie in the padding, past every row: it reads the last one)
+    const int w_first = kGate ? min(n0, p.n - 1) : n0;
+    const W w(p.w[0].stride, w_first, p.n, kGate ? n0 + (wave >> 1) * (kGroups * 8) : n0 + wave * (kGroups * 8), wn * T::kWaveN);
     // in registers from here on: a scalar load in the loop would make every
     // wait for LDS a wait for all of it
     const Matrix x0 = p.x[0], w0 = kGate ? p.w[wave & 1] : p.w[0];
@@ -274,7 +282,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     };
     auto load_w = [&](int i, int s, lds_ptr d) {
         const bool second = kOver == kTwice && s >= seg;
-        w.load(second ? w1 : w0, n0, channels, i, second ? s - seg : s, k, s < end, d);
+        w.load(second ? w1 : w0, w_first, channels, i, second ? s - seg : s, k, s < end, d);
     };
     // between stages: each wave has waited for its own loads and reads
     auto barrier = [] {
