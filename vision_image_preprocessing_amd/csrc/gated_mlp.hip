@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
     if (c < columns) part[int64_t(blockIdx.y) * columns + c] = sum;
 }
 
-// Up to 16 rows: the weights are read once, and that is what such a call waits
+// Few rows: the weights are read once, and that is what such a call waits
 // for.  A workgroup takes up to 16 channels (with kGate of both projections);
 // its waves share K, 32 values a product, and each has the operands of kDeep
 // products on the way from memory at once; their sums meet in LDS.  Operands
@@ -413,50 +413,61 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
 //
 // v_mfma_f32_16x16x32_bf16, weights first: lane l holds row l % 16 and k = 8 (l /
 // 16) .. + 7 of an operand, and channels 4 (l / 16) + r of x's row l % 16 of the
-// result.
-template <bool kGate, bool kRagged, int kWaves, int kDeep>
+// result; kRows blocks of 16 rows.
+template <bool kGate, bool kRagged, int kRows, int kWaves, int kDeep>
 __global__ __launch_bounds__(kWaves * 64) void mlp_few_kernel(MlpArgs a) {
     constexpr int kParts = kGate ? 2 : 1;
-    __shared__ f32x4 sums[kWaves][kParts][64];
+    __shared__ f32x4 sums[kWaves][kParts][kRows][64];
     const Product &p = a.p[0];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = int(blockIdx.x) * a.channels, l16 = lane & 15, at = 8 * (lane >> 4);
-    const uint16_t *w[kParts], *x = p.x[0].p + min(int64_t(l16), p.m - 1) * p.x[0].stride + at;
+    const uint16_t *w[kParts], *x[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) x[j] = p.x[0].p + min(int64_t(16 * j + l16), p.m - 1) * p.x[0].stride + at;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) w[i] = p.w[i].p + int64_t(min(n0 + l16, p.n - 1)) * p.w[i].stride + at;
     // lanes of other channels and of no row ask for nothing
-    const int k_w = l16 < a.channels ? p.k - at : 0, k_x = l16 < p.m ? p.k - at : 0;
+    const int k_w = l16 < a.channels ? p.k - at : 0;
+    int k_x[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) k_x[j] = 16 * j + l16 < p.m ? p.k - at : 0;
     auto load = [&](const uint16_t *q, int k, int end) -> bf16x8 {
         if constexpr (kRagged) return __builtin_bit_cast(bf16x8, load_ragged(q + k, end - k));
         return k < end ? *reinterpret_cast<const bf16x8 *>(q + k) : bf16x8{};
     };
-    f32x4 acc[kParts] = {};
+    f32x4 acc[kParts][kRows] = {};
     for (int k0 = 32 * wave; k0 < p.k; k0 += 32 * kWaves * kDeep) {
-        bf16x8 fw[kDeep][kParts], fx[kDeep];
+        bf16x8 fw[kDeep][kParts], fx[kDeep][kRows];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
             const int k = k0 + 32 * kWaves * d;
 #pragma unroll
             for (int i = 0; i < kParts; ++i) fw[d][i] = load(w[i], k, k_w);
-            fx[d] = load(x, k, k_x);
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) fx[d][j] = load(x[j], k, k_x[j]);
         }
 #pragma unroll
         for (int d = 0; d < kDeep; ++d)
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[d][i], fx[d], acc[i], 0, 0, 0);
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[d][i], fx[d][j], acc[i][j], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) sums[wave][i][lane] = acc[i];
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) sums[wave][i][j][lane] = acc[i][j];
     __syncthreads();
     // one value a thread: a channel of a row
+    static_assert(kWaves * 64 >= kRows * 256, "a thread for each value");
     const int c = threadIdx.x % 16, r = threadIdx.x / 16, col = n0 + c;
-    if (r >= p.m || c >= a.channels || col >= a.all_channels) return;
+    if (r >= p.m || c >= a.channels || col >= a.all_channels) return;  // m <= 16 kRows
     float v[kParts];
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
         v[i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kWaves; ++s) v[i] += sums[s][i][(c / 4) * 16 + r][c % 4];
+        for (int s = 0; s < kWaves; ++s) v[i] += sums[s][i][r / 16][(c / 4) * 16 + r % 16][c % 4];
     }
     if constexpr (kGate) {
         const bool in = col < p.n;
@@ -484,7 +495,6 @@ struct Cut {
 };
 constexpr int kCus = 256;
 constexpr int kMinStages = 6;  // of a part
-constexpr int kFewRows = 16;
 
 // What a round of the card's tiles takes, in microseconds, fitted to 17 to 32768
 // rows of widths 264 to 2048 and 520 to 5120 hidden values: a stage of the
@@ -564,7 +574,12 @@ struct Sizes {
     int64_t dp, hp;      // strides of such copies; hp of hidden values too
     Sizes(int64_t rows, int64_t d, int64_t h)
         : rows(rows), d(d), h(h), pad_d(d % 8 != 0), pad_h(h % 8 != 0), dp(pad_to(d, kPad)), hp(pad_to(h, kPad)) {}
-    bool few() const { return rows <= kFewRows; }  // the forward pass's other kernels
+    // The forward pass's kernels for few rows.  us of them and of 64 x 64 tiles:
+    // width 1280, hidden 5120: 1 row 12.4, 21.5; 16 rows 17.4, 21.5; 32 rows 24.7,
+    // 22.1, each CU then taking in all of x twice; width 2048, hidden 2048: 32 rows
+    // 15.7, 18.6; width 264, hidden 520: 32 rows 7.2, 9.1; width 64, hidden 6000, whose
+    // second product has few channels: 4 rows 9.3, 11.1, 16 rows 12.6, 10.8.
+    bool few() const { return rows <= 16 || (rows <= 32 && hp <= 16 * kCus); }
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
     Cut gate(bool saved) const { return few() ? Cut{} : cut(rows, hp, ceil_div(d, kStageK), false, saved, true); }  // the padding is written too
@@ -697,16 +712,16 @@ int launch_products(MlpArgs &a, const Cut &c, float *part, hipStream_t s) {
 }
 
 // As many workgroups as CUs, or a multiple of that, of as many channels each.
-template <bool kGate, int kWaves, int kDeep>
+template <bool kGate, int kRows, int kWaves, int kDeep>
 void launch_few_kernel(MlpArgs &a, int64_t channels, bool ragged, hipStream_t s) {
     const int64_t groups = kCus * ceil_div(channels, kCus * 16);
     a.channels = int32_t(ceil_div(channels, groups));
     a.all_channels = int32_t(channels);
     const dim3 grid(unsigned(ceil_div(channels, a.channels)), 1, 1), block(kWaves * 64, 1, 1);
     if (ragged)
-        hipLaunchKernelGGL((mlp_few_kernel<kGate, true, kWaves, kDeep>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mlp_few_kernel<kGate, true, kRows, kWaves, kDeep>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((mlp_few_kernel<kGate, false, kWaves, kDeep>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mlp_few_kernel<kGate, false, kRows, kWaves, kDeep>), grid, block, 0, s, a);
 }
 
 // The forward pass of few rows, operands as they are.
@@ -720,12 +735,18 @@ void launch_few(const Sizes &z, const mimo_mlp &args, uint16_t *hidden, uint16_t
     a.gate_up = args.gate_up;
     a.hidden = hidden;
     a.ldh = z.hp;
-        launch_few_kernel<true, 8, 5>(a, z.hp, z.pad_d, s);
+        if (z.rows <= 16)
+        launch_few_kernel<true, 1, 8, 5>(a, z.hp, z.pad_d, s);
+    else
+        launch_few_kernel<true, 2, 8, 5>(a, z.hp, z.pad_d, s);
     a.p[0] = product(matrix(hidden, z.hp), matrix(args.w_down, z.h), z.rows, z.d, z.h, 128, 128);
     a.bias0 = args.b_down;
     a.out[0] = out;
     a.ldo[0] = z.d;
-    launch_few_kernel<false, 16, 10>(a, z.d, z.pad_h, s);
+    if (z.rows <= 16)
+        launch_few_kernel<false, 1, 16, 10>(a, z.d, z.pad_h, s);
+    else
+        launch_few_kernel<false, 2, 16, 5>(a, z.d, z.pad_h, s);
 }
 
 int check_mlp(const mimo_mlp *p, const char *who) {
