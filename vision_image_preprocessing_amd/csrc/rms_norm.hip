@@ -373,7 +373,8 @@ int32_t backward_groups(int64_t rows, int32_t width) {
     const int64_t per = width <= 64 * 8 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
     const int64_t most = width <= 64 * 8 ? 1024 : width <= 256 * 8 ? 1536 : width <= 256 * 8 * 3 ? 768 : 256;
-    return int32_t(groups < most ? groups : most);
+    const int64_t few = groups < 256 ? groups : groups / 4 > 256 ? groups / 4 : 256;
+    return int32_t(few < most ? few : most);
 }
 
 bool is_dtype(int32_t d) { return d == MIMO_F32 || d == MIMO_BF16; }
