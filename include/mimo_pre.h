@@ -820,8 +820,8 @@ size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidde
  * another one.
  *   workspace  device, >= mimo_gated_mlp_workspace_bytes(...), 16-byte
  *              aligned; calls that may run at the same time need one each.
- * Two kernel launches; one more where K of the second is split (few rows), and
- * one for each operand that is copied.  Returns MIMO_OK, MIMO_E_INVALID,
+ * Two kernel launches; one more where sums of the second are split, and one
+ * where operands are copied.  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE (rows or widths, or more than 2^24 - 1
  * tiles of 256 x 256, of both products together) or MIMO_E_HIP.
  */
@@ -840,8 +840,9 @@ size_t mimo_gated_mlp_backward_workspace_bytes(int64_t rows, int32_t width, int3
  * made.  None may be an input or another one.
  *   workspace  device, >= mimo_gated_mlp_backward_workspace_bytes(...), 16-byte
  *              aligned; calls that may run at the same time need one each.
- * Three kernel launches, one or two more for each bias, and as above.  Returns
- * MIMO_OK, MIMO_E_INVALID, MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
+ * Three kernel launches, one for the biases and one more for db_down, one each
+ * where sums of dx or of the weights' gradients are split, and one where operands
+ * are copied.  Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_CAPACITY, MIMO_E_TOO_LARGE or MIMO_E_HIP.
  */
 int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, void *workspace, size_t workspace_bytes,
                             void *stream);

@@ -1,4 +1,4 @@
-// column_sums.h -- the last step of a sum over rows: every workgroup of a
+// column_sums.h -- the last step of sums over rows: every workgroup of a
 // kernel over rows leaves its partial sum of each column, and these are added
 // up in a fixed order, so that no atomics are needed.
 #pragma once
@@ -6,22 +6,44 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 namespace mimo {
 namespace {
 
 constexpr int kSumColumns = 32, kSumParts = 32;  // of the workgroup
+constexpr int kMaxSums = 3;                      // of a launch
 
 // out[c] = the sum over g of part[g * stride + c], for `columns` columns.
-__global__ __launch_bounds__(kSumColumns *kSumParts) void column_sums_kernel(const float *part, int32_t groups, int64_t stride,
-                                                                             int64_t columns, float *out) {
+struct ColumnSum {
+    const float *part;
+    float *out;
+    int64_t stride, columns;
+    int32_t groups;
+    int32_t first;  // of its workgroups
+};
+struct ColumnSums {
+    ColumnSum of[kMaxSums];
+    int32_t count, workgroups;
+    ColumnSums() { std::memset(this, 0, sizeof(*this)); }
+    void add(const float *part, int32_t groups, int64_t stride, int64_t columns, float *out) {
+        of[count++] = ColumnSum{part, out, stride, columns, groups, workgroups};
+        workgroups += int32_t((columns + kSumColumns - 1) / kSumColumns);
+    }
+};
+
+// 1024 sums of 1280 columns, 5 MB from L2: 5 us, a launch's length.
+__global__ __launch_bounds__(kSumColumns *kSumParts) void column_sums_kernel(ColumnSums a) {
     __shared__ float lds[kSumParts][kSumColumns + 1];
+    int n = 0;
+    while (n + 1 < a.count && int(blockIdx.x) >= a.of[n + 1].first) ++n;
+    const ColumnSum s = a.of[n];
     const int column = threadIdx.x % kSumColumns, first = threadIdx.x / kSumColumns;
-    const int64_t c = int64_t(blockIdx.x) * kSumColumns + column;
+    const int64_t c = int64_t(int(blockIdx.x) - s.first) * kSumColumns + column;
     float v = 0.0f;
-    if (c < columns) {
+    if (c < s.columns) {
 #pragma unroll 8
-        for (int g = first; g < groups; g += kSumParts) v += part[int64_t(g) * stride + c];
+        for (int g = first; g < s.groups; g += kSumParts) v += s.part[int64_t(g) * s.stride + c];
     }
     lds[first][column] = v;
     __syncthreads();
@@ -30,12 +52,14 @@ __global__ __launch_bounds__(kSumColumns *kSumParts) void column_sums_kernel(con
         if (first < n) lds[first][column] += lds[first + n][column];
         __syncthreads();
     }
-    if (first == 0 && c < columns) out[c] = lds[0][column];
+    if (first == 0 && c < s.columns) s.out[c] = lds[0][column];
 }
 
-inline void launch_column_sums(const float *part, int32_t groups, int64_t stride, int64_t columns, float *out, hipStream_t stream) {
-    hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned((columns + kSumColumns - 1) / kSumColumns), 1, 1),
-                       dim3(kSumColumns * kSumParts, 1, 1), 0, stream, part, groups, stride, columns, out);
+// The launches made.
+inline int launch_column_sums(const ColumnSums &sums, hipStream_t stream) {
+    if (!sums.count) return 0;
+    hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned(sums.workgroups), 1, 1), dim3(kSumColumns * kSumParts, 1, 1), 0, stream, sums);
+    return 1;
 }
 
 }  // namespace

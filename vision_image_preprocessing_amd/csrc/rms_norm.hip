@@ -592,7 +592,11 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
             else
                 launch_backward<__bf16, __bf16>(shape, a, groups, s);
         }
-        if (dweight) launch_column_sums(a.part, groups, width, width, dweight, s);
+        if (dweight) {
+            ColumnSums sums;
+            sums.add(a.part, groups, width, width, dweight);
+            launch_column_sums(sums, s);
+        }
     });
     if (e != hipSuccess) return hip_error(e, "rms_norm_backward: kernel launch");
     g_dispatches.fetch_add((rows > 0 ? 1 : 0) + (rows > 0 && dweight && shape.threads == 0 ? 1 : 0) + (dweight ? 1 : 0));
