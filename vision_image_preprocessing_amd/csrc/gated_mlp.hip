@@ -144,6 +144,14 @@ __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
 }
 
 // h = silu(x Wg' + bg) (x Wu' + bu).
+//
+// Width 1280, hidden 5120: 131072 rows in 2.99 to 3.11 ms, 1.10 to 1.15 PFLOP/s; K
+// is 20 stages, 30 us of a tile's 37, and for its first loads and the epilogue the
+// matrix cores wait.  32768 rows with g and u saved 838 to 885 us: 0.86 TFLOP, 1.26
+// GB read and 1.68 written, 3.4 TB/s, in tiles of 256 x 256 (of 128 x 128 952 to
+// 1022, of 64 x 64 1584).  216 rows 15 us, in tiles of 64 x 64 that take 210 MB in
+// from L2 and wait for that.  hidden is read again by the next product, so its
+// stores stay in the caches (non-temporal ones made the kernel 5% slower).
 template <int kTile>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
@@ -191,6 +199,10 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
 
 // dg and du from dh = dout Wd and the saved g, u; partial sums of both over
 // the rows of each half of the tile.
+//
+// 32768 x 1280, hidden 5120: 647 to 668 us, 2.15 GB read, 1.34 of them g and u, and
+// 0.76 written, 4.4 TB/s: memory bounds it, in every tile size (of 128 x 128 670 to
+// 685 us, of 64 x 64 935).
 template <int kTile>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
@@ -257,6 +269,12 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
 
 // Products whose sums are the output: out = h Wd' + bd (kWAcross false), dx
 // (kWAcross), the weights' gradients (both across), or a split's partial sums.
+//
+// 32768 x 1280, hidden 5120, with the join: out 341 + 14 us, 1.21 PFLOP/s; dx 664 + 14,
+// 1.27; the weights' gradients 979 + 11, 1.30.  The matrix cores are busy 70 to 76%
+// of their cycles at the clock that the card's power leaves; 1960 rows, in tiles
+// of 128 x 128, which wait for what a CU takes in, 31 + 7, 58 + 7 and 84 us, 0.67 to
+// 0.92 PFLOP/s.
 template <int kTile, bool kXAcross, bool kWAcross>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
@@ -314,8 +332,10 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpA
     }
 }
 
-// The tiles in parts: their sums in the parts' order, + bias.  32 (8, of 128 x
-// 128) workgroups a tile, eight channels a thread.
+// The tiles in parts: their sums in the parts' order, + bias.  32 (8 of 128 x
+// 128, 2 of 64 x 64) workgroups a tile, eight channels a thread.  The sums come
+// from caches: 128 tiles of 256 x 256 in two parts 14 us, 80 of 64 x 64 in twelve 4,
+// a launch's length.
 template <int kTile>
 __global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
     constexpr int kPieces = kTile / 8, kWgs = kTile * kPieces / 256;
@@ -354,7 +374,8 @@ __global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
 
 // Rows of any width to rows of a multiple of kPad values, zeros behind: the
 // products read 16 bytes at a time.  A wave takes a row; all of a call's
-// operands are one launch.
+// operands are one launch.  4099 x 1283 and the weights of 3421 hidden values,
+// forward: 16 to 19 us, 37 MB read and 38 written, 4.0 to 4.6 TB/s.
 struct PadArgs {
     const uint16_t *from[5];
     uint16_t *to[5];
@@ -411,7 +432,9 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
 //
 // A CU takes in about 25 GB/s of them, whatever waves and loads it has (80
 // workgroups of 16 channels: 4.2, 5.6, 9.0, 15.6 us for K 1280, 2560, 5120,
-// 10240), so what counts is that all CUs have as many channels.
+// 10240), so what counts is that all CUs have as many channels.  4 rows of 1280,
+// hidden 5120: 7.6 us for gate and up, 26 MB at 3.4 TB/s, and 6.8 for down, 13 MB;
+// a launch that does nothing is 2 to 3 of each.
 //
 // v_mfma_f32_16x16x32_bf16, weights first: lane l holds row l % 16 and k = 8 (l /
 // 16) .. + 7 of an operand, and channels 4 (l / 16) + r of x's row l % 16 of the
@@ -737,7 +760,7 @@ void launch_few(const Sizes &z, const mimo_mlp &args, uint16_t *hidden, uint16_t
     a.gate_up = args.gate_up;
     a.hidden = hidden;
     a.ldh = z.hp;
-        if (z.rows <= 16)
+    if (z.rows <= 16)
         launch_few_kernel<true, 1, 8, 5>(a, z.hp, z.pad_d, s);
     else
         launch_few_kernel<true, 2, 8, 5>(a, z.hp, z.pad_d, s);
