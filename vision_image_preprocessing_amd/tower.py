@@ -584,11 +584,15 @@ def rotate_heads(x, cos, sin, inverse: bool = False, out=None, stream=None):
     if stream is not None or _device_now() != index:
         with _entered(what, index, stream, (x, cos, sin, out)):
             return rotate_heads(x, cos, sin, inverse, out)
-    source = _HEADS.pack(*_heads(what, "x", x, x.shape))
+    shape = (rows, heads, dim)
+    source = _HEADS.pack(*_heads(what, "x", x, shape))
     if out is None:
-        out = _dense_like(x)
-    code = _library().mimo_rotate_heads(rows, heads, dim, source, cos.data_ptr(), sin.data_ptr(), 1 if inverse else 0,
-                                        _HEADS.pack(*_heads(what, "out", out, x.shape)), _raw_stream(index))
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        target = _HEADS.pack(out.data_ptr(), heads * dim, dim)
+    else:
+        target = _HEADS.pack(*_heads(what, "out", out, shape))
+    code = _library().mimo_rotate_heads(rows, heads, dim, source, cos.data_ptr(), sin.data_ptr(), 1 if inverse else 0, target,
+                                        _raw_stream(index))
     if code:
         _abi._check(code, what)
     return out
