@@ -90,30 +90,35 @@ __device__ __forceinline__ void load_bias(const float *bias, int c, int count, f
 template <typename T>
 struct Panel {
     __amdgpu_buffer_rsrc_t r;
-    uint32_t off;  // the lane's column
-    int ldh;
-    __device__ __forceinline__ Panel(const T *p, int64_t m0, int64_t m, int tile, int64_t ldh_, int col) : ldh(int(ldh_)) {
-        const int rows = int(min(m - m0, int64_t(tile)));
-        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p + m0 * ldh_), 0, rows * ldh * int(sizeof(T)), kWord3);
-        off = col < ldh ? uint32_t(col) * sizeof(T) : kOutside;
+    uint32_t off, step;  // the lane's channels in its first row; from one of its rows to the next
+    __device__ __forceinline__ Panel(const T *p, int64_t m0, int64_t m, int tile, int64_t ldh, int row, int rows_apart, int col) {
+        const int rows = int(min(m - m0, int64_t(tile))), stride = int(ldh) * int(sizeof(T));
+        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p + m0 * ldh), 0, rows * stride, kWord3);
+        const bool in = col < int(ldh);
+        off = in ? uint32_t(row * stride + col * int(sizeof(T))) : kOutside;
+        step = in ? uint32_t(rows_apart * stride) : 0;
     }
-    // past the rows, or from kOutside, an offset is outside the resource; it
-    // must not wrap back into it
-    __device__ __forceinline__ uint32_t at(int row) const { return off == kOutside ? kOutside : off + uint32_t(row * ldh) * uint32_t(sizeof(T)); }
+    // One row's after the other.  Past the rows, or from kOutside, an offset is
+    // outside the resource.
+    __device__ __forceinline__ uint32_t next() {
+        const uint32_t at = off;
+        off += step;
+        return at;
+    }
 };
 constexpr int kStream = 2;  // non-temporal: what is not read again soon
-__device__ __forceinline__ void load4(const Panel<float> &p, int row, float (&v)[4]) {
-    const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.r, p.at(row), 0, kStream));
+__device__ __forceinline__ void load4(Panel<float> &p, float (&v)[4]) {
+    const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.r, p.next(), 0, kStream));
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = w[j];
 }
-__device__ __forceinline__ void store4(const Panel<float> &p, int row, const float (&v)[4]) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), p.r, p.at(row), 0, kStream);
+__device__ __forceinline__ void store4(Panel<float> &p, const float (&v)[4]) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), p.r, p.next(), 0, kStream);
 }
-__device__ __forceinline__ void store4(const Panel<uint16_t> &p, int row, const float (&v)[4]) {
+__device__ __forceinline__ void store4(Panel<uint16_t> &p, const float (&v)[4]) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const bf16x4 h = {__bf16(v[0]), __bf16(v[1]), __bf16(v[2]), __bf16(v[3])};
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), p.r, p.at(row), 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), p.r, p.next(), 0, 0);
 }
 
 // Eight bf16 values from any address of the type, `left` of them inside (any
@@ -145,14 +150,14 @@ __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
 
 // h = silu(x Wg' + bg) (x Wu' + bu).
 //
-// Width 1280, hidden 5120: 131072 rows in 2.99 to 3.11 ms, 1.10 to 1.15 PFLOP/s; K
-// is 20 stages, 30 us of a tile's 37, and for its first loads and the epilogue the
+// Width 1280, hidden 5120: 131072 rows in 2.83 to 3.00 ms, 1.15 to 1.21 PFLOP/s; K
+// is 20 stages, 30 us of a tile's 36, and for its first loads and the epilogue the
 // matrix cores wait.  32768 rows with g and u saved 838 to 885 us: 0.86 TFLOP, 1.26
 // GB read and 1.68 written, 3.4 TB/s, in tiles of 256 x 256 (of 128 x 128 952 to
 // 1022, of 64 x 64 1584).  216 rows 15 us, in tiles of 64 x 64 that take 210 MB in
 // from L2 and wait for that.  hidden is read again by the next product, so its
 // stores stay in the caches (non-temporal ones made the kernel 5% slower).
-template <int kTile>
+template <int kTile, bool kSaved>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
     typedef Tile<kTile> T;
@@ -170,28 +175,46 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
     float bg[4], bu[4];
     load_bias(a.bias0, col, p.n, bg);
     load_bias(a.bias1, col, p.n, bu);
-    const Panel<uint16_t> hidden(a.hidden, m0, p.m, kTile, a.ldh, col);
-    const Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, col);
+    const int row = (wave / T::kWavesN) * T::kWaveM + lane / kLanes;
+    Panel<uint16_t> hidden(a.hidden, m0, p.m, kTile, a.ldh, row, kPass, col);
+    Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, row, kPass, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, row, kPass, col);
+    const bool edge = n0 + kTile / 2 > p.n;  // some of the channels are padding, and zeros
+    constexpr int kPasses = 32 / kPass;
 #pragma unroll
     for (int i = 0; i < T::kBlocksM; ++i) {
         turned.put(acc[i]);
+        float g[kPasses][4], u[kPasses][4];
 #pragma unroll
-        for (int t = 0; t < 32 / kPass; ++t) {
-            const int r = t * kPass + lane / kLanes, row = (wave / T::kWavesN) * T::kWaveM + i * 32 + r;
-            float g[4], u[4], h[4];
-            turned.get(r, piece, g);
-            turned.get(r, kHalf + piece, u);
+        for (int t = 0; t < kPasses; ++t) {
+            turned.get(t * kPass + lane / kLanes, piece, g[t]);
+            turned.get(t * kPass + lane / kLanes, kHalf + piece, u[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < kPasses; ++t) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool in = col + j < p.n;
-                g[j] = in ? g[j] + bg[j] : 0.0f;
-                u[j] = in ? u[j] + bu[j] : 0.0f;
-                h[j] = g[j] * sigmoid(g[j]) * u[j];
+                g[t][j] += bg[j];
+                u[t][j] += bu[j];
             }
-            store4(hidden, row, h);
-            if (a.gate_up) {
-                store4(gate, row, g);
-                store4(up, row, u);
+        }
+        if (edge) {
+#pragma unroll
+            for (int t = 0; t < kPasses; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    g[t][j] = col + j < p.n ? g[t][j] : 0.0f;
+                    u[t][j] = col + j < p.n ? u[t][j] : 0.0f;
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < kPasses; ++t) {
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = g[t][j] * sigmoid(g[t][j]) * u[t][j];
+            store4(hidden, h);
+            if constexpr (kSaved) {
+                store4(gate, g[t]);
+                store4(up, u[t]);
             }
         }
     }
@@ -200,9 +223,10 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
 // dg and du from dh = dout Wd and the saved g, u; partial sums of both over
 // the rows of each half of the tile.
 //
-// 32768 x 1280, hidden 5120: 647 to 668 us, 2.15 GB read, 1.34 of them g and u, and
-// 0.76 written, 4.4 TB/s: memory bounds it, in every tile size (of 128 x 128 670 to
-// 685 us, of 64 x 64 935).
+// 32768 x 1280, hidden 5120: 586 to 612 us, 2.15 GB read, 1.34 of them g and u, and
+// 0.76 written, 4.8 TB/s: memory bounds it (tiles of 128 x 128, two workgroups a
+// CU, 670 to 685, of 64 x 64 935).  g and u stay on their way from one block of
+// rows to the next.
 template <int kTile>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpArgs a) {
     MIMO_TILE_BUFFERS(kTile);
@@ -217,40 +241,42 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
     constexpr int kLanes = T::kWaveN / 4, kPass = 64 / kLanes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int piece = (lane % kLanes) * 4, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece;
-    const Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, col);
-    const Panel<uint16_t> dgate(a.dgate, m0, p.m, kTile, a.ldh, col), dup(a.dup, m0, p.m, kTile, a.ldh, col);
+    const int row = (wave / T::kWavesN) * T::kWaveM + lane / kLanes;
+    Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, row, kPass, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, row, kPass, col);
+    Panel<uint16_t> dgate(a.dgate, m0, p.m, kTile, a.ldh, row, kPass, col), dup(a.dup, m0, p.m, kTile, a.ldh, row, kPass, col);
     float sg[4] = {}, su[4] = {};
+    constexpr int kPasses = 32 / kPass, kAll = T::kBlocksM * kPasses;
+    constexpr int kAhead = 8;  // passes whose g and u are on the way (2: 614 us, 4: 612, 8: 608, 12: 614)
+    float g[kAll][4], u[kAll][4];
+    auto load = [&](int t) __attribute__((always_inline)) {
+        if (t >= kAll) return;
+        load4(gate, g[t]);
+        load4(up, u[t]);
+    };
 #pragma unroll
-    for (int i = 0; i < T::kBlocksM; ++i) {
-        const int first = (wave / T::kWavesN) * T::kWaveM + i * 32 + lane / kLanes;
-        constexpr int kAhead = 2;  // passes whose g and u are on the way; more need registers that there are not
-        float g[32 / kPass][4], u[32 / kPass][4];
-        auto load = [&](int t) __attribute__((always_inline)) {
-            if (t >= 32 / kPass) return;
-            load4(gate, first + t * kPass, g[t]);
-            load4(up, first + t * kPass, u[t]);
-        };
+    for (int t = 0; t < kAhead; ++t) load(t);
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t) load(t);
-        turned.put(acc[i]);
+    for (int t = 0; t < kAll; ++t) {
+        if (t % kPasses == 0) turned.put(acc[t / kPasses]);
+        load(t + kAhead);
+        float dh[4];
+        turned.get(t % kPasses * kPass + lane / kLanes, piece, dh);
+        // past the columns dh is any value, and has to be zero for the
+        // padding; past the rows g and u read as zeros, and with them dg and du
 #pragma unroll
-        for (int t = 0; t < 32 / kPass; ++t) {
-            load(t + kAhead);
-            float dh[4];
-            turned.get(t * kPass + lane / kLanes, piece, dh);
-            // past the columns dh is any value, and has to be zero for the
-            // padding; past the rows g and u read as zeros, and with them dg and du
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s = sigmoid(g[t][j]), d = col + j < p.n ? dh[j] : 0.0f;
-                dh[j] = d * u[t][j] * (s * (1.0f + g[t][j] * (1.0f - s)));
-                u[t][j] = d * (g[t][j] * s);
-                sg[j] += dh[j];
-                su[j] += u[t][j];
-            }
-            store4(dgate, first + t * kPass, dh);
-            store4(dup, first + t * kPass, u[t]);
+        for (int j = 0; j < 4; ++j) {
+            const float s = sigmoid(g[t][j]), d = col + j < p.n ? dh[j] : 0.0f;
+            dh[j] = d * u[t][j] * (s * (1.0f + g[t][j] * (1.0f - s)));
+            u[t][j] = d * (g[t][j] * s);
+            sg[j] += dh[j];
+            su[j] += u[t][j];
         }
+        store4(dgate, dh);
+        store4(dup, u[t]);
+        // added here and now: the compiler would put it off to where the sums
+        // are written, keep every value until then and spill (662 us, not 608)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(sg[j]), "+v"(su[j]));
     }
     if (!a.part) return;
 #pragma unroll
@@ -716,6 +742,15 @@ struct Padding {
     }
 };
 
+template <int kTile>
+void launch_gate(const MlpArgs &a, const dim3 &grid, hipStream_t s) {
+    const dim3 block(Tile<kTile>::kThreads, 1, 1);
+    if (a.gate_up)
+        hipLaunchKernelGGL((mlp_gate_kernel<kTile, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((mlp_gate_kernel<kTile, false>), grid, block, 0, s, a);
+}
+
 // A launch of mlp_product_kernel, and its join; the launches made.
 template <bool kXAcross, bool kWAcross>
 int launch_products(MlpArgs &a, const Cut &c, float *part, hipStream_t s) {
@@ -862,11 +897,11 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
         a.ldh = z.hp;
         const dim3 grid(unsigned(gate.tiles), 1, 1);
         if (gate.tile == 256)
-            hipLaunchKernelGGL(mlp_gate_kernel<256>, grid, dim3(Tile<256>::kThreads, 1, 1), 0, s, a);
+            launch_gate<256>(a, grid, s);
         else if (gate.tile == 128)
-            hipLaunchKernelGGL(mlp_gate_kernel<128>, grid, dim3(Tile<128>::kThreads, 1, 1), 0, s, a);
+            launch_gate<128>(a, grid, s);
         else
-            hipLaunchKernelGGL(mlp_gate_kernel<64>, grid, dim3(Tile<64>::kThreads, 1, 1), 0, s, a);
+            launch_gate<64>(a, grid, s);
         a.p[0] = product(matrix(hidden, z.hp), matrix(wd, z.lh()), z.rows, z.d, z.h, down.tile, down.tile);
         a.out[0] = static_cast<uint16_t *>(out);
         a.ldo[0] = z.d;
