@@ -152,9 +152,9 @@ __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
 //
 // Width 1280, hidden 5120: 131072 rows in 2.83 to 3.00 ms, 1.15 to 1.21 PFLOP/s; K
 // is 20 stages, 30 us of a tile's 36, and for its first loads and the epilogue the
-// matrix cores wait.  32768 rows with g and u saved 838 to 885 us: 0.86 TFLOP, 1.26
+// matrix cores wait.  32768 rows with g and u saved 842 to 888 us: 0.86 TFLOP, 1.26
 // GB read and 1.68 written, 3.4 TB/s, in tiles of 256 x 256 (of 128 x 128 952 to
-// 1022, of 64 x 64 1584).  216 rows 15 us, in tiles of 64 x 64 that take 210 MB in
+// 1047, of 64 x 64 1574).  216 rows 15 us, in tiles of 64 x 64 that take 210 MB in
 // from L2 and wait for that.  hidden is read again by the next product, so its
 // stores stay in the caches (non-temporal ones made the kernel 5% slower).
 template <int kTile, bool kSaved>
@@ -223,9 +223,9 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
 // dg and du from dh = dout Wd and the saved g, u; partial sums of both over
 // the rows of each half of the tile.
 //
-// 32768 x 1280, hidden 5120: 586 to 612 us, 2.15 GB read, 1.34 of them g and u, and
-// 0.76 written, 4.8 TB/s: memory bounds it (tiles of 128 x 128, two workgroups a
-// CU, 670 to 685, of 64 x 64 935).  g and u stay on their way from one block of
+// 32768 x 1280, hidden 5120: 586 to 619 us, 2.10 GB read, 1.34 of them g and u, and
+// 0.68 written, 4.5 to 4.7 TB/s: memory bounds it (tiles of 128 x 128, two
+// workgroups a CU, 652 to 665, of 64 x 64 901 to 928).  g and u stay on their way from one block of
 // rows to the next.
 template <int kTile>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpArgs a) {
