@@ -703,7 +703,8 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
  *            dtypes agree.
  *   out      device, out_dtype: y; may be x or the residual where the dtypes
  *            agree, but not residual_out.
- *   rstd     device float32 [rows], or NULL: the backward pass takes it.
+ *   rstd     device float32 [rows], or NULL: the backward pass takes it.  Not an
+ *            input nor another output.
  * Pointers are aligned to their values.  Returns MIMO_OK, MIMO_E_INVALID,
  * MIMO_E_TOO_LARGE (width, or more than 2^31 - 1 rows) or MIMO_E_HIP.
  */
@@ -722,7 +723,7 @@ int mimo_rms_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, c
  *   q        device int8 [rows][padded], padded = width rounded up to a
  *            multiple of 128 (the rest is set to zero), 16-byte aligned, not
  *            an input.
- *   scale    device float32 [rows].
+ *   scale    device float32 [rows]; not an input nor another output.
  * Other arguments and results as for mimo_rms_norm.
  */
 int mimo_rms_norm_quantized(int64_t rows, int32_t width, const void *x, int32_t x_dtype, const void *residual,
@@ -742,7 +743,7 @@ size_t mimo_rms_norm_workspace_bytes(int64_t rows, int32_t width);
  *   dresidual  device, h_dtype, or NULL (zeros).
  *   dx       device, h_dtype; may be dresidual, but not h or dout.
  *   dweight  device float32 [width], or NULL; overwritten, its sum has a fixed
- *            order; not an input.
+ *            order; not an input, nor dx.
  *   workspace  device, >= mimo_rms_norm_workspace_bytes(rows, width), 16-byte
  *            aligned, or NULL if dweight is; calls that may run at the same
  *            time need one each.
@@ -822,7 +823,7 @@ size_t mimo_gated_mlp_workspace_bytes(int64_t rows, int32_t width, int32_t hidde
  *              aligned; calls that may run at the same time need one each.
  * Two kernel launches; one more where sums of the second are split, and one
  * where operands are copied.  Returns MIMO_OK, MIMO_E_INVALID,
- * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE (rows or widths, or more than 2^24 - 1
+ * MIMO_E_CAPACITY, MIMO_E_TOO_LARGE (rows or widths, or more than 2^23 - 1
  * tiles of 256 x 256, of both products together) or MIMO_E_HIP.
  */
 int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t workspace_bytes, void *stream);

@@ -39,6 +39,18 @@ def test_quantized_norm_refuses(bad):
     assert _quantized(**bad) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm_quantized:")
 
 
+def test_norm_refuses_outputs_that_are_one_array():
+    """What is written a value a row is no array whose other rows are read."""
+    for at in (P, 2 * P, 4 * P, 5 * P):
+        assert _forward(rstd=at) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm: rstd")
+        assert _quantized(s=at) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm_quantized: scale")
+    need = V.rms_norm_workspace_bytes(4, 64)
+    for dweight in (P, 2 * P, 5 * P, 6 * P):
+        assert V.load().mimo_rms_norm_backward(4, 64, P, F, 2 * P, F, 3 * P, 4 * P, 5 * P, 6 * P, dweight, 8 * P, need,
+                                               None) == V.MIMO_E_INVALID
+        assert V.last_error().startswith("rms_norm_backward: dweight")
+
+
 def test_norm_sizes():
     for call in (_forward, _quantized):
         assert call(width=65537) == V.MIMO_E_TOO_LARGE and call(rows=1 << 31) == V.MIMO_E_TOO_LARGE
@@ -120,6 +132,15 @@ def test_mlp_refuses():
     assert forward(rows=0, x=0, out=None, ws=None) == V.MIMO_OK and V.dispatch_count() == before
     for sizes in ((-1, 64, 72), (4, 0, 72), (4, 64, 0), (1 << 31, 64, 72), (4, 65537, 72), (4, 64, 65537), (1 << 30, 64, 65536)):
         assert V.gated_mlp_workspace_bytes(*sizes) == 0 and V.gated_mlp_backward_workspace_bytes(*sizes) == 0
+
+
+def test_mlp_tiles():
+    """A workgroup of a 256 x 256 tile has 512 threads, and a launch fewer than
+    2^32: one more row of tiles than fits is refused."""
+    rows = 256 * ((1 << 23) // (1 + 1))  # tiles of 128 hidden values and of 256 outputs
+    assert V.gated_mlp_workspace_bytes(rows, 256, 128) == 0 and V.gated_mlp_backward_workspace_bytes(rows, 256, 128) == 0
+    assert V.gated_mlp_workspace_bytes(rows - 256, 256, 128) > 0 and V.gated_mlp_backward_workspace_bytes(rows - 256, 256, 128) > 0
+    assert V.load().mimo_gated_mlp(_mlp(rows=rows, width=256, hidden=128), 10 * P, 20 * P, 1 << 62, None) == V.MIMO_E_TOO_LARGE
 
 
 def test_mlp_backward_refuses():

@@ -43,7 +43,7 @@ using rows::row_grid;
 using rows::row_group;
 
 constexpr int kMaxWidth = 65536;
-constexpr int kMaxTiles = (1 << 24) - 1;
+constexpr int kMaxTiles = (1 << 23) - 1;  // of up to 512 threads: a launch has fewer than 2^32
 constexpr int kPad = 64;  // rows of hidden values, and copied operands, are multiples of this
 
 struct MlpArgs {
@@ -818,7 +818,7 @@ int check_mlp(const mimo_mlp *p, const char *who) {
         return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^31 - 1 rows, or a width above 65536");
     // of 256 x 256; cut() takes no smaller ones where there would be more
     const int64_t m = ceil_div(p->rows, 256), n = ceil_div(p->hidden_width, 128) + ceil_div(p->width, 256);
-    if (m * n > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^24 - 1 tiles");
+    if (m * n > kMaxTiles) return set_error(MIMO_E_TOO_LARGE, w + ": more than 2^23 - 1 tiles");
     return MIMO_OK;
 }
 

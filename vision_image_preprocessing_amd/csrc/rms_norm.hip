@@ -464,6 +464,12 @@ int check_forward(const char *who, int64_t rows, int32_t width, const void *x, i
     return MIMO_OK;
 }
 
+// Whether `p`, which is written a value a row while other rows are still read,
+// is one of these.
+bool is_one_of(const void *p, const void *x, const void *residual, const void *residual_out, const void *out) {
+    return p && (p == x || p == residual || p == residual_out || p == out);
+}
+
 RmsArgs forward_args(int64_t rows, int32_t width, const void *x, const void *residual, const float *weight, double eps,
                      void *residual_out, void *out) {
     RmsArgs a;
@@ -502,6 +508,8 @@ int mimo_rms_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, c
     // workgroups that still read the weight run next to the ones that write
     if (weight && (rstd == weight || out == weight || residual_out == weight))
         return set_error(MIMO_E_INVALID, "rms_norm: no output may be the weight");
+    if (is_one_of(rstd, x, residual, residual ? residual_out : nullptr, out))
+        return set_error(MIMO_E_INVALID, "rms_norm: rstd must not be an input or another output");
     if ((out == x && out_dtype != x_dtype) || (residual && out == residual && out_dtype != residual_dtype))
         return set_error(MIMO_E_INVALID, "rms_norm: out may be x or the residual only in its dtype");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, out);
@@ -531,6 +539,8 @@ int mimo_rms_norm_quantized(int64_t rows, int32_t width, const void *x, int32_t 
     if (q == x || (residual && q == residual)) return set_error(MIMO_E_INVALID, "rms_norm_quantized: q must not be an input");
     if (weight && (scale == weight || q == weight || residual_out == weight))
         return set_error(MIMO_E_INVALID, "rms_norm_quantized: no output may be the weight");
+    if (is_one_of(scale, x, residual, residual ? residual_out : nullptr, q))
+        return set_error(MIMO_E_INVALID, "rms_norm_quantized: scale must not be an input or another output");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, q);
     a.scale = scale;
     const Shape shape = forward_shape(width, all_aligned(a));
@@ -567,8 +577,8 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
         if (dweight && workspace_bytes < mimo_rms_norm_workspace_bytes(rows, width))
             return set_error(MIMO_E_CAPACITY, "rms_norm_backward: workspace smaller than mimo_rms_norm_workspace_bytes");
         if (dx == h || dx == dout) return set_error(MIMO_E_INVALID, "rms_norm_backward: dx must not be h or dout");
-        if (dweight && (dweight == weight || dweight == rstd))
-            return set_error(MIMO_E_INVALID, "rms_norm_backward: dweight must not be an input");
+        if (dweight && (dweight == weight || dweight == rstd || is_one_of(dweight, h, dout, dresidual, dx)))
+            return set_error(MIMO_E_INVALID, "rms_norm_backward: dweight must not be an input, nor dx");
         if (dx == weight || dx == rstd) return set_error(MIMO_E_INVALID, "rms_norm_backward: dx must not be the weight or rstd");
     }
     RmsArgs a;
