@@ -141,6 +141,13 @@ def test_mlp_tiles():
     assert V.gated_mlp_workspace_bytes(rows, 256, 128) == 0 and V.gated_mlp_backward_workspace_bytes(rows, 256, 128) == 0
     assert V.gated_mlp_workspace_bytes(rows - 256, 256, 128) > 0 and V.gated_mlp_backward_workspace_bytes(rows - 256, 256, 128) > 0
     assert V.load().mimo_gated_mlp(_mlp(rows=rows, width=256, hidden=128), 10 * P, 20 * P, 1 << 62, None) == V.MIMO_E_TOO_LARGE
+    # in Python before outputs of such a size are allocated
+    x, w, wd = (torch.empty(s, dtype=torch.bfloat16, device="meta") for s in ((rows, 256), (128, 256), (256, 128)))
+    gate_up, hidden = torch.empty((2, rows, 128), device="meta"), torch.empty((rows, 128), dtype=torch.bfloat16, device="meta")
+    for call in (lambda: V.gated_mlp(x, w, w, wd), lambda: V.gated_mlp_backward(x, x, w, w, wd, gate_up, hidden)):
+        with pytest.raises(V.MimoError) as error:
+            call()
+        assert error.value.code == V.MIMO_E_TOO_LARGE
 
 
 def test_mlp_backward_refuses():

@@ -616,6 +616,8 @@ def _check_mlp(what, x, w_gate, w_up, w_down, gate_up, hidden):
         _refuse(f"{what}: x and w_gate must have columns and w_gate rows, got {tuple(x.shape)} and {tuple(w_gate.shape)}")
     if width > 65536 or inner > 65536 or rows > 0x7FFFFFFF:
         _refuse_size(f"{what}: a width above 65536 or more than 2^31 - 1 rows: {rows} x {width}, hidden {inner}")
+    if (rows + 255 >> 8) * ((inner + 127 >> 7) + (width + 255 >> 8)) > 0x7FFFFF:
+        _refuse_size(f"{what}: more than 2^23 - 1 tiles: {rows} x {width}, hidden {inner}")
     _check_bf16(what, "x", x, (rows, width))
     _check_bf16(what, "w_gate", w_gate, (inner, width))
     _check_bf16(what, "w_up", w_up, (inner, width))
@@ -636,7 +638,7 @@ def gated_mlp(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, out=
 
     x bf16 [rows, width]; w_gate, w_up bf16 [hidden, width] and w_down bf16
     [width, hidden], as a checkpoint has them; biases float32 or None; all
-    contiguous.  Returns out bf16 [rows, width], or with return_saved=True (out,
+    contiguous, the bf16 ones 16-byte aligned.  Returns out bf16 [rows, width], or with return_saved=True (out,
     gate_up, hidden), which the backward pass takes: float32 [2, rows, padded]
     and bf16 [rows, padded], padded = hidden rounded up to a multiple of 64.
     ``workspace``: uint8, at least gated_mlp_workspace_bytes(rows, width, hidden)
