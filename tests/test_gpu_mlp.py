@@ -149,6 +149,13 @@ def test_large(V, rows, d, h):
     _check(V, rows, d, h, True, 7)
 
 
+@pytest.mark.parametrize("rows,d,h", [(14394, 947, 967), (14394, 947, 968), (10955, 132, 3634), (19658, 194, 3313)])
+def test_tiles_of_256(V, rows, d, h):
+    """Sizes whose products go by tiles of 256 x 256, all of them, and those
+    whose sums for out, dx and the weights' gradients are made in parts."""
+    _check(V, rows, d, h, True, 3)
+
+
 @pytest.mark.parametrize("scale", [1e-3, 30.0])
 def test_gates_near_zero_and_saturated(V, scale):
     _check(V, 70, 96, 200, True, 11, scale=scale)
