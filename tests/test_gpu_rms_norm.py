@@ -132,6 +132,13 @@ def test_types(V, x_kind, r_kind, o_kind, g_kind):
         _check(V, 37, width, x_kind, r_kind, o_kind, g_kind, width != 333, seed=3, dres_too=o_kind == "f32")
 
 
+@pytest.mark.parametrize("width", [504, 509, 1288, 1283, 2040, 2041, 5128, 5121, 8200, 8193, 16384, 16383])
+@pytest.mark.parametrize("x_kind,r_kind,o_kind,g_kind", [("bf16", "f32", "f32", "f32"), ("bf16", "f32", "bf16", "bf16"),
+                                                         ("bf16", "bf16", "f32", "f32"), ("f32", "f32", "bf16", "bf16")])
+def test_mixed_types_in_every_shape(V, width, x_kind, r_kind, o_kind, g_kind):
+    _check(V, 9, width, x_kind, r_kind, o_kind, g_kind, True, seed=width)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 4, 5, 1023, 1025, 4097, 9001])
 def test_rows(V, rows):
     _check(V, rows, 72, "bf16", "bf16", "bf16", "bf16", True, seed=rows)
