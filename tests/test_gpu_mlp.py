@@ -143,7 +143,8 @@ def test_sizes(V, rows, d, h, bias):
 
 
 @pytest.mark.parametrize("rows,d,h", [(4200, 136, 2056), (8300, 72, 2051), (16500, 1032, 80), (40, 4100, 4104), (1, 2000, 5000), (3, 5000, 2000),
-                                      (9, 4099, 1283), (31, 1280, 5120), (32, 2048, 2048), (29, 1283, 3421)])
+                                      (9, 4099, 1283), (31, 1280, 5120), (32, 2048, 2048), (29, 1283, 3421),
+                                      (29, 1283, 1027)])
 def test_large(V, rows, d, h):
     """Every kernel's large tiles, long sums, and one row."""
     _check(V, rows, d, h, True, 7)

@@ -137,12 +137,6 @@ __device__ __forceinline__ u32x4 load_ragged(const uint16_t *p, int left) {
 // about a unit in the last place of float32.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// The tile's five buffers: 160 KB, one workgroup a CU, with 256; 80 KB, two, with 128.
-#define MIMO_TILE_BUFFERS(kTile)                                                                  \
-    __shared__ __attribute__((aligned(16))) uint8_t sx0[kTile * 128], sx1[kTile * 128], sx2[kTile * 128]; \
-    __shared__ __attribute__((aligned(16))) uint8_t sw0[kTile * 128], sw1[kTile * 128];           \
-    const Buffers<kTile> lds{{(lds_ptr)sx0, (lds_ptr)sx1, (lds_ptr)sx2}, {(lds_ptr)sw0, (lds_ptr)sw1}}
-
 // Which product of a launch a tile is of.
 __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
     return a.products > 2 && tile >= a.p[2].first ? 2 : a.products > 1 && tile >= a.p[1].first ? 1 : 0;
@@ -159,7 +153,7 @@ __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
 // stores stay in the caches (non-temporal ones made the kernel 5% slower).
 template <int kTile, bool kSaved>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs a) {
-    MIMO_TILE_BUFFERS(kTile);
+    const Buffers<kTile> lds = tile_buffers<kTile>();
     typedef Tile<kTile> T;
     constexpr int kHalf = T::kWaveN / 2;
     const Product &p = a.p[0];
@@ -229,7 +223,7 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
 // rows to the next.
 template <int kTile>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpArgs a) {
-    MIMO_TILE_BUFFERS(kTile);
+    const Buffers<kTile> lds = tile_buffers<kTile>();
     typedef Tile<kTile> T;
     const Product &p = a.p[0];
     const Place at(p, int(xcd_contiguous_tile(blockIdx.x, gridDim.x)));
@@ -303,7 +297,7 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
 // 0.92 PFLOP/s.
 template <int kTile, bool kXAcross, bool kWAcross>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpArgs a) {
-    MIMO_TILE_BUFFERS(kTile);
+    const Buffers<kTile> lds = tile_buffers<kTile>();
     typedef Tile<kTile> T;
     const Unit unit(a.units);
     const int n = kXAcross ? product_of(a, unit.tile) : 0;
@@ -549,14 +543,14 @@ constexpr int kMinStages = 6;  // of a part
 
 // What a round of the card's tiles takes, in microseconds, fitted to 17 to 32768
 // rows of widths 264 to 2048 and 520 to 5120 hidden values: a stage of the
-// tiles that the CUs have at once (one of 256 x 256, two of 128 x 128, four of 64
+// tiles that the CUs have at once (one of 256 x 256, two of 128 x 128, three of 64
 // x 64), by how many there are; a tile's first loads and its store (more where g
 // and u are read or written); and what parts cost, which are written in
 // float32 and joined.
 double stage_us(int tile, int64_t units) {
     if (tile == 256) return 1.5;
     if (tile == 128) return units <= kCus ? 0.6 : 1.07;
-    return units <= kCus ? 0.33 : units <= 2 * kCus ? 0.42 : units <= 3 * kCus ? 0.55 : 0.7;
+    return units <= kCus ? 0.25 : units <= 2 * kCus ? 0.42 : 0.58;
 }
 double ends_us(int tile, bool wide) { return tile == 256 ? (wide ? 20.0 : 11.0) : tile == 128 ? (wide ? 6.0 : 4.0) : (wide ? 4.0 : 3.0); }
 double parts_us(int tile) { return tile == 256 ? 19.0 : 6.0; }
@@ -566,7 +560,7 @@ double parts_us(int tile) { return tile == 256 ? 19.0 : 6.0; }
 // that is quicker.
 Cut cut_tiles(int tile, int64_t tiles, int64_t stages, bool splittable, bool wide, double *cost) {
     Cut c{tile, {int32_t(tiles), 0, 1}, tiles};
-    const int64_t slots = int64_t(kCus) * (tile == 256 ? 1 : tile == 128 ? 2 : 4), full = tiles / slots * slots, tail = tiles - full;
+    const int64_t slots = int64_t(kCus) * (tile == 256 ? 1 : tile == 128 ? 2 : 3), full = tiles / slots * slots, tail = tiles - full;
     const double ends = ends_us(tile, wide);
     double rest = tail ? double(stages) * stage_us(tile, tail) + ends : 0.0;
     if (splittable && tail) {
@@ -593,10 +587,10 @@ int64_t tiles_of(const Extent *e, int count, int tile, int columns) {
     return tiles;
 }
 // The quickest of the three sizes by that.  us of the forward and the backward
-// pass on 64, 128 and 256, width 1280, hidden 5120: 64 rows 23, 27, 47 and 47, 53,
-// 76; 512 rows 50, 49, 54 and 98, 79, 114; 1960 rows 135, 94, 107 and 278, 200, 202;
-// 4096 rows 257, 172, 171 and 564, 378, 355; width 640, hidden 1000: 1024 rows 14,
-// 20, 41 and 39, 44, 76; 4096 rows 34, 32, 46 and 80, 69, 104.
+// pass on 64, 128 and 256, width 1280, hidden 5120: 64 rows 19, 27, 46 and 45, 48,
+// 76; 512 rows 42, 42, 51 and 90, 76, 110; 1960 rows 132, 93, 102 and 275, 191, 195;
+// 4096 rows 250, 167, 166 and 543, 371, 346; width 640, hidden 1000: 1024 rows 12,
+// 20, 40 and 33, 43, 75; 4096 rows 33, 29, 44 and 70, 70, 100.
 // gate: both projections of a channel lie in one tile, which then has half as
 // many.
 Cut cut(const Extent *e, int count, int64_t stages, bool splittable, bool wide, bool gate) {
@@ -626,11 +620,12 @@ struct Sizes {
     Sizes(int64_t rows, int64_t d, int64_t h)
         : rows(rows), d(d), h(h), pad_d(d % 8 != 0), pad_h(h % 8 != 0), dp(pad_to(d, kPad)), hp(pad_to(h, kPad)) {}
     // The forward pass's kernels for few rows.  us of them and of 64 x 64 tiles:
-    // width 1280, hidden 5120: 1 row 12.4, 21.5; 16 rows 17.4, 21.5; 32 rows 24.7,
-    // 22.1, each CU then taking in all of x twice; width 2048, hidden 2048: 32 rows
-    // 15.7, 18.6; width 264, hidden 520: 32 rows 7.2, 9.1; width 64, hidden 6000, whose
-    // second product has few channels: 4 rows 9.3, 11.1, 16 rows 12.6, 10.8.
-    bool few() const { return rows <= 16 || (rows <= 32 && hp <= 16 * kCus); }
+    // width 1280, hidden 5120: 1 row 12.4, 17.6; 16 rows 17.4, 17.8; 32 rows 24.6,
+    // 18.1, each CU then taking in all of x twice; width 2048, hidden 2048: 17 rows
+    // 13.0, 14.8, 32 rows 15.7, 15.3; width 264, hidden 520: 32 rows 7.2, 8.8; width 64,
+    // hidden 6000, whose second product has few channels: 4 rows 9.3, 10.8, 16 rows
+    // 12.5, 10.6.
+    bool few() const { return rows <= 16 || (rows <= 32 && hp <= 8 * kCus); }
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
     Cut gate(bool saved) const { return few() ? Cut{} : cut(rows, hp, ceil_div(d, kStageK), false, saved, true); }  // the padding is written too

@@ -8,13 +8,16 @@
 //
 // A workgroup makes a kTile x kTile tile: 256 x 256 (eight waves of 128 x 64, 128
 // accumulators a lane, one workgroup a CU), 128 x 128 (four of 64 x 64, two
-// workgroups a CU) or 64 x 64 (four of 32 x 32, four workgroups a CU).  K
+// workgroups a CU) or 64 x 64 (four of 32 x 32, three workgroups a CU).  K
 // advances 64 values a stage.  Operands go from memory straight into LDS
 // (buffer_load ... lds), two stages ahead of the products; x has three buffers,
-// w two, which are filled again as soon as they are read.  The five buffers are
-// arrays of their own, so that the compiler sees that loads into one never meet
-// reads of another, and the stage loop is unrolled six times, after which both
-// rings are back where they were.  Stages past the end are loaded through an
+// w two, which are filled again as soon as they are read.  In a tile of 64 x 64,
+// whose stages are short, w has three, too, and its loads another stage's time
+// (33 rows of 1280, hidden 5120, 21.8 to 18.2 us; 216 rows of 2048, hidden 2048, 26.6
+// to 21.5; the fourth workgroup that a CU then has no room for gave less).  The
+// buffers are arrays of their own, so that the compiler sees that loads into
+// one never meet reads of another, and the stage loop is unrolled six times,
+// after which both rings are back where they were.  Stages past the end are loaded through an
 // empty resource: zeros, without memory traffic.
 //
 // 256 x 256, K 5120: 131072 x 1280 in 1.25 to 1.31 ms, 1.31 to 1.37 PFLOP/s, next
@@ -112,6 +115,7 @@ struct Tile {
     static constexpr int kWaveM = kTile / 2, kWaveN = kTile / kWavesN;
     static constexpr int kBlocksM = kWaveM / 32, kBlocksN = kWaveN / 32;
     static constexpr int kGroups = kTile / 8 / kWaves;  // 1 KB loads a wave makes of each operand a stage
+    static constexpr int kWBuffers = kTile == 64 ? 3 : 2;
 };
 template <int kTile>
 using Sums = f32x16[Tile<kTile>::kBlocksM][Tile<kTile>::kBlocksN];
@@ -140,11 +144,22 @@ struct Place {
 
 // The tile's buffers.  Every address in them is one of these plus a lane's
 // offset and a constant: through longer chains the compiler no longer sees
-// which array a read is of, and waits for all loads in flight.
+// which array a read is of, and waits for all loads in flight.  160 KB with
+// 256, one workgroup a CU; 80 KB with 128, two; 48 KB with 64, three.
 template <int kTile>
 struct Buffers {
-    lds_ptr x[3], w[2];
+    lds_ptr x[3], w[Tile<kTile>::kWBuffers];
 };
+template <int kTile>
+__device__ __forceinline__ Buffers<kTile> tile_buffers() {
+    __shared__ __attribute__((aligned(16))) uint8_t x0[kTile * 128], x1[kTile * 128], x2[kTile * 128], w0[kTile * 128], w1[kTile * 128];
+    Buffers<kTile> b{{(lds_ptr)x0, (lds_ptr)x1, (lds_ptr)x2}, {(lds_ptr)w0, (lds_ptr)w1}};
+    if constexpr (Tile<kTile>::kWBuffers == 3) {
+        __shared__ __attribute__((aligned(16))) uint8_t w2[kTile * 128];
+        b.w[2] = (lds_ptr)w2;
+    }
+    return b;
+}
 
 // One operand's loads by a wave, kGroups of 1 KB a stage, and its operands.
 // kAcross: stored across k.  kTile rows (columns, if across) from `first` on, of
@@ -251,14 +266,16 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     constexpr int kM = T::kBlocksM, kN = T::kBlocksN, kGroups = T::kGroups, kSteps = 4;
     // Loads go out one after each row of products: first w's of two stages on,
     // from the last step on, when their buffer is free, then x's.  kEarly of
-    // w's are sent before the next stage begins.
+    // w's are sent before the next stage begins.  With three buffers of each
+    // (kDeep) x's, of three stages on, are the first, then w's.
     constexpr int kEarly = kGroups < kM ? kGroups : kM;
+    constexpr bool kDeep = T::kWBuffers == 3;
     static_assert(kGroups <= 15 && 2 * kGroups <= kSteps * kM, "a stage's loads fit its rows of products");
-    // vmcnt (bits 3:0 and 15:14) and lgkmcnt: one stage of x and w's early loads
-    // may stay in flight; one of x, and lgkmcnt(0)
-    constexpr int kFlight = kGroups + kEarly;
+    // vmcnt (bits 3:0 and 15:14) and lgkmcnt: one stage of x (kDeep: of both) and
+    // the early loads may stay in flight; that without these, and lgkmcnt(0)
+    constexpr int kStageFlight = kDeep ? 2 * kGroups : kGroups, kFlight = kStageFlight + kEarly;
     constexpr int kWaitFirst = 0x0F70 | (kFlight & 15) | (kFlight >> 4 << 14);
-    constexpr int kWaitStage = 0x0070 | kGroups;
+    constexpr int kWaitStage = 0x0070 | kStageFlight;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / T::kWavesN, wn = wave % T::kWavesN;
     const int seg = (p.k + kStageK - 1) / kStageK;  // stages of a segment
@@ -309,7 +326,11 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) load_x(i, begin + 1, lds.x[1]);
 #pragma unroll
-    for (int i = 0; i < kEarly; ++i) load_w(i, begin + 1, lds.w[1]);
+    for (int i = 0; i < (kDeep ? kGroups : kEarly); ++i) load_w(i, begin + 1, lds.w[1]);
+    if constexpr (kDeep) {
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i) load_x(i, begin + 2, lds.x[2]);
+    }
     __builtin_amdgcn_s_waitcnt(kWaitFirst);
     barrier();
 #pragma unroll
@@ -320,7 +341,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     // half a step and hold the products at issue).  Before the last step's
     // products, whose operands are in registers, the waves meet, and read the
     // next stage's first operands between them.
-    auto stage = [&](int s, lds_ptr tx, lds_ptr tw, lds_ptr nw, lds_ptr nx2, lds_ptr nx) __attribute__((always_inline)) {
+    auto stage = [&](int s, lds_ptr tx, lds_ptr tw, lds_ptr nw, lds_ptr nx2, lds_ptr nx, lds_ptr nw2) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
             if (ks + 1 == kSteps) {
@@ -340,18 +361,25 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
 #pragma unroll
                 for (int j = 0; j < kN; ++j) acc[i][j] = mfma(fw[ks & 1][j], fx[ks & 1][i], acc[i][j]);
                 const int q = (ks + 1) % kSteps * kM + i;
-                if (q < kGroups)
-                    load_w(q, ks + 1 == kSteps ? s + 2 : s + 1, ks + 1 == kSteps ? tw : nw);
-                else if (q < 2 * kGroups)
-                    load_x(q - kGroups, s + 2, nx2);
+                if constexpr (kDeep) {
+                    if (q < kGroups)
+                        load_x(q, ks + 1 == kSteps ? s + 3 : s + 2, ks + 1 == kSteps ? tx : nx2);
+                    else if (q < 2 * kGroups)
+                        load_w(q - kGroups, s + 2, nw2);
+                } else {
+                    if (q < kGroups)
+                        load_w(q, ks + 1 == kSteps ? s + 2 : s + 1, ks + 1 == kSteps ? tw : nw);
+                    else if (q < 2 * kGroups)
+                        load_x(q - kGroups, s + 2, nx2);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
     // stage u of a group of six
     auto ring = [&](int s, auto number) __attribute__((always_inline)) {
-        constexpr int u = decltype(number)::value;
-        stage(s, lds.x[u % 3], lds.w[u % 2], lds.w[(u + 1) % 2], lds.x[(u + 2) % 3], lds.x[(u + 1) % 3]);
+        constexpr int u = decltype(number)::value, kW = T::kWBuffers;
+        stage(s, lds.x[u % 3], lds.w[u % kW], lds.w[(u + 1) % kW], lds.x[(u + 2) % 3], lds.x[(u + 1) % 3], lds.w[(u + 2) % kW]);
     };
     typedef std::integral_constant<int, 0> U0;
     typedef std::integral_constant<int, 1> U1;
