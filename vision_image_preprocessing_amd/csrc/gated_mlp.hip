@@ -148,8 +148,8 @@ __device__ __forceinline__ int product_of(const MlpArgs &a, int tile) {
 // is 20 stages, 30 us of a tile's 36, and for its first loads and the epilogue the
 // matrix cores wait.  32768 rows with g and u saved 842 to 888 us: 0.86 TFLOP, 1.26
 // GB read and 1.68 written, 3.4 TB/s, in tiles of 256 x 256 (of 128 x 128 952 to
-// 1047, of 64 x 64 1574).  216 rows 15 us, in tiles of 64 x 64 that take 210 MB in
-// from L2 and wait for that.  hidden is read again by the next product, so its
+// 1047, of 64 x 64 1574).  216 rows 15 to 16 us, in tiles of 64 x 64 that take
+// 210 MB in from L2 and wait for that.  hidden is read again by the next product, so its
 // stores stay in the caches (non-temporal ones made the kernel 5% slower).
 template <int kTile, bool kSaved>
 __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs a) {
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_product_kernel(MlpA
 
 // The tiles in parts: their sums in the parts' order, + bias.  32 (8 of 128 x
 // 128, 2 of 64 x 64) workgroups a tile, eight channels a thread.  The sums come
-// from caches: 128 tiles of 256 x 256 in two parts 14 us, 80 of 64 x 64 in twelve 4,
+// from caches: 128 tiles of 256 x 256 in two parts 14 us, 20 of 128 x 128 in twelve 4,
 // a launch's length.
 template <int kTile>
 __global__ __launch_bounds__(256) void mlp_join_kernel(MlpArgs a) {
