@@ -193,6 +193,26 @@ def test_rows_do_not_reach_others(V):
         assert torch.equal(dx2[keep], dx[keep])
 
 
+@pytest.mark.parametrize("rows,d,h", [(37, 64, 200), (1100, 1280, 1288), (14300, 944, 968)])
+def test_infinities_of_the_last_row(V, rows, d, h):
+    """An infinity of dout in the last row makes dg and du of that row infinite,
+    and so the biases' gradients: with u's and silu's sign, not NaN from the
+    rows behind the last one, which are none."""
+    _say("infinities", (rows, d, h))
+    x, w, _, dout = _inputs(rows, d, h, False, 5)
+    xd, gd, wd = _dev(x), _dev(dout), [_dev(t) for t in w]
+    wd[2] = wd[2].abs() + 2.0 ** -6
+    gd[-1, 3] = float("inf")
+    _, gate_up, hidden = V.gated_mlp(xd, *wd, return_saved=True)
+    *_, db_gate, db_up, db_down = V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, bias_grads=True)
+    g, u = (gate_up[i, -1, :h].double() for i in (0, 1))
+    s = torch.sigmoid(g)
+    inf = torch.full_like(g, float("inf"))
+    assert torch.equal(db_gate.double(), torch.copysign(inf, u * s * (1 + g * (1 - s))))
+    assert torch.equal(db_up.double(), torch.copysign(inf, g * s))
+    assert db_down[3] == float("inf") and torch.isfinite(torch.cat([db_down[:3], db_down[4:]])).all()
+
+
 def test_parts_of_the_gradients(V):
     """Only those that are asked for, into tensors that are passed in."""
     _say("parts")

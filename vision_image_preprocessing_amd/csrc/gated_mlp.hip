@@ -256,7 +256,7 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
         float dh[4];
         turned.get(t % kPasses * kPass + lane / kLanes, piece, dh);
         // past the columns dh is any value, and has to be zero for the
-        // padding; past the rows g and u read as zeros, and with them dg and du
+        // padding; past the rows it, g and u are zeros, and with them dg and du
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float s = sigmoid(g[t][j]), d = col + j < p.n ? dh[j] : 0.0f;

@@ -176,7 +176,8 @@ struct Operand {
     // across, rows 8 (n % 8) .. + 7 of k in panel n / 8.  Lane l lands at row l /
     // 8, chunk l % 8 of it, so it fetches the chunk that the swizzle puts there.
     // `rows_from`: what row of the matrix the wave's first row of the tile is
-    // (along); rows past the last one read the last one, and are not stored.
+    // (along); rows past the last one read as zeros (of the last one's values,
+    // an infinity would be multiplied by zeros of what is saved of no row).
     // `at`: the first row (column) of the tile that the wave's operands are of.
     __device__ __forceinline__ Operand(int64_t stride, int64_t first, int64_t count, int64_t rows_from, int at) {
         const int lane = threadIdx.x & 63, l8 = lane >> 3;
@@ -198,8 +199,10 @@ struct Operand {
             base = (at + r) * 128 + (((lane >> 5) ^ ((r ^ ((at + r) >> 3)) & 7)) << 4);
             chunk = ((lane & 7) ^ l8 ^ (wave * kGroups)) & 7;
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-                off[i] = uint32_t(int(min(rows_from + i * 8 + l8, count - 1) - first) * int(stride) + ((chunk ^ i) & 7) * 8) * 2;
+            for (int i = 0; i < kGroups; ++i) {
+                const int64_t row = rows_from + i * 8 + l8;
+                off[i] = row < count ? uint32_t(int(row - first) * int(stride) + ((chunk ^ i) & 7) * 8) * 2 : kOutside;
+            }
         }
     }
 
@@ -284,7 +287,7 @@ __device__ __forceinline__ void multiply(const Product &p, int64_t m0, int n0, i
     // same rows of the two weights; so the rows that a wave loads are of one of
     // them, gate's in even ones
     static_assert(!kGate || kGroups * 8 == T::kWaveN / 2, "a wave loads rows of one of the two");
-    // (a tile may lie in the padding, past every row: it reads the last one)
+    // (a tile may lie in the padding, past every row)
     const int w_first = kGate ? min(n0, p.n - 1) : n0;
     const W w(p.w[0].stride, w_first, p.n, kGate ? n0 + (wave >> 1) * (kGroups * 8) : n0 + wave * (kGroups * 8), wn * T::kWaveN);
     // in registers from here on: a scalar load in the loop would make every
