@@ -380,3 +380,32 @@ def test_refusals(V):
                 lambda: V.gated_mlp_backward(gd, xd, wg, wu, wd, gate_up, hidden, workspace=small)):
         with pytest.raises(V.MimoError):
             bad()
+
+
+@pytest.mark.parametrize("rows,d,h", [(1, 64, 200), (37, 64, 200), (63, 71, 203), (1100, 1280, 1288), (14300, 944, 968)])
+def test_infinities_of_the_weights(V, rows, d, h):
+    """An infinite weight of the product back makes a hidden channel's dh
+    infinite in every row: dg and du are too, all of one sign here, and so are
+    the biases' gradients; the rows behind the last one, which are none, add no
+    zero times infinity to them."""
+    _say("infinite weights", (rows, d, h))
+    x, w, b, dout = _inputs(rows, d, h, True, 17)
+    xd, gd, wd, bd = _dev(x), _dev(dout), [_dev(t) for t in w], [_dev(t) for t in b]
+    wd[2][3, 8], wd[2][5, h - 1] = float("inf"), float("-inf")
+    _, gate_up, hidden = V.gated_mlp(xd, *wd, *bd, return_saved=True)
+    g, u = (gate_up[i, :, :h].double() for i in (0, 1))
+    s = torch.sigmoid(g)
+    one = torch.ones(rows, dtype=torch.bfloat16, device="cuda")
+    gd[:, 3] = torch.copysign(one, (u * s * (1 + g * (1 - s)))[:, 8].float())
+    gd[:, 5] = torch.copysign(one, (g * s)[:, h - 1].float())
+    got = V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, bias_grads=True)
+    db_gate, db_up = got[4], got[5]
+    assert db_gate[8] == float("inf") and db_up[h - 1] == float("-inf")
+    keep = torch.ones(h, dtype=torch.bool, device="cuda")
+    keep[[8, h - 1]] = False
+    assert torch.isfinite(db_gate[keep]).all() and torch.isfinite(db_up[keep]).all()
+    with np.errstate(invalid="ignore"):
+        r = tower.gated_mlp(_wide(xd), *[_wide(t) for t in wd], *[_wide(t) for t in bd], _wide(gd))
+    for name, t in (("db_gate", db_gate), ("db_up", db_up)):
+        want = torch.from_numpy(r[name]).cuda()
+        assert torch.equal(torch.isinf(t), torch.isinf(want)) and torch.equal(torch.isnan(t), torch.isnan(want)), name

@@ -236,6 +236,7 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int piece = (lane % kLanes) * 4, col = n0 + (wave % T::kWavesN) * T::kWaveN + piece;
     const int row = (wave / T::kWavesN) * T::kWaveM + lane / kLanes;
+    const int rows = int(min(p.m - m0, int64_t(kTile)));
     Panel<float> gate(a.gate_up, m0, p.m, kTile, a.ldh, row, kPass, col), up(a.gate_up + p.m * a.ldh, m0, p.m, kTile, a.ldh, row, kPass, col);
     Panel<uint16_t> dgate(a.dgate, m0, p.m, kTile, a.ldh, row, kPass, col), dup(a.dup, m0, p.m, kTile, a.ldh, row, kPass, col);
     float sg[4] = {}, su[4] = {};
@@ -256,10 +257,12 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_dhidden_kernel(MlpA
         float dh[4];
         turned.get(t % kPasses * kPass + lane / kLanes, piece, dh);
         // past the columns dh is any value, and has to be zero for the
-        // padding; past the rows it, g and u are zeros, and with them dg and du
+        // padding; past the rows g and u are zeros, but dh is zeros times the
+        // weights, NaN where one is infinite, and has to be zero for the sums
+        const int columns = row + t * kPass < rows ? p.n : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float s = sigmoid(g[t][j]), d = col + j < p.n ? dh[j] : 0.0f;
+            const float s = sigmoid(g[t][j]), d = col + j < columns ? dh[j] : 0.0f;
             dh[j] = d * u[t][j] * (s * (1.0f + g[t][j] * (1.0f - s)));
             u[t][j] = d * (g[t][j] * s);
             sg[j] += dh[j];
