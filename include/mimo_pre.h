@@ -691,8 +691,10 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
  * ------------------------------------------------------------------------ */
 
 /*
- * Forward, one kernel launch; float32 inside, out rounded once.  Where a row's
- * sum of squares passes float32's range (no values below 2^56 do) rstd is 0.
+ * Forward, one kernel launch; float32 inside, out rounded once.  Rows of any
+ * finite values, whether float32 holds their squares or not; rstd itself is
+ * float32: infinite where mean h^2 + eps is below 2^-256 (a row of zeros with
+ * eps 0), and of fewer bits where it is above 2^252.
  *   width    in [1, 65536].
  *   x        device, x_dtype (MIMO_F32 or MIMO_BF16).
  *   residual device, residual_dtype (x_dtype or MIMO_F32), or NULL.

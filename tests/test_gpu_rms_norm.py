@@ -363,3 +363,39 @@ def test_refusals(V):
                 lambda: V.rms_norm(torch.zeros((2, 65537), device="cuda"))):
         with pytest.raises(V.MimoError):
             bad()
+
+
+@pytest.mark.parametrize("width", [8, 509, 1280, 1283, 5120, 8193, 16384, 20001])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-60])
+def test_small_and_large_rows(V, width, eps):
+    """Rows whose squares pass float32's range on either side, as eps allows
+    them: rstd, out and the gradients are the formula's, and the 8-bit form's
+    integers too.  The bars are relative, so they hold at any power of two that
+    rstd and the gradients can be held at.  Gradients of the largest rows are
+    not: below 2^-126 a type's steps stay what they are there, 2^-149 in float32
+    and 2^-133 in bf16, and a rounding is off by half of one at most (the float64
+    gradient rounded to bf16 alone is 3.8 of the relative bars away at width
+    509, in the row of 2^120), so dx has these halves in its bar."""
+    _say("small and large rows", width, eps)
+    x, _, dout, _, w = _inputs(12, width, "f32", None, "f32", True, seed=width)
+    powers = [-120, -110, -100, -80, -70, -60, -50, 0, 60, 70, 100, 120]
+    x = x * torch.tensor([2.0 ** p for p in powers])[:, None]
+    for kind in ("f32", "bf16"):
+        xk, gk = x.to(KIND[kind]), dout.to(KIND[kind])
+        r = tower.rms_norm(_wide(xk), _wide(w), eps, _wide(gk))
+        xd, gd, wd = _dev(xk, gk, w)
+        rel, out_rel, dx_bar, dw_bar = _bars(r, _wide(gk), 12, width)
+        out, rstd = V.rms_norm(xd, wd, eps=eps, return_rstd=True)
+        assert (np.abs(_wide(rstd) / r["rstd"] - 1) <= rel + EPS).all()
+        _within(out, r["out"], (out_rel + ROUND[xk.dtype]) * np.abs(r["out"]), "out")
+        # with a residual of zeros the sum is x, and a float32 stream's rows go the same way
+        two = V.rms_norm(xd, wd, torch.zeros_like(xd, dtype=torch.float32), eps=eps, out_dtype="f32", return_rstd=True)
+        assert torch.equal(two[1], xd.float()) and torch.equal(two[2], rstd)
+        dx, dw = V.rms_norm_backward(gd, xd, rstd, wd)
+        unit = 1 / r["rstd"][:, None]  # a row's gradients next to one
+        step = 2.0 ** -150 + (2.0 ** -134 if kind == "bf16" else 0.0)
+        _within(dx.double().cpu() * torch.from_numpy(unit), r["dx"] * unit, (dx_bar + ROUND[dx.dtype] * np.abs(r["dx"]) + step) * unit, "dx")
+        _within(dw, r["dweight"], dw_bar + EPS * np.abs(r["dweight"]), "dweight")
+        q, scale = tower.rms_norm_quantized(_wide(xk), _wide(w), eps)
+        got_q, got_scale = V.rms_norm_quantized(xd, wd, eps=eps)
+        assert np.array_equal(got_q[:, :width].cpu().numpy(), q) and np.array_equal(got_scale.cpu().numpy(), scale)
