@@ -399,3 +399,31 @@ def test_small_and_large_rows(V, width, eps):
         q, scale = tower.rms_norm_quantized(_wide(xk), _wide(w), eps)
         got_q, got_scale = V.rms_norm_quantized(xd, wd, eps=eps)
         assert np.array_equal(got_q[:, :width].cpu().numpy(), q) and np.array_equal(got_scale.cpu().numpy(), scale)
+
+
+def test_quantized_norm_and_product_from_its_definition(V):
+    """Norm to 8 bits and product, as a projection uses them, from the
+    definition's integers and scales of the rounded sum; and next to the norm in
+    float32 whose rows are quantised by a call of their own, whose rstd may
+    differ in its last bits: no integer is more than one away, and only those
+    whose quotient lies next to the middle of two are."""
+    _say("norm, integers and product")
+    x, res, _, _, w = _inputs(300, 1283, "bf16", "bf16", "bf16", True, 15)
+    xd, rd, wd = _dev(x, res, w)
+    wq, ws = V.quantize_rows(torch.randn((640, 1283), generator=torch.Generator().manual_seed(16)).cuda())
+    got = V.quantized_linear(*V.rms_norm_quantized(xd, wd, rd)[:2], wq, ws)
+    q, s = tower.rms_norm_quantized(_wide(_h(x, res)), _wide(w), 1e-6)
+    padded = np.zeros((300, wq.shape[1]), dtype=np.int8)
+    padded[:, :1283] = q
+    ref, mag = tower.quantized_linear(padded, s, wq.cpu().numpy(), ws.cpu().numpy())
+    _within(got, ref, (2.0 ** -8 + 4 * EPS) * np.abs(ref) + 4 * EPS * mag, "product")
+    y = V.rms_norm(xd, wd, rd, out_dtype="f32")[0]
+    q2, s2 = V.quantize_rows(y)
+    r = tower.rms_norm(_wide(_h(x, res)), _wide(w), 1e-6)["out"]
+    # relative to a value: rstd's bar and the products' roundings of both forms; a scale's holds the division's too
+    rel = 2 * ((1283 / 64 + 20) * EPS / 2 + 12 * EPS)
+    assert (np.abs(_wide(s2) - s.astype(np.float64)) <= rel * s).all()
+    apart = np.abs(q2[:, :1283].cpu().numpy().astype(int) - q.astype(int))
+    quotient = np.abs(r) / s.astype(np.float64)[:, None]
+    middle = np.abs(quotient - np.floor(quotient) - 0.5)
+    assert apart.max() <= 1 and (middle[apart > 0] <= 2 * rel * 128).all() and not q2[:, 1283:].any()
