@@ -768,8 +768,9 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
  *   heads    in [1, 65536].
  *   head_dim a multiple of 8 in [8, 2 * MIMO_ROPE_DIM_MAX].
  *   x, out   bf16, as mimo_chunk_attention takes them; out may be x with x's
- *            strides, and otherwise must not overlap it.
- *   cos, sin device float32 [rows][half], 16-byte aligned.
+ *            strides, and otherwise must not overlap it: heads of one array next
+ *            to each other, with one row stride, are fine.
+ *   cos, sin device float32 [rows][half], 16-byte aligned, not among out's rows.
  * One kernel launch.  Returns MIMO_OK, MIMO_E_INVALID, MIMO_E_TOO_LARGE or MIMO_E_HIP.
  */
 int mimo_rotate_heads(int64_t rows, int32_t heads, int32_t head_dim, const mimo_heads *x, const float *cos, const float *sin,

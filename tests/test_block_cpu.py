@@ -174,3 +174,75 @@ def test_mlp_backward_refuses():
 
 def test_mlp_structs_are_as_the_header_lays_them_out():
     assert V.tower._MLP.size == 16 + 9 * 8 and V.tower._MLP_GRADS.size == 8 * 8
+
+
+def _overlap_refused(rows, n, d, x, out):
+    """Whether the rotation refuses (base, row stride, head stride), in values,
+    for where they lie: looked at before the tables, which are missing here, so
+    that no call gets further."""
+    pack = lambda t: struct.pack("<Qqq", P + 2 * t[0], t[1], t[2])
+    assert V.load().mimo_rotate_heads(rows, n, d, pack(x), None, None, 0, pack(out), None) == V.MIMO_E_INVALID
+    message = V.last_error()
+    assert "overlap" in message or "cos and sin" in message, message
+    return "overlap" in message
+
+
+def test_rotation_refuses_out_that_overlaps_x_in_part():
+    """Eight heads further in the same rows is written over what others read;
+    the heads behind x's, in x's rows, are not."""
+    row = 48 * 64
+    for shift, refused in ((8, True), (16, True), (40, False), (-8, True)):
+        assert _overlap_refused(1001, 40 if shift != 40 else 8, 64, (1 << 20, row, 64), ((1 << 20) + shift * 64, row, 64)) == refused
+    assert not _overlap_refused(1001, 8, 64, (40 * 64, row, 64), (0, row, 64))
+    # the next rows of one array; a head's halves
+    assert _overlap_refused(100, 4, 64, (0, 256, 64), (256, 256, 64)) and not _overlap_refused(100, 4, 64, (0, 256, 64), (25600, 256, 64))
+    assert _overlap_refused(1, 1, 64, (0, 64, 64), (8, 64, 64)) and not _overlap_refused(1, 1, 64, (0, 64, 64), (64, 64, 64))
+    # one head, read again and again, and the heads behind it; every second head
+    assert not _overlap_refused(100, 4, 64, (0, 320, 0), (64, 320, 64)) and _overlap_refused(100, 4, 64, (64, 320, 0), (64 * 2 - 8, 320, 64))
+    assert not _overlap_refused(100, 4, 64, (0, 1024, 128), (64, 1024, 128)) and not _overlap_refused(9, 4, 64, (0, 1024, 128), (512, 1024, 64))
+
+
+def test_rotation_tells_what_overlaps():
+    """Small tensors at every kind of place in one array, against the sets of
+    their values: none that overlaps passes, and of those with one row stride
+    whose heads lie within it, or that have one head stride too, none that does
+    not is refused."""
+    import random
+
+    rng = random.Random(5)
+    told = 0
+    for _ in range(6000):
+        rows, n, d = rng.randint(1, 4), rng.randint(1, 4), rng.choice([8, 16])
+        strides = []
+        for _ in range(2):
+            head = 8 * rng.randint(d // 8, 6)
+            turned = rng.random() < 0.3
+            row = 8 * rng.randint(d // 8, 30)
+            if turned:
+                head = (rows - 1) * row + d + 8 * rng.randint(0, 12)
+            else:
+                row = max(row, (n - 1) * head + d)
+            strides.append((row, head))
+        if rng.random() < 0.7:
+            strides[0] = strides[1] if rng.random() < 0.5 else (strides[1][0], strides[0][1])
+        if rng.random() < 0.2:
+            strides[0] = (strides[0][0], 0)
+        x, out = (512, *strides[0]), (512 + 8 * rng.randint(-60, 60), *strides[1])
+        if x[0] == out[0]:
+            continue
+        values = [{t[0] + r * t[1] + h * t[2] + i for r in range(rows) for h in range(n) for i in range(d)} for t in (x, out)]
+        meet = bool(values[0] & values[1])
+        refused = _overlap_refused(rows, n, d, x, out)
+        assert refused or not meet, (rows, n, d, x, out)
+        inside = all((n - 1) * t[2] + d <= t[1] for t in (x, out))
+        if rows == 1 or (x[1] == out[1] and (inside or n == 1 or x[2] == out[2])):
+            assert refused == meet, (rows, n, d, x, out)
+            told += not meet
+    assert told > 300
+
+
+def test_rotation_refuses_tables_among_the_outputs():
+    heads = lambda p: struct.pack("<Qqq", p, 256, 64)
+    for cos, sin in ((4 * P, 3 * P), (2 * P, 4 * P + 16), (4 * P - 1264, 3 * P)):
+        assert V.load().mimo_rotate_heads(10, 4, 64, heads(P), cos, sin, 0, heads(4 * P), None) == V.MIMO_E_INVALID
+        assert V.last_error().startswith("rotate_heads: cos and sin must not lie")

@@ -159,3 +159,28 @@ def test_refusals(V):
                 lambda: V.rotate_heads(x, cos, sin, out=torch.as_strided(x, (4, 3, 64), (64, 256, 1)))):
         with pytest.raises(V.MimoError):
             bad()
+
+
+def test_into_other_heads_of_the_same_array(V):
+    """Heads next to each other in the rows of one array are no overlap; heads
+    that are, in part, those that are read are refused, and nothing is written."""
+    _say("one array")
+    rows, d = 500, 64
+    qkv = _noise((rows, 24, d), 14)
+    cos, sin = _tables(rows, d // 2, 15)
+    want = V.rotate_heads(qkv[:, :8], cos, sin)
+    kept = qkv.clone()
+    with pytest.raises(V.MimoError, match="overlap"):
+        V.rotate_heads(qkv[:, :16], cos, sin, out=qkv[:, 8:])
+    with pytest.raises(V.MimoError, match="overlap"):
+        V.rotate_heads(qkv[:-1], cos[:-1], sin[:-1], out=qkv[1:])
+    assert torch.equal(qkv, kept)
+    V.rotate_heads(qkv[:, :8], cos, sin, out=qkv[:, 16:])
+    assert torch.equal(qkv[:, 16:], want) and torch.equal(qkv[:, :16], kept[:, :16])
+    # every second head to the one behind it
+    qkv[:, 0:16:2] = kept[:, :8]
+    V.rotate_heads(qkv[:, 0:16:2], cos, sin, out=qkv[:, 1:16:2])
+    assert torch.equal(qkv[:, 1:16:2], want) and torch.equal(qkv[:, 0:16:2], kept[:, :8])
+    # the first rows of an array to its last ones
+    V.rotate_heads(kept[:100], cos[:100], sin[:100], out=kept[400:])
+    assert torch.equal(kept[400:, :8], want[:100])

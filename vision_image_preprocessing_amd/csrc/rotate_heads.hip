@@ -105,6 +105,52 @@ bool heads_ok(const mimo_heads *t, int64_t rows, int32_t heads, int32_t head_dim
            t->head_stride >= (rows - 1) * t->row_stride + head_dim;
 }
 
+// Whether two rows of heads, the second `offset` values behind the first, share
+// a value: both by ascending addresses, going on from whichever head is behind.
+bool rows_meet(int64_t offset, int64_t x_head, int64_t out_head, int32_t heads, int32_t head_dim) {
+    for (int32_t i = 0, j = 0; i < heads && j < heads;) {
+        const int64_t apart = offset + j * out_head - i * x_head;
+        if (apart > -head_dim && apart < head_dim) return true;
+        if (apart > 0)
+            ++i;
+        else
+            ++j;
+    }
+    return false;
+}
+
+// Whether a value of out lies where one of x does: waves would write heads that
+// others, or their own next pass, still read.  Tensors that are apart, and those
+// of one row stride that go through one array side by side (heads of one
+// projection's output), are told apart; others that go through the same
+// addresses are taken to meet.
+bool heads_meet(const mimo_heads &x, const mimo_heads &out, int64_t rows, int32_t heads, int32_t head_dim) {
+    const int64_t delta = (reinterpret_cast<intptr_t>(out.data) - reinterpret_cast<intptr_t>(x.data)) / 2;
+    const int64_t x_span = (heads - 1) * x.head_stride + head_dim, out_span = (heads - 1) * out.head_stride + head_dim;  // of a row
+    if (delta >= (rows - 1) * x.row_stride + x_span || -delta >= (rows - 1) * out.row_stride + out_span) return false;
+    if (rows == 1) return rows_meet(delta, x.head_stride, out.head_stride, heads, head_dim);
+    const int64_t stride = x.row_stride;
+    if (out.row_stride != stride) return true;
+    // rows of out from here on lie `behind` behind a row of x, `shift` rows on
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    if (x_span <= stride && out_span <= stride) {
+        const int64_t shift = floor_div(delta, stride), behind = delta - shift * stride;
+        auto exists = [&](int64_t s) { return s > -rows && s < rows; };
+        return (exists(shift) && rows_meet(behind, x.head_stride, out.head_stride, heads, head_dim)) ||
+               (exists(shift + 1) && rows_meet(behind - stride, x.head_stride, out.head_stride, heads, head_dim));
+    }
+    if (heads > 1 && out.head_stride != x.head_stride) return true;
+    // heads as far from each other in both: any two of them, by how many heads apart, with the nearest rows
+    for (int64_t apart = 1 - heads; apart < heads; ++apart) {
+        const int64_t at = delta + apart * x.head_stride, near = floor_div(at, stride);
+        for (int64_t s = near; s <= near + 1; ++s) {
+            const int64_t k = s < 1 - rows ? 1 - rows : s > rows - 1 ? rows - 1 : s, left = at - k * stride;
+            if (left > -head_dim && left < head_dim) return true;
+        }
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace mimo
 
@@ -123,10 +169,15 @@ int mimo_rotate_heads(int64_t rows, int32_t heads, int32_t head_dim, const mimo_
     if (!heads_ok(x, rows, heads, head_dim, false) || !heads_ok(out, rows, heads, head_dim, true))
         return set_error(MIMO_E_INVALID, "rotate_heads: x and out must be non-null and 16-byte aligned, their strides multiples of 8 "
                                          "(row_stride in [head_dim, 2^22], head_stride >= 0), out's rows and heads apart");
-    if (!cos || !sin || !check_ptr_align(cos, 16) || !check_ptr_align(sin, 16))
-        return set_error(MIMO_E_INVALID, "rotate_heads: cos and sin must be non-null and 16-byte aligned");
     if (out->data == x->data && ((rows > 1 && out->row_stride != x->row_stride) || (heads > 1 && out->head_stride != x->head_stride)))
         return set_error(MIMO_E_INVALID, "rotate_heads: out may be x only with x's strides");
+    if (out->data != x->data && heads_meet(*x, *out, rows, heads, head_dim))
+        return set_error(MIMO_E_INVALID, "rotate_heads: out must not overlap x, unless it is x");
+    if (!cos || !sin || !check_ptr_align(cos, 16) || !check_ptr_align(sin, 16))
+        return set_error(MIMO_E_INVALID, "rotate_heads: cos and sin must be non-null and 16-byte aligned");
+    const int64_t out_bytes = ((rows - 1) * out->row_stride + (heads - 1) * out->head_stride + head_dim) * 2, table_bytes = rows * head_dim * 2;
+    if (arrays_meet(cos, table_bytes, out->data, out_bytes) || arrays_meet(sin, table_bytes, out->data, out_bytes))
+        return set_error(MIMO_E_INVALID, "rotate_heads: cos and sin must not lie among out's rows");
     RotateArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = static_cast<const uint16_t *>(x->data);

@@ -38,4 +38,10 @@ inline int check_ptr_align(const void *p, uintptr_t align) {
     return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0;
 }
 
+// Whether two arrays, of so many bytes each, share one.
+inline bool arrays_meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + uintptr_t(b_bytes) && q < p + uintptr_t(a_bytes);
+}
+
 }  // namespace mimo
