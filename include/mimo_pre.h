@@ -687,7 +687,9 @@ int mimo_quantized_linear(int64_t n_rows, int32_t k, const void *xq, const float
  *   rstd = 1 / sqrt(sum h^2 / n + eps),  y = h rstd weight
  * The norm is that of the rounded h, which the backward pass is given.  Rows
  * are dense [rows][width]; those of a width that is a multiple of 8 at 16-byte
- * aligned addresses run fastest.  No output may be the weight.
+ * aligned addresses run fastest.  No output may be the weight; where an output
+ * may be another argument, it is the whole of it: none may overlap an argument in
+ * part, nor the workspace any.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -246,3 +246,27 @@ def test_rotation_refuses_tables_among_the_outputs():
     for cos, sin in ((4 * P, 3 * P), (2 * P, 4 * P + 16), (4 * P - 1264, 3 * P)):
         assert V.load().mimo_rotate_heads(10, 4, 64, heads(P), cos, sin, 0, heads(4 * P), None) == V.MIMO_E_INVALID
         assert V.last_error().startswith("rotate_heads: cos and sin must not lie")
+
+
+def test_norm_refuses_arrays_that_overlap_in_part():
+    """4 rows of 64 float32 values are 1024 bytes, the weight 256, rstd and
+    scale 16, 8-bit rows 512: one more or one less address further."""
+    for bad in (dict(out=P + 4), dict(out=P - 1020), dict(out=2 * P + 1020), dict(out=3 * P - 1020), dict(out=3 * P + 252), dict(out=4 * P + 1020),
+                dict(out=6 * P - 1020), dict(h=P + 4), dict(h=2 * P + 512), dict(h=3 * P + 252), dict(rstd=P + 1020), dict(rstd=2 * P - 12),
+                dict(rstd=3 * P + 252), dict(rstd=4 * P + 4), dict(rstd=5 * P - 12), dict(xd=B, rd=B, od=B, out=P + 510)):
+        assert _forward(**bad) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm:"), bad
+        assert "in part" in V.last_error()
+    for bad in (dict(q=P + 16), dict(q=2 * P - 496), dict(q=3 * P + 240), dict(q=4 * P + 1008), dict(h=P + 4), dict(h=3 * P - 4), dict(s=P + 1020),
+                dict(s=2 * P + 4), dict(s=3 * P + 252), dict(s=4 * P - 12), dict(s=5 * P + 508), dict(xd=B, rd=B, q=2 * P + 496)):
+        assert _quantized(**bad) == V.MIMO_E_INVALID and V.last_error().startswith("rms_norm_quantized:"), bad
+        assert "in part" in V.last_error()
+    need = V.rms_norm_workspace_bytes(4, 64)
+
+    def backward(h=P, g=2 * P, w=3 * P, rstd=4 * P, dr=5 * P, dx=6 * P, dw=7 * P, ws=8 * P):
+        return V.load().mimo_rms_norm_backward(4, 64, h, F, g, F, w, rstd, dr, dx, dw, ws, need, None)
+
+    for bad in (dict(dx=P + 4), dict(dx=2 * P - 1020), dict(dx=3 * P + 252), dict(dx=4 * P + 12), dict(dx=5 * P + 4), dict(dx=7 * P - 1020),
+                dict(dw=P + 1020), dict(dw=2 * P + 4), dict(dw=3 * P + 4), dict(dw=4 * P - 252), dict(dw=5 * P + 1020), dict(dw=6 * P + 512)):
+        assert backward(**bad) == V.MIMO_E_INVALID and "in part" in V.last_error(), bad
+    for at in (P, P + 1008, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P + 512, 7 * P):
+        assert backward(ws=at) == V.MIMO_E_INVALID and "workspace" in V.last_error(), at

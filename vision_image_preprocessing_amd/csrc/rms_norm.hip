@@ -539,6 +539,11 @@ int mimo_rms_norm(int64_t rows, int32_t width, const void *x, int32_t x_dtype, c
         return set_error(MIMO_E_INVALID, "rms_norm: rstd must not be an input or another output");
     if ((out == x && out_dtype != x_dtype) || (residual && out == residual && out_dtype != residual_dtype))
         return set_error(MIMO_E_INVALID, "rms_norm: out may be x or the residual only in its dtype");
+    const int64_t values = rows * width;
+    const int res_size = residual ? size_of(residual_dtype) : 0;
+    if (overlap_in_part({{out, values * size_of(out_dtype)}, {residual ? residual_out : nullptr, values * res_size}, {rstd, rows * 4}},
+                        {{x, values * size_of(x_dtype)}, {residual, values * res_size}, {weight, width * 4}}))
+        return set_error(MIMO_E_INVALID, "rms_norm: an output must not overlap an input or another output in part");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, out);
     a.rstd = rstd;
     const Shape shape = forward_shape(width, all_aligned(a));
@@ -568,6 +573,11 @@ int mimo_rms_norm_quantized(int64_t rows, int32_t width, const void *x, int32_t 
         return set_error(MIMO_E_INVALID, "rms_norm_quantized: no output may be the weight");
     if (is_one_of(scale, x, residual, residual ? residual_out : nullptr, q))
         return set_error(MIMO_E_INVALID, "rms_norm_quantized: scale must not be an input or another output");
+    const int64_t values = rows * width;
+    const int res_size = residual ? size_of(residual_dtype) : 0;
+    if (overlap_in_part({{q, rows * ((width + kPad - 1) / kPad * kPad)}, {residual ? residual_out : nullptr, values * res_size}, {scale, rows * 4}},
+                        {{x, values * size_of(x_dtype)}, {residual, values * res_size}, {weight, width * 4}}))
+        return set_error(MIMO_E_INVALID, "rms_norm_quantized: an output must not overlap an input or another output in part");
     RmsArgs a = forward_args(rows, width, x, residual, weight, eps, residual_out, q);
     a.scale = scale;
     const Shape shape = forward_shape(width, all_aligned(a));
@@ -607,6 +617,13 @@ int mimo_rms_norm_backward(int64_t rows, int32_t width, const void *h, int32_t h
         if (dweight && (dweight == weight || dweight == rstd || is_one_of(dweight, h, dout, dresidual, dx)))
             return set_error(MIMO_E_INVALID, "rms_norm_backward: dweight must not be an input, nor dx");
         if (dx == weight || dx == rstd) return set_error(MIMO_E_INVALID, "rms_norm_backward: dx must not be the weight or rstd");
+        const int64_t h_bytes = rows * width * size_of(h_dtype);
+        const Span made_x{dx, h_bytes}, made_w{dweight, width * 4}, in_h{h, h_bytes}, in_g{dout, rows * width * size_of(dout_dtype)},
+            in_w{weight, width * 4}, in_rstd{rstd, rows * 4}, in_res{dresidual, h_bytes};
+        if (overlap_in_part({made_x, made_w}, {in_h, in_g, in_w, in_rstd, in_res}))
+            return set_error(MIMO_E_INVALID, "rms_norm_backward: a gradient must not overlap an input or the other one in part");
+        if (dweight && overlaps_any({workspace, int64_t(mimo_rms_norm_workspace_bytes(rows, width))}, {made_x, made_w, in_h, in_g, in_w, in_rstd, in_res}))
+            return set_error(MIMO_E_INVALID, "rms_norm_backward: workspace must not overlap another argument");
     }
     RmsArgs a;
     std::memset(&a, 0, sizeof(a));

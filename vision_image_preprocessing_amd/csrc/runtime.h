@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "internal.h"
 
@@ -41,7 +42,32 @@ inline int check_ptr_align(const void *p, uintptr_t align) {
 // Whether two arrays, of so many bytes each, share one.
 inline bool arrays_meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-    return p < q + uintptr_t(b_bytes) && q < p + uintptr_t(a_bytes);
+    return a_bytes > 0 && b_bytes > 0 && p < q + uintptr_t(b_bytes) && q < p + uintptr_t(a_bytes);
+}
+
+// A dense array of a call's arguments, or none (null).
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+// Whether one that is written shares bytes with another that is, or with one
+// that is read, without beginning where that begins (some may be the same
+// array; who may is for the caller to say).
+inline bool overlap_in_part(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span *w = written.begin(); w != written.end(); ++w) {
+        if (!w->p) continue;
+        for (const Span *o = written.begin(); o != w; ++o)
+            if (o->p && o->p != w->p && arrays_meet(o->p, o->bytes, w->p, w->bytes)) return true;
+        for (const Span &r : read)
+            if (r.p && r.p != w->p && arrays_meet(r.p, r.bytes, w->p, w->bytes)) return true;
+    }
+    return false;
+}
+// Whether `space` shares bytes with one of the others.
+inline bool overlaps_any(const Span &space, std::initializer_list<Span> others) {
+    for (const Span &o : others)
+        if (o.p && arrays_meet(o.p, o.bytes, space.p, space.bytes)) return true;
+    return false;
 }
 
 }  // namespace mimo
