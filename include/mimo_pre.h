@@ -787,7 +787,8 @@ int mimo_rotate_heads(int64_t rows, int32_t heads, int32_t head_dim, const mimo_
  * Runs on the matrix cores in bf16; sums are float32, h and the gradients dg
  * and du are rounded to bf16 as operands of the next product, outputs once.
  * Results do not depend on how calls run next to each other (no atomics); how
- * sums are split depends on the sizes alone.
+ * sums are split depends on the sizes alone.  What is written, the workspace
+ * included, must not overlap any other argument.
  * ------------------------------------------------------------------------ */
 
 /* Matrices are dense, on the device, 16-byte aligned, bf16 unless said.  Widths

@@ -270,3 +270,31 @@ def test_norm_refuses_arrays_that_overlap_in_part():
         assert backward(**bad) == V.MIMO_E_INVALID and "in part" in V.last_error(), bad
     for at in (P, P + 1008, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P + 512, 7 * P):
         assert backward(ws=at) == V.MIMO_E_INVALID and "workspace" in V.last_error(), at
+
+
+def test_mlp_refuses_arrays_that_overlap_in_part():
+    """x, out, dout and dx are 512 bytes, the weights 9216, gate's and up's
+    biases 288 and down's 256, hidden 1024, gate_up 4096."""
+    lib = V.load()
+    need = V.gated_mlp_workspace_bytes(4, 64, 72)
+
+    def forward(out=10 * P, ws=20 * P, **kw):
+        return lib.mimo_gated_mlp(_mlp(**kw), out, ws, need, None)
+
+    for bad in (dict(out=P + 496), dict(out=2 * P + 9200), dict(out=3 * P - 496), dict(out=4 * P + 16), dict(out=5 * P + 272), dict(out=6 * P + 16),
+                dict(out=7 * P + 240), dict(out=8 * P + 4080), dict(out=9 * P + 1008), dict(h=P + 16), dict(h=8 * P + 2048), dict(gu=4 * P - 16),
+                dict(gu=9 * P - 4080), dict(gu=7 * P + 240)):
+        assert forward(**bad) == V.MIMO_E_INVALID and "in part" in V.last_error(), bad
+    for at in (P, 2 * P + 9200, 3 * P, 4 * P, 5 * P, 6 * P, 7 * P + 240, 8 * P, 9 * P, 10 * P + 496, 10 * P - need + 16):
+        assert forward(ws=at) == V.MIMO_E_INVALID and "workspace" in V.last_error(), at
+    need = V.gated_mlp_backward_workspace_bytes(4, 64, 72)
+
+    def backward(args=None, ws=20 * P, **kw):
+        return lib.mimo_gated_mlp_backward(_mlp(**(args or {})), _mlp_grads(**kw), ws, need, None)
+
+    for bad in (dict(dx=P + 496), dict(dx=11 * P - 496), dict(dx=13 * P + 9200), dict(dwg=2 * P + 9200), dict(dwu=3 * P - 16), dict(dwd=4 * P + 16),
+                dict(dwd=9 * P + 1008), dict(dwg=8 * P + 4080), dict(dbg=16 * P + 4, dbu=16 * P), dict(dbu=12 * P + 508), dict(dbd=15 * P + 9212),
+                dict(dbd=11 * P + 4)):
+        assert backward(**bad) == V.MIMO_E_INVALID and "in part" in V.last_error(), bad
+    for at in (P, 2 * P, 3 * P, 4 * P, 8 * P, 9 * P, 11 * P, 12 * P, 13 * P + 9200, 14 * P, 15 * P, 16 * P, 17 * P, 18 * P + 240, 18 * P - need + 16):
+        assert backward(ws=at) == V.MIMO_E_INVALID and "workspace" in V.last_error(), at

@@ -864,6 +864,14 @@ int mimo_gated_mlp(const mimo_mlp *args, void *out, void *workspace, size_t work
     const ForwardSpace space(z, down, workspace);
     if (workspace_bytes < space.bytes)
         return set_error(MIMO_E_CAPACITY, "gated_mlp: workspace smaller than mimo_gated_mlp_workspace_bytes");
+    const int64_t x_bytes = z.rows * z.d * 2, w_bytes = z.h * z.d * 2, h_bytes = z.rows * z.hp * 2;
+    const Span made_out{out, x_bytes}, made_gu{args->gate_up, 4 * h_bytes}, made_h{args->hidden, h_bytes}, in_x{args->x, x_bytes},
+        in_wg{args->w_gate, w_bytes}, in_wu{args->w_up, w_bytes}, in_wd{args->w_down, w_bytes}, in_bg{args->b_gate, z.h * 4},
+        in_bu{args->b_up, z.h * 4}, in_bd{args->b_down, z.d * 4};
+    if (overlap_in_part({made_out, made_gu, made_h}, {in_x, in_wg, in_wu, in_wd, in_bg, in_bu, in_bd}))
+        return set_error(MIMO_E_INVALID, "gated_mlp: out, gate_up and hidden must not overlap inputs or each other in part");
+    if (overlaps_any({workspace, int64_t(space.bytes)}, {made_out, made_gu, made_h, in_x, in_wg, in_wu, in_wd, in_bg, in_bu, in_bd}))
+        return set_error(MIMO_E_INVALID, "gated_mlp: workspace must not overlap another argument");
     hipStream_t s = static_cast<hipStream_t>(stream);
     int launches = 0;
     const void *x = args->x, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
@@ -954,6 +962,17 @@ int mimo_gated_mlp_backward(const mimo_mlp *args, const mimo_mlp_grads *grads, v
     const BackwardSpace space(z, dhidden, dx, workspace);
     if (workspace_bytes < space.bytes)
         return set_error(MIMO_E_CAPACITY, "gated_mlp_backward: workspace smaller than mimo_gated_mlp_backward_workspace_bytes");
+    const int64_t x_bytes = z.rows * z.d * 2, w_bytes = z.h * z.d * 2, h_bytes = z.rows * z.hp * 2;
+    const Span dx_made{grads->dx, x_bytes}, dwg_made{grads->dw_gate, w_bytes}, dwu_made{grads->dw_up, w_bytes}, dwd_made{grads->dw_down, w_bytes},
+        dbg_made{grads->db_gate, z.h * 4}, dbu_made{grads->db_up, z.h * 4}, dbd_made{grads->db_down, z.d * 4};
+    const int64_t some = z.rows > 0;  // without rows nothing is read
+    const Span in_x{args->x, some * x_bytes}, in_wg{args->w_gate, some * w_bytes}, in_wu{args->w_up, some * w_bytes}, in_wd{args->w_down, some * w_bytes},
+        in_g{grads->dout, some * x_bytes}, in_gu{args->gate_up, some * 4 * h_bytes}, in_h{args->hidden, some * h_bytes};
+    if (overlap_in_part({dx_made, dwg_made, dwu_made, dwd_made, dbg_made, dbu_made, dbd_made}, {in_x, in_wg, in_wu, in_wd, in_g, in_gu, in_h}))
+        return set_error(MIMO_E_INVALID, "gated_mlp_backward: a gradient must not overlap an input or another one in part");
+    if (overlaps_any({workspace, int64_t(space.bytes)}, {dx_made, dwg_made, dwu_made, dwd_made, dbg_made, dbu_made, dbd_made, in_x, in_wg, in_wu, in_wd,
+                                                         in_g, in_gu, in_h}))
+        return set_error(MIMO_E_INVALID, "gated_mlp_backward: workspace must not overlap another argument");
     hipStream_t s = static_cast<hipStream_t>(stream);
     int launches = 0;
     const void *x = args->x, *dout = grads->dout, *wg = args->w_gate, *wu = args->w_up, *wd = args->w_down;
