@@ -21,6 +21,7 @@ silu by 2 e at most.
 import numpy as np
 import pytest
 
+import mlp_tiles
 from oracle import tower
 
 torch = pytest.importorskip("torch")
@@ -409,3 +410,10 @@ def test_infinities_of_the_weights(V, rows, d, h):
     for name, t in (("db_gate", db_gate), ("db_up", db_up)):
         want = torch.from_numpy(r[name]).cuda()
         assert torch.equal(torch.isinf(t), torch.isinf(want)) and torch.equal(torch.isnan(t), torch.isnan(want)), name
+
+
+@pytest.mark.parametrize("rows,d,h", mlp_tiles.SIZES)
+def test_whole_tiles_next_to_parts(V, rows, d, h):
+    """Launches of whole tiles and, behind them, tiles in parts of K: of one
+    product, and of the three weights' gradients, at each tile size."""
+    _check(V, rows, d, h, True, 13)
