@@ -417,3 +417,28 @@ def test_whole_tiles_next_to_parts(V, rows, d, h):
     """Launches of whole tiles and, behind them, tiles in parts of K: of one
     product, and of the three weights' gradients, at each tile size."""
     _check(V, rows, d, h, True, 13)
+
+
+def test_each_gradient_against_differences(V):
+    """Each tensor's gradient along the signs of the oracle's, against the
+    central difference of the loss in float64: off by that gradient's own bars,
+    and by the step squared times the loss's third derivative (relative to the
+    first, the square of what a step of one moves g by, some 50: 3e-7 at most for
+    a step of 1e-4 and a direction of the tensor's size).  The bar is far below
+    the slope, so a gradient that is missing, halved or of the wrong sign shows."""
+    _say("differences, one by one")
+    x, w, b, dout = _inputs(20, 40, 72, True, 21)
+    wide = [_wide(t) for t in (x, *w, *b)]
+    gw = _wide(dout)
+    dev = [_dev(t) for t in (x, *w, *b)]
+    _, gate_up, hidden = V.gated_mlp(*dev, return_saved=True)
+    got = V.gated_mlp_backward(_dev(dout), *dev[:4], gate_up, hidden, bias_grads=True)
+    r = tower.gated_mlp(*wide, gw)
+    bars = _bars(wide[0], wide[1:4], wide[4:], gw, r)
+    step = 1e-4
+    for i, name in enumerate(GRADS):
+        way = np.sign(r[name]) * np.abs(wide[i]).mean()
+        loss = lambda s: float((tower.gated_mlp(*wide[:i], wide[i] + s * way, *wide[i + 1:])["out"] * gw).sum())
+        slope = (loss(step) - loss(-step)) / (2 * step)
+        bar = 1.05 * float((bars[name] * np.abs(way)).sum()) + 1e-6 * abs(slope)
+        assert abs(float((_wide(got[i]) * way).sum()) - slope) <= bar and bar < slope / 4, name
