@@ -427,3 +427,19 @@ def test_quantized_norm_and_product_from_its_definition(V):
     quotient = np.abs(r) / s.astype(np.float64)[:, None]
     middle = np.abs(quotient - np.floor(quotient) - 0.5)
     assert apart.max() <= 1 and (middle[apart > 0] <= 2 * rel * 128).all() and not q2[:, 1283:].any()
+
+
+def test_partial_sums_are_added_in_more_than_float32(V):
+    """256 rows over 256 workgroups, every partial sum one row's, exactly: the
+    weight's gradient is the sum rounded once, although a float32 one would lose
+    each 1 that is added to 2^24."""
+    _say("partial sums")
+    width = 1280
+    assert V.rms_norm_workspace_bytes(256, width) == 256 * width * 4
+    x = torch.ones((256, width), device="cuda")
+    dout = torch.ones((256, width), device="cuda")
+    dout[torch.arange(width) % 256, torch.arange(width)] = 2.0 ** 24
+    _, rstd = V.rms_norm(x, eps=0.0, return_rstd=True)
+    assert (rstd == 1).all()
+    dw = V.rms_norm_backward(dout, x, rstd, affine=True)[1]
+    assert torch.equal(dw, dout.double().sum(0).float()) and (dw == 2.0 ** 24 + 256).all()

@@ -20,8 +20,9 @@
 // in; outputs are rounded once.  For the backward pass g and u are kept in
 // float32: in bf16 their rounding would add half as much again to the error of
 // dx and the weights' gradients as the operands' own (relative to them 1.85
-// roundings instead of 1.41), and to the biases' gradients, which are float32
-// sums of unrounded dg and du, all of theirs.
+// roundings instead of 1.41), and to the biases' gradients, which are sums of
+// unrounded dg and du, all of theirs: float32 over a tile's rows (db_down: over
+// every 1024th row), and float64 over the tiles' sums.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
