@@ -442,3 +442,23 @@ def test_each_gradient_against_differences(V):
         slope = (loss(step) - loss(-step)) / (2 * step)
         bar = 1.05 * float((bars[name] * np.abs(way)).sum()) + 1e-6 * abs(slope)
         assert abs(float((_wide(got[i]) * way).sum()) - slope) <= bar and bar < slope / 4, name
+
+
+def test_without_the_inputs_gradient(V):
+    """dx left out: the other gradients' bits are the same, on another stream
+    too; made all the same where it is passed in."""
+    _say("without dx")
+    x, w, b, dout = _inputs(200, 72, 136, True, 5)
+    xd, wd, bd, gd = _dev(x), [_dev(t) for t in w], [_dev(t) for t in b], _dev(dout)
+    _, gate_up, hidden = V.gated_mlp(xd, *wd, *bd, return_saved=True)
+    want = V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, bias_grads=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {"stream": side}):
+        got = V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, bias_grads=True, input_grad=False, **kw)
+        side.synchronize()
+        assert got[0] is None and all(torch.equal(a, c) for a, c in zip(got[1:], want[1:]))
+    held = torch.full_like(xd, float("nan"))
+    got = V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, dx=held, weight_grads=False, input_grad=False)
+    assert got[0] is held and torch.equal(held, want[0]) and got[1:] == (None,) * 6
+    assert V.gated_mlp_backward(gd, xd, *wd, gate_up, hidden, weight_grads=False, input_grad=False) == (None,) * 7

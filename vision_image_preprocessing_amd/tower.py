@@ -685,14 +685,17 @@ def gated_mlp(x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, out=
 
 
 def gated_mlp_backward(dout, x, w_gate, w_up, w_down, gate_up, hidden, bias_grads: bool = False, dx=None, dw_gate=None, dw_up=None,
-                       dw_down=None, db_gate=None, db_up=None, db_down=None, weight_grads: bool = True, workspace=None, stream=None):
+                       dw_down=None, db_gate=None, db_up=None, db_down=None, weight_grads: bool = True, workspace=None, stream=None,
+                       input_grad: bool = True):
     """mimo_gated_mlp_backward: the gradients of gated_mlp's inputs for dout
     bf16 [rows, width], given its gate_up and hidden.
 
     Returns (dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down): bf16 of x's
-    and the weights' shapes, and float32 of the biases'.  The weights' gradients
-    are made unless weight_grads is False, the biases' with bias_grads=True;
-    apart from that, those that are passed in are made and the others are None.
+    and the weights' shapes, and float32 of the biases'.  dx is made unless
+    input_grad is False (where x needs no gradient, two of six products less),
+    the weights' gradients unless weight_grads is False, the biases' with
+    bias_grads=True; apart from that, those that are passed in are made and the
+    others are None.
     Gradients are overwritten.  ``workspace``: uint8, at least
     gated_mlp_backward_workspace_bytes(rows, width, hidden) bytes; calls that
     may run at the same time need one each.
@@ -718,8 +721,8 @@ def gated_mlp_backward(dout, x, w_gate, w_up, w_down, gate_up, hidden, bias_grad
     if stream is not None or _device_now() != index:
         with _entered(what, index, stream, tensors):
             return gated_mlp_backward(dout, x, w_gate, w_up, w_down, gate_up, hidden, bias_grads, dx, dw_gate, dw_up, dw_down, db_gate,
-                                      db_up, db_down, weight_grads, workspace)
-    if dx is None:
+                                      db_up, db_down, weight_grads, workspace, None, input_grad)
+    if dx is None and input_grad:
         dx = torch.empty_like(x)
     if weight_grads:
         dw_gate = torch.empty_like(w_gate) if dw_gate is None else dw_gate
