@@ -36,8 +36,8 @@ struct ColumnSums {
     }
 };
 
-// 1536 sums of 1280 columns, 8 MB: 5.6 to 6.4 us; 256 of two times 5120 and 128 of
-// 1280 6.5 (16 columns a workgroup 6.4 to 7.0 and 9.5, 8 columns 8 and 12.5).
+// 1536 sums of 1280 columns, 8 MB: 5.4 to 7.0 us; 256 of two times 5120 and 128 of
+// 1280 6.3 to 7.0 (16 columns a workgroup 6.4 to 7.0 and 9.5, 8 columns 8 and 12.5).
 __global__ __launch_bounds__(kSumColumns *kSumParts) void column_sums_kernel(ColumnSums a) {
     __shared__ double lds[kSumParts][kSumColumns + 1];
     int n = 0;

@@ -134,8 +134,10 @@ __device__ __forceinline__ u32x4 load_ragged(const uint16_t *p, int left) {
     return __builtin_bit_cast(u32x4, h);
 }
 
-// s = 1 / (1 + exp -g): the hardware's exponential and reciprocal, each to
-// about a unit in the last place of float32.
+// s = 1 / (1 + exp -g) by the hardware's exponential and reciprocal.  The
+// exponential is one of 2 of a float32 product, so its error grows with the
+// gate: at most (2 |g| + 2) 2^-24 relative, tens of units in the last place at g =
+// -80, where s is next to 0; it moves silu by 2 2^-24 at most, since g^2 s (1 - s) < 1.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // Which product of a launch a tile is of.
@@ -218,8 +220,8 @@ __global__ __launch_bounds__(Tile<kTile>::kThreads) void mlp_gate_kernel(MlpArgs
 // dg and du from dh = dout Wd and the saved g, u; partial sums of both over
 // the rows of each half of the tile.
 //
-// 32768 x 1280, hidden 5120: 586 to 619 us, 2.10 GB read, 1.34 of them g and u, and
-// 0.68 written, 4.5 to 4.7 TB/s: memory bounds it (tiles of 128 x 128, two
+// 32768 x 1280, hidden 5120: 566 to 619 us, 2.10 GB read, 1.34 of them g and u, and
+// 0.68 written, 4.5 to 4.9 TB/s: memory bounds it (tiles of 128 x 128, two
 // workgroups a CU, 652 to 665, of 64 x 64 901 to 928).  g and u stay on their way from one block of
 // rows to the next.
 template <int kTile>
@@ -457,8 +459,8 @@ __global__ __launch_bounds__(256) void mlp_columns_kernel(const uint16_t *x, int
 // A CU takes in about 25 GB/s of them, whatever waves and loads it has (80
 // workgroups of 16 channels: 4.2, 5.6, 9.0, 15.6 us for K 1280, 2560, 5120,
 // 10240), so what counts is that all CUs have as many channels.  4 rows of 1280,
-// hidden 5120: 7.6 us for gate and up, 26 MB at 3.4 TB/s, and 6.8 for down, 13 MB;
-// a launch that does nothing is 2 to 3 of each.
+// hidden 5120: medians of 7.7 to 8.9 us for gate and up (shortest 7.5), 26 MB at 2.9 to
+// 3.4 TB/s, 7.0 for down (6.1), 13 MB; a launch that does nothing is 2 to 3 of each.
 //
 // v_mfma_f32_16x16x32_bf16, weights first: lane l holds row l % 16 and k = 8 (l /
 // 16) .. + 7 of an operand, and channels 4 (l / 16) + r of x's row l % 16 of the
@@ -627,8 +629,10 @@ struct Sizes {
     // width 1280, hidden 5120: 1 row 12.4, 17.6; 16 rows 17.4, 17.8; 32 rows 24.6,
     // 18.1, each CU then taking in all of x twice; width 2048, hidden 2048: 17 rows
     // 13.0, 14.8, 32 rows 15.7, 15.3; width 264, hidden 520: 32 rows 7.2, 8.8; width 64,
-    // hidden 6000, whose second product has few channels: 4 rows 9.3, 10.8, 16 rows
-    // 12.5, 10.6.
+    // hidden 6000: 4 rows 9.3, 10.8, 16 rows 12.5, 10.6.  So the rule, of rows and hidden
+    // values alone, gives up to 2 us away where the second product has few channels
+    // (64: as many workgroups, each with all of K) and rows pass a handful, and half
+    // a microsecond at its upper corner.
     bool few() const { return rows <= 16 || (rows <= 32 && hp <= 8 * kCus); }
     int64_t ld() const { return pad_d ? dp : d; }   // of x, dout, the gate's and the up projection's weights
     int64_t lh() const { return pad_h ? hp : h; }   // of the down projection's weight
