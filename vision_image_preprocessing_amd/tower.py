@@ -565,7 +565,8 @@ def rotate_heads(x, cos, sin, inverse: bool = False, out=None, stream=None):
 
     x bf16 [rows, heads, head_dim], head_dim a multiple of 8, strides as
     chunk_attention takes them: query and key heads that are one slice of a
-    projection's output are one call.  Returns out, of x's shape; it may be x.
+    projection's output are one call.  Returns out, of x's shape; it may be x, or
+    other heads of x's array, but must not overlap x in part.
     """
     what = "rotate_heads"
     if x.dim() != 3:
